@@ -5,7 +5,10 @@ kernels of ``libozaki2.so`` behind the C ABI declared in ``include/ozaki2.h``.
 PyTorch supplies device memory and streams.  There is no CPU fallback: if
 the library is not built, loading it raises.
 
-Matrices follow the library's column-major convention: a (p, q) tensor with
+The layer operators (``linear``, ``dropout``, ``qk_norm_rope`` and their
+gradients) are in ``layers.py``; they are row-major.
+
+Matrices of the FP64 GEMM follow the library's column-major convention: a (p, q) tensor with
 strides (1, ld), ld >= p, is passed as is.  Any other layout (row-major,
 or a non-unit row stride) is first copied into a column-major tensor on the
 same device, so the library always sees column-major operands.
@@ -15,10 +18,13 @@ from __future__ import annotations
 import ctypes
 import os
 
+_LAYERS = ("ACTIVATIONS", "linear", "linear_backward", "dropout", "dropout_backward", "qk_norm_rope",
+           "qk_norm_rope_backward")  # layers.py
 __all__ = [
     "FAST", "ACCU", "Ozaki2Error", "load_library", "library_path", "moduli", "dgemm",
     "dgemm_debug", "dgemm_stages", "dgemm_host", "last_error", "workspace_release",
     "selftest_wait_timeout", "STAGE_NAMES", "profile_begin", "profile_end", "launch_count",
+    *_LAYERS,
 ]
 
 FAST = 0
@@ -279,3 +285,13 @@ def workspace_release() -> None:
 
 def selftest_wait_timeout(limit_us: int = 2000) -> int:
     return load_library().ozaki2_selftest_wait_timeout(int(limit_us))
+
+
+def __getattr__(name):
+    # the layer operators are loaded on first use: their module imports torch
+    if name in _LAYERS:
+        from . import layers
+
+        value = globals()[name] = getattr(layers, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -15,7 +15,8 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libozaki2.so")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
-SOURCES = ["oz2_api.cu", "oz2_prep.cu", "oz2_residue.cu", "oz2_gemm.cu", "oz2_crt.cu", "oz2_noalloc.cu"]
+SOURCES = ["oz2_api.cu", "oz2_prep.cu", "oz2_residue.cu", "oz2_gemm.cu", "oz2_crt.cu", "oz2_noalloc.cu",
+           "oz2_layers_api.cu", "oz2_linear.cu", "oz2_pointwise.cu", "oz2_qk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,7 +41,8 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB_PATH)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(os.path.dirname(PKG_DIR), "include", "ozaki2.h"))
+    include = os.path.join(os.path.dirname(PKG_DIR), "include")
+    deps += [os.path.join(include, f) for f in os.listdir(include)]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 

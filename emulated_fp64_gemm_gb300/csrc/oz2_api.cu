@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "oz2_internal.cuh"
+#include "oz2_layers.cuh"
 
 namespace oz2 {
 namespace {
@@ -761,6 +762,18 @@ const HostConsts* host_consts(int s) {
 }
 
 const int* greedy_moduli20() { return tables().moduli; }
+
+std::mutex& library_mutex() { return g_mutex; }
+
+oz2_status acquire_resources(cudaStream_t st, size_t bytes, DeviceResources* out) {
+  DeviceState* ds = nullptr;
+  const oz2_status e = device_state(&ds);
+  if (e != OZ2_OK) return e;
+  out->workspace = nullptr;
+  out->err = ds->err;
+  out->num_sms = ds->num_sms;
+  return bytes ? get_workspace(st, bytes, &out->workspace) : OZ2_OK;
+}
 
 }  // namespace oz2
 
