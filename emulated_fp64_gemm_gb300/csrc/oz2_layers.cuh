@@ -67,14 +67,22 @@ inline bool aligned16(const void* p, int64_t ld, oz2_dtype t) {
 }
 
 // ------------------------------------------------------------ launchers
-// C[i][j] = sum_k A(i, k) B(j, k), then the epilogue.  Operands are addressed
-// by the strides of their row and of k, in elements.
+// C[i][j] = sum_k A(i, k) B(j, k), then the epilogue.  An operand is a
+// row-major matrix of 16-bit elements whose rows start on 16-byte boundaries:
+// [rows][k], or [k][rows] with rows_contiguous.
 struct Operand {
   const void* p;
-  int64_t row_stride, k_stride;
+  int64_t ld;
+  bool rows_contiguous;
 };
-cudaError_t launch_linear_strided(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
-                                  cudaStream_t st);
+// Bytes of `partial` that a product needs.
+size_t linear_workspace(int64_t k, const Epilogue& ep, int num_sms);
+// B is rows_contiguous wherever A is.
+cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
+                          const DeviceResources& res, float* partial, cudaStream_t st);
+
+// A copy of a 16-bit matrix whose rows are ld_out (a multiple of 8) elements apart.
+cudaError_t launch_pack(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* out, int64_t ld_out, cudaStream_t st);
 
 cudaError_t launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                            void* y, int64_t ldy, oz2_dtype dtype, const Dropout& drop, cudaStream_t st);

@@ -1,5 +1,6 @@
 // C ABI of the layer operators: argument checks, workspace and the choice of
 // kernels.
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -32,14 +33,48 @@ Dropout make_dropout(double p, uint64_t seed, uint64_t offset) {
   return d;
 }
 
-size_t round256(size_t bytes) { return (bytes + 255) / 256 * 256; }
+// Regions of the workspace, on 256-byte boundaries: sizes are collected first, addresses given out afterwards.
+struct Carver {
+  size_t used = 0;
+  size_t take(size_t bytes) {
+    const size_t at = used;
+    used += (bytes + 255) / 256 * 256;
+    return at;
+  }
+};
+
+// A 16-bit matrix on its way into a product.  Rows that do not start on 16-byte
+// boundaries are copied into the workspace first: one more read and write of
+// the operand, for which the product itself has one fast form only.
+struct Input {
+  const void* p;
+  int64_t rows, cols, ld;
+  bool copy;
+  size_t at;
+
+  Input(const void* p_, int64_t rows_, int64_t cols_, int64_t ld_, bool used, Carver& c)
+      : p(p_), rows(rows_), cols(cols_), ld(rows_ > 1 ? ld_ : ceil_div(cols_, 8) * 8), copy(false), at(0) {
+    copy = used && rows > 0 && cols > 0 && !aligned16(p, ld, OZ2_BF16);
+    if (copy) {
+      ld = ceil_div(cols, 8) * 8;
+      at = c.take(static_cast<size_t>(rows) * ld * 2);
+    }
+  }
+  // `from`'s leading dimension before the copy
+  cudaError_t place(uint8_t* base, int64_t from_ld, cudaStream_t st) {
+    if (!copy) return cudaSuccess;
+    const void* from = p;
+    p = base + at;
+    return launch_pack(rows, cols, from, from_ld, base + at, ld, st);
+  }
+};
 
 oz2_status linear(int64_t m, int64_t k, int64_t n, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
                   const void* residual, int64_t ldr, void* y, int64_t ldy, void* preact, int64_t ldz, oz2_dtype dtype,
                   oz2_act act, double dropout, uint64_t seed, uint64_t offset, cudaStream_t st) {
   if (m == 0 || n == 0) return OZ2_OK;
   DeviceResources res;
-  const oz2_status e = acquire_resources(st, 0, &res);
+  oz2_status e = acquire_resources(st, 0, &res);
   if (e != OZ2_OK) return e;
   Epilogue ep{};
   ep.bias = bias;
@@ -55,7 +90,15 @@ oz2_status linear(int64_t m, int64_t k, int64_t n, const void* x, int64_t ldx, c
   ep.drop = make_dropout(dropout, seed, offset);
   ep.vec = aligned16(y, ldy, dtype) && (!bias || aligned16(bias, 0, dtype)) &&
            (!residual || aligned16(residual, ldr, dtype)) && (!preact || aligned16(preact, ldz, dtype));
-  OZ2_TRY(launch_linear_strided(Operand{x, ldx, 1}, Operand{w, ldw, 1}, k, ep, dtype, st));
+  Carver c;
+  Input xi(x, m, k, ldx, true, c), wi(w, n, k, ldw, true, c);
+  const size_t partial = c.take(linear_workspace(k, ep, res.num_sms));
+  e = acquire_resources(st, c.used, &res);
+  if (e != OZ2_OK) return e;
+  OZ2_TRY(xi.place(res.workspace, ldx, st));
+  OZ2_TRY(wi.place(res.workspace, ldw, st));
+  OZ2_TRY(launch_linear(Operand{xi.p, xi.ld, false}, Operand{wi.p, wi.ld, false}, k, ep, dtype, res,
+                        reinterpret_cast<float*>(res.workspace + partial), st));
   return OZ2_OK;
 }
 
@@ -75,13 +118,8 @@ oz2_status linear_backward(int64_t m, int64_t k, int64_t n, const void* dy, int6
                            int64_t lddw, void* dbias, oz2_dtype dtype, oz2_act act, double dropout, uint64_t seed,
                            uint64_t offset, cudaStream_t st) {
   const Dropout drop = make_dropout(dropout, seed, offset);
-  // dz is dy itself where nothing follows the product
-  const bool make_dz = (act != OZ2_ACT_NONE || drop.threshold != 0) && (dx || dw);
-  const int64_t lddz = ceil_div(n, 8) * 8;
-  const size_t dz_bytes = make_dz ? round256(static_cast<size_t>(m) * lddz * 2) : 0;
-  const size_t partial_bytes = dbias ? round256(static_cast<size_t>(dz_partial_rows(m, n)) * n * 4) : 0;
   DeviceResources res;
-  const oz2_status e = acquire_resources(st, dz_bytes + partial_bytes, &res);
+  oz2_status e = acquire_resources(st, 0, &res);
   if (e != OZ2_OK) return e;
   // sums over nothing
   if (m == 0 || n == 0) {
@@ -90,8 +128,21 @@ oz2_status linear_backward(int64_t m, int64_t k, int64_t n, const void* dy, int6
     if (dbias && n > 0) OZ2_TRY(cudaMemsetAsync(dbias, 0, n * 2, st));
     return OZ2_OK;
   }
-  const void* dz = dy;
-  int64_t ld = lddy;
+  if (k == 0) dx = dw = nullptr;
+  // dz is dy itself where nothing follows the product and its rows are aligned
+  const bool products = dx || dw;
+  const bool make_dz = products && (act != OZ2_ACT_NONE || drop.threshold != 0 || !aligned16(dy, lddy, dtype));
+  const int64_t ld = make_dz ? ceil_div(n, 8) * 8 : lddy;
+  Carver c;
+  const size_t dz_at = c.take(make_dz ? static_cast<size_t>(m) * ld * 2 : 0);
+  const size_t sums_at = c.take(dbias ? static_cast<size_t>(dz_partial_rows(m, n)) * n * 4 : 0);
+  Input xi(x, m, k, ldx, dw, c), wi(w, n, k, ldw, dx, c);
+  const Epilogue ep_dx = plain_epilogue(dx, lddx, m, k, dtype), ep_dw = plain_epilogue(dw, lddw, n, k, dtype);
+  // the two products run one after the other and share the room for partial sums
+  const size_t partial_at = c.take(std::max(dx ? linear_workspace(n, ep_dx, res.num_sms) : 0,
+                                            dw ? linear_workspace(m, ep_dw, res.num_sms) : 0));
+  e = acquire_resources(st, c.used, &res);
+  if (e != OZ2_OK) return e;
   if (make_dz || dbias) {
     DzArgs a{};
     a.m = m;
@@ -100,23 +151,20 @@ oz2_status linear_backward(int64_t m, int64_t k, int64_t n, const void* dy, int6
     a.lddy = lddy;
     a.preact = preact;
     a.ldz = ldz;
-    a.dz = make_dz ? res.workspace : nullptr;
-    a.lddz = lddz;
+    a.dz = make_dz ? res.workspace + dz_at : nullptr;
+    a.lddz = ld;
     a.dbias = dbias;
-    a.partial = reinterpret_cast<float*>(res.workspace + dz_bytes);
+    a.partial = reinterpret_cast<float*>(res.workspace + sums_at);
     a.act = act;
     a.drop = drop;
     OZ2_TRY(launch_dz(a, dtype, st));
-    if (make_dz) {
-      dz = res.workspace;
-      ld = lddz;
-    }
   }
-  if (k == 0) return OZ2_OK;
-  if (dx)
-    OZ2_TRY(launch_linear_strided(Operand{dz, ld, 1}, Operand{w, 1, ldw}, n, plain_epilogue(dx, lddx, m, k, dtype), dtype, st));
-  if (dw)
-    OZ2_TRY(launch_linear_strided(Operand{dz, 1, ld}, Operand{x, 1, ldx}, m, plain_epilogue(dw, lddw, n, k, dtype), dtype, st));
+  const void* dz = make_dz ? res.workspace + dz_at : dy;
+  float* partial = reinterpret_cast<float*>(res.workspace + partial_at);
+  OZ2_TRY(xi.place(res.workspace, ldx, st));
+  OZ2_TRY(wi.place(res.workspace, ldw, st));
+  if (dx) OZ2_TRY(launch_linear(Operand{dz, ld, false}, Operand{wi.p, wi.ld, true}, n, ep_dx, dtype, res, partial, st));
+  if (dw) OZ2_TRY(launch_linear(Operand{dz, ld, true}, Operand{xi.p, xi.ld, true}, m, ep_dw, dtype, res, partial, st));
   return OZ2_OK;
 }
 

@@ -1,70 +1,412 @@
-// The linear products y = epilogue(x w^T), dx = dz w and dw = dz^T x with any
-// strides, on the general-purpose cores.
+// The linear products on the 5th-generation tensor cores: C = A B^T in 16-bit
+// operands and 32-bit sums, with a linear layer's epilogue fused behind it.
 //
-// C[i][j] = sum_k A(i, k) B(j, k).  A block of 256 threads forms a 64 x 64
-// tile: 16 terms of both operands at a time go through shared memory as 32-bit
-// values, and each thread keeps two rows of eight neighbouring columns in
-// registers, which is the epilogue's unit.  Bound by the FMA pipe and shared
-// memory.
+// C[i][j] = sum_k A(i, k) B(j, k).  The three products of a layer differ only
+// in which direction of an operand is contiguous in memory, and the tensor
+// core takes both: forward (x, w) has k contiguous in both operands, dx
+// (dz, w) has it in A only, dw (dz, x) in neither.  So nothing is transposed.
+//
+// Structure: a cluster of two CTAs on two SMs forms 256 x 256 tiles with
+// tcgen05.mma.cta_group::2, each CTA holding 128 rows of A and 128 of B's 256
+// rows in shared memory (six stages of 64 k) and 128 x 256 sums in tensor
+// memory, twice: while the epilogue warps empty one accumulator, the tensor
+// core fills the other.  Warp 0 loads by TMA, one lane of the leader's warp 1
+// issues the MMAs, warps 2-9 are the epilogue (two per tensor-memory lane
+// quadrant, 128 columns each).  The grid is persistent: one pair per two SMs,
+// walking over the work units.
+//
+// Epilogue: a warp moves 32 x 32 sums at a time through 4 KB of shared memory
+// of its own, so that each lane ends up with eight neighbouring columns of a
+// row (16 bytes of output, one generator call) and four lanes with 64
+// contiguous bytes.
+//
+// Bound by the tensor pipe for large products.  Where the tiles do not fill the
+// pairs evenly, the last ones are split along k: their partial sums go to the
+// workspace in 32 bits and linear_join_kernel adds them in order and finishes
+// them, so the result does not depend on timing.
+//
+// Every wait is bounded in time; a timeout sets the device error word and the
+// kernel winds down.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <type_traits>
+
 #include "oz2_layers.cuh"
+#include "oz2_pair.cuh"
+#include "oz2_tcgen05.cuh"
 
 namespace oz2 {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
+constexpr int kBK = 64;                        // k per stage: 128 bytes
+constexpr int kStages = 6;
+constexpr int kOperandBytes = 128 * kBK * 2;   // a CTA's share of one operand per stage
+constexpr int kStageTx = 4 * kOperandBytes;    // bytes landing per stage across the pair
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kSmem = 1024 + kStages * 2 * kOperandBytes + kEpiWarps * 4096 + 256;
+constexpr int kTileFloats = 256 * 256;
 
-template <typename T>
-__device__ __forceinline__ void stage_tile(const Operand& o, int64_t row0, int64_t rows, int64_t k0, int64_t k,
-                                           float (*s)[kTile + 4]) {
-  // neighbouring threads take neighbouring elements of the contiguous direction
-  const bool k_fast = o.k_stride == 1;
-#pragma unroll
-  for (int u = 0; u < kTile * kDepth / 256; ++u) {
-    const int e = u * 256 + threadIdx.x;
-    const int r = k_fast ? e / kDepth : e % kTile, kk = k_fast ? e % kDepth : e / kTile;
-    const int64_t row = row0 + r, at = k0 + kk;
-    s[kk][r] = row < rows && at < k
-                   ? Elem<T>::up(static_cast<const T*>(o.p)[row * o.row_stride + at * o.k_stride]) : 0.0f;
+struct GemmParams {
+  Epilogue ep;
+  int tiles_m, tiles_n, nkb;
+  int full;      // the first `full` tiles are whole units, the others `splits` units each
+  int splits;
+  int units;
+  float* partial;  // [(tile - full) * splits + split][256][256]
+  int* err;
+};
+
+struct Unit {
+  int tm, tn, kb0, kb1;
+  int slot;  // partial slot, -1: finished by this unit
+};
+
+// Tiles follow a raster of eight row tiles per group, so that the operands in flight stay in L2.
+__device__ __forceinline__ void tile_position(int tile, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int per_group = 8 * tiles_n, g = tile / per_group, at = tile % per_group, rows = min(tiles_m - g * 8, 8);
+  tm = g * 8 + at % rows;
+  tn = at / rows;
+}
+
+__device__ __forceinline__ Unit decode_unit(int u, const GemmParams& p) {
+  Unit U;
+  int tile = u;
+  U.kb0 = 0;
+  U.kb1 = p.nkb;
+  U.slot = -1;
+  if (u >= p.full) {
+    U.slot = u - p.full;
+    tile = p.full + U.slot / p.splits;
+    const int s = U.slot % p.splits;
+    U.kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * s / p.splits);
+    U.kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (s + 1) / p.splits);
+  }
+  tile_position(tile, p.tiles_m, p.tiles_n, U.tm, U.tn);
+  return U;
+}
+
+// This CTA's 128 rows of an operand, 64 k: one box of 64 k x 128 rows, or, with
+// the rows contiguous in memory, two boxes of 64 rows x 64 k.
+template <bool ROWS_CONTIGUOUS>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int row, int kb, uint32_t bar) {
+  if (ROWS_CONTIGUOUS) {
+    tma_load_2d_pair(dst, map, row, kb * kBK, bar);
+    tma_load_2d_pair(dst + kOperandBytes / 2, map, row + 64, kb * kBK, bar);
+  } else {
+    tma_load_2d_pair(dst, map, kb * kBK, row, bar);
   }
 }
 
+// Shared-memory descriptor of 16 k at step s of a stage.  k contiguous: rows of
+// 128 bytes, 8-row groups 1024 bytes apart, 32 bytes per step.  Rows contiguous:
+// lines of 64 rows (128 bytes) for one k, groups of 8 k 1024 bytes apart, the
+// next 64 rows 8192 bytes on, 16 lines per step.
+template <bool ROWS_CONTIGUOUS>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int s) {
+  if (!ROWS_CONTIGUOUS) return smem_desc(base + s * 32);
+  return (smem_desc(base + s * 2048) & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(kOperandBytes / 2 >> 4) << 16);
+}
+
+// The epilogue of a 32 x 32 block at (row0, col0): lane l takes eight columns of rows l / 4, l / 4 + 8, ...
 template <typename T>
-__global__ void __launch_bounds__(256) linear_strided_kernel(const Operand a, const Operand b, int64_t k, int64_t tiles_n,
-                                                             const Epilogue ep) {
-  __shared__ float sa[kDepth][kTile + 4], sb[kDepth][kTile + 4];
-  const int64_t row0 = blockIdx.x / tiles_n * kTile, col0 = blockIdx.x % tiles_n * kTile;
-  const int r = threadIdx.x / 8, c = threadIdx.x % 8 * 8;  // rows r and r + 32, columns c .. c + 7 of the tile
-  float v[2][8] = {};
-  for (int64_t k0 = 0; k0 < k; k0 += kDepth) {
-    stage_tile<T>(a, row0, ep.rows, k0, k, sa);
-    stage_tile<T>(b, col0, ep.cols, k0, k, sb);
-    __syncthreads();
+__device__ __forceinline__ void finish_block(const Epilogue& e, const float* tile, int lane, int64_t row0, int64_t col0) {
+  const int64_t col = col0 + (lane & 3) * 8;
 #pragma unroll
-    for (int kk = 0; kk < kDepth; ++kk)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[h][i] = fmaf(sa[kk][r + 32 * h], sb[kk][c + i], v[h][i]);
-    __syncthreads();
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    if (row0 + r < e.rows && col < e.cols) {
+      float v[8];
+      get_eight(tile, r, lane & 3, v);
+      epilogue8<T>(e, row0 + r, col, v);
+    }
   }
+}
+
+// The block's sums as they are, into a partial tile.
+__device__ __forceinline__ void save_block(float* partial, const float* tile, int lane, int row0, int col0) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (row0 + r + 32 * h < ep.rows && col0 + c < ep.cols) epilogue8<T>(ep, row0 + r + 32 * h, col0 + c, v[h]);
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    float v[8];
+    get_eight(tile, r, lane & 3, v);
+    store8(partial + (row0 + r) * 256 + col0 + (lane & 3) * 8, true, 8, v);
+  }
+}
+
+template <typename T, bool A_ROWS, bool B_ROWS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                       const __grid_constant__ GemmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_a = smem;
+  uint8_t* s_b = s_a + kStages * kOperandBytes;
+  uint8_t* s_epi = s_b + kStages * kOperandBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_epi + kEpiWarps * 4096);  // [kStages] used in the leader only
+  uint64_t* empty = full + kStages;                                        // [kStages] in both CTAs
+  uint64_t* acc_full = empty + kStages;                                    // [2] in both CTAs
+  uint64_t* acc_empty = acc_full + 2;                                      // [2] used in the leader only
+  uint64_t* drain = acc_empty + 2;                                         // leader
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&acc_full[i]), 1);
+      mbar_init(smem_u32(&acc_empty[i]), 2 * kEpiWarps);  // one lane per epilogue warp, both CTAs
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  // both CTAs run before the collective allocation, and both have their barriers before any remote signal
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = pair; u < p.units && ok; u += pairs) {
+        const Unit U = decode_unit(u, p);
+        const int row_a = U.tm * 256 + static_cast<int>(rank) * 128, row_b = U.tn * 256 + static_cast<int>(rank) * 128;
+        for (int kb = U.kb0; kb < U.kb1; ++kb) {
+          if (!mbar_wait_cluster_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = smem_u32(&full[stage]), bar_leader = map_to_rank(bar, 0);
+          if (leader) mbar_arrive_expect_tx(bar, kStageTx);
+          load_operand<A_ROWS>(smem_u32(s_a + stage * kOperandBytes), &map_a, row_a, kb, bar_leader);
+          load_operand<B_ROWS>(smem_u32(s_b + stage * kOperandBytes), &map_b, row_b, kb, bar_leader);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(p.err, kErrTimeout);
+        // copies in flight land before the block ends
+        volatile int never = 0;
+        if (leader) mbar_wait_bounded(smem_u32(&full[(stage + kStages - 1) % kStages]), stage ? phase : phase ^ 1, &never, kDrainLimitNs);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs (leader only)
+    if (leader && lane == 0) {
+      // kind::f16: 32-bit sums, both operands of type T, M = 256 (the pair), N = 256
+      constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      constexpr uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(A_ROWS) << 15) |
+                                 (static_cast<uint32_t>(B_ROWS) << 16) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
+      int stage = 0, n = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = pair; u < p.units && ok; u += pairs, ++n) {
+        const Unit U = decode_unit(u, p);
+        const int slot = n & 1;
+        if (!mbar_wait_cluster_bounded(smem_u32(&acc_empty[slot]), ((n >> 1) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = U.kb0; kb < U.kb1; ++kb) {
+          if (!mbar_wait_cluster_bounded(smem_u32(&full[stage]), phase, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(s_a + stage * kOperandBytes), b = smem_u32(s_b + stage * kOperandBytes);
+#pragma unroll
+          for (int s = 0; s < kBK / 16; ++s)
+            mma_f16_pair(tmem + slot * 256, operand_desc<A_ROWS>(a, s), operand_desc<B_ROWS>(b, s), idesc,
+                         kb == U.kb0 && s == 0 ? 0u : 1u);
+          mma_commit_pair(smem_u32(&empty[stage]));
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) mma_commit_pair(smem_u32(&acc_full[slot]));
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(p.err, kErrTimeout);
+      }
+      mma_commit_pair(smem_u32(drain));
+      mbar_wait_bounded(smem_u32(drain), 0, abort_flag, kWaitLimitNs);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int quad = warp & 3, half = (warp - 2) >> 2;  // the lanes this warp may read; its 128 columns
+    float* tile = reinterpret_cast<float*>(s_epi + (warp - 2) * 4096);
+    bool ok = true;
+    int n = 0;
+    for (int u = pair; u < p.units; u += pairs, ++n) {
+      const Unit U = decode_unit(u, p);
+      const int slot = n & 1;
+      const bool got = mbar_wait_cluster_bounded(smem_u32(&acc_full[slot]), (n >> 1) & 1, abort_flag, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, got)) {  // warp-uniform: the tensor-memory loads below are .aligned
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int local_row = static_cast<int>(rank) * 128 + quad * 32;
+#pragma unroll 1
+      for (int cb = 0; cb < 4; ++cb) {
+        uint32_t v[32];
+        const int local_col = half * 128 + cb * 32;
+        tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + slot * 256 + local_col, v);
+        tmem_wait_ld();
+        if (cb == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[slot]), 0));
+        }
+        put_block(tile, lane, v);
+        __syncwarp();
+        if (U.slot < 0)
+          finish_block<T>(p.ep, tile, lane, static_cast<int64_t>(U.tm) * 256 + local_row, static_cast<int64_t>(U.tn) * 256 + local_col);
+        else
+          save_block(p.partial + static_cast<int64_t>(U.slot) * kTileFloats, tile, lane, local_row, local_col);
+        __syncwarp();
+      }
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      atomicOr(p.err, kErrTimeout);
+    }
+  }
+
+  __syncthreads();
+  cluster_sync_all();  // the leader's MMAs are done with both CTAs' shared and tensor memory
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// Adds the partial sums of the split tiles in order and finishes them: one
+// thread per eight columns, a warp per row of a tile.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ GemmParams p) {
+  const int tile = blockIdx.x / 32, lane = threadIdx.x & 31, row = blockIdx.x % 32 * 8 + (threadIdx.x >> 5);
+  int tm, tn;
+  tile_position(p.full + tile, p.tiles_m, p.tiles_n, tm, tn);
+  const int64_t r = static_cast<int64_t>(tm) * 256 + row, c = static_cast<int64_t>(tn) * 256 + lane * 8;
+  if (r >= p.ep.rows || c >= p.ep.cols) return;
+  const float* at = p.partial + static_cast<int64_t>(tile) * p.splits * kTileFloats + row * 256 + lane * 8;
+  float v[8] = {};
+  for (int s = 0; s < p.splits; ++s, at += kTileFloats) {
+    float add[8];
+    load8(at, true, 8, add);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += add[i];
+  }
+  epilogue8<T>(p.ep, r, c, v);
+}
+
+// ------------------------------------------------------------------ host side
+bool make_map(CUtensorMap* map, const Operand& o, int64_t rows, int64_t k) {
+  return o.rows_contiguous ? encode_map_2d(map, o.p, rows, k, o.ld, 64, kBK) : encode_map_2d(map, o.p, k, rows, o.ld, kBK, 128);
+}
+
+// How to spread `tiles` of nkb k blocks over the pairs: `full` whole tiles, the
+// others split `splits` ways.  Times in k blocks of one tile on one pair (0.27 us
+// at 1.9 GHz): a wave of units lasts its longest unit, each unit adds about one
+// block of pipeline fill, and joining costs a launch (about 12 blocks) and the
+// partial sums' way through L2 (about 0.25 blocks per slot and pair-load).
+void plan_units(int tiles, int nkb, int pairs, int* full, int* splits) {
+  auto waves = [&](int units) { return (units + pairs - 1) / pairs; };
+  *full = nkb ? tiles : 0;
+  *splits = nkb ? 1 : 0;  // no terms: nothing but the epilogue
+  double best = waves(tiles) * (nkb + 1.0);
+  for (int f = tiles / pairs * pairs; f >= 0 && f >= tiles - 3 * pairs; f -= pairs) {
+    const int rest = tiles - f;
+    if (rest == 0) continue;
+    for (int s = 2; s <= 32 && s * 4 <= nkb; ++s) {
+      if (static_cast<int64_t>(rest) * s > 4 * pairs) break;
+      const double cost = f / pairs * (nkb + 1.0) + waves(rest * s) * ((nkb + s - 1) / s + 1.0) + 12 + 0.25 * rest * s;
+      if (cost < best) {
+        best = cost;
+        *full = f;
+        *splits = s;
+      }
+    }
+  }
+}
+
+GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms) {
+  GemmParams p{};
+  p.ep = ep;
+  p.tiles_m = static_cast<int>(ceil_div(ep.rows, 256));
+  p.tiles_n = static_cast<int>(ceil_div(ep.cols, 256));
+  p.nkb = static_cast<int>(ceil_div(k, kBK));
+  plan_units(p.tiles_m * p.tiles_n, p.nkb, num_sms / 2, &p.full, &p.splits);
+  p.units = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
+  return p;
+}
+
+template <typename T, bool A_ROWS, bool B_ROWS>
+cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p, int num_sms, cudaStream_t st) {
+  auto kernel = linear_gemm_kernel<T, A_ROWS, B_ROWS>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  kernel<<<2 * std::min(p.units, num_sms / 2), kThreads, kSmem, st>>>(ma, mb, p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_typed(const Operand& a, const Operand& b, const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p,
+                         int num_sms, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (p.units > 0)
+    e = a.rows_contiguous   ? launch_product<T, true, true>(ma, mb, p, num_sms, st)
+        : b.rows_contiguous ? launch_product<T, false, true>(ma, mb, p, num_sms, st)
+                            : launch_product<T, false, false>(ma, mb, p, num_sms, st);
+  const int join = p.tiles_m * p.tiles_n - p.full;
+  if (e != cudaSuccess || join == 0) return e;
+  linear_join_kernel<T><<<join * 32, 256, 0, st>>>(p);
+  count_launches(1);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_linear_strided(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
-                                  cudaStream_t st) {
-  const int64_t tiles_n = ceil_div(ep.cols, kTile), tiles = ceil_div(ep.rows, kTile) * tiles_n;
-  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const unsigned grid = static_cast<unsigned>(tiles);
-  if (dtype == OZ2_BF16)
-    linear_strided_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a, b, k, tiles_n, ep);
-  else
-    linear_strided_kernel<__half><<<grid, 256, 0, st>>>(a, b, k, tiles_n, ep);
-  count_launches(1);
-  return cudaGetLastError();
+size_t linear_workspace(int64_t k, const Epilogue& ep, int num_sms) {
+  const GemmParams p = make_params(k, ep, num_sms);
+  return static_cast<size_t>(p.tiles_m * p.tiles_n - p.full) * p.splits * kTileFloats * 4;
+}
+
+cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
+                               const DeviceResources& res, float* partial, cudaStream_t st) {
+  if (ceil_div(ep.rows, 256) * ceil_div(ep.cols, 256) > (1 << 24)) return cudaErrorInvalidConfiguration;
+  GemmParams p = make_params(k, ep, res.num_sms);
+  p.partial = partial;
+  p.err = res.err;
+  CUtensorMap ma{}, mb{};
+  if (k > 0 && (!make_map(&ma, a, ep.rows, k) || !make_map(&mb, b, ep.cols, k))) return cudaErrorInvalidValue;
+  return dtype == OZ2_BF16 ? launch_typed<__nv_bfloat16>(a, b, ma, mb, p, res.num_sms, st)
+                           : launch_typed<__half>(a, b, ma, mb, p, res.num_sms, st);
 }
 
 }  // namespace oz2

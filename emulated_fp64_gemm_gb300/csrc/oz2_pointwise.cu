@@ -2,6 +2,8 @@
 // layer's pre-activation with its column sums.  Both are one pass over their
 // matrices, in groups of eight neighbouring columns: one 16-byte vector of a
 // 16-bit type and one call of the generator.
+#include <algorithm>
+
 #include "oz2_layers.cuh"
 
 namespace oz2 {
@@ -32,19 +34,37 @@ __global__ void __launch_bounds__(256) dropout_kernel(uint32_t groups, FastDiv p
   store8(y + row * ldy + col, vec, n, v);
 }
 
+// Group numbers of one launch stay below 2^31 (FastDiv): rows per launch.
+int64_t rows_per_launch(int64_t per_row) { return (int64_t(1) << 30) / per_row; }
+
 template <typename T>
 cudaError_t dropout_impl(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                          void* y, int64_t ldy, bool aligned, const Dropout& drop, cudaStream_t st) {
-  const int64_t per_row = ceil_div(cols, 8);
-  const int64_t most = (int64_t(1) << 30) / per_row;  // rows per launch: group numbers stay below 2^31
+  const int64_t per_row = ceil_div(cols, 8), most = rows_per_launch(per_row);
   for (int64_t row0 = 0; row0 < rows; row0 += most) {
-    const uint32_t groups = static_cast<uint32_t>((rows - row0 < most ? rows - row0 : most) * per_row);
+    const uint32_t groups = static_cast<uint32_t>(std::min(rows - row0, most) * per_row);
     dropout_kernel<T><<<(groups + 255) / 256, 256, 0, st>>>(
         groups, make_fast_div(static_cast<uint32_t>(per_row)), row0, cols, static_cast<const T*>(x), ldx,
         static_cast<const T*>(residual), ldr, static_cast<T*>(y), ldy, aligned, drop);
     count_launches(1);
   }
   return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ aligned copies
+// Rows that do not start on 16-byte boundaries cannot be loaded by TMA: they
+// are copied once, eight elements per thread.
+__global__ void __launch_bounds__(256) pack_kernel(uint32_t groups, FastDiv per_row, int64_t row0, int64_t cols,
+                                                   const uint16_t* x, int64_t ldx, uint16_t* out, int64_t ld_out) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= groups) return;
+  const uint32_t r = (__umulhi(i, per_row.mul) + i) >> per_row.shift;
+  const int64_t row = row0 + r, col = static_cast<int64_t>(i - r * per_row.d) * 8;
+  uint32_t v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = col + e < cols ? x[row * ldx + col + e] : 0u;
+  *reinterpret_cast<uint4*>(out + row * ld_out + col) =
+      make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 
 // ------------------------------------------------------------------ dz and its column sums
@@ -129,6 +149,17 @@ cudaError_t launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t ld
     case OZ2_F16: return dropout_impl<__half>(rows, cols, x, ldx, residual, ldr, y, ldy, aligned, drop, st);
     default: return dropout_impl<float>(rows, cols, x, ldx, residual, ldr, y, ldy, aligned, drop, st);
   }
+}
+
+cudaError_t launch_pack(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* out, int64_t ld_out, cudaStream_t st) {
+  const int64_t per_row = ceil_div(cols, 8), most = rows_per_launch(per_row);
+  for (int64_t row0 = 0; row0 < rows; row0 += most) {
+    const uint32_t groups = static_cast<uint32_t>(std::min(rows - row0, most) * per_row);
+    pack_kernel<<<(groups + 255) / 256, 256, 0, st>>>(groups, make_fast_div(static_cast<uint32_t>(per_row)), row0, cols,
+                                                      static_cast<const uint16_t*>(x), ldx, static_cast<uint16_t*>(out), ld_out);
+    count_launches(1);
+  }
+  return cudaGetLastError();
 }
 
 cudaError_t launch_dz(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
