@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libozaki2.so")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 SOURCES = ["oz2_api.cu", "oz2_prep.cu", "oz2_residue.cu", "oz2_gemm.cu", "oz2_crt.cu", "oz2_noalloc.cu",
-           "oz2_layers_api.cu", "oz2_linear.cu", "oz2_pointwise.cu", "oz2_qk.cu"]
+           "oz2_layers_api.cu", "oz2_linear.cu", "oz2_linear_few.cu", "oz2_pointwise.cu", "oz2_qk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

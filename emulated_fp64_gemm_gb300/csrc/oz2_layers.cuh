@@ -76,10 +76,15 @@ struct Operand {
   bool rows_contiguous;
 };
 // Bytes of `partial` that a product needs.
-size_t linear_workspace(int64_t k, const Epilogue& ep, int num_sms);
+size_t linear_workspace(const Operand& a, int64_t k, const Epilogue& ep, int num_sms);
 // B is rows_contiguous wherever A is.
 cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
                           const DeviceResources& res, float* partial, cudaStream_t st);
+
+// The form for few rows of A, which launch_linear takes where it can.
+bool linear_few_supported(const Operand& a, int64_t k, const Epilogue& ep);
+cudaError_t launch_linear_few(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
+                              const DeviceResources& res, cudaStream_t st);
 
 // A copy of a 16-bit matrix whose rows are ld_out (a multiple of 8) elements apart.
 cudaError_t launch_pack(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* out, int64_t ld_out, cudaStream_t st);
@@ -106,23 +111,11 @@ struct DzArgs {
 };
 cudaError_t launch_dz(const DzArgs& a, oz2_dtype dtype, cudaStream_t st);
 
-struct QkArgs {
-  int64_t tokens;
-  int dim, rot;
-  oz2_heads q, k, q_out, k_out;      // backward: q, k the inputs, q_out / k_out the inputs' gradients
-  oz2_heads dq_out, dk_out;          // backward only
-  const void *q_weight, *k_weight;
-  const float *cos, *sin;
-  int64_t table_rows;
-  const int64_t* positions;
-  float eps;
-  int interleaved;
-  void *dq_weight, *dk_weight;       // backward only, may be null
-  float* partial;                    // backward only: qk_partial_rows() x 2 dim floats
-};
-int64_t qk_partial_rows(int64_t tokens, int64_t heads, int num_sms);
-cudaError_t launch_qk(const QkArgs& a, oz2_dtype dtype, cudaStream_t st);
-cudaError_t launch_qk_backward(const QkArgs& a, oz2_dtype dtype, int64_t partial_rows, cudaStream_t st);
+cudaError_t launch_qk(const oz2_qk_args& a, const DeviceResources& res, cudaStream_t st);
+// Blocks of the backward pass, each with a row of 2 dim floats in `partial`
+// (null: the weights' gradients are not formed).
+int64_t qk_partial_rows(const oz2_qk_args& a, int num_sms);
+cudaError_t launch_qk_backward(const oz2_qk_args& a, int64_t rows, float* partial, cudaStream_t st);
 
 }  // namespace oz2
 

@@ -69,35 +69,34 @@ struct Input {
   }
 };
 
-oz2_status linear(int64_t m, int64_t k, int64_t n, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
-                  const void* residual, int64_t ldr, void* y, int64_t ldy, void* preact, int64_t ldz, oz2_dtype dtype,
-                  oz2_act act, double dropout, uint64_t seed, uint64_t offset, cudaStream_t st) {
-  if (m == 0 || n == 0) return OZ2_OK;
+oz2_status linear(const oz2_linear_args& a, cudaStream_t st) {
+  if (a.m == 0 || a.n == 0) return OZ2_OK;
+  const oz2_dtype dtype = static_cast<oz2_dtype>(a.dtype);
   DeviceResources res;
   oz2_status e = acquire_resources(st, 0, &res);
   if (e != OZ2_OK) return e;
   Epilogue ep{};
-  ep.bias = bias;
-  ep.residual = residual;
-  ep.y = y;
-  ep.z = preact;
-  ep.ldr = ldr;
-  ep.ldy = ldy;
-  ep.ldz = ldz;
-  ep.rows = m;
-  ep.cols = n;
-  ep.act = act;
-  ep.drop = make_dropout(dropout, seed, offset);
-  ep.vec = aligned16(y, ldy, dtype) && (!bias || aligned16(bias, 0, dtype)) &&
-           (!residual || aligned16(residual, ldr, dtype)) && (!preact || aligned16(preact, ldz, dtype));
+  ep.bias = a.bias;
+  ep.residual = a.residual;
+  ep.y = a.y;
+  ep.z = a.preact;
+  ep.ldr = a.ldr;
+  ep.ldy = a.ldy;
+  ep.ldz = a.ldz;
+  ep.rows = a.m;
+  ep.cols = a.n;
+  ep.act = a.act;
+  ep.drop = make_dropout(a.dropout, a.seed, a.offset);
+  ep.vec = aligned16(a.y, a.ldy, dtype) && (!a.bias || aligned16(a.bias, 0, dtype)) &&
+           (!a.residual || aligned16(a.residual, a.ldr, dtype)) && (!a.preact || aligned16(a.preact, a.ldz, dtype));
   Carver c;
-  Input xi(x, m, k, ldx, true, c), wi(w, n, k, ldw, true, c);
-  const size_t partial = c.take(linear_workspace(k, ep, res.num_sms));
+  Input xi(a.x, a.m, a.k, a.ldx, true, c), wi(a.w, a.n, a.k, a.ldw, true, c);
+  const size_t partial = c.take(linear_workspace(Operand{xi.p, xi.ld, false}, a.k, ep, res.num_sms));
   e = acquire_resources(st, c.used, &res);
   if (e != OZ2_OK) return e;
-  OZ2_TRY(xi.place(res.workspace, ldx, st));
-  OZ2_TRY(wi.place(res.workspace, ldw, st));
-  OZ2_TRY(launch_linear(Operand{xi.p, xi.ld, false}, Operand{wi.p, wi.ld, false}, k, ep, dtype, res,
+  OZ2_TRY(xi.place(res.workspace, a.ldx, st));
+  OZ2_TRY(wi.place(res.workspace, a.ldw, st));
+  OZ2_TRY(launch_linear(Operand{xi.p, xi.ld, false}, Operand{wi.p, wi.ld, false}, a.k, ep, dtype, res,
                         reinterpret_cast<float*>(res.workspace + partial), st));
   return OZ2_OK;
 }
@@ -113,71 +112,114 @@ Epilogue plain_epilogue(void* out, int64_t ld, int64_t rows, int64_t cols, oz2_d
   return ep;
 }
 
-oz2_status linear_backward(int64_t m, int64_t k, int64_t n, const void* dy, int64_t lddy, const void* x, int64_t ldx,
-                           const void* w, int64_t ldw, const void* preact, int64_t ldz, void* dx, int64_t lddx, void* dw,
-                           int64_t lddw, void* dbias, oz2_dtype dtype, oz2_act act, double dropout, uint64_t seed,
-                           uint64_t offset, cudaStream_t st) {
-  const Dropout drop = make_dropout(dropout, seed, offset);
+oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
+  const int64_t m = a.m, k = a.k, n = a.n;
+  const oz2_dtype dtype = static_cast<oz2_dtype>(a.dtype);
+  void *dx = a.dx, *dw = a.dw, *dbias = a.dbias;
+  const Dropout drop = make_dropout(a.dropout, a.seed, a.offset);
   DeviceResources res;
   oz2_status e = acquire_resources(st, 0, &res);
   if (e != OZ2_OK) return e;
   // sums over nothing
   if (m == 0 || n == 0) {
-    if (dx && m > 0 && k > 0) OZ2_TRY(cudaMemset2DAsync(dx, lddx * 2, 0, k * 2, m, st));
-    if (dw && n > 0 && k > 0) OZ2_TRY(cudaMemset2DAsync(dw, lddw * 2, 0, k * 2, n, st));
+    if (dx && m > 0 && k > 0) OZ2_TRY(cudaMemset2DAsync(dx, a.lddx * 2, 0, k * 2, m, st));
+    if (dw && n > 0 && k > 0) OZ2_TRY(cudaMemset2DAsync(dw, a.lddw * 2, 0, k * 2, n, st));
     if (dbias && n > 0) OZ2_TRY(cudaMemsetAsync(dbias, 0, n * 2, st));
     return OZ2_OK;
   }
   if (k == 0) dx = dw = nullptr;
   // dz is dy itself where nothing follows the product and its rows are aligned
   const bool products = dx || dw;
-  const bool make_dz = products && (act != OZ2_ACT_NONE || drop.threshold != 0 || !aligned16(dy, lddy, dtype));
-  const int64_t ld = make_dz ? ceil_div(n, 8) * 8 : lddy;
+  const bool make_dz = products && (a.act != OZ2_ACT_NONE || drop.threshold != 0 || !aligned16(a.dy, a.lddy, dtype));
+  const int64_t ld = make_dz ? ceil_div(n, 8) * 8 : a.lddy;
   Carver c;
   const size_t dz_at = c.take(make_dz ? static_cast<size_t>(m) * ld * 2 : 0);
   const size_t sums_at = c.take(dbias ? static_cast<size_t>(dz_partial_rows(m, n)) * n * 4 : 0);
-  Input xi(x, m, k, ldx, dw, c), wi(w, n, k, ldw, dx, c);
-  const Epilogue ep_dx = plain_epilogue(dx, lddx, m, k, dtype), ep_dw = plain_epilogue(dw, lddw, n, k, dtype);
+  Input xi(a.x, m, k, a.ldx, dw, c), wi(a.w, n, k, a.ldw, dx, c);
+  const Epilogue ep_dx = plain_epilogue(dx, a.lddx, m, k, dtype), ep_dw = plain_epilogue(dw, a.lddw, n, k, dtype);
   // the two products run one after the other and share the room for partial sums
-  const size_t partial_at = c.take(std::max(dx ? linear_workspace(n, ep_dx, res.num_sms) : 0,
-                                            dw ? linear_workspace(m, ep_dw, res.num_sms) : 0));
+  const size_t partial_at = c.take(std::max(dx ? linear_workspace(Operand{nullptr, ld, false}, n, ep_dx, res.num_sms) : 0,
+                                            dw ? linear_workspace(Operand{nullptr, ld, true}, m, ep_dw, res.num_sms) : 0));
   e = acquire_resources(st, c.used, &res);
   if (e != OZ2_OK) return e;
   if (make_dz || dbias) {
-    DzArgs a{};
-    a.m = m;
-    a.n = n;
-    a.dy = dy;
-    a.lddy = lddy;
-    a.preact = preact;
-    a.ldz = ldz;
-    a.dz = make_dz ? res.workspace + dz_at : nullptr;
-    a.lddz = ld;
-    a.dbias = dbias;
-    a.partial = reinterpret_cast<float*>(res.workspace + sums_at);
-    a.act = act;
-    a.drop = drop;
-    OZ2_TRY(launch_dz(a, dtype, st));
+    DzArgs d{};
+    d.m = m;
+    d.n = n;
+    d.dy = a.dy;
+    d.lddy = a.lddy;
+    d.preact = a.act == OZ2_ACT_NONE ? nullptr : a.preact;
+    d.ldz = a.ldz;
+    d.dz = make_dz ? res.workspace + dz_at : nullptr;
+    d.lddz = ld;
+    d.dbias = dbias;
+    d.partial = reinterpret_cast<float*>(res.workspace + sums_at);
+    d.act = a.act;
+    d.drop = drop;
+    OZ2_TRY(launch_dz(d, dtype, st));
   }
-  const void* dz = make_dz ? res.workspace + dz_at : dy;
+  const void* dz = make_dz ? res.workspace + dz_at : a.dy;
   float* partial = reinterpret_cast<float*>(res.workspace + partial_at);
-  OZ2_TRY(xi.place(res.workspace, ldx, st));
-  OZ2_TRY(wi.place(res.workspace, ldw, st));
+  OZ2_TRY(xi.place(res.workspace, a.ldx, st));
+  OZ2_TRY(wi.place(res.workspace, a.ldw, st));
   if (dx) OZ2_TRY(launch_linear(Operand{dz, ld, false}, Operand{wi.p, wi.ld, true}, n, ep_dx, dtype, res, partial, st));
   if (dw) OZ2_TRY(launch_linear(Operand{dz, ld, true}, Operand{xi.p, xi.ld, true}, m, ep_dw, dtype, res, partial, st));
   return OZ2_OK;
 }
+
+oz2_status dropout(const oz2_dropout_args& a, cudaStream_t st) {
+  if (a.rows == 0 || a.cols == 0) return OZ2_OK;
+  DeviceResources res;
+  const oz2_status e = acquire_resources(st, 0, &res);
+  if (e != OZ2_OK) return e;
+  OZ2_TRY(launch_dropout(a.rows, a.cols, a.x, a.ldx, a.residual, a.ldr, a.y, a.ldy, static_cast<oz2_dtype>(a.dtype),
+                         make_dropout(a.dropout, a.seed, a.offset), st));
+  return OZ2_OK;
+}
+
+oz2_status qk(const oz2_qk_args& a, cudaStream_t st) {
+  if (a.tokens == 0 || a.q.heads + a.k.heads == 0) return OZ2_OK;
+  DeviceResources res;
+  const oz2_status e = acquire_resources(st, 0, &res);
+  if (e != OZ2_OK) return e;
+  OZ2_TRY(launch_qk(a, res, st));
+  return OZ2_OK;
+}
+
+oz2_status qk_backward(const oz2_qk_args& a, cudaStream_t st) {
+  DeviceResources res;
+  oz2_status e = acquire_resources(st, 0, &res);
+  if (e != OZ2_OK) return e;
+  if (a.tokens == 0 || a.q.heads + a.k.heads == 0) {  // sums over nothing
+    const size_t bytes = a.dim * dtype_bytes(static_cast<oz2_dtype>(a.dtype));
+    if (a.dq_weight) OZ2_TRY(cudaMemsetAsync(a.dq_weight, 0, bytes, st));
+    if (a.dk_weight) OZ2_TRY(cudaMemsetAsync(a.dk_weight, 0, bytes, st));
+    return OZ2_OK;
+  }
+  const int64_t rows = qk_partial_rows(a, res.num_sms);
+  float* partial = nullptr;
+  if (a.dq_weight || a.dk_weight) {
+    e = acquire_resources(st, static_cast<size_t>(rows) * 2 * a.dim * 4, &res);
+    if (e != OZ2_OK) return e;
+    partial = reinterpret_cast<float*>(res.workspace);
+  }
+  OZ2_TRY(launch_qk_backward(a, rows, partial, st));
+  return OZ2_OK;
+}
+
+bool dtype_ok(int t) { return t >= OZ2_BF16 && t <= OZ2_F32; }
+bool act_ok(int t) { return t >= OZ2_ACT_NONE && t <= OZ2_ACT_GELU_TANH; }
 
 bool side_ok(const oz2_heads& h, int64_t tokens, int64_t heads) {
   return h.heads == heads && heads >= 0 && heads <= (1 << 20) && h.token_stride >= 0 && h.head_stride >= 0 &&
          (h.data != nullptr || heads == 0 || tokens == 0);
 }
 
-bool qk_ok(const QkArgs& a, double eps, int dtype) {
+bool qk_ok(const oz2_qk_args& a) {
   return size_ok(a.tokens) && a.dim >= 1 && a.dim <= OZ2_HEAD_DIM_MAX && a.rot >= 0 && a.rot <= a.dim && a.rot % 2 == 0 &&
-         dtype >= OZ2_BF16 && dtype <= OZ2_F32 && side_ok(a.q, a.tokens, a.q.heads) && side_ok(a.k, a.tokens, a.k.heads) &&
+         dtype_ok(a.dtype) && side_ok(a.q, a.tokens, a.q.heads) && side_ok(a.k, a.tokens, a.k.heads) &&
          side_ok(a.q_out, a.tokens, a.q.heads) && side_ok(a.k_out, a.tokens, a.k.heads) &&
-         (a.q_weight || a.q.heads == 0) && (a.k_weight || a.k.heads == 0) && eps >= 0.0 && a.table_rows >= 0 &&
+         (a.q_weight || a.q.heads == 0) && (a.k_weight || a.k.heads == 0) && a.eps >= 0.0 && a.table_rows >= 0 &&
          (a.rot == 0 || a.tokens == 0 || (a.cos && a.sin && a.positions));
 }
 
@@ -201,132 +243,46 @@ using namespace oz2;
 
 extern "C" {
 
-oz2_status ozaki2_linear(int64_t m, int64_t k, int64_t n, const void* x, int64_t ldx, const void* w, int64_t ldw,
-                         const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy, void* preact,
-                         int64_t ldz, oz2_dtype dtype, oz2_act act, double dropout, uint64_t seed, uint64_t offset,
-                         void* stream) {
-  if (!size_ok(m) || !size_ok(k) || !size_ok(n) || !is_16bit(dtype) || act < OZ2_ACT_NONE || act > OZ2_ACT_GELU_TANH ||
-      !dropout_ok(dropout) || !matrix_ok(x, m, k, ldx) || !matrix_ok(w, n, k, ldw) || !matrix_ok(y, m, n, ldy) ||
-      (residual && ldr < n) || (preact && ldz < n))
+oz2_status ozaki2_linear(const oz2_linear_args* args, void* stream) {
+  if (!args) return OZ2_ERR_INVALID_ARG;
+  const oz2_linear_args& a = *args;
+  if (!size_ok(a.m) || !size_ok(a.k) || !size_ok(a.n) || !is_16bit(a.dtype) || !act_ok(a.act) || !dropout_ok(a.dropout) ||
+      !matrix_ok(a.x, a.m, a.k, a.ldx) || !matrix_ok(a.w, a.n, a.k, a.ldw) || !matrix_ok(a.y, a.m, a.n, a.ldy) ||
+      (a.residual && a.ldr < a.n) || (a.preact && a.ldz < a.n))
     return OZ2_ERR_INVALID_ARG;
-  return guarded([&] {
-    return linear(m, k, n, x, ldx, w, ldw, bias, residual, ldr, y, ldy, preact, ldz, dtype, act, dropout, seed, offset,
-                  static_cast<cudaStream_t>(stream));
-  });
+  return guarded([&] { return linear(a, static_cast<cudaStream_t>(stream)); });
 }
 
-oz2_status ozaki2_linear_backward(int64_t m, int64_t k, int64_t n, const void* dy, int64_t lddy, const void* x,
-                                  int64_t ldx, const void* w, int64_t ldw, const void* preact, int64_t ldz, void* dx,
-                                  int64_t lddx, void* dw, int64_t lddw, void* dbias, oz2_dtype dtype, oz2_act act,
-                                  double dropout, uint64_t seed, uint64_t offset, void* stream) {
-  if (!size_ok(m) || !size_ok(k) || !size_ok(n) || !is_16bit(dtype) || act < OZ2_ACT_NONE || act > OZ2_ACT_GELU_TANH ||
-      !dropout_ok(dropout) || !matrix_ok(dy, m, n, lddy) || (dw && !matrix_ok(x, m, k, ldx)) ||
-      (dx && !matrix_ok(w, n, k, ldw)) || (act != OZ2_ACT_NONE && !matrix_ok(preact, m, n, ldz)) || (dx && lddx < k) ||
-      (dw && lddw < k))
+oz2_status ozaki2_linear_backward(const oz2_linear_backward_args* args, void* stream) {
+  if (!args) return OZ2_ERR_INVALID_ARG;
+  const oz2_linear_backward_args& a = *args;
+  if (!size_ok(a.m) || !size_ok(a.k) || !size_ok(a.n) || !is_16bit(a.dtype) || !act_ok(a.act) || !dropout_ok(a.dropout) ||
+      !matrix_ok(a.dy, a.m, a.n, a.lddy) || (a.dw && !matrix_ok(a.x, a.m, a.k, a.ldx)) ||
+      (a.dx && !matrix_ok(a.w, a.n, a.k, a.ldw)) || (a.act != OZ2_ACT_NONE && !matrix_ok(a.preact, a.m, a.n, a.ldz)) ||
+      (a.dx && a.lddx < a.k) || (a.dw && a.lddw < a.k))
     return OZ2_ERR_INVALID_ARG;
-  return guarded([&] {
-    return linear_backward(m, k, n, dy, lddy, x, ldx, w, ldw, act == OZ2_ACT_NONE ? nullptr : preact, ldz, dx, lddx, dw,
-                           lddw, dbias, dtype, act, dropout, seed, offset, static_cast<cudaStream_t>(stream));
-  });
+  return guarded([&] { return linear_backward(a, static_cast<cudaStream_t>(stream)); });
 }
 
-oz2_status ozaki2_dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
-                          void* y, int64_t ldy, oz2_dtype dtype, double dropout, uint64_t seed, uint64_t offset,
-                          void* stream) {
-  if (!size_ok(rows) || !size_ok(cols) || dtype < OZ2_BF16 || dtype > OZ2_F32 || !dropout_ok(dropout) ||
-      !matrix_ok(x, rows, cols, ldx) || !matrix_ok(y, rows, cols, ldy) || (residual && ldr < cols))
+oz2_status ozaki2_dropout(const oz2_dropout_args* args, void* stream) {
+  if (!args) return OZ2_ERR_INVALID_ARG;
+  const oz2_dropout_args& a = *args;
+  if (!size_ok(a.rows) || !size_ok(a.cols) || !dtype_ok(a.dtype) || a.reserved != 0 || !dropout_ok(a.dropout) ||
+      !matrix_ok(a.x, a.rows, a.cols, a.ldx) || !matrix_ok(a.y, a.rows, a.cols, a.ldy) || (a.residual && a.ldr < a.cols))
     return OZ2_ERR_INVALID_ARG;
-  return guarded([&] {
-    if (rows == 0 || cols == 0) return OZ2_OK;
-    DeviceResources res;
-    const oz2_status e = acquire_resources(static_cast<cudaStream_t>(stream), 0, &res);
-    if (e != OZ2_OK) return e;
-    OZ2_TRY(launch_dropout(rows, cols, x, ldx, residual, ldr, y, ldy, dtype, make_dropout(dropout, seed, offset),
-                           static_cast<cudaStream_t>(stream)));
-    return OZ2_OK;
-  });
+  return guarded([&] { return dropout(a, static_cast<cudaStream_t>(stream)); });
 }
 
-oz2_status ozaki2_qk_norm_rope(int64_t tokens, int64_t dim, int64_t rot, oz2_heads q, oz2_heads k, const void* q_weight,
-                               const void* k_weight, const float* cos, const float* sin, int64_t table_rows,
-                               const int64_t* positions, double eps, int interleaved, oz2_dtype dtype, oz2_heads q_out,
-                               oz2_heads k_out, void* stream) {
-  if (dim < 0 || dim > OZ2_HEAD_DIM_MAX || rot < 0 || rot > dim) return OZ2_ERR_INVALID_ARG;
-  QkArgs a{};
-  a.tokens = tokens;
-  a.dim = static_cast<int>(dim);
-  a.rot = static_cast<int>(rot);
-  a.q = q;
-  a.k = k;
-  a.q_out = q_out;
-  a.k_out = k_out;
-  a.q_weight = q_weight;
-  a.k_weight = k_weight;
-  a.cos = cos;
-  a.sin = sin;
-  a.table_rows = table_rows;
-  a.positions = positions;
-  a.eps = static_cast<float>(eps);
-  a.interleaved = interleaved != 0;
-  if (!qk_ok(a, eps, dtype)) return OZ2_ERR_INVALID_ARG;
-  return guarded([&] {
-    if (tokens == 0 || q.heads + k.heads == 0) return OZ2_OK;
-    DeviceResources res;
-    const oz2_status e = acquire_resources(static_cast<cudaStream_t>(stream), 0, &res);
-    if (e != OZ2_OK) return e;
-    OZ2_TRY(launch_qk(a, dtype, static_cast<cudaStream_t>(stream)));
-    return OZ2_OK;
-  });
+oz2_status ozaki2_qk_norm_rope(const oz2_qk_args* args, void* stream) {
+  if (!args || !qk_ok(*args)) return OZ2_ERR_INVALID_ARG;
+  return guarded([&] { return qk(*args, static_cast<cudaStream_t>(stream)); });
 }
 
-oz2_status ozaki2_qk_norm_rope_backward(int64_t tokens, int64_t dim, int64_t rot, oz2_heads dq_out, oz2_heads dk_out,
-                                        oz2_heads q, oz2_heads k, const void* q_weight, const void* k_weight,
-                                        const float* cos, const float* sin, int64_t table_rows,
-                                        const int64_t* positions, double eps, int interleaved, oz2_dtype dtype,
-                                        oz2_heads dq, oz2_heads dk, void* dq_weight, void* dk_weight, void* stream) {
-  if (dim < 0 || dim > OZ2_HEAD_DIM_MAX || rot < 0 || rot > dim) return OZ2_ERR_INVALID_ARG;
-  QkArgs a{};
-  a.tokens = tokens;
-  a.dim = static_cast<int>(dim);
-  a.rot = static_cast<int>(rot);
-  a.q = q;
-  a.k = k;
-  a.q_out = dq;
-  a.k_out = dk;
-  a.dq_out = dq_out;
-  a.dk_out = dk_out;
-  a.q_weight = q_weight;
-  a.k_weight = k_weight;
-  a.cos = cos;
-  a.sin = sin;
-  a.table_rows = table_rows;
-  a.positions = positions;
-  a.eps = static_cast<float>(eps);
-  a.interleaved = interleaved != 0;
-  a.dq_weight = dq_weight;
-  a.dk_weight = dk_weight;
-  if (!qk_ok(a, eps, dtype) || !side_ok(dq_out, tokens, q.heads) || !side_ok(dk_out, tokens, k.heads))
+oz2_status ozaki2_qk_norm_rope_backward(const oz2_qk_args* args, void* stream) {
+  if (!args || !qk_ok(*args) || !side_ok(args->dq_out, args->tokens, args->q.heads) ||
+      !side_ok(args->dk_out, args->tokens, args->k.heads))
     return OZ2_ERR_INVALID_ARG;
-  return guarded([&] {
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool none = tokens == 0 || q.heads + k.heads == 0, weights = dq_weight || dk_weight;
-    DeviceResources res;
-    oz2_status e = acquire_resources(st, 0, &res);
-    if (e != OZ2_OK) return e;
-    if (none) {
-      if (dq_weight) OZ2_TRY(cudaMemsetAsync(dq_weight, 0, dim * dtype_bytes(dtype), st));
-      if (dk_weight) OZ2_TRY(cudaMemsetAsync(dk_weight, 0, dim * dtype_bytes(dtype), st));
-      return OZ2_OK;
-    }
-    const int64_t rows = qk_partial_rows(tokens, q.heads + k.heads, res.num_sms);
-    if (weights) {
-      e = acquire_resources(st, static_cast<size_t>(rows) * 2 * dim * 4, &res);
-      if (e != OZ2_OK) return e;
-      a.partial = reinterpret_cast<float*>(res.workspace);
-    }
-    OZ2_TRY(launch_qk_backward(a, dtype, rows, st));
-    return OZ2_OK;
-  });
+  return guarded([&] { return qk_backward(*args, static_cast<cudaStream_t>(stream)); });
 }
 
 }  // extern "C"

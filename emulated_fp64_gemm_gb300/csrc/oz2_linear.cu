@@ -100,16 +100,6 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 
-// Shared-memory descriptor of 16 k at step s of a stage.  k contiguous: rows of
-// 128 bytes, 8-row groups 1024 bytes apart, 32 bytes per step.  Rows contiguous:
-// lines of 64 rows (128 bytes) for one k, groups of 8 k 1024 bytes apart, the
-// next 64 rows 8192 bytes on, 16 lines per step.
-template <bool ROWS_CONTIGUOUS>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int s) {
-  if (!ROWS_CONTIGUOUS) return smem_desc(base + s * 32);
-  return (smem_desc(base + s * 2048) & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(kOperandBytes / 2 >> 4) << 16);
-}
-
 // The epilogue of a 32 x 32 block at (row0, col0): lane l takes eight columns of rows l / 4, l / 4 + 8, ...
 template <typename T>
 __device__ __forceinline__ void finish_block(const Epilogue& e, const float* tile, int lane, int64_t row0, int64_t col0) {
@@ -392,13 +382,15 @@ cudaError_t launch_typed(const Operand& a, const Operand& b, const CUtensorMap& 
 
 }  // namespace
 
-size_t linear_workspace(int64_t k, const Epilogue& ep, int num_sms) {
+size_t linear_workspace(const Operand& a, int64_t k, const Epilogue& ep, int num_sms) {
+  if (linear_few_supported(a, k, ep)) return 0;
   const GemmParams p = make_params(k, ep, num_sms);
   return static_cast<size_t>(p.tiles_m * p.tiles_n - p.full) * p.splits * kTileFloats * 4;
 }
 
 cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
                                const DeviceResources& res, float* partial, cudaStream_t st) {
+  if (linear_few_supported(a, k, ep)) return launch_linear_few(a, b, k, ep, dtype, res, st);
   if (ceil_div(ep.rows, 256) * ceil_div(ep.cols, 256) > (1 << 24)) return cudaErrorInvalidConfiguration;
   GemmParams p = make_params(k, ep, res.num_sms);
   p.partial = partial;

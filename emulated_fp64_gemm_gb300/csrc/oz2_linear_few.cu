@@ -1,0 +1,279 @@
+// The linear products of few rows (a serving batch's single tokens): C = A B^T
+// with at most 128 rows of A, on the tensor cores with the roles exchanged.
+//
+// The weights B are the big operand and are read once, so the floor is their
+// bytes.  A CTA takes 128 of B's rows as the MMA's M dimension and all rows of
+// A, padded to MP, as its N dimension (tcgen05.mma.cta_group::1); the weights
+// come through a ring of TMA stages that fills the SM's shared memory, which
+// keeps tens of megabytes in flight over the device.  A cluster of CTAs splits
+// k: each forms its partial sums in tensor memory, puts them into its shared
+// memory, and every CTA then adds its share of the outputs from all of them, in
+// the order of their ranks, through distributed shared memory, and finishes it.
+// So there is one launch, no workspace, and no result that depends on timing.
+//
+// Every wait is bounded in time; a timeout sets the device error word and the
+// kernel winds down.
+#include <algorithm>
+#include <type_traits>
+
+#include "oz2_layers.cuh"
+#include "oz2_pair.cuh"
+#include "oz2_tcgen05.cuh"
+
+namespace oz2 {
+namespace {
+
+constexpr int kBK = 64;
+constexpr int kTileN = 128;  // rows of B per CTA
+constexpr int kThreads = 128;
+constexpr int kWBytes = kTileN * kBK * 2;
+
+template <int MP>
+struct Few {
+  static constexpr int X_BYTES = MP * kBK * 2;
+  static constexpr int STAGES = std::min(11, 196 * 1024 / (kWBytes + X_BYTES));
+  static constexpr int SMEM = 1024 + STAGES * (kWBytes + X_BYTES) + 256;
+  static constexpr int TMEM_COLS = MP < 32 ? 32 : MP;
+  static_assert(MP * kTileN * 4 <= STAGES * (kWBytes + X_BYTES), "the partial sums take the stages' place");
+};
+
+struct FewParams {
+  Epilogue ep;
+  int nkb;
+  int* err;
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void load_cluster4(uint32_t addr, float* v) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// W_ROWS: B is [k][rows] (its rows contiguous in memory).
+template <typename T, int MP, bool W_ROWS>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ FewParams p) {
+  using F = Few<MP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_w = smem;
+  uint8_t* s_x = s_w + F::STAGES * kWBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_x + F::STAGES * F::X_BYTES);
+  uint64_t* empty = full + F::STAGES;
+  uint64_t* done = empty + F::STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
+  const int row_w = static_cast<int>(blockIdx.x / ranks) * kTileN;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / ranks);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / ranks);
+
+  auto load_stage = [&](int stage, int kb) {
+    const uint32_t bar = smem_u32(&full[stage]), w = smem_u32(s_w + stage * kWBytes);
+    mbar_arrive_expect_tx(bar, kWBytes + F::X_BYTES);
+    if (W_ROWS) {
+      tma_load_2d(w, &map_w, row_w, kb * kBK, bar);
+      tma_load_2d(w + kWBytes / 2, &map_w, row_w + 64, kb * kBK, bar);
+    } else {
+      tma_load_2d(w, &map_w, kb * kBK, row_w, bar);
+    }
+    tma_load_2d(smem_u32(s_x + stage * F::X_BYTES), &map_x, kb * kBK, 0, bar);
+  };
+
+  const int ahead = min(F::STAGES, kb1 - kb0);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < F::STAGES; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    mbar_init(smem_u32(done), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    // the first loads need nothing that the other warps set up
+    for (int i = 0; i < ahead; ++i) load_stage(i, kb0 + i);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(F::TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = ahead;
+      for (int kb = kb0 + ahead; kb < kb1; ++kb, ++issued) {
+        const int stage = issued % F::STAGES;
+        if (!mbar_wait_bounded(smem_u32(&empty[stage]), (issued / F::STAGES - 1) & 1, abort_flag, kWaitLimitNs)) {
+          *abort_flag = 1;
+          atomicOr(p.err, kErrTimeout);
+          break;
+        }
+        load_stage(stage, kb);
+      }
+      if (*abort_flag) {  // copies in flight land before the block ends
+        volatile int never = 0;
+        for (int i = max(0, issued - F::STAGES); i < issued; ++i)
+          mbar_wait_bounded(smem_u32(&full[i % F::STAGES]), (i / F::STAGES) & 1, &never, kDrainLimitNs);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // kind::f16: 32-bit sums, both operands of type T, M = 128, N = MP
+      constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      constexpr uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(W_ROWS) << 15) |
+                                 (static_cast<uint32_t>(MP >> 3) << 17) | ((128u >> 4) << 24);
+      for (int i = 0; i < kb1 - kb0; ++i) {
+        const int stage = i % F::STAGES;
+        if (!mbar_wait_bounded(smem_u32(&full[stage]), (i / F::STAGES) & 1, abort_flag, kWaitLimitNs)) {
+          *abort_flag = 1;
+          atomicOr(p.err, kErrTimeout);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t w = smem_u32(s_w + stage * kWBytes), x = smem_u32(s_x + stage * F::X_BYTES);
+#pragma unroll
+        for (int s = 0; s < kBK / 16; ++s)
+          mma_f16(tmem, operand_desc<W_ROWS>(w, s), operand_desc<false>(x, s), idesc, i == 0 && s == 0 ? 0u : 1u);
+        mma_commit(smem_u32(&empty[stage]));
+      }
+      mma_commit(smem_u32(done));
+    }
+  }
+  __syncwarp();
+  if (!mbar_wait_bounded(smem_u32(done), 0, abort_flag, kWaitLimitNs)) {
+    *abort_flag = 1;
+    atomicOr(p.err, kErrTimeout);
+  }
+  __syncthreads();
+  tc_fence_after();
+  // every MMA and so every load is done: the sums take the stages' place, as [row of A][row of B]
+  float* sums = reinterpret_cast<float*>(smem);
+  const int rows = static_cast<int>(p.ep.rows);
+#pragma unroll 1
+  for (int c = 0; c < rows; c += 32) {
+    uint32_t v[32];
+    tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i < rows) sums[(c + i) * kTileN + threadIdx.x] = __uint_as_float(v[i]);
+  }
+  tc_fence_before();
+  if (ranks > 1) cluster_sync_all(); else __syncthreads();
+  // groups of eight columns, shared out among the ranks
+  const int items = rows * (kTileN / 8), per_rank = (items + ranks - 1) / ranks;
+  const int end = min(items, (rank + 1) * per_rank);
+  for (int i = rank * per_rank + static_cast<int>(threadIdx.x); i < end; i += kThreads) {
+    const int r = i / (kTileN / 8), g = i % (kTileN / 8);
+    const int64_t col = row_w + g * 8;
+    if (col >= p.ep.cols) continue;
+    const uint32_t at = smem_u32(sums + r * kTileN + g * 8);
+    float v[8] = {};
+    for (int s = 0; s < ranks; ++s) {
+      const uint32_t from = map_to_rank(at, s);
+      float add[8];
+      load_cluster4(from, add);
+      load_cluster4(from + 16, add + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += add[e];
+    }
+    epilogue8<T>(p.ep, r, col, v);
+  }
+  if (ranks > 1) cluster_sync_all(); else __syncthreads();  // the peers have read this CTA's sums
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F::TMEM_COLS) : "memory");
+  }
+}
+
+// CTAs per cluster: as many as the device has room for beside the tiles, each with two k blocks at least.
+int cluster_for(int64_t tiles, int nkb, int num_sms) {
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= num_sms && nkb >= s * 4) s *= 2;
+  return s;
+}
+
+template <typename T, int MP, bool W_ROWS>
+cudaError_t launch_few_impl(const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p, int64_t tiles, int ranks,
+                            cudaStream_t st) {
+  auto kernel = linear_few_kernel<T, MP, W_ROWS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<MP>::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Few<MP>::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, mx, mw, p);
+  count_launches(1);
+  return e;
+}
+
+template <typename T, int MP>
+cudaError_t launch_few_mp(const Operand& x, const Operand& w, int64_t k, FewParams& p, int num_sms, cudaStream_t st) {
+  const int64_t tiles = ceil_div(p.ep.cols, kTileN);
+  CUtensorMap mx, mw;
+  if (!encode_map_2d(&mx, x.p, k, p.ep.rows, x.ld, kBK, MP)) return cudaErrorInvalidValue;
+  if (w.rows_contiguous) {
+    if (!encode_map_2d(&mw, w.p, p.ep.cols, k, w.ld, 64, kBK)) return cudaErrorInvalidValue;
+    return launch_few_impl<T, MP, true>(mx, mw, p, tiles, cluster_for(tiles, p.nkb, num_sms), st);
+  }
+  if (!encode_map_2d(&mw, w.p, k, p.ep.cols, w.ld, kBK, kTileN)) return cudaErrorInvalidValue;
+  return launch_few_impl<T, MP, false>(mx, mw, p, tiles, cluster_for(tiles, p.nkb, num_sms), st);
+}
+
+template <typename T>
+cudaError_t launch_few_typed(const Operand& x, const Operand& w, int64_t k, FewParams& p, int num_sms, cudaStream_t st) {
+  const int64_t m = p.ep.rows;
+  if (m <= 16) return launch_few_mp<T, 16>(x, w, k, p, num_sms, st);
+  if (m <= 32) return launch_few_mp<T, 32>(x, w, k, p, num_sms, st);
+  if (m <= 64) return launch_few_mp<T, 64>(x, w, k, p, num_sms, st);
+  return launch_few_mp<T, 128>(x, w, k, p, num_sms, st);
+}
+
+}  // namespace
+
+bool linear_few_supported(const Operand& a, int64_t k, const Epilogue& ep) {
+  return !a.rows_contiguous && k > 0 && ep.rows <= 128;
+}
+
+cudaError_t launch_linear_few(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
+                              const DeviceResources& res, cudaStream_t st) {
+  FewParams p{};
+  p.ep = ep;
+  p.nkb = static_cast<int>(ceil_div(k, kBK));
+  p.err = res.err;
+  return dtype == OZ2_BF16 ? launch_few_typed<__nv_bfloat16>(a, b, k, p, res.num_sms, st)
+                           : launch_few_typed<__half>(a, b, k, p, res.num_sms, st);
+}
+
+}  // namespace oz2

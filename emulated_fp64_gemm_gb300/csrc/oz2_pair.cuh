@@ -1,4 +1,4 @@
-// CTA-pair (tcgen05 cta_group::2) and TMA helpers of the linear products
+// CTA-pair (tcgen05 cta_group::2), descriptor and TMA helpers of the linear products
 // (inline PTX for sm_103a), and their host side.
 #pragma once
 
@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include "oz2_internal.cuh"
+#include "oz2_tcgen05.cuh"
 
 namespace oz2 {
 
@@ -91,6 +92,16 @@ __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint32_t addr, uint32_
     if (mbar_try_wait_cluster(addr, parity)) return true;
     if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > limit_ns)) return false;
   }
+}
+
+// Shared-memory descriptor of 16 k at step s of a stage.  k contiguous: rows of
+// 128 bytes, 8-row groups 1024 bytes apart, 32 bytes per step.  Rows contiguous:
+// lines of 64 rows (128 bytes) for one k, groups of 8 k 1024 bytes apart, the
+// next 64 rows 8192 bytes on, 16 lines per step.
+template <bool ROWS_CONTIGUOUS>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int s) {
+  if (!ROWS_CONTIGUOUS) return smem_desc(base + s * 32);
+  return (smem_desc(base + s * 2048) & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(8192 >> 4) << 16);
 }
 
 // ------------------------------------------------------------------ epilogue through shared memory

@@ -23,6 +23,17 @@ namespace {
 
 constexpr int kWarps = 8;  // per block
 
+struct QkParams {
+  int64_t tokens, table_rows;
+  int dim, rot;
+  float eps;
+  const float *cos, *sin;
+  const int64_t* positions;
+  oz2_heads q, k, q_out, k_out, dq_out, dk_out;
+  const void *q_weight, *k_weight;
+  float* partial;  // backward: [gridDim.x][2 dim], may be null
+};
+
 // V features per chunk and ITEMS chunk pairs per lane: 8 and 1 where rows are
 // 16-byte aligned, dim is a multiple of 8 and rot of 16 (32 lanes hold up to
 // 512 features); else 1 and 8.
@@ -33,7 +44,7 @@ struct Lane {
   bool bad;
   float c[ITEMS][V], s[ITEMS][V];
 
-  __device__ __forceinline__ void init(const QkArgs& a, int64_t token, int lanes_) {
+  __device__ __forceinline__ void init(const QkParams& a, int64_t token, int lanes_) {
     lanes = lanes_;
     const int l = threadIdx.x & 31;
     lane = l % lanes;
@@ -136,7 +147,7 @@ __device__ __forceinline__ T* head_ptr(const oz2_heads& h, int64_t token, int64_
 
 // A warp takes `steps` steps of one token's heads (per_warp heads each), `parts` warps share a token.
 template <typename T, int V, int ITEMS, bool INTER>
-__global__ void __launch_bounds__(32 * kWarps) qk_kernel(const QkArgs a, int lanes, int parts, int steps) {
+__global__ void __launch_bounds__(32 * kWarps) qk_kernel(const __grid_constant__ QkParams a, int lanes, int parts, int steps) {
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t token = warp / parts;
   if (token >= a.tokens) return;
@@ -162,7 +173,7 @@ __global__ void __launch_bounds__(32 * kWarps) qk_kernel(const QkArgs a, int lan
 
 // One side (queries or keys) of one token's gradients; dw collects this lane's features.
 template <typename T, int V, int ITEMS, bool INTER>
-__device__ __forceinline__ void backward_side(const QkArgs& a, const Lane<T, V, ITEMS, INTER>& l, int64_t token, const oz2_heads& dy,
+__device__ __forceinline__ void backward_side(const QkParams& a, const Lane<T, V, ITEMS, INTER>& l, int64_t token, const oz2_heads& dy,
                                               const oz2_heads& xs, const oz2_heads& dx, const T* weight,
                                               float (&dw)[ITEMS][2 * V]) {
   float w[ITEMS][2 * V];
@@ -195,7 +206,7 @@ __device__ __forceinline__ void backward_side(const QkArgs& a, const Lane<T, V, 
 
 // Warps stride over the tokens; the block's weight-gradient sums go to its row of `partial`.
 template <typename T, int V, int ITEMS, bool INTER>
-__global__ void __launch_bounds__(32 * kWarps) qk_backward_kernel(const QkArgs a, int lanes) {
+__global__ void __launch_bounds__(32 * kWarps) qk_backward_kernel(const __grid_constant__ QkParams a, int lanes) {
   __shared__ float sums[kWarps][2 * OZ2_HEAD_DIM_MAX];
   const int warp = threadIdx.x >> 5;
   float dwq[ITEMS][2 * V] = {}, dwk[ITEMS][2 * V] = {};
@@ -258,9 +269,10 @@ bool side_aligned(const oz2_heads& h, oz2_dtype t) {
 }
 
 // Whether whole 16-byte chunks can be used, and the lanes per head.
-bool chunked(const QkArgs& a, oz2_dtype t) {
+bool chunked(const oz2_qk_args& a, bool backward) {
+  const oz2_dtype t = static_cast<oz2_dtype>(a.dtype);
   return a.dim % 8 == 0 && a.rot % 16 == 0 && side_aligned(a.q, t) && side_aligned(a.k, t) && side_aligned(a.q_out, t) &&
-         side_aligned(a.k_out, t) && side_aligned(a.dq_out, t) && side_aligned(a.dk_out, t) &&
+         side_aligned(a.k_out, t) && (!backward || (side_aligned(a.dq_out, t) && side_aligned(a.dk_out, t))) &&
          reinterpret_cast<uintptr_t>(a.q_weight) % 16 == 0 && reinterpret_cast<uintptr_t>(a.k_weight) % 16 == 0;
 }
 int lanes_for(int dim) {
@@ -269,57 +281,81 @@ int lanes_for(int dim) {
   return lanes;
 }
 
+QkParams make_params(const oz2_qk_args& a, float* partial) {
+  QkParams p{};
+  p.tokens = a.tokens;
+  p.table_rows = a.table_rows;
+  p.dim = static_cast<int>(a.dim);
+  p.rot = static_cast<int>(a.rot);
+  p.eps = static_cast<float>(a.eps);
+  p.cos = a.cos;
+  p.sin = a.sin;
+  p.positions = a.positions;
+  p.q = a.q;
+  p.k = a.k;
+  p.q_out = a.q_out;
+  p.k_out = a.k_out;
+  p.dq_out = a.dq_out;
+  p.dk_out = a.dk_out;
+  p.q_weight = a.q_weight;
+  p.k_weight = a.k_weight;
+  p.partial = partial;
+  return p;
+}
+
 template <typename T>
-cudaError_t qk_impl(const QkArgs& a, oz2_dtype dtype, cudaStream_t st) {
-  const bool wide = chunked(a, dtype);
-  const int lanes = wide ? lanes_for(a.dim) : 32, per_warp = 32 / lanes;
+cudaError_t qk_impl(const oz2_qk_args& a, int num_sms, cudaStream_t st) {
+  const bool wide = chunked(a, false);
+  const int lanes = wide ? lanes_for(static_cast<int>(a.dim)) : 32, per_warp = 32 / lanes;
   const int64_t all = ceil_div(a.q.heads + a.k.heads, per_warp);  // steps of a token
   // few tokens: share each among as many warps as the device has room for
-  const int64_t room = 152 * 32 / a.tokens;
+  const int64_t room = static_cast<int64_t>(num_sms) * 32 / a.tokens;
   const int64_t parts = std::max<int64_t>(1, std::min(all, room)), steps = ceil_div(all, parts);
   const int64_t blocks = ceil_div(a.tokens * parts, kWarps);
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   auto kernel = wide ? (a.interleaved ? qk_kernel<T, 8, 1, true> : qk_kernel<T, 8, 1, false>)
                      : (a.interleaved ? qk_kernel<T, 1, 8, true> : qk_kernel<T, 1, 8, false>);
-  kernel<<<static_cast<unsigned>(blocks), 32 * kWarps, 0, st>>>(a, lanes, static_cast<int>(parts), static_cast<int>(steps));
+  kernel<<<static_cast<unsigned>(blocks), 32 * kWarps, 0, st>>>(make_params(a, nullptr), lanes, static_cast<int>(parts),
+                                                                static_cast<int>(steps));
   count_launches(1);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t qk_backward_impl(const QkArgs& a, oz2_dtype dtype, int64_t rows, cudaStream_t st) {
-  const bool wide = chunked(a, dtype);
+cudaError_t qk_backward_impl(const oz2_qk_args& a, int64_t rows, float* partial, cudaStream_t st) {
+  const bool wide = chunked(a, true);
+  const int dim = static_cast<int>(a.dim);
   auto kernel = wide ? (a.interleaved ? qk_backward_kernel<T, 8, 1, true> : qk_backward_kernel<T, 8, 1, false>)
                      : (a.interleaved ? qk_backward_kernel<T, 1, 8, true> : qk_backward_kernel<T, 1, 8, false>);
-  kernel<<<static_cast<unsigned>(rows), 32 * kWarps, 0, st>>>(a, wide ? lanes_for(a.dim) : 32);
+  kernel<<<static_cast<unsigned>(rows), 32 * kWarps, 0, st>>>(make_params(a, partial), wide ? lanes_for(dim) : 32);
   count_launches(1);
-  if (a.partial) {
-    qk_weight_kernel<T><<<static_cast<unsigned>(ceil_div(2 * a.dim, 32)), 1024, 0, st>>>(
-        a.partial, rows, a.dim, static_cast<T*>(a.dq_weight), static_cast<T*>(a.dk_weight));
-    count_launches(1);
-  }
+  const cudaError_t e = cudaGetLastError();
+  if (!partial || e != cudaSuccess) return e;
+  qk_weight_kernel<T><<<static_cast<unsigned>(ceil_div(2 * dim, 32)), 1024, 0, st>>>(
+      partial, rows, dim, static_cast<T*>(a.dq_weight), static_cast<T*>(a.dk_weight));
+  count_launches(1);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int64_t qk_partial_rows(int64_t tokens, int64_t, int num_sms) {
-  return std::min<int64_t>(ceil_div(tokens, kWarps), 2 * static_cast<int64_t>(num_sms));
+int64_t qk_partial_rows(const oz2_qk_args& a, int num_sms) {
+  return std::min<int64_t>(ceil_div(a.tokens, kWarps), 2 * static_cast<int64_t>(num_sms));
 }
 
-cudaError_t launch_qk(const QkArgs& a, oz2_dtype dtype, cudaStream_t st) {
-  switch (dtype) {
-    case OZ2_BF16: return qk_impl<__nv_bfloat16>(a, dtype, st);
-    case OZ2_F16: return qk_impl<__half>(a, dtype, st);
-    default: return qk_impl<float>(a, dtype, st);
+cudaError_t launch_qk(const oz2_qk_args& a, const DeviceResources& res, cudaStream_t st) {
+  switch (a.dtype) {
+    case OZ2_BF16: return qk_impl<__nv_bfloat16>(a, res.num_sms, st);
+    case OZ2_F16: return qk_impl<__half>(a, res.num_sms, st);
+    default: return qk_impl<float>(a, res.num_sms, st);
   }
 }
 
-cudaError_t launch_qk_backward(const QkArgs& a, oz2_dtype dtype, int64_t partial_rows, cudaStream_t st) {
-  switch (dtype) {
-    case OZ2_BF16: return qk_backward_impl<__nv_bfloat16>(a, dtype, partial_rows, st);
-    case OZ2_F16: return qk_backward_impl<__half>(a, dtype, partial_rows, st);
-    default: return qk_backward_impl<float>(a, dtype, partial_rows, st);
+cudaError_t launch_qk_backward(const oz2_qk_args& a, int64_t rows, float* partial, cudaStream_t st) {
+  switch (a.dtype) {
+    case OZ2_BF16: return qk_backward_impl<__nv_bfloat16>(a, rows, partial, st);
+    case OZ2_F16: return qk_backward_impl<__half>(a, rows, partial, st);
+    default: return qk_backward_impl<float>(a, rows, partial, st);
   }
 }
 

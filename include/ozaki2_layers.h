@@ -61,36 +61,76 @@ typedef enum {
 
 /*
  * z = x w^T + bias, y = residual + keep * act(z) / (1 - p).
- * x [m][k] (ldx), w [n][k] (ldw), bias [n] or NULL, residual [m][n] (ldr) or
- * NULL, y [m][n] (ldy), preact [m][n] (ldz) or NULL: z, for linear_backward.
- * dtype: OZ2_BF16 or OZ2_F16, of every matrix.  dropout: p in [0, 1].
+ * x [m][k], w [n][k], bias [n] or NULL, residual [m][n] or NULL, y [m][n],
+ * preact [m][n] or NULL: z, for linear_backward.  dtype: OZ2_BF16 or OZ2_F16,
+ * of every matrix.  dropout: p in [0, 1].
  * y may be residual itself (ldy == ldr); otherwise outputs overlap nothing.
  */
-oz2_status ozaki2_linear(int64_t m, int64_t k, int64_t n, const void* x, int64_t ldx, const void* w, int64_t ldw,
-                         const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy, void* preact,
-                         int64_t ldz, oz2_dtype dtype, oz2_act act, double dropout, uint64_t seed, uint64_t offset,
-                         void* stream);
+typedef struct {
+  int64_t m, k, n;
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  int64_t ldw;
+  const void* bias;
+  const void* residual;
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  void* preact;
+  int64_t ldz;
+  uint64_t seed, offset;
+  double dropout;
+  int32_t dtype, act; /* oz2_dtype, oz2_act */
+} oz2_linear_args;
+oz2_status ozaki2_linear(const oz2_linear_args* args, void* stream);
 
 /*
- * Gradients of ozaki2_linear from dy [m][n] (lddy): with
+ * Gradients of ozaki2_linear from dy [m][n]: with
  * dz = act'(preact) * keep * dy / (1 - p),
- *   dx [m][k] (lddx) = dz w,  dw [n][k] (lddw) = dz^T x,  dbias [n] = column sums of dz;
+ *   dx [m][k] = dz w,  dw [n][k] = dz^T x,  dbias [n] = column sums of dz;
  * each of the three may be NULL.  preact is ozaki2_linear's, NULL for
  * OZ2_ACT_NONE.  The residual's gradient is dy itself.
  */
-oz2_status ozaki2_linear_backward(int64_t m, int64_t k, int64_t n, const void* dy, int64_t lddy, const void* x,
-                                  int64_t ldx, const void* w, int64_t ldw, const void* preact, int64_t ldz, void* dx,
-                                  int64_t lddx, void* dw, int64_t lddw, void* dbias, oz2_dtype dtype, oz2_act act,
-                                  double dropout, uint64_t seed, uint64_t offset, void* stream);
+typedef struct {
+  int64_t m, k, n;
+  const void* dy;
+  int64_t lddy;
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  int64_t ldw;
+  const void* preact;
+  int64_t ldz;
+  void* dx;
+  int64_t lddx;
+  void* dw;
+  int64_t lddw;
+  void* dbias;
+  uint64_t seed, offset;
+  double dropout;
+  int32_t dtype, act;
+} oz2_linear_backward_args;
+oz2_status ozaki2_linear_backward(const oz2_linear_backward_args* args, void* stream);
 
 /*
  * y = residual + keep * x / (1 - p), all [rows][cols]; residual may be NULL.
  * With x the gradient dy and no residual it is its own backward pass.  y may
  * be x or residual itself (same leading dimension).
  */
-oz2_status ozaki2_dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
-                          void* y, int64_t ldy, oz2_dtype dtype, double dropout, uint64_t seed, uint64_t offset,
-                          void* stream);
+typedef struct {
+  int64_t rows, cols;
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  uint64_t seed, offset;
+  double dropout;
+  int32_t dtype, reserved; /* any oz2_dtype; reserved is 0 */
+} oz2_dropout_args;
+oz2_status ozaki2_dropout(const oz2_dropout_args* args, void* stream);
 
 /* A [tokens][heads][dim] view: element (t, h, i) at data[t * token_stride + h * head_stride + i]. */
 typedef struct {
@@ -100,7 +140,7 @@ typedef struct {
 
 /*
  * For every token t and head: u = x * weight / sqrt(mean(x^2) + eps), then the
- * first `rot` features of u are rotated by the angles of position[t]: pairs
+ * first `rot` features of u are rotated by the angles of positions[t]: pairs
  * (i, i + rot/2), or (2 i, 2 i + 1) if interleaved, become
  * (a c - b s, b c + a s) with c = cos[position][i], s = sin[position][i]
  * (float tables [table_rows][rot / 2]); features past rot are only normed.
@@ -108,23 +148,28 @@ typedef struct {
  * zero heads is left out.  A position outside [0, table_rows) gives NaN in
  * that token's outputs.  An output may be its input itself.
  * dtype: any, of heads and weights.  rot even, 0 <= rot <= dim <= OZ2_HEAD_DIM_MAX.
+ *
+ * Backward: dq_out, dk_out are the gradients of the outputs, q and k the
+ * inputs; writes q_out, k_out (the inputs' gradients; either may be dq_out or
+ * dk_out itself) and dq_weight [dim], dk_weight [dim] (sums over all tokens
+ * and heads; may be NULL).  The forward call ignores these four.
  */
-oz2_status ozaki2_qk_norm_rope(int64_t tokens, int64_t dim, int64_t rot, oz2_heads q, oz2_heads k,
-                               const void* q_weight, const void* k_weight, const float* cos, const float* sin,
-                               int64_t table_rows, const int64_t* positions, double eps, int interleaved,
-                               oz2_dtype dtype, oz2_heads q_out, oz2_heads k_out, void* stream);
-
-/*
- * Gradients of ozaki2_qk_norm_rope: dq_out, dk_out are the gradients of its
- * outputs, q and k its inputs; writes dq, dk (the inputs' gradients; dq may be
- * dq_out itself) and dq_weight [dim], dk_weight [dim] (sums over all tokens
- * and heads; may be NULL).
- */
-oz2_status ozaki2_qk_norm_rope_backward(int64_t tokens, int64_t dim, int64_t rot, oz2_heads dq_out, oz2_heads dk_out,
-                                        oz2_heads q, oz2_heads k, const void* q_weight, const void* k_weight,
-                                        const float* cos, const float* sin, int64_t table_rows,
-                                        const int64_t* positions, double eps, int interleaved, oz2_dtype dtype,
-                                        oz2_heads dq, oz2_heads dk, void* dq_weight, void* dk_weight, void* stream);
+typedef struct {
+  int64_t tokens, dim, rot, table_rows;
+  const float* cos;
+  const float* sin;
+  const int64_t* positions;
+  oz2_heads q, k, q_out, k_out;
+  const void* q_weight;
+  const void* k_weight;
+  oz2_heads dq_out, dk_out;
+  void* dq_weight;
+  void* dk_weight;
+  double eps;
+  int32_t dtype, interleaved;
+} oz2_qk_args;
+oz2_status ozaki2_qk_norm_rope(const oz2_qk_args* args, void* stream);
+oz2_status ozaki2_qk_norm_rope_backward(const oz2_qk_args* args, void* stream);
 
 #ifdef __cplusplus
 }

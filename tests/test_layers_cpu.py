@@ -2,7 +2,6 @@
 point is exported, argument errors come back before any device work, a machine
 without a GPU gets a loud error, and the generator of the 64-bit definitions
 spreads its draws evenly."""
-import ctypes
 import os
 import re
 
@@ -18,7 +17,7 @@ from emulated_fp64_gemm_gb300 import layers  # noqa: E402
 from tests._layers_ref import keep_mask, philox  # noqa: E402
 
 INVALID, CUDA = 1, 4
-P = ctypes.c_void_p(16)
+P = 16  # a pointer that is not null
 
 
 @pytest.fixture(scope="module")
@@ -39,44 +38,78 @@ def test_exports_every_declared_symbol(lib):
     assert enum == oz2.ACTIVATIONS
 
 
-def linear(lib, m=4, k=8, n=8, x=P, ldx=8, w=P, ldw=8, bias=None, res=None, ldr=8, y=P, ldy=8, z=None, ldz=8, dtype=0, act=0,
-           p=0.0):
-    return lib.ozaki2_linear(m, k, n, x, ldx, w, ldw, bias, res, ldr, y, ldy, z, ldz, dtype, act, p, 1, 2, None)
+def fields(name):
+    """Names and struct codes of an argument structure, as the header declares it."""
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "ozaki2_layers.h")).read(), flags=re.S)
+    body = re.search(r"typedef struct \{([^}]*)\} " + name + ";", text).group(1)
+    out = []
+    for line in body.split(";"):
+        line = " ".join(line.split())
+        if not line:
+            continue
+        kind, names = re.match(r"((?:const )?\w+\*?) (.*)", line).groups()
+        for n in names.split(","):
+            n = n.strip()
+            if kind == "oz2_heads":
+                out += [(n + "." + f, c) for f, c in fields("oz2_heads")]
+            else:
+                out.append((n, "P" if kind.endswith("*") else {"int64_t": "q", "uint64_t": "Q", "double": "d", "int32_t": "i"}[kind]))
+    return out
 
 
-def backward(lib, m=4, k=8, n=8, dy=P, lddy=8, x=P, ldx=8, w=P, ldw=8, z=P, ldz=8, dx=P, lddx=8, dw=P, lddw=8, db=P, dtype=0,
-             act=2, p=0.0):
-    return lib.ozaki2_linear_backward(m, k, n, dy, lddy, x, ldx, w, ldw, z, ldz, dx, lddx, dw, lddw, db, dtype, act, p, 1, 2,
-                                      None)
+def call(lib, what, struct_name, packer, defaults, changes):
+    names = fields(struct_name)
+    assert "@" + "".join(c for _, c in names) == packer.format
+    values = {**{n: 0 for n, _ in names}, **defaults, **changes}
+    assert set(values) == {n for n, _ in names}
+    return getattr(lib, what)(packer.pack(*(values[n] for n, _ in names)), None)
 
 
-def drop(lib, rows=4, cols=8, x=P, ldx=8, res=None, ldr=8, y=P, ldy=8, dtype=0, p=0.1):
-    return lib.ozaki2_dropout(rows, cols, x, ldx, res, ldr, y, ldy, dtype, p, 1, 2, None)
+def linear(lib, **kw):
+    return call(lib, "ozaki2_linear", "oz2_linear_args", layers._LINEAR_ARGS,
+                dict(m=4, k=8, n=8, x=P, ldx=8, w=P, ldw=8, ldr=8, y=P, ldy=8, ldz=8), kw)
 
 
-def qk(lib, tokens=4, dim=16, rot=16, q=None, k=None, wq=P, cos=P, pos=P, eps=1e-6, dtype=0, q_out=None, rows=4):
-    h = layers._Heads
-    q, k, q_out = q or h(16, 2, 32, 16), k or h(16, 1, 16, 16), q_out or h(16, 2, 32, 16)
-    return lib.ozaki2_qk_norm_rope(tokens, dim, rot, q, k, wq, P, cos, P, rows, pos, eps, 0, dtype, q_out, h(16, 1, 16, 16), None)
+def backward(lib, **kw):
+    return call(lib, "ozaki2_linear_backward", "oz2_linear_backward_args", layers._LINEAR_BACKWARD_ARGS,
+                dict(m=4, k=8, n=8, dy=P, lddy=8, x=P, ldx=8, w=P, ldw=8, preact=P, ldz=8, dx=P, lddx=8, dw=P, lddw=8, dbias=P,
+                     act=2), kw)
+
+
+def drop(lib, **kw):
+    return call(lib, "ozaki2_dropout", "oz2_dropout_args", layers._DROPOUT_ARGS,
+                dict(rows=4, cols=8, x=P, ldx=8, ldr=8, y=P, ldy=8, dropout=0.1), kw)
+
+
+def qk(lib, **kw):
+    heads = {}
+    for n, h in (("q", 2), ("k", 1), ("q_out", 2), ("k_out", 1), ("dq_out", 2), ("dk_out", 1)):
+        heads |= {n + ".data": P, n + ".heads": h, n + ".token_stride": 16 * h, n + ".head_stride": 16}
+    base = dict(tokens=4, dim=16, rot=16, table_rows=4, cos=P, sin=P, positions=P, q_weight=P, k_weight=P, dq_weight=P, dk_weight=P,
+                eps=1e-6, **heads)
+    codes = [call(lib, f, "oz2_qk_args", layers._QK_ARGS, base, kw) for f in ("ozaki2_qk_norm_rope", "ozaki2_qk_norm_rope_backward")]
+    assert codes[0] == codes[1]
+    return codes[0]
 
 
 def test_argument_errors_come_before_any_device_work(lib):
+    nan = float("nan")
     for f, cases in (
-        (linear, [dict(m=-1), dict(k=-1), dict(n=2**31), dict(x=None), dict(w=None), dict(y=None), dict(ldx=7), dict(ldw=7),
-                  dict(ldy=7), dict(res=P, ldr=7), dict(z=P, ldz=7), dict(dtype=2), dict(dtype=-1), dict(act=5), dict(act=-1),
-                  dict(p=-0.1), dict(p=1.1), dict(p=float("nan"))]),
-        (backward, [dict(m=-1), dict(dy=None), dict(lddy=7), dict(x=None), dict(w=None), dict(z=None), dict(ldz=7), dict(lddx=7),
-                    dict(lddw=7), dict(dtype=2), dict(act=9), dict(p=2.0)]),
-        (drop, [dict(rows=-1), dict(cols=2**31), dict(x=None), dict(y=None), dict(ldx=7), dict(ldy=7), dict(res=P, ldr=7),
-                dict(dtype=3), dict(p=float("nan"))]),
-        (qk, [dict(tokens=-1), dict(dim=0), dict(dim=513), dict(dim=2**33), dict(rot=17), dict(rot=3), dict(rot=-2), dict(wq=None),
-              dict(cos=None), dict(pos=None), dict(eps=-1.0), dict(eps=float("nan")), dict(dtype=3), dict(rows=-1),
-              dict(q=layers._Heads(None, 2, 32, 16)), dict(q=layers._Heads(16, -1, 32, 16)),
-              dict(q=layers._Heads(16, 2, -32, 16)), dict(q_out=layers._Heads(16, 3, 32, 16)),
-              dict(q_out=layers._Heads(None, 2, 32, 16))]),
+        (linear, [dict(m=-1), dict(k=-1), dict(n=2**31), dict(x=0), dict(w=0), dict(y=0), dict(ldx=7), dict(ldw=7), dict(ldy=7),
+                  dict(residual=P, ldr=7), dict(preact=P, ldz=7), dict(dtype=2), dict(dtype=-1), dict(act=5), dict(act=-1),
+                  dict(dropout=-0.1), dict(dropout=1.1), dict(dropout=nan)]),
+        (backward, [dict(m=-1), dict(dy=0), dict(lddy=7), dict(x=0), dict(w=0), dict(preact=0), dict(ldz=7), dict(lddx=7),
+                    dict(lddw=7), dict(dtype=2), dict(act=9), dict(dropout=2.0)]),
+        (drop, [dict(rows=-1), dict(cols=2**31), dict(x=0), dict(y=0), dict(ldx=7), dict(ldy=7), dict(residual=P, ldr=7),
+                dict(dtype=3), dict(dropout=nan), dict(reserved=1)]),
+        (qk, [dict(tokens=-1), dict(dim=0), dict(dim=513), dict(dim=2**33), dict(rot=17), dict(rot=3), dict(rot=-2),
+              dict(q_weight=0), dict(cos=0), dict(positions=0), dict(eps=-1.0), dict(eps=nan), dict(dtype=3), dict(table_rows=-1),
+              {"q.data": 0}, {"q.heads": -1}, {"q.token_stride": -32}, {"q_out.heads": 3}, {"k_out.data": 0}]),
     ):
         for kw in cases:
             assert f(lib, **kw) == INVALID, (f.__name__, kw)
+    for name in ("linear", "linear_backward", "dropout", "qk_norm_rope", "qk_norm_rope_backward"):
+        assert getattr(lib, "ozaki2_" + name)(None, None) == INVALID
 
 
 def test_no_gpu_means_a_loud_error(lib):

@@ -91,6 +91,14 @@ def test_linear_sizes(oz2, m, k, n, dtype):
     check_linear(oz2, x, w, b, "gelu_tanh", r, 0.25, save=True)
 
 
+@pytest.mark.parametrize("m,k,n", [(3, 8200, 1000), (24, 4096, 20488), (120, 2056, 24640), (2000, 4104, 4360), (9000, 520, 2100)])
+def test_linear_long(oz2, m, k, n):
+    # more blocks of k than stages, more tiles than the device holds at once
+    x, w, b = normal(m, k, dtype=BF16), normal(n, k, dtype=BF16, seed=1, scale=k**-0.5), normal(n, dtype=BF16, seed=2)
+    check_linear(oz2, x, w, b, "silu", save=True)
+    check_backward(oz2, normal(m, n, dtype=BF16, seed=3), x, w)
+
+
 @pytest.mark.parametrize("activation", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("m,n", [(4, 264), (300, 519)])
 def test_linear_activations_and_options(oz2, activation, m, n):
