@@ -52,6 +52,7 @@ constexpr int kTileFloats = 256 * 256;
 struct GemmParams {
   Epilogue ep;
   int tiles_m, tiles_n, nkb;
+  int group;     // row tiles per raster group
   int full;      // the first `full` tiles are whole units, the others `splits` units each
   int splits;
   int units;
@@ -64,10 +65,11 @@ struct Unit {
   int slot;  // partial slot, -1: finished by this unit
 };
 
-// Tiles follow a raster of eight row tiles per group, so that the operands in flight stay in L2.
-__device__ __forceinline__ void tile_position(int tile, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int per_group = 8 * tiles_n, g = tile / per_group, at = tile % per_group, rows = min(tiles_m - g * 8, 8);
-  tm = g * 8 + at % rows;
+// Tiles follow a raster of `group` row tiles, whose rows of A stay in L2 while B passes by.
+__device__ __forceinline__ void tile_position(int tile, const GemmParams& p, int& tm, int& tn) {
+  const int per_group = p.group * p.tiles_n, g = tile / per_group, at = tile % per_group;
+  const int rows = min(p.tiles_m - g * p.group, p.group);
+  tm = g * p.group + at % rows;
   tn = at / rows;
 }
 
@@ -84,7 +86,7 @@ __device__ __forceinline__ Unit decode_unit(int u, const GemmParams& p) {
     U.kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * s / p.splits);
     U.kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (s + 1) / p.splits);
   }
-  tile_position(tile, p.tiles_m, p.tiles_n, U.tm, U.tn);
+  tile_position(tile, p, U.tm, U.tn);
   return U;
 }
 
@@ -181,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Unit U = decode_unit(u, p);
         const int row_a = U.tm * 256 + static_cast<int>(rank) * 128, row_b = U.tn * 256 + static_cast<int>(rank) * 128;
         for (int kb = U.kb0; kb < U.kb1; ++kb) {
-          if (!mbar_wait_cluster_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, kWaitLimitNs)) {
+          if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, kWaitLimitNs)) {
             ok = false;
             break;
           }
@@ -205,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (leader only)
-    if (leader && lane == 0) {
+    if (leader && elect_one()) {
       // kind::f16: 32-bit sums, both operands of type T, M = 256 (the pair), N = 256
       constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(A_ROWS) << 15) |
@@ -216,17 +218,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int u = pair; u < p.units && ok; u += pairs, ++n) {
         const Unit U = decode_unit(u, p);
         const int slot = n & 1;
-        if (!mbar_wait_cluster_bounded(smem_u32(&acc_empty[slot]), ((n >> 1) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
+        if (!mbar_wait_bounded(smem_u32(&acc_empty[slot]), ((n >> 1) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        bool ready = mbar_try_wait(smem_u32(&full[stage]), phase);
         for (int kb = U.kb0; kb < U.kb1; ++kb) {
-          if (!mbar_wait_cluster_bounded(smem_u32(&full[stage]), phase, abort_flag, kWaitLimitNs)) {
+          if (!ready && !mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, kWaitLimitNs)) {
             ok = false;
             break;
           }
-          tc_fence_after();
+          // the next stage is asked for before this one's MMAs are issued: the answer takes as long as
+          // half an MMA, and the queue in front of the tensor core does not cover it
+          const int next = stage + 1 == kStages ? 0 : stage + 1;
+          ready = mbar_try_wait(smem_u32(&full[next]), next ? phase : phase ^ 1);
           const uint32_t a = smem_u32(s_a + stage * kOperandBytes), b = smem_u32(s_b + stage * kOperandBytes);
 #pragma unroll
           for (int s = 0; s < kBK / 16; ++s)
@@ -256,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int u = pair; u < p.units; u += pairs, ++n) {
       const Unit U = decode_unit(u, p);
       const int slot = n & 1;
-      const bool got = mbar_wait_cluster_bounded(smem_u32(&acc_full[slot]), (n >> 1) & 1, abort_flag, kWaitLimitNs);
+      const bool got = mbar_wait_bounded(smem_u32(&acc_full[slot]), (n >> 1) & 1, abort_flag, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) {  // warp-uniform: the tensor-memory loads below are .aligned
         ok = false;
         break;
@@ -300,7 +306,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ GemmParams p) {
   const int tile = blockIdx.x / 32, lane = threadIdx.x & 31, row = blockIdx.x % 32 * 8 + (threadIdx.x >> 5);
   int tm, tn;
-  tile_position(p.full + tile, p.tiles_m, p.tiles_n, tm, tn);
+  tile_position(p.full + tile, p, tm, tn);
   const int64_t r = static_cast<int64_t>(tm) * 256 + row, c = static_cast<int64_t>(tn) * 256 + lane * 8;
   if (r >= p.ep.rows || c >= p.ep.cols) return;
   const float* at = p.partial + static_cast<int64_t>(tile) * p.splits * kTileFloats + row * 256 + lane * 8;
@@ -350,6 +356,9 @@ GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms) {
   p.tiles_m = static_cast<int>(ceil_div(ep.rows, 256));
   p.tiles_n = static_cast<int>(ceil_div(ep.cols, 256));
   p.nkb = static_cast<int>(ceil_div(k, kBK));
+  // 32 MB of A per group: each of the two dies keeps its own copy in its half of the 129 MB L2.  At k = 4096 with
+  // 16384 columns groups of 4, 8, 16 and 32 row tiles took 604, 572, 562 and 583 us.
+  p.group = static_cast<int>(std::clamp<int64_t>((32 << 20) / (256 * 2 * std::max<int64_t>(k, 1)), 4, 16));
   plan_units(p.tiles_m * p.tiles_n, p.nkb, num_sms / 2, &p.full, &p.splits);
   p.units = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
   return p;

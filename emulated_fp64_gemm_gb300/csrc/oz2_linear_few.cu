@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // kind::f16: 32-bit sums, both operands of type T, M = 128, N = MP
       constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(W_ROWS) << 15) |

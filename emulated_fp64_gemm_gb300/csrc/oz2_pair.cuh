@@ -19,6 +19,18 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+// True in one lane of a converged warp.  The compiler knows that code behind it
+// runs in a single lane and keeps the MMAs' operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(one));
+  return one != 0;
+}
+
 // The address of this shared-memory location in another CTA of the cluster.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t rank) {
   uint32_t out;
@@ -69,29 +81,6 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t tmem, uint32_t column
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(addr), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// mbar_wait_bounded for signals from the cluster.
-__device__ __forceinline__ bool mbar_wait_cluster_bounded(uint32_t addr, uint32_t parity, volatile int* abort,
-                                                          uint64_t limit_ns) {
-  if (mbar_try_wait_cluster(addr, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(addr, parity)) return true;
-    if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > limit_ns)) return false;
-  }
 }
 
 // Shared-memory descriptor of 16 k at step s of a stage.  k contiguous: rows of
