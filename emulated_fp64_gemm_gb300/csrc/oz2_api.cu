@@ -772,6 +772,7 @@ oz2_status acquire_resources(cudaStream_t st, size_t bytes, DeviceResources* out
   out->workspace = nullptr;
   out->err = ds->err;
   out->num_sms = ds->num_sms;
+  if (cudaGetDevice(&out->device) != cudaSuccess) return OZ2_ERR_CUDA;
   return bytes ? get_workspace(st, bytes, &out->workspace) : OZ2_OK;
 }
 

@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <utility>
 
 #include "../../include/ozaki2_layers.h"
 #include "oz2_internal.cuh"
@@ -22,12 +23,14 @@ struct DeviceResources {
   uint8_t* workspace;  // at least the bytes asked for; of this device and stream
   int* err;            // device error word
   int num_sms;
+  int device;
 };
 oz2_status acquire_resources(cudaStream_t st, size_t bytes, DeviceResources* out);
 
 // ------------------------------------------------------------ dropout parameters
 struct Dropout {
   uint32_t threshold;  // T = round(65536 p): an element is kept iff its 16-bit draw >= T
+  uint32_t limit;      // 65536 T - 1: iff the draw's 16 bits, on top of a word, are above this
   float scale;         // 65536 / (65536 - T), 0 for T = 65536
   uint32_t seed0, seed1, offset0, offset1;
 };
@@ -111,11 +114,14 @@ struct DzArgs {
 };
 cudaError_t launch_dz(const DzArgs& a, oz2_dtype dtype, cudaStream_t st);
 
+// out[c] = the sum of partial[r][c] over the rows, in a fixed order.
+cudaError_t launch_column_sums(const float* partial, int64_t rows, int64_t cols, oz2_dtype dtype, void* out, cudaStream_t st);
+
 cudaError_t launch_qk(const oz2_qk_args& a, const DeviceResources& res, cudaStream_t st);
-// Blocks of the backward pass, each with a row of 2 dim floats in `partial`
-// (null: the weights' gradients are not formed).
+// Rows of dim floats that the backward pass needs in `partial` (null: the
+// weights' gradients are not formed).
 int64_t qk_partial_rows(const oz2_qk_args& a, int num_sms);
-cudaError_t launch_qk_backward(const oz2_qk_args& a, int64_t rows, float* partial, cudaStream_t st);
+cudaError_t launch_qk_backward(const oz2_qk_args& a, const DeviceResources& res, float* partial, cudaStream_t st);
 
 }  // namespace oz2
 
@@ -128,7 +134,7 @@ struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
   }
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -154,6 +160,30 @@ struct Elem<float> {
   static __device__ __forceinline__ float up(float v) { return v; }
   static __device__ __forceinline__ float down(float v) { return v; }
 };
+
+// The eight elements of one 16-byte piece, or of two, `stride` pieces apart (32-bit).
+template <typename T>
+__device__ __forceinline__ void values8(const uint4* u, float* v, int stride = 1) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 a = *u;
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = Elem<T>::unpack(w[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 f = *reinterpret_cast<const float4*>(u + i * stride);
+      v[4 * i] = f.x;
+      v[4 * i + 1] = f.y;
+      v[4 * i + 2] = f.z;
+      v[4 * i + 3] = f.w;
+    }
+  }
+}
 
 // Eight neighbouring elements of a row: whole vectors where `vec` (16-byte
 // aligned, all eight inside), else one by one, the first n (zeros after them).
@@ -224,28 +254,58 @@ __device__ __forceinline__ uint4 philox7(uint32_t c0, uint32_t c1, uint32_t c2, 
 }
 
 // v <- keep * v * scale for the eight columns of group g (columns 8g .. 8g + 7)
-// of `row`.  A dropped element becomes +0 whatever it was.
+// of `row`; T > 0.  A dropped element becomes +0 whatever it was.  A high half's
+// draw is compared as the whole word: the bits below it cannot reach the next T.
 __device__ __forceinline__ void drop8(const Dropout& d, uint32_t row, uint32_t g, float (&v)[8]) {
   const uint4 u = philox7(g, row, d.offset0, d.offset1, d.seed0, d.seed1);
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = (w[i] & 0xFFFFu) >= d.threshold ? v[2 * i] * d.scale : 0.0f;
-    v[2 * i + 1] = (w[i] >> 16) >= d.threshold ? v[2 * i + 1] * d.scale : 0.0f;
+    v[2 * i] = (w[i] << 16) > d.limit ? v[2 * i] * d.scale : 0.0f;
+    v[2 * i + 1] = w[i] > d.limit ? v[2 * i + 1] * d.scale : 0.0f;
   }
 }
 
 // ------------------------------------------------------------ activations
-// The results go to 16 bits, so the fast exponential and quotient (relative
+// The results go to 16 bits, so the fast exponential and reciprocal (relative
 // errors of about 1e-6 here) stay far below the final rounding (2^-11 at best).
+// These kernels are bound by instructions more than by anything else, so the
+// constants of a chain (log2 e, 2 sqrt(2/pi)) are folded into one.
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ float logistic(float t) { return __fdividef(1.0f, 1.0f + __expf(-t)); }
+__device__ __forceinline__ float fast_exp2(float t) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float t) {  // 0 for infinity
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+// 1 / (1 + 2^t); the logistic function of x is this of -x log2 e
+__device__ __forceinline__ float logistic2(float t) { return fast_rcp(1.0f + fast_exp2(t)); }
 
-// act(z) over eight values.  gelu_tanh by (1 + tanh(t)) / 2 = logistic(2 t).
-// The fast quotient gives 0 for denominators from 2^126 on, which is act's
-// limit there (z >= -88 or so is needed for anything else).
+// The factor of gelu_tanh: (1 + tanh(c (z + a z^3))) / 2 = logistic(2 c (z + a z^3)).
+// z2 = z^2, limited so that no product with the slope's zero becomes 0 * inf.
+__device__ __forceinline__ float gelu_tanh_factor(float z, float z2) {
+  return logistic2(z * fmaf(z2, -kGeluC2 * kGeluA * kLog2e, -kGeluC2 * kLog2e));
+}
+
+// Phi(z), and exp(-z^2 / 2): Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26 (erf to 1.5e-7) at x = |z| / sqrt(2), where its factor
+// exp(-x^2) is the other output.
+__device__ __forceinline__ float normal_cdf(float z, float& bell) {
+  const float x = fabsf(z) * 0.7071067811865476f, t = fast_rcp(fmaf(0.3275911f, x, 1.0f));
+  bell = fast_exp2(z * z * (-0.5f * kLog2e));
+  const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+  const float tail = 0.5f * poly * bell;  // Phi(-|z|)
+  return z < 0.0f ? tail : 1.0f - tail;   // NaN stays
+}
+
+// act(z) over eight values.
 __device__ __forceinline__ void activate8(int act, float (&v)[8]) {
   switch (act) {
     case OZ2_ACT_RELU:
@@ -254,48 +314,50 @@ __device__ __forceinline__ void activate8(int act, float (&v)[8]) {
       break;
     case OZ2_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= logistic(v[i]);
+      for (int i = 0; i < 8; ++i) v[i] *= logistic2(v[i] * -kLog2e);
       break;
     case OZ2_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= normcdff(v[i]);
+      for (int i = 0; i < 8; ++i) {
+        float bell;
+        v[i] *= normal_cdf(v[i], bell);
+      }
       break;
     case OZ2_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= logistic(kGeluC2 * v[i] * (1.0f + kGeluA * v[i] * v[i]));
+      for (int i = 0; i < 8; ++i) v[i] *= gelu_tanh_factor(v[i], v[i] * v[i]);
       break;
     default: break;
   }
 }
 
-// g <- g * act'(z).  Where the slope's decaying factor has reached zero its
-// growing partner is left out, so no 0 * inf is formed for large finite z.
+// g <- g * act'(z).
 __device__ __forceinline__ void activate_grad8(int act, const float (&z)[8], float (&g)[8]) {
   switch (act) {
     case OZ2_ACT_RELU:
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = z[i] > 0.0f ? g[i] : (z[i] <= 0.0f ? 0.0f : z[i]);  // NaN passes on
       break;
-    case OZ2_ACT_SILU:
+    case OZ2_ACT_SILU:  // s + z s (1 - s)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float s = logistic(z[i]), d = s * (1.0f - s);
-        g[i] *= s + (d == 0.0f ? 0.0f : z[i] * d);
+        const float s = logistic2(z[i] * -kLog2e), t = z[i] * s;
+        g[i] *= s + fmaf(-t, s, t);
       }
       break;
-    case OZ2_ACT_GELU:
+    case OZ2_ACT_GELU:  // Phi(z) + z phi(z)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = 0.3989422804014327f * __expf(-0.5f * z[i] * z[i]);  // 1 / sqrt(2 pi)
-        g[i] *= normcdff(z[i]) + (d == 0.0f ? 0.0f : z[i] * d);
+        float bell;
+        const float cdf = normal_cdf(z[i], bell);
+        g[i] *= fmaf(z[i] * 0.3989422804014327f, bell, cdf);  // 1 / sqrt(2 pi)
       }
       break;
-    case OZ2_ACT_GELU_TANH:
+    case OZ2_ACT_GELU_TANH:  // s + z s (1 - s) 2 c (1 + 3 a z^2)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float q = kGeluA * z[i] * z[i];
-        const float s = logistic(kGeluC2 * z[i] * (1.0f + q)), d = s * (1.0f - s);
-        g[i] *= s + (d == 0.0f ? 0.0f : z[i] * d * kGeluC2 * (1.0f + 3.0f * q));
+        const float z2 = fminf(z[i] * z[i], 1e30f), s = gelu_tanh_factor(z[i], z2), t = z[i] * s;
+        g[i] *= fmaf(fmaf(-t, s, t), fmaf(z2, 3.0f * kGeluC2 * kGeluA, kGeluC2), s);
       }
       break;
     default: break;
@@ -303,29 +365,119 @@ __device__ __forceinline__ void activate_grad8(int act, const float (&z)[8], flo
 }
 
 // ------------------------------------------------------------ epilogue
-// v: the 32-bit sums of eight neighbouring columns from col (a multiple of 8,
-// below cols) of one row; everything after the product, rounded once per output.
+// Eight neighbouring 16-bit elements as they are in memory, the first n.
+template <typename T>
+__device__ __forceinline__ uint4 load8_raw(const T* p, bool vec, int n) {
+  if (vec) return *reinterpret_cast<const uint4*>(p);
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = i < n ? reinterpret_cast<const uint16_t*>(p)[i] : 0u;
+  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+template <typename T>
+__device__ __forceinline__ void add8(uint4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Elem<T>::unpack(w[i]);
+    v[2 * i] += f.x;
+    v[2 * i + 1] += f.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]), Elem<T>::pack(v[4], v[5]), Elem<T>::pack(v[6], v[7]));
+}
+
+// What the epilogue reads for eight neighbouring columns from col (a multiple
+// of 8) of a row.  Reading it ahead of the sums takes its latency off the path.
+template <typename T>
+__device__ __forceinline__ uint4 read_bias8(const Epilogue& e, int64_t col) {
+  if (!e.bias || col >= e.cols) return make_uint4(0, 0, 0, 0);
+  const int64_t left = e.cols - col;
+  return load8_raw(static_cast<const T*>(e.bias) + col, e.vec && left >= 8, left < 8 ? static_cast<int>(left) : 8);
+}
+template <typename T>
+__device__ __forceinline__ uint4 read_residual8(const Epilogue& e, int64_t row, int64_t col) {
+  if (!e.residual || row >= e.rows || col >= e.cols) return make_uint4(0, 0, 0, 0);
+  const int64_t left = e.cols - col;
+  return load8_raw(static_cast<const T*>(e.residual) + row * e.ldr + col, e.vec && left >= 8,
+                   left < 8 ? static_cast<int>(left) : 8);
+}
+// Everything after the product, in 32 bits: v becomes y (to be rounded once), the return value is z, rounded.
+template <typename T>
+__device__ __forceinline__ uint4 finish8(const Epilogue& e, int64_t row, int64_t col, uint4 bias, uint4 residual, float (&v)[8]) {
+  if (e.bias) add8<T>(bias, v);
+  const uint4 z = e.z ? pack8<T>(v) : make_uint4(0, 0, 0, 0);
+  activate8(e.act, v);
+  if (e.drop.threshold) drop8(e.drop, static_cast<uint32_t>(row), static_cast<uint32_t>(col >> 3), v);
+  if (e.residual) add8<T>(residual, v);
+  return z;
+}
+template <typename T>
+__device__ __forceinline__ void store8_raw(T* p, bool vec, int n, uint4 u) {
+  if (vec) {
+    *reinterpret_cast<uint4*>(p) = u;
+    return;
+  }
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
+}
+// The whole epilogue of eight columns, row and col inside the output.
 template <typename T>
 __device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int64_t col, float (&v)[8]) {
   const int64_t left = e.cols - col;
   const bool vec = e.vec && left >= 8;
   const int n = left < 8 ? static_cast<int>(left) : 8;
-  if (e.bias) {
-    float b[8];
-    load8(static_cast<const T*>(e.bias) + col, vec, n, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
-  if (e.z) store8(static_cast<T*>(e.z) + row * e.ldz + col, vec, n, v);
-  activate8(e.act, v);
-  if (e.drop.threshold) drop8(e.drop, static_cast<uint32_t>(row), static_cast<uint32_t>(col >> 3), v);
-  if (e.residual) {
-    float r[8];
-    load8(static_cast<const T*>(e.residual) + row * e.ldr + col, vec, n, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += r[i];
-  }
-  store8(static_cast<T*>(e.y) + row * e.ldy + col, vec, n, v);
+  const uint4 z = finish8<T>(e, row, col, read_bias8<T>(e, col), read_residual8<T>(e, row, col), v);
+  if (e.z) store8_raw(static_cast<T*>(e.z) + row * e.ldz + col, vec, n, z);
+  store8_raw(static_cast<T*>(e.y) + row * e.ldy + col, vec, n, pack8<T>(v));
+}
+
+// ------------------------------------------------------------ launches
+// Every layer kernel is launched so that it may start while the kernel before
+// it on the stream ends (programmatic stream serialization).  It waits, before
+// it touches memory, until its predecessor is done, and lets its own successor
+// come once its blocks near their ends.  This hides launch latency between the
+// kernels of a call and of successive calls (dropout of 64 x 1000: 1.8 -> 1.4 us).
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_successor_come() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+}  // namespace oz2
+
+namespace oz2 {
+
+// One launch; clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cluster, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+// Lets a kernel use `bytes` of shared memory, once per device (the attribute is the device's).
+template <auto kernel>
+cudaError_t allow_smem(size_t bytes, int device) {
+  static uint64_t known = 0;  // under the library's lock
+  const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+  if (known & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) known |= bit;
+  return e;
 }
 
 }  // namespace oz2

@@ -25,6 +25,7 @@ bool dropout_ok(double p) { return p >= 0.0 && p <= 1.0; }  // false for NaN
 Dropout make_dropout(double p, uint64_t seed, uint64_t offset) {
   Dropout d;
   d.threshold = static_cast<uint32_t>(std::lround(65536.0 * p));
+  d.limit = static_cast<uint32_t>((static_cast<uint64_t>(d.threshold) << 16) - 1);
   d.scale = d.threshold == 65536 ? 0.0f : 65536.0f / static_cast<float>(65536 - d.threshold);
   d.seed0 = static_cast<uint32_t>(seed);
   d.seed1 = static_cast<uint32_t>(seed >> 32);
@@ -196,14 +197,13 @@ oz2_status qk_backward(const oz2_qk_args& a, cudaStream_t st) {
     if (a.dk_weight) OZ2_TRY(cudaMemsetAsync(a.dk_weight, 0, bytes, st));
     return OZ2_OK;
   }
-  const int64_t rows = qk_partial_rows(a, res.num_sms);
   float* partial = nullptr;
   if (a.dq_weight || a.dk_weight) {
-    e = acquire_resources(st, static_cast<size_t>(rows) * 2 * a.dim * 4, &res);
+    e = acquire_resources(st, static_cast<size_t>(qk_partial_rows(a, res.num_sms)) * a.dim * 4, &res);
     if (e != OZ2_OK) return e;
     partial = reinterpret_cast<float*>(res.workspace);
   }
-  OZ2_TRY(launch_qk_backward(a, rows, partial, st));
+  OZ2_TRY(launch_qk_backward(a, res, partial, st));
   return OZ2_OK;
 }
 

@@ -102,18 +102,52 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 
-// The epilogue of a 32 x 32 block at (row0, col0): lane l takes eight columns of rows l / 4, l / 4 + 8, ...
+// A 32 x 32 block of the epilogue at (row0, col0): lane l takes the eight columns
+// col0 + 8 (l % 4) of rows l / 4, l / 4 + 8, ...
+struct BlockReads {
+  uint4 bias, residual[4];
+};
 template <typename T>
-__device__ __forceinline__ void finish_block(const Epilogue& e, const float* tile, int lane, int64_t row0, int64_t col0) {
+__device__ __forceinline__ void read_block(const Epilogue& e, int lane, int64_t row0, int64_t col0, BlockReads& in) {
   const int64_t col = col0 + (lane & 3) * 8;
+  in.bias = read_bias8<T>(e, col);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) in.residual[i] = read_residual8<T>(e, row0 + i * 8 + (lane >> 2), col);
+}
+template <typename T>
+__device__ __forceinline__ void finish_block(const Epilogue& e, float* tile, int lane, int64_t row0, int64_t col0,
+                                             const BlockReads& in) {
+  const int g = lane & 3;
+  const int64_t col = col0 + g * 8;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * 8 + (lane >> 2);
-    if (row0 + r < e.rows && col < e.cols) {
-      float v[8];
-      get_eight(tile, r, lane & 3, v);
-      epilogue8<T>(e, row0 + r, col, v);
+    const int64_t row = row0 + r;
+    float v[8];
+    get_eight(tile, r, g, v);
+    const uint4 z = finish8<T>(e, row, col, in.bias, in.residual[i], v);
+    if (e.vec) {
+      if (row < e.rows && col < e.cols) {
+        const int64_t left = e.cols - col;
+        const int n = left < 8 ? static_cast<int>(left) : 8;
+        if (e.z) store8_raw(static_cast<T*>(e.z) + row * e.ldz + col, left >= 8, n, z);
+        store8_raw(static_cast<T*>(e.y) + row * e.ldy + col, left >= 8, n, pack8<T>(v));
+      }
+    } else {  // rows off 16-byte boundaries go back to shared memory, in place of the row's sums: y, then z
+      __syncwarp();
+      uint4* out = reinterpret_cast<uint4*>(tile + r * 32);
+      out[g] = pack8<T>(v);
+      out[4 + g] = z;
     }
+  }
+  if (e.vec) return;
+  __syncwarp();
+  // and out element by element, a row's 64 bytes per instruction
+  if (col0 + lane >= e.cols) return;
+  for (int r = 0; r < 32 && row0 + r < e.rows; ++r) {
+    const T* from = reinterpret_cast<const T*>(tile + r * 32) + lane;
+    static_cast<T*>(e.y)[(row0 + r) * e.ldy + col0 + lane] = from[0];
+    if (e.z) static_cast<T*>(e.z)[(row0 + r) * e.ldz + col0 + lane] = from[32];
   }
 }
 
@@ -129,7 +163,7 @@ __device__ __forceinline__ void save_block(float* partial, const float* tile, in
 }
 
 template <typename T, bool A_ROWS, bool B_ROWS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -163,6 +197,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  if (threadIdx.x == 32) {
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+  }
+  wait_for_predecessor();
   // both CTAs run before the collective allocation, and both have their barriers before any remote signal
   __syncthreads();
   cluster_sync_all();
@@ -262,13 +301,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int u = pair; u < p.units; u += pairs, ++n) {
       const Unit U = decode_unit(u, p);
       const int slot = n & 1;
+      const int local_row = static_cast<int>(rank) * 128 + quad * 32;
+      const int64_t row0 = static_cast<int64_t>(U.tm) * 256 + local_row, col0 = static_cast<int64_t>(U.tn) * 256 + half * 128;
+      BlockReads next{};
+      if (U.slot < 0) read_block<T>(p.ep, lane, row0, col0, next);
       const bool got = mbar_wait_bounded(smem_u32(&acc_full[slot]), (n >> 1) & 1, abort_flag, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) {  // warp-uniform: the tensor-memory loads below are .aligned
         ok = false;
         break;
       }
       tc_fence_after();
-      const int local_row = static_cast<int>(rank) * 128 + quad * 32;
 #pragma unroll 1
       for (int cb = 0; cb < 4; ++cb) {
         uint32_t v[32];
@@ -282,10 +324,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         put_block(tile, lane, v);
         __syncwarp();
-        if (U.slot < 0)
-          finish_block<T>(p.ep, tile, lane, static_cast<int64_t>(U.tm) * 256 + local_row, static_cast<int64_t>(U.tn) * 256 + local_col);
-        else
+        if (U.slot < 0) {
+          const BlockReads in = next;
+          if (cb < 3) read_block<T>(p.ep, lane, row0, col0 + cb * 32 + 32, next);
+          finish_block<T>(p.ep, tile, lane, row0, col0 + cb * 32, in);
+        } else {
           save_block(p.partial + static_cast<int64_t>(U.slot) * kTileFloats, tile, lane, local_row, local_col);
+        }
         __syncwarp();
       }
     }
@@ -295,6 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
 
+  let_successor_come();
   __syncthreads();
   cluster_sync_all();  // the leader's MMAs are done with both CTAs' shared and tensor memory
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
@@ -304,20 +350,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // thread per eight columns, a warp per row of a tile.
 template <typename T>
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ GemmParams p) {
-  const int tile = blockIdx.x / 32, lane = threadIdx.x & 31, row = blockIdx.x % 32 * 8 + (threadIdx.x >> 5);
+  __shared__ uint4 rows[8][64];
+  wait_for_predecessor();
+  let_successor_come();
+  const int tile = blockIdx.x / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x % 32 * 8 + warp;
   int tm, tn;
   tile_position(p.full + tile, p, tm, tn);
-  const int64_t r = static_cast<int64_t>(tm) * 256 + row, c = static_cast<int64_t>(tn) * 256 + lane * 8;
-  if (r >= p.ep.rows || c >= p.ep.cols) return;
+  const Epilogue& e = p.ep;
+  const int64_t r = static_cast<int64_t>(tm) * 256 + row, col0 = static_cast<int64_t>(tn) * 256, c = col0 + lane * 8;
+  if (r >= e.rows) return;
+  const uint4 bias = read_bias8<T>(e, c), residual = read_residual8<T>(e, r, c);
   const float* at = p.partial + static_cast<int64_t>(tile) * p.splits * kTileFloats + row * 256 + lane * 8;
   float v[8] = {};
+#pragma unroll 4
   for (int s = 0; s < p.splits; ++s, at += kTileFloats) {
     float add[8];
     load8(at, true, 8, add);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += add[i];
   }
-  epilogue8<T>(p.ep, r, c, v);
+  const uint4 z = finish8<T>(e, r, c, bias, residual, v);
+  if (e.vec) {
+    if (c >= e.cols) return;
+    const int64_t left = e.cols - c;
+    const int n = left < 8 ? static_cast<int>(left) : 8;
+    if (e.z) store8_raw(static_cast<T*>(e.z) + r * e.ldz + c, left >= 8, n, z);
+    store8_raw(static_cast<T*>(e.y) + r * e.ldy + c, left >= 8, n, pack8<T>(v));
+    return;
+  }
+  // rows off 16-byte boundaries: element by element, neighbouring lanes neighbouring elements
+  rows[warp][lane] = pack8<T>(v);
+  rows[warp][32 + lane] = z;
+  __syncwarp();
+  const T* from = reinterpret_cast<const T*>(rows[warp]);
+  for (int i = lane; i < 256 && col0 + i < e.cols; i += 32) {
+    static_cast<T*>(e.y)[r * e.ldy + col0 + i] = from[i];
+    if (e.z) static_cast<T*>(e.z)[r * e.ldz + col0 + i] = from[256 + i];
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -365,28 +434,25 @@ GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms) {
 }
 
 template <typename T, bool A_ROWS, bool B_ROWS>
-cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p, int num_sms, cudaStream_t st) {
-  auto kernel = linear_gemm_kernel<T, A_ROWS, B_ROWS>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p, const DeviceResources& res,
+                           cudaStream_t st) {
+  const cudaError_t e = allow_smem<linear_gemm_kernel<T, A_ROWS, B_ROWS>>(kSmem, res.device);
   if (e != cudaSuccess) return e;
-  kernel<<<2 * std::min(p.units, num_sms / 2), kThreads, kSmem, st>>>(ma, mb, p);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_kernel(linear_gemm_kernel<T, A_ROWS, B_ROWS>, 2 * std::min(p.units, res.num_sms / 2), kThreads, kSmem, 2, st, ma,
+                       mb, p);
 }
 
 template <typename T>
 cudaError_t launch_typed(const Operand& a, const Operand& b, const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p,
-                         int num_sms, cudaStream_t st) {
+                         const DeviceResources& res, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (p.units > 0)
-    e = a.rows_contiguous   ? launch_product<T, true, true>(ma, mb, p, num_sms, st)
-        : b.rows_contiguous ? launch_product<T, false, true>(ma, mb, p, num_sms, st)
-                            : launch_product<T, false, false>(ma, mb, p, num_sms, st);
+    e = a.rows_contiguous   ? launch_product<T, true, true>(ma, mb, p, res, st)
+        : b.rows_contiguous ? launch_product<T, false, true>(ma, mb, p, res, st)
+                            : launch_product<T, false, false>(ma, mb, p, res, st);
   const int join = p.tiles_m * p.tiles_n - p.full;
   if (e != cudaSuccess || join == 0) return e;
-  linear_join_kernel<T><<<join * 32, 256, 0, st>>>(p);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_kernel(linear_join_kernel<T>, join * 32, 256, 0, 1, st, p);
 }
 
 }  // namespace
@@ -406,8 +472,8 @@ cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t k, const E
   p.err = res.err;
   CUtensorMap ma{}, mb{};
   if (k > 0 && (!make_map(&ma, a, ep.rows, k) || !make_map(&mb, b, ep.cols, k))) return cudaErrorInvalidValue;
-  return dtype == OZ2_BF16 ? launch_typed<__nv_bfloat16>(a, b, ma, mb, p, res.num_sms, st)
-                           : launch_typed<__half>(a, b, ma, mb, p, res.num_sms, st);
+  return dtype == OZ2_BF16 ? launch_typed<__nv_bfloat16>(a, b, ma, mb, p, res, st)
+                           : launch_typed<__half>(a, b, ma, mb, p, res, st);
 }
 
 }  // namespace oz2

@@ -106,6 +106,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(done), 1);
     *abort_flag = 0;
     fence_barrier_init();
+    prefetch_map(&map_x);
+    prefetch_map(&map_w);
+  }
+  wait_for_predecessor();
+  if (threadIdx.x == 0) {
     // the first loads need nothing that the other warps set up
     for (int i = 0; i < ahead; ++i) load_stage(i, kb0 + i);
   }
@@ -168,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   tc_fence_after();
+  let_successor_come();
   // every MMA and so every load is done: the sums take the stages' place, as [row of A][row of B]
   float* sums = reinterpret_cast<float*>(smem);
   const int rows = static_cast<int>(p.ep.rows);
@@ -218,46 +224,32 @@ int cluster_for(int64_t tiles, int nkb, int num_sms) {
 
 template <typename T, int MP, bool W_ROWS>
 cudaError_t launch_few_impl(const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p, int64_t tiles, int ranks,
-                            cudaStream_t st) {
-  auto kernel = linear_few_kernel<T, MP, W_ROWS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<MP>::SMEM);
+                            const DeviceResources& res, cudaStream_t st) {
+  const cudaError_t e = allow_smem<linear_few_kernel<T, MP, W_ROWS>>(Few<MP>::SMEM, res.device);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ranks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Few<MP>::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(ranks);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, mx, mw, p);
-  count_launches(1);
-  return e;
+  return launch_kernel(linear_few_kernel<T, MP, W_ROWS>, tiles * ranks, kThreads, Few<MP>::SMEM, ranks, st, mx, mw, p);
 }
 
 template <typename T, int MP>
-cudaError_t launch_few_mp(const Operand& x, const Operand& w, int64_t k, FewParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_few_mp(const Operand& x, const Operand& w, int64_t k, const FewParams& p, const DeviceResources& res, cudaStream_t st) {
   const int64_t tiles = ceil_div(p.ep.cols, kTileN);
   CUtensorMap mx, mw;
   if (!encode_map_2d(&mx, x.p, k, p.ep.rows, x.ld, kBK, MP)) return cudaErrorInvalidValue;
   if (w.rows_contiguous) {
     if (!encode_map_2d(&mw, w.p, p.ep.cols, k, w.ld, 64, kBK)) return cudaErrorInvalidValue;
-    return launch_few_impl<T, MP, true>(mx, mw, p, tiles, cluster_for(tiles, p.nkb, num_sms), st);
+    return launch_few_impl<T, MP, true>(mx, mw, p, tiles, cluster_for(tiles, p.nkb, res.num_sms), res, st);
   }
   if (!encode_map_2d(&mw, w.p, k, p.ep.cols, w.ld, kBK, kTileN)) return cudaErrorInvalidValue;
-  return launch_few_impl<T, MP, false>(mx, mw, p, tiles, cluster_for(tiles, p.nkb, num_sms), st);
+  return launch_few_impl<T, MP, false>(mx, mw, p, tiles, cluster_for(tiles, p.nkb, res.num_sms), res, st);
 }
 
 template <typename T>
-cudaError_t launch_few_typed(const Operand& x, const Operand& w, int64_t k, FewParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_few_typed(const Operand& x, const Operand& w, int64_t k, const FewParams& p, const DeviceResources& res, cudaStream_t st) {
   const int64_t m = p.ep.rows;
-  if (m <= 16) return launch_few_mp<T, 16>(x, w, k, p, num_sms, st);
-  if (m <= 32) return launch_few_mp<T, 32>(x, w, k, p, num_sms, st);
-  if (m <= 64) return launch_few_mp<T, 64>(x, w, k, p, num_sms, st);
-  return launch_few_mp<T, 128>(x, w, k, p, num_sms, st);
+  if (m <= 16) return launch_few_mp<T, 16>(x, w, k, p, res, st);
+  if (m <= 32) return launch_few_mp<T, 32>(x, w, k, p, res, st);
+  if (m <= 64) return launch_few_mp<T, 64>(x, w, k, p, res, st);
+  return launch_few_mp<T, 128>(x, w, k, p, res, st);
 }
 
 }  // namespace
@@ -272,8 +264,8 @@ cudaError_t launch_linear_few(const Operand& a, const Operand& b, int64_t k, con
   p.ep = ep;
   p.nkb = static_cast<int>(ceil_div(k, kBK));
   p.err = res.err;
-  return dtype == OZ2_BF16 ? launch_few_typed<__nv_bfloat16>(a, b, k, p, res.num_sms, st)
-                           : launch_few_typed<__half>(a, b, k, p, res.num_sms, st);
+  return dtype == OZ2_BF16 ? launch_few_typed<__nv_bfloat16>(a, b, k, p, res, st)
+                           : launch_few_typed<__half>(a, b, k, p, res, st);
 }
 
 }  // namespace oz2

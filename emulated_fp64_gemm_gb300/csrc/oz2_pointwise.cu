@@ -1,82 +1,145 @@
-// Dropout with a mask that is never stored, and the gradient at a linear
-// layer's pre-activation with its column sums.  Both are one pass over their
-// matrices, in groups of eight neighbouring columns: one 16-byte vector of a
-// 16-bit type and one call of the generator.
+// Dropout with a mask that is never stored, the gradient at a linear layer's
+// pre-activation with its column sums, and aligned copies.  All are one pass
+// over their matrices, in groups of eight neighbouring columns: one 16-byte
+// vector of a 16-bit type and one call of the generator.
 #include <algorithm>
+#include <array>
 
 #include "oz2_layers.cuh"
 
 namespace oz2 {
 namespace {
 
-// ------------------------------------------------------------------ dropout
-// One thread per group.  Bound by HBM for long inputs (one read of x and the
-// residual, one write), by launch latency for short ones.
-template <typename T>
-__global__ void __launch_bounds__(256) dropout_kernel(uint32_t groups, FastDiv per_row, int64_t row0, int64_t cols,
-                                                      const T* x, int64_t ldx, const T* residual, int64_t ldr, T* y,
-                                                      int64_t ldy, bool aligned, const Dropout drop) {
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  if (i >= groups) return;
-  const uint32_t r = (__umulhi(i, per_row.mul) + i) >> per_row.shift, g = i - r * per_row.d;
-  const int64_t row = row0 + r, col = static_cast<int64_t>(g) * 8, left = cols - col;
-  const bool vec = aligned && left >= 8;
-  const int n = left < 8 ? static_cast<int>(left) : 8;
-  float v[8];
-  load8(x + row * ldx + col, vec, n, v);
-  if (drop.threshold) drop8(drop, static_cast<uint32_t>(row), g, v);
-  if (residual) {
-    float add[8];
-    load8(residual + row * ldr + col, vec, n, add);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += add[e];
+// Threads are numbered over a matrix's groups, below 2^31 in one launch (FastDiv).
+struct Groups {
+  uint32_t count;
+  FastDiv per_row;
+  int64_t row0, cols;
+  __device__ __forceinline__ void place(uint32_t i, int64_t& row, uint32_t& g) const {
+    const uint32_t r = (__umulhi(i, per_row.mul) + i) >> per_row.shift;
+    row = row0 + r;
+    g = i - r * per_row.d;
   }
-  store8(y + row * ldy + col, vec, n, v);
+};
+// Calls f(Groups) for as many rows at a time as one launch can number.
+template <typename F>
+cudaError_t for_rows(int64_t rows, int64_t cols, F&& f) {
+  const int64_t per_row = ceil_div(cols, 8), most = (int64_t(1) << 30) / per_row;
+  for (int64_t row0 = 0; row0 < rows; row0 += most) {
+    const cudaError_t e = f(Groups{static_cast<uint32_t>(std::min(rows - row0, most) * per_row),
+                                   make_fast_div(static_cast<uint32_t>(per_row)), row0, cols});
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
-// Group numbers of one launch stay below 2^31 (FastDiv): rows per launch.
-int64_t rows_per_launch(int64_t per_row) { return (int64_t(1) << 30) / per_row; }
+// ------------------------------------------------------------------ dropout
+// A thread takes U groups, 256 apart, and has all of their loads in flight at
+// once.  FLAT: the matrices are contiguous, with whole groups in every row, so a
+// group's number is its address; the general form multiplies rows by strides.
+// Long inputs are bound by the generator's instructions beside HBM (a copy of
+// 16384 x 8192 bf16 by the same kernel, p = 0, takes 83 us).
+template <typename T, int U, bool FLAT>
+__global__ void __launch_bounds__(256) dropout_kernel(const Groups groups, const T* x, int64_t ldx, const T* residual, int64_t ldr,
+                                                      T* y, int64_t ldy, bool aligned, const Dropout drop) {
+  wait_for_predecessor();
+  const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
+  constexpr int kPieces = sizeof(T) / 2;
+  if (FLAT) {
+    const int64_t base = (groups.row0 * groups.per_row.d + first) * 8;
+    uint4 xs[U][kPieces], rs[U][kPieces];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (first + u * 256 >= groups.count) break;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        xs[u][k] = reinterpret_cast<const uint4*>(x + base + u * 2048)[k];
+        if (residual) rs[u][k] = reinterpret_cast<const uint4*>(residual + base + u * 2048)[k];
+      }
+    }
+    let_successor_come();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (first + u * 256 >= groups.count) break;
+      int64_t row;
+      uint32_t g;
+      groups.place(first + u * 256, row, g);
+      float v[8];
+      values8<T>(xs[u], v);
+      if (drop.threshold) drop8(drop, static_cast<uint32_t>(row), g, v);
+      if (residual) {
+        float add[8];
+        values8<T>(rs[u], add);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += add[e];
+      }
+      store8(y + base + u * 2048, true, 8, v);
+    }
+  } else {
+    if (first < groups.count) {
+      int64_t row;
+      uint32_t g;
+      groups.place(first, row, g);
+      const int64_t col = static_cast<int64_t>(g) * 8, left = groups.cols - col;
+      const bool vec = aligned && left >= 8;
+      const int n = left < 8 ? static_cast<int>(left) : 8;
+      float v[8], add[8];
+      load8(x + row * ldx + col, vec, n, v);
+      if (residual) load8(residual + row * ldr + col, vec, n, add);
+      if (drop.threshold) drop8(drop, static_cast<uint32_t>(row), g, v);
+      if (residual) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += add[e];
+      }
+      store8(y + row * ldy + col, vec, n, v);
+    }
+    let_successor_come();
+  }
+}
 
 template <typename T>
 cudaError_t dropout_impl(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                          void* y, int64_t ldy, bool aligned, const Dropout& drop, cudaStream_t st) {
-  const int64_t per_row = ceil_div(cols, 8), most = rows_per_launch(per_row);
-  for (int64_t row0 = 0; row0 < rows; row0 += most) {
-    const uint32_t groups = static_cast<uint32_t>(std::min(rows - row0, most) * per_row);
-    dropout_kernel<T><<<(groups + 255) / 256, 256, 0, st>>>(
-        groups, make_fast_div(static_cast<uint32_t>(per_row)), row0, cols, static_cast<const T*>(x), ldx,
-        static_cast<const T*>(residual), ldr, static_cast<T*>(y), ldy, aligned, drop);
-    count_launches(1);
-  }
-  return cudaGetLastError();
+  const bool flat = aligned && cols % 8 == 0 && ((ldx == cols && ldy == cols && (!residual || ldr == cols)) || rows == 1);
+  return for_rows(rows, cols, [&](const Groups& g) {
+    // one group per thread until the device is full
+    const bool deep = g.count > 152u * 2048u;
+    auto kernel = flat ? (deep ? dropout_kernel<T, 4, true> : dropout_kernel<T, 1, true>) : dropout_kernel<T, 1, false>;
+    return launch_kernel(kernel, ceil_div(g.count, flat && deep ? 1024 : 256), 256, 0, 1, st, g, static_cast<const T*>(x), ldx,
+                         static_cast<const T*>(residual), ldr, static_cast<T*>(y), ldy, aligned, drop);
+  });
 }
 
 // ------------------------------------------------------------------ aligned copies
 // Rows that do not start on 16-byte boundaries cannot be loaded by TMA: they
 // are copied once, eight elements per thread.
-__global__ void __launch_bounds__(256) pack_kernel(uint32_t groups, FastDiv per_row, int64_t row0, int64_t cols,
-                                                   const uint16_t* x, int64_t ldx, uint16_t* out, int64_t ld_out) {
+__global__ void __launch_bounds__(256) pack_kernel(const Groups groups, const uint16_t* x, int64_t ldx, uint16_t* out,
+                                                   int64_t ld_out) {
+  wait_for_predecessor();
+  let_successor_come();
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  if (i >= groups) return;
-  const uint32_t r = (__umulhi(i, per_row.mul) + i) >> per_row.shift;
-  const int64_t row = row0 + r, col = static_cast<int64_t>(i - r * per_row.d) * 8;
+  if (i >= groups.count) return;
+  int64_t row;
+  uint32_t g;
+  groups.place(i, row, g);
+  const int64_t col = static_cast<int64_t>(g) * 8;
   uint32_t v[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = col + e < cols ? x[row * ldx + col + e] : 0u;
+  for (int e = 0; e < 8; ++e) v[e] = col + e < groups.cols ? x[row * ldx + col + e] : 0u;
   *reinterpret_cast<uint4*>(out + row * ld_out + col) =
       make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 
 // ------------------------------------------------------------------ dz and its column sums
-// A block of 8 warps takes a strip of 256 columns (one group per lane) and
-// kDzRows rows, warp w the rows w, w + 8, ...; each thread keeps its eight
-// column sums in 32 bits.  The strip's sums go to one row of `partial`, which
-// dbias_kernel adds up in order, so the result does not depend on timing.
-constexpr int kDzRows = 128;
-
-template <typename T>
-__global__ void __launch_bounds__(256) dz_kernel(const DzArgs a, bool aligned) {
+// A block of 8 warps takes a strip of 256 columns (one group per lane) and `rows`
+// rows, warp w the rows w, w + 8, ..., two of them in flight; each thread keeps
+// its eight column sums in 32 bits.  The strip's sums go to one row of `partial`,
+// which column_sums_kernel adds up in order, so the result does not depend on
+// timing.  Bound by HBM: dy and z read, dz written once.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzArgs a, bool aligned, int rows) {
   __shared__ float sums[8][256];
+  wait_for_predecessor();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t strips = (a.n + 255) / 256;
   const int64_t rb = blockIdx.x / strips, col = (blockIdx.x % strips * 32 + lane) * 8, left = a.n - col;
@@ -84,21 +147,45 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzArgs a, bool aligned) {
   const int n = left < 8 ? static_cast<int>(left) : 8;  // may be <= 0
   float sum[8] = {};
   if (n > 0) {
-    const int64_t end = min(a.m, (rb + 1) * kDzRows);
-    for (int64_t row = rb * kDzRows + warp; row < end; row += 8) {
-      float g[8];
-      load8(static_cast<const T*>(a.dy) + row * a.lddy + col, vec, n, g);
-      if (a.act != OZ2_ACT_NONE) {
-        float z[8];
-        load8(static_cast<const T*>(a.preact) + row * a.ldz + col, vec, n, z);
-        activate_grad8(a.act, z, g);
-      }
-      if (a.drop.threshold) drop8(a.drop, static_cast<uint32_t>(row), static_cast<uint32_t>(col >> 3), g);
-      if (a.dz) store8(static_cast<T*>(a.dz) + row * a.lddz + col, vec, n, g);
+    const int64_t row0 = rb * rows + warp;
+    const int count = static_cast<int>(min(a.m - rb * rows, static_cast<int64_t>(rows)));
+    const T* dy = static_cast<const T*>(a.dy) + row0 * a.lddy + col;
+    const T* pre = static_cast<const T*>(a.preact) + row0 * a.ldz + col;
+    T* dz = static_cast<T*>(a.dz) + row0 * a.lddz + col;
+    uint32_t row = static_cast<uint32_t>(row0);
+    for (int r = warp; r < count; r += 16, row += 16) {
+      uint4 gs[2], zs[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += g[e];
+      for (int u = 0; u < 2; ++u) {
+        if (r + u * 8 >= count) break;
+        gs[u] = load8_raw(dy, vec, n);
+        dy += 8 * a.lddy;
+        if (ACT != OZ2_ACT_NONE) {
+          zs[u] = load8_raw(pre, vec, n);
+          pre += 8 * a.ldz;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (r + u * 8 >= count) break;
+        float g[8];
+        values8<T>(&gs[u], g);
+        if (ACT != OZ2_ACT_NONE) {
+          float z[8];
+          values8<T>(&zs[u], z);
+          activate_grad8(ACT, z, g);
+        }
+        if (a.drop.threshold) drop8(a.drop, row + u * 8, static_cast<uint32_t>(col >> 3), g);
+        if (a.dz) {
+          *reinterpret_cast<uint4*>(dz) = pack8<T>(g);
+          dz += 8 * a.lddz;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += g[e];  // columns past n: their sums are not used
+      }
     }
   }
+  let_successor_come();
   if (!a.dbias) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) sums[warp][lane * 8 + e] = sum[e];
@@ -112,34 +199,51 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzArgs a, bool aligned) {
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) dbias_kernel(const float* partial, int64_t rows, int64_t n, T* dbias) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (c >= n) return;
-  float s = 0.0f;
-  for (int64_t r = 0; r < rows; ++r) s += partial[r * n + c];
-  dbias[c] = Elem<T>::down(s);
-}
+// Rows per block: enough blocks to fill the device, then fewer partial rows.
+int dz_rows(int64_t m, int64_t n) { return ceil_div(n, 256) * ceil_div(m, 64) >= 608 ? 64 : 16; }
 
 template <typename T>
 cudaError_t dz_impl(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
-  const bool aligned = aligned16(a.dy, a.lddy, dtype) && (!a.preact || aligned16(a.preact, a.ldz, dtype)) &&
-                       (!a.dz || aligned16(a.dz, a.lddz, dtype));
-  const int64_t blocks = ceil_div(a.n, 256) * dz_partial_rows(a.m, a.n);
+  const bool aligned = aligned16(a.dy, a.lddy, dtype) && (!a.preact || aligned16(a.preact, a.ldz, dtype));
+  const int64_t rows = dz_partial_rows(a.m, a.n), blocks = ceil_div(a.n, 256) * rows;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  dz_kernel<T><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, aligned);
-  count_launches(1);
-  if (a.dbias) {
-    dbias_kernel<T><<<static_cast<unsigned>(ceil_div(a.n, 256)), 256, 0, st>>>(
-        a.partial, dz_partial_rows(a.m, a.n), a.n, static_cast<T*>(a.dbias));
-    count_launches(1);
+  static constexpr auto kernels = std::array{dz_kernel<T, OZ2_ACT_NONE>, dz_kernel<T, OZ2_ACT_RELU>, dz_kernel<T, OZ2_ACT_SILU>,
+                                             dz_kernel<T, OZ2_ACT_GELU>, dz_kernel<T, OZ2_ACT_GELU_TANH>};
+  const cudaError_t e = launch_kernel(kernels[a.act], blocks, 256, 0, 1, st, a, aligned, dz_rows(a.m, a.n));
+  if (e != cudaSuccess || !a.dbias) return e;
+  return launch_column_sums(a.partial, rows, a.n, dtype, a.dbias, st);
+}
+
+// ------------------------------------------------------------------ column sums
+// A block of 8 warps per 32 columns: warp w adds the rows w, w + 8, ..., then the warps' sums are added.
+template <typename T>
+__global__ void __launch_bounds__(256) column_sums_kernel(const float* partial, int64_t rows, int64_t cols, T* out) {
+  __shared__ float sums[8][32];
+  wait_for_predecessor();
+  let_successor_come();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float s = 0.0f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int64_t r = warp; r < rows; r += 8) s += partial[r * cols + c];
   }
-  return cudaGetLastError();
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp || c >= cols) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) s += sums[w][lane];
+  out[c] = Elem<T>::down(s);
+}
+
+template <typename T>
+cudaError_t column_sums_impl(const float* partial, int64_t rows, int64_t cols, void* out, cudaStream_t st) {
+  return launch_kernel(column_sums_kernel<T>, ceil_div(cols, 32), 256, 0, 1, st, partial, rows, cols, static_cast<T*>(out));
 }
 
 }  // namespace
 
-int64_t dz_partial_rows(int64_t m, int64_t) { return ceil_div(m, kDzRows); }
+int64_t dz_partial_rows(int64_t m, int64_t n) { return ceil_div(m, dz_rows(m, n)); }
 
 cudaError_t launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                            void* y, int64_t ldy, oz2_dtype dtype, const Dropout& drop, cudaStream_t st) {
@@ -152,18 +256,22 @@ cudaError_t launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t ld
 }
 
 cudaError_t launch_pack(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* out, int64_t ld_out, cudaStream_t st) {
-  const int64_t per_row = ceil_div(cols, 8), most = rows_per_launch(per_row);
-  for (int64_t row0 = 0; row0 < rows; row0 += most) {
-    const uint32_t groups = static_cast<uint32_t>(std::min(rows - row0, most) * per_row);
-    pack_kernel<<<(groups + 255) / 256, 256, 0, st>>>(groups, make_fast_div(static_cast<uint32_t>(per_row)), row0, cols,
-                                                      static_cast<const uint16_t*>(x), ldx, static_cast<uint16_t*>(out), ld_out);
-    count_launches(1);
-  }
-  return cudaGetLastError();
+  return for_rows(rows, cols, [&](const Groups& g) {
+    return launch_kernel(pack_kernel, ceil_div(g.count, 256), 256, 0, 1, st, g, static_cast<const uint16_t*>(x), ldx,
+                         static_cast<uint16_t*>(out), ld_out);
+  });
 }
 
 cudaError_t launch_dz(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
   return dtype == OZ2_BF16 ? dz_impl<__nv_bfloat16>(a, dtype, st) : dz_impl<__half>(a, dtype, st);
+}
+
+cudaError_t launch_column_sums(const float* partial, int64_t rows, int64_t cols, oz2_dtype dtype, void* out, cudaStream_t st) {
+  switch (dtype) {
+    case OZ2_BF16: return column_sums_impl<__nv_bfloat16>(partial, rows, cols, out, st);
+    case OZ2_F16: return column_sums_impl<__half>(partial, rows, cols, out, st);
+    default: return column_sums_impl<float>(partial, rows, cols, out, st);
+  }
 }
 
 }  // namespace oz2
