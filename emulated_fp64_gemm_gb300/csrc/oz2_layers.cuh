@@ -78,19 +78,37 @@ struct Operand {
   int64_t ld;
   bool rows_contiguous;
 };
-// Bytes of `partial` that a product needs.
-size_t linear_workspace(const Operand& a, int64_t k, const Epilogue& ep, int num_sms);
+// The form for small outputs, which launch_linear takes where it is the faster
+// one: tiles of mp x 128, k split over clusters of `ranks`; its time, estimated.
+struct FewPlan {
+  int mp, ranks;
+  double us;
+};
+FewPlan plan_few(bool x_rows, int64_t rows, int64_t cols, int nkb, int num_sms);
+cudaError_t launch_linear_few(const FewPlan& plan, const Operand& a, const Operand& b, int64_t k, const Epilogue& ep,
+                              oz2_dtype dtype, const DeviceResources& res, cudaStream_t st);
+
+// How a product is run, and the bytes of `partial` that it needs.
+struct LinearPlan {
+  FewPlan few;
+  bool use_few;
+  size_t partial_bytes;
+  LinearPlan() : few{}, use_few(false), partial_bytes(0) {}
+  LinearPlan(const Operand& a, int64_t k, const Epilogue& ep, int num_sms);
+};
 // B is rows_contiguous wherever A is.
-cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
-                          const DeviceResources& res, float* partial, cudaStream_t st);
+cudaError_t launch_linear(const LinearPlan& plan, const Operand& a, const Operand& b, int64_t k, const Epilogue& ep,
+                          oz2_dtype dtype, const DeviceResources& res, float* partial, cudaStream_t st);
 
-// The form for few rows of A, which launch_linear takes where it can.
-bool linear_few_supported(const Operand& a, int64_t k, const Epilogue& ep);
-cudaError_t launch_linear_few(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
-                              const DeviceResources& res, cudaStream_t st);
-
-// A copy of a 16-bit matrix whose rows are ld_out (a multiple of 8) elements apart.
-cudaError_t launch_pack(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* out, int64_t ld_out, cudaStream_t st);
+// Copies of 16-bit matrices whose rows are ld_out (a multiple of 8) elements apart, in one launch; rows may be 0.
+struct PackJob {
+  int64_t rows, cols;
+  const void* x;
+  int64_t ldx;
+  void* out;
+  int64_t ld_out;
+};
+cudaError_t launch_pack(const PackJob& a, const PackJob& b, cudaStream_t st);
 
 cudaError_t launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                            void* y, int64_t ldy, oz2_dtype dtype, const Dropout& drop, cudaStream_t st);

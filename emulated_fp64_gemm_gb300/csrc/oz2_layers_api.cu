@@ -61,12 +61,12 @@ struct Input {
       at = c.take(static_cast<size_t>(rows) * ld * 2);
     }
   }
-  // `from`'s leading dimension before the copy
-  cudaError_t place(uint8_t* base, int64_t from_ld, cudaStream_t st) {
-    if (!copy) return cudaSuccess;
+  // The copy that is to be made, if any (from_ld: the leading dimension before it).
+  PackJob place(uint8_t* base, int64_t from_ld) {
+    if (!copy) return PackJob{};
     const void* from = p;
     p = base + at;
-    return launch_pack(rows, cols, from, from_ld, base + at, ld, st);
+    return PackJob{rows, cols, from, from_ld, base + at, ld};
   }
 };
 
@@ -92,12 +92,13 @@ oz2_status linear(const oz2_linear_args& a, cudaStream_t st) {
            (!a.residual || aligned16(a.residual, a.ldr, dtype)) && (!a.preact || aligned16(a.preact, a.ldz, dtype));
   Carver c;
   Input xi(a.x, a.m, a.k, a.ldx, true, c), wi(a.w, a.n, a.k, a.ldw, true, c);
-  const size_t partial = c.take(linear_workspace(Operand{xi.p, xi.ld, false}, a.k, ep, res.num_sms));
+  const LinearPlan plan(Operand{xi.p, xi.ld, false}, a.k, ep, res.num_sms);
+  const size_t partial = c.take(plan.partial_bytes);
   e = acquire_resources(st, c.used, &res);
   if (e != OZ2_OK) return e;
-  OZ2_TRY(xi.place(res.workspace, a.ldx, st));
-  OZ2_TRY(wi.place(res.workspace, a.ldw, st));
-  OZ2_TRY(launch_linear(Operand{xi.p, xi.ld, false}, Operand{wi.p, wi.ld, false}, a.k, ep, dtype, res,
+  const PackJob x_job = xi.place(res.workspace, a.ldx), w_job = wi.place(res.workspace, a.ldw);
+  OZ2_TRY(launch_pack(x_job, w_job, st));
+  OZ2_TRY(launch_linear(plan, Operand{xi.p, xi.ld, false}, Operand{wi.p, wi.ld, false}, a.k, ep, dtype, res,
                         reinterpret_cast<float*>(res.workspace + partial), st));
   return OZ2_OK;
 }
@@ -139,8 +140,10 @@ oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
   Input xi(a.x, m, k, a.ldx, dw, c), wi(a.w, n, k, a.ldw, dx, c);
   const Epilogue ep_dx = plain_epilogue(dx, a.lddx, m, k, dtype), ep_dw = plain_epilogue(dw, a.lddw, n, k, dtype);
   // the two products run one after the other and share the room for partial sums
-  const size_t partial_at = c.take(std::max(dx ? linear_workspace(Operand{nullptr, ld, false}, n, ep_dx, res.num_sms) : 0,
-                                            dw ? linear_workspace(Operand{nullptr, ld, true}, m, ep_dw, res.num_sms) : 0));
+  LinearPlan plan_dx, plan_dw;
+  if (dx) plan_dx = LinearPlan(Operand{nullptr, ld, false}, n, ep_dx, res.num_sms);
+  if (dw) plan_dw = LinearPlan(Operand{nullptr, ld, true}, m, ep_dw, res.num_sms);
+  const size_t partial_at = c.take(std::max(plan_dx.partial_bytes, plan_dw.partial_bytes));
   e = acquire_resources(st, c.used, &res);
   if (e != OZ2_OK) return e;
   if (make_dz || dbias) {
@@ -161,10 +164,10 @@ oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
   }
   const void* dz = make_dz ? res.workspace + dz_at : a.dy;
   float* partial = reinterpret_cast<float*>(res.workspace + partial_at);
-  OZ2_TRY(xi.place(res.workspace, a.ldx, st));
-  OZ2_TRY(wi.place(res.workspace, a.ldw, st));
-  if (dx) OZ2_TRY(launch_linear(Operand{dz, ld, false}, Operand{wi.p, wi.ld, true}, n, ep_dx, dtype, res, partial, st));
-  if (dw) OZ2_TRY(launch_linear(Operand{dz, ld, true}, Operand{xi.p, xi.ld, true}, m, ep_dw, dtype, res, partial, st));
+  const PackJob x_job = xi.place(res.workspace, a.ldx), w_job = wi.place(res.workspace, a.ldw);
+  OZ2_TRY(launch_pack(x_job, w_job, st));
+  if (dx) OZ2_TRY(launch_linear(plan_dx, Operand{dz, ld, false}, Operand{wi.p, wi.ld, true}, n, ep_dx, dtype, res, partial, st));
+  if (dw) OZ2_TRY(launch_linear(plan_dw, Operand{dz, ld, true}, Operand{xi.p, xi.ld, true}, m, ep_dw, dtype, res, partial, st));
   return OZ2_OK;
 }
 

@@ -398,8 +398,8 @@ bool make_map(CUtensorMap* map, const Operand& o, int64_t rows, int64_t k) {
 // others split `splits` ways.  Times in k blocks of one tile on one pair (0.27 us
 // at 1.9 GHz): a wave of units lasts its longest unit, each unit adds about one
 // block of pipeline fill, and joining costs a launch (about 12 blocks) and the
-// partial sums' way through L2 (about 0.25 blocks per slot and pair-load).
-void plan_units(int tiles, int nkb, int pairs, int* full, int* splits) {
+// partial sums' way through L2 (about 0.25 blocks per slot).  Returns the time.
+double plan_units(int tiles, int nkb, int pairs, int* full, int* splits) {
   auto waves = [&](int units) { return (units + pairs - 1) / pairs; };
   *full = nkb ? tiles : 0;
   *splits = nkb ? 1 : 0;  // no terms: nothing but the epilogue
@@ -417,9 +417,10 @@ void plan_units(int tiles, int nkb, int pairs, int* full, int* splits) {
       }
     }
   }
+  return best;
 }
 
-GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms) {
+GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms, double* us) {
   GemmParams p{};
   p.ep = ep;
   p.tiles_m = static_cast<int>(ceil_div(ep.rows, 256));
@@ -428,7 +429,8 @@ GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms) {
   // 32 MB of A per group: each of the two dies keeps its own copy in its half of the 129 MB L2.  At k = 4096 with
   // 16384 columns groups of 4, 8, 16 and 32 row tiles took 604, 572, 562 and 583 us.
   p.group = static_cast<int>(std::clamp<int64_t>((32 << 20) / (256 * 2 * std::max<int64_t>(k, 1)), 4, 16));
-  plan_units(p.tiles_m * p.tiles_n, p.nkb, num_sms / 2, &p.full, &p.splits);
+  // 8 us: what a launch of one tile with one block takes, launch and epilogue included
+  *us = 8.0 + 0.27 * plan_units(p.tiles_m * p.tiles_n, p.nkb, num_sms / 2, &p.full, &p.splits);
   p.units = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
   return p;
 }
@@ -457,17 +459,23 @@ cudaError_t launch_typed(const Operand& a, const Operand& b, const CUtensorMap& 
 
 }  // namespace
 
-size_t linear_workspace(const Operand& a, int64_t k, const Epilogue& ep, int num_sms) {
-  if (linear_few_supported(a, k, ep)) return 0;
-  const GemmParams p = make_params(k, ep, num_sms);
-  return static_cast<size_t>(p.tiles_m * p.tiles_n - p.full) * p.splits * kTileFloats * 4;
+LinearPlan::LinearPlan(const Operand& a, int64_t k, const Epilogue& ep, int num_sms)
+    : few(plan_few(a.rows_contiguous, ep.rows, ep.cols, static_cast<int>(ceil_div(k, kBK)), num_sms)),
+      use_few(k > 0 && ep.rows <= 64),
+      partial_bytes(0) {
+  if (use_few) return;
+  double gemm_us;
+  const GemmParams p = make_params(k, ep, num_sms, &gemm_us);
+  use_few = k > 0 && few.us < gemm_us;
+  if (!use_few) partial_bytes = static_cast<size_t>(p.tiles_m * p.tiles_n - p.full) * p.splits * kTileFloats * 4;
 }
 
-cudaError_t launch_linear(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
-                               const DeviceResources& res, float* partial, cudaStream_t st) {
-  if (linear_few_supported(a, k, ep)) return launch_linear_few(a, b, k, ep, dtype, res, st);
-  if (ceil_div(ep.rows, 256) * ceil_div(ep.cols, 256) > (1 << 24)) return cudaErrorInvalidConfiguration;
-  GemmParams p = make_params(k, ep, res.num_sms);
+cudaError_t launch_linear(const LinearPlan& plan, const Operand& a, const Operand& b, int64_t k, const Epilogue& ep,
+                          oz2_dtype dtype, const DeviceResources& res, float* partial, cudaStream_t st) {
+  if (ceil_div(ep.rows, 16) * ceil_div(ep.cols, 128) > (1 << 28)) return cudaErrorInvalidConfiguration;
+  if (plan.use_few) return launch_linear_few(plan.few, a, b, k, ep, dtype, res, st);
+  double us;
+  GemmParams p = make_params(k, ep, res.num_sms, &us);
   p.partial = partial;
   p.err = res.err;
   CUtensorMap ma{}, mb{};

@@ -1,15 +1,16 @@
-// The linear products of few rows (a serving batch's single tokens): C = A B^T
-// with at most 128 rows of A, on the tensor cores with the roles exchanged.
+// The linear products whose output is too small to fill the device with 256 x 256
+// tiles (a serving batch's single tokens, short or narrow layers): C = A B^T in
+// tiles of MP x 128, MP = 16 to 128, on the tensor cores with the roles exchanged.
 //
-// The weights B are the big operand and are read once, so the floor is their
-// bytes.  A CTA takes 128 of B's rows as the MMA's M dimension and all rows of
-// A, padded to MP, as its N dimension (tcgen05.mma.cta_group::1); the weights
-// come through a ring of TMA stages that fills the SM's shared memory, which
-// keeps tens of megabytes in flight over the device.  A cluster of CTAs splits
-// k: each forms its partial sums in tensor memory, puts them into its shared
-// memory, and every CTA then adds its share of the outputs from all of them, in
-// the order of their ranks, through distributed shared memory, and finishes it.
-// So there is one launch, no workspace, and no result that depends on timing.
+// A CTA takes 128 of B's rows as the MMA's M dimension and up to MP rows of A as
+// its N dimension (tcgen05.mma.cta_group::1), so a single token wastes no weight
+// traffic: for few rows of A the floor is B's bytes, read once.  They come through
+// a ring of TMA stages that fills the SM's shared memory, which keeps tens of
+// megabytes in flight over the device.  A cluster of CTAs splits k: each forms its
+// partial sums in tensor memory, puts them into its shared memory, and every CTA
+// then adds its share of the outputs from all of them, in the order of their
+// ranks, through distributed shared memory, and finishes it.  So there is one
+// launch, no workspace, and no result that depends on timing.
 //
 // Every wait is bounded in time; a timeout sets the device error word and the
 // kernel winds down.
@@ -25,7 +26,7 @@ namespace {
 
 constexpr int kBK = 64;
 constexpr int kTileN = 128;  // rows of B per CTA
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWBytes = kTileN * kBK * 2;
 
 template <int MP>
@@ -34,12 +35,12 @@ struct Few {
   static constexpr int STAGES = std::min(11, 196 * 1024 / (kWBytes + X_BYTES));
   static constexpr int SMEM = 1024 + STAGES * (kWBytes + X_BYTES) + 256;
   static constexpr int TMEM_COLS = MP < 32 ? 32 : MP;
-  static_assert(MP * kTileN * 4 <= STAGES * (kWBytes + X_BYTES), "the partial sums take the stages' place");
+  static_assert(MP * kTileN * 8 <= STAGES * (kWBytes + X_BYTES), "the partial sums and 16-bit outputs take the stages' place");
 };
 
 struct FewParams {
   Epilogue ep;
-  int nkb;
+  int nkb, tiles_n;
   int* err;
 };
 
@@ -63,8 +64,8 @@ __device__ __forceinline__ void load_cluster4(uint32_t addr, float* v) {
                : "memory");
 }
 
-// W_ROWS: B is [k][rows] (its rows contiguous in memory).
-template <typename T, int MP, bool W_ROWS>
+// X_ROWS, W_ROWS: A, B are [k][rows] (their rows contiguous in memory).
+template <typename T, int MP, bool X_ROWS, bool W_ROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ FewParams p) {
@@ -81,7 +82,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
-  const int row_w = static_cast<int>(blockIdx.x / ranks) * kTileN;
+  const int tile = static_cast<int>(blockIdx.x) / ranks;
+  const int row_x = tile / p.tiles_n * MP, row_w = tile % p.tiles_n * kTileN;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / ranks);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / ranks);
 
@@ -94,7 +96,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       tma_load_2d(w, &map_w, kb * kBK, row_w, bar);
     }
-    tma_load_2d(smem_u32(s_x + stage * F::X_BYTES), &map_x, kb * kBK, 0, bar);
+    const uint32_t x = smem_u32(s_x + stage * F::X_BYTES);
+    if (X_ROWS) {
+#pragma unroll
+      for (int h = 0; h < MP / 64; ++h) tma_load_2d(x + h * 8192, &map_x, row_x + h * 64, kb * kBK, bar);
+    } else {
+      tma_load_2d(x, &map_x, kb * kBK, row_x, bar);
+    }
   };
 
   const int ahead = min(F::STAGES, kb1 - kb0);
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // kind::f16: 32-bit sums, both operands of type T, M = 128, N = MP
       constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(W_ROWS) << 15) |
-                                 (static_cast<uint32_t>(MP >> 3) << 17) | ((128u >> 4) << 24);
+                                 (static_cast<uint32_t>(X_ROWS) << 16) | (static_cast<uint32_t>(MP >> 3) << 17) | ((128u >> 4) << 24);
       for (int i = 0; i < kb1 - kb0; ++i) {
         const int stage = i % F::STAGES;
         if (!mbar_wait_bounded(smem_u32(&full[stage]), (i / F::STAGES) & 1, abort_flag, kWaitLimitNs)) {
@@ -160,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t w = smem_u32(s_w + stage * kWBytes), x = smem_u32(s_x + stage * F::X_BYTES);
 #pragma unroll
         for (int s = 0; s < kBK / 16; ++s)
-          mma_f16(tmem, operand_desc<W_ROWS>(w, s), operand_desc<false>(x, s), idesc, i == 0 && s == 0 ? 0u : 1u);
+          mma_f16(tmem, operand_desc<W_ROWS>(w, s), operand_desc<X_ROWS>(x, s), idesc, i == 0 && s == 0 ? 0u : 1u);
         mma_commit(smem_u32(&empty[stage]));
       }
       mma_commit(smem_u32(done));
@@ -176,36 +184,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   let_successor_come();
   // every MMA and so every load is done: the sums take the stages' place, as [row of A][row of B]
   float* sums = reinterpret_cast<float*>(smem);
-  const int rows = static_cast<int>(p.ep.rows);
+  const int rows = static_cast<int>(min(p.ep.rows - row_x, static_cast<int64_t>(MP)));
 #pragma unroll 1
-  for (int c = 0; c < rows; c += 32) {
+  for (int c = warp / 4 * 32; c < rows; c += 64) {  // warp w: lanes 32 (w % 4) .., every other 32 columns
     uint32_t v[32];
-    tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+    tmem_ld32(tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + c, v);
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      if (c + i < rows) sums[(c + i) * kTileN + threadIdx.x] = __uint_as_float(v[i]);
+      if (c + i < rows) sums[(c + i) * kTileN + warp % 4 * 32 + lane] = __uint_as_float(v[i]);
   }
   tc_fence_before();
   if (ranks > 1) cluster_sync_all(); else __syncthreads();
-  // groups of eight columns, shared out among the ranks
+  // groups of eight columns, shared out among the ranks; a thread takes four at a time
   const int items = rows * (kTileN / 8), per_rank = (items + ranks - 1) / ranks;
-  const int end = min(items, (rank + 1) * per_rank);
-  for (int i = rank * per_rank + static_cast<int>(threadIdx.x); i < end; i += kThreads) {
-    const int r = i / (kTileN / 8), g = i % (kTileN / 8);
-    const int64_t col = row_w + g * 8;
-    if (col >= p.ep.cols) continue;
-    const uint32_t at = smem_u32(sums + r * kTileN + g * 8);
-    float v[8] = {};
-    for (int s = 0; s < ranks; ++s) {
-      const uint32_t from = map_to_rank(at, s);
-      float add[8];
-      load_cluster4(from, add);
-      load_cluster4(from + 16, add + 4);
+  const int begin = min(items, rank * per_rank), end = min(items, begin + per_rank);
+  T* y_out = reinterpret_cast<T*>(smem + MP * kTileN * 4);  // for rows off 16-byte boundaries: y, then z
+  T* z_out = y_out + MP * kTileN;
+  for (int i0 = begin + static_cast<int>(threadIdx.x); i0 < end; i0 += 4 * kThreads) {
+    uint4 bias[4], residual[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += add[e];
+    for (int u = 0; u < 4; ++u) {
+      const int i = min(i0 + u * kThreads, end - 1);
+      const int64_t row = row_x + i / (kTileN / 8), col = row_w + i % (kTileN / 8) * 8;
+      bias[u] = read_bias8<T>(p.ep, col);
+      residual[u] = read_residual8<T>(p.ep, row, col);
     }
-    epilogue8<T>(p.ep, r, col, v);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= end) break;
+      const int64_t row = row_x + i / (kTileN / 8), col = row_w + i % (kTileN / 8) * 8, left = p.ep.cols - col;
+      const uint32_t at = smem_u32(sums + i * 8);
+      float v[8] = {};
+      for (int s = 0; s < ranks; ++s) {
+        const uint32_t from = map_to_rank(at, s);
+        float add[8];
+        load_cluster4(from, add);
+        load_cluster4(from + 16, add + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += add[e];
+      }
+      const uint4 z = finish8<T>(p.ep, row, col, bias[u], residual[u], v);
+      if (p.ep.vec) {
+        if (left <= 0) continue;
+        const int n = left < 8 ? static_cast<int>(left) : 8;
+        if (p.ep.z) store8_raw(static_cast<T*>(p.ep.z) + row * p.ep.ldz + col, left >= 8, n, z);
+        store8_raw(static_cast<T*>(p.ep.y) + row * p.ep.ldy + col, left >= 8, n, pack8<T>(v));
+      } else {
+        reinterpret_cast<uint4*>(y_out)[i - begin] = pack8<T>(v);
+        reinterpret_cast<uint4*>(z_out)[i - begin] = z;
+      }
+    }
+  }
+  if (!p.ep.vec) {  // element by element, neighbouring threads neighbouring elements
+    __syncthreads();
+    for (int e = threadIdx.x; e < (end - begin) * 8; e += kThreads) {
+      const int64_t row = row_x + (begin * 8 + e) / kTileN, col = row_w + (begin * 8 + e) % kTileN;
+      if (col >= p.ep.cols) continue;
+      static_cast<T*>(p.ep.y)[row * p.ep.ldy + col] = y_out[e];
+      if (p.ep.z) static_cast<T*>(p.ep.z)[row * p.ep.ldz + col] = z_out[e];
+    }
   }
   if (ranks > 1) cluster_sync_all(); else __syncthreads();  // the peers have read this CTA's sums
   if (warp == 1) {
@@ -215,57 +254,66 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// CTAs per cluster: as many as the device has room for beside the tiles, each with two k blocks at least.
-int cluster_for(int64_t tiles, int nkb, int num_sms) {
-  int s = 1;
-  while (s < 8 && tiles * s * 2 <= num_sms && nkb >= s * 4) s *= 2;
-  return s;
-}
-
-template <typename T, int MP, bool W_ROWS>
-cudaError_t launch_few_impl(const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p, int64_t tiles, int ranks,
+template <typename T, int MP, bool X_ROWS, bool W_ROWS>
+cudaError_t launch_few_impl(const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p, int64_t ctas, int ranks,
                             const DeviceResources& res, cudaStream_t st) {
-  const cudaError_t e = allow_smem<linear_few_kernel<T, MP, W_ROWS>>(Few<MP>::SMEM, res.device);
+  const cudaError_t e = allow_smem<linear_few_kernel<T, MP, X_ROWS, W_ROWS>>(Few<MP>::SMEM, res.device);
   if (e != cudaSuccess) return e;
-  return launch_kernel(linear_few_kernel<T, MP, W_ROWS>, tiles * ranks, kThreads, Few<MP>::SMEM, ranks, st, mx, mw, p);
+  return launch_kernel(linear_few_kernel<T, MP, X_ROWS, W_ROWS>, ctas, kThreads, Few<MP>::SMEM, ranks, st, mx, mw, p);
 }
 
 template <typename T, int MP>
-cudaError_t launch_few_mp(const Operand& x, const Operand& w, int64_t k, const FewParams& p, const DeviceResources& res, cudaStream_t st) {
-  const int64_t tiles = ceil_div(p.ep.cols, kTileN);
+cudaError_t launch_few_mp(const Operand& x, const Operand& w, int64_t k, FewParams& p, int ranks, const DeviceResources& res,
+                          cudaStream_t st) {
   CUtensorMap mx, mw;
-  if (!encode_map_2d(&mx, x.p, k, p.ep.rows, x.ld, kBK, MP)) return cudaErrorInvalidValue;
-  if (w.rows_contiguous) {
-    if (!encode_map_2d(&mw, w.p, p.ep.cols, k, w.ld, 64, kBK)) return cudaErrorInvalidValue;
-    return launch_few_impl<T, MP, true>(mx, mw, p, tiles, cluster_for(tiles, p.nkb, res.num_sms), res, st);
-  }
-  if (!encode_map_2d(&mw, w.p, k, p.ep.cols, w.ld, kBK, kTileN)) return cudaErrorInvalidValue;
-  return launch_few_impl<T, MP, false>(mx, mw, p, tiles, cluster_for(tiles, p.nkb, res.num_sms), res, st);
+  if (x.rows_contiguous ? !encode_map_2d(&mx, x.p, p.ep.rows, k, x.ld, 64, kBK) : !encode_map_2d(&mx, x.p, k, p.ep.rows, x.ld, kBK, MP))
+    return cudaErrorInvalidValue;
+  if (w.rows_contiguous ? !encode_map_2d(&mw, w.p, p.ep.cols, k, w.ld, 64, kBK)
+                        : !encode_map_2d(&mw, w.p, k, p.ep.cols, w.ld, kBK, kTileN))
+    return cudaErrorInvalidValue;
+  p.tiles_n = static_cast<int>(ceil_div(p.ep.cols, kTileN));
+  const int64_t ctas = ceil_div(p.ep.rows, MP) * p.tiles_n * ranks;
+  if constexpr (MP >= 64)
+    if (x.rows_contiguous) return launch_few_impl<T, MP, true, true>(mx, mw, p, ctas, ranks, res, st);
+  return w.rows_contiguous ? launch_few_impl<T, MP, false, true>(mx, mw, p, ctas, ranks, res, st)
+                           : launch_few_impl<T, MP, false, false>(mx, mw, p, ctas, ranks, res, st);
 }
 
 template <typename T>
-cudaError_t launch_few_typed(const Operand& x, const Operand& w, int64_t k, const FewParams& p, const DeviceResources& res, cudaStream_t st) {
-  const int64_t m = p.ep.rows;
-  if (m <= 16) return launch_few_mp<T, 16>(x, w, k, p, res, st);
-  if (m <= 32) return launch_few_mp<T, 32>(x, w, k, p, res, st);
-  if (m <= 64) return launch_few_mp<T, 64>(x, w, k, p, res, st);
-  return launch_few_mp<T, 128>(x, w, k, p, res, st);
+cudaError_t launch_few_typed(const FewPlan& plan, const Operand& x, const Operand& w, int64_t k, FewParams& p,
+                             const DeviceResources& res, cudaStream_t st) {
+  switch (plan.mp) {
+    case 16: return launch_few_mp<T, 16>(x, w, k, p, plan.ranks, res, st);
+    case 32: return launch_few_mp<T, 32>(x, w, k, p, plan.ranks, res, st);
+    case 64: return launch_few_mp<T, 64>(x, w, k, p, plan.ranks, res, st);
+    default: return launch_few_mp<T, 128>(x, w, k, p, plan.ranks, res, st);
+  }
 }
 
 }  // namespace
 
-bool linear_few_supported(const Operand& a, int64_t k, const Epilogue& ep) {
-  return !a.rows_contiguous && k > 0 && ep.rows <= 128;
+FewPlan plan_few(bool x_rows, int64_t rows, int64_t cols, int nkb, int num_sms) {
+  FewPlan p{};
+  p.mp = x_rows ? (rows <= 64 ? 64 : 128) : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int64_t tiles = ceil_div(rows, p.mp) * ceil_div(cols, kTileN);
+  // CTAs per cluster: as many as the device has room for beside the tiles, each with two k blocks at least
+  p.ranks = 1;
+  while (p.ranks < 8 && tiles * p.ranks * 2 <= num_sms && nkb >= p.ranks * 4) p.ranks *= 2;
+  // a k block takes its operands' way from L2 (about 64 bytes per SM and cycle); the ends of a CTA 2.5 us and its outputs' share
+  const double block_us = (kWBytes + p.mp * kBK * 2) / 64.0 / 1900.0;
+  const double waves = static_cast<double>(ceil_div(tiles * p.ranks, num_sms));
+  p.us = 2.0 + waves * (2.5 + p.mp / 64.0 + ceil_div(nkb, p.ranks) * block_us);
+  return p;
 }
 
-cudaError_t launch_linear_few(const Operand& a, const Operand& b, int64_t k, const Epilogue& ep, oz2_dtype dtype,
-                              const DeviceResources& res, cudaStream_t st) {
+cudaError_t launch_linear_few(const FewPlan& plan, const Operand& a, const Operand& b, int64_t k, const Epilogue& ep,
+                              oz2_dtype dtype, const DeviceResources& res, cudaStream_t st) {
   FewParams p{};
   p.ep = ep;
   p.nkb = static_cast<int>(ceil_div(k, kBK));
   p.err = res.err;
-  return dtype == OZ2_BF16 ? launch_few_typed<__nv_bfloat16>(a, b, k, p, res, st)
-                           : launch_few_typed<__half>(a, b, k, p, res, st);
+  return dtype == OZ2_BF16 ? launch_few_typed<__nv_bfloat16>(plan, a, b, k, p, res, st)
+                           : launch_few_typed<__half>(plan, a, b, k, p, res, st);
 }
 
 }  // namespace oz2

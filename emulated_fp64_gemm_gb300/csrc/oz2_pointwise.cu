@@ -113,21 +113,34 @@ cudaError_t dropout_impl(int64_t rows, int64_t cols, const void* x, int64_t ldx,
 // ------------------------------------------------------------------ aligned copies
 // Rows that do not start on 16-byte boundaries cannot be loaded by TMA: they
 // are copied once, eight elements per thread.
-__global__ void __launch_bounds__(256) pack_kernel(const Groups groups, const uint16_t* x, int64_t ldx, uint16_t* out,
-                                                   int64_t ld_out) {
+struct PackPart {
+  Groups groups;
+  const uint16_t* x;
+  int64_t ldx;
+  uint16_t* out;
+  int64_t ld_out;
+};
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackPart a, const __grid_constant__ PackPart b,
+                                                   uint32_t a_blocks) {
   wait_for_predecessor();
   let_successor_come();
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  if (i >= groups.count) return;
+  const PackPart& p = blockIdx.x < a_blocks ? a : b;
+  const uint32_t i = (blockIdx.x < a_blocks ? blockIdx.x : blockIdx.x - a_blocks) * 256u + threadIdx.x;
+  if (i >= p.groups.count) return;
   int64_t row;
   uint32_t g;
-  groups.place(i, row, g);
+  p.groups.place(i, row, g);
   const int64_t col = static_cast<int64_t>(g) * 8;
+  const uint16_t* x = p.x + row * p.ldx + col;
   uint32_t v[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = col + e < groups.cols ? x[row * ldx + col + e] : 0u;
-  *reinterpret_cast<uint4*>(out + row * ld_out + col) =
+  for (int e = 0; e < 8; ++e) v[e] = col + e < p.groups.cols ? x[e] : 0u;
+  *reinterpret_cast<uint4*>(p.out + row * p.ld_out + col) =
       make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+cudaError_t launch_parts(const PackPart& a, const PackPart& b, cudaStream_t st) {
+  const int64_t a_blocks = ceil_div(a.groups.count, 256), blocks = a_blocks + ceil_div(b.groups.count, 256);
+  return blocks == 0 ? cudaSuccess : launch_kernel(pack_kernel, blocks, 256, 0, 1, st, a, b, static_cast<uint32_t>(a_blocks));
 }
 
 // ------------------------------------------------------------------ dz and its column sums
@@ -255,11 +268,26 @@ cudaError_t launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t ld
   }
 }
 
-cudaError_t launch_pack(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* out, int64_t ld_out, cudaStream_t st) {
-  return for_rows(rows, cols, [&](const Groups& g) {
-    return launch_kernel(pack_kernel, ceil_div(g.count, 256), 256, 0, 1, st, g, static_cast<const uint16_t*>(x), ldx,
-                         static_cast<uint16_t*>(out), ld_out);
-  });
+cudaError_t launch_pack(const PackJob& a, const PackJob& b, cudaStream_t st) {
+  auto part = [](const PackJob& j, const Groups& g) {
+    return PackPart{g, static_cast<const uint16_t*>(j.x), j.ldx, static_cast<uint16_t*>(j.out), j.ld_out};
+  };
+  // both in one launch where each is numbered by one (PackPart{}: nothing)
+  PackPart waiting{};
+  for (const PackJob* j : {&a, &b}) {
+    if (j->rows == 0 || j->cols == 0) continue;
+    const cudaError_t e = for_rows(j->rows, j->cols, [&](const Groups& g) {
+      if (waiting.groups.count == 0) {
+        waiting = part(*j, g);
+        return cudaSuccess;
+      }
+      const cudaError_t r = launch_parts(waiting, part(*j, g), st);
+      waiting = PackPart{};
+      return r;
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return launch_parts(waiting, PackPart{}, st);
 }
 
 cudaError_t launch_dz(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
