@@ -114,8 +114,8 @@ cudaError_t launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t ld
                            void* y, int64_t ldy, oz2_dtype dtype, const Dropout& drop, cudaStream_t st);
 
 // dz = act'(preact) * keep * dy / (1 - p) into dz (null: not written) and its
-// column sums into dbias (null: not formed), through `partial`:
-// dz_partial_rows(m, n) x n floats.
+// column sums into dbias (null: not formed), through `partial`: dz_partial_rows
+// x n floats, null for one row.
 int64_t dz_partial_rows(int64_t m, int64_t n);
 struct DzArgs {
   int64_t m, n;

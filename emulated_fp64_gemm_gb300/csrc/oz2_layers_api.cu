@@ -136,7 +136,8 @@ oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
   const int64_t ld = make_dz ? ceil_div(n, 8) * 8 : a.lddy;
   Carver c;
   const size_t dz_at = c.take(make_dz ? static_cast<size_t>(m) * ld * 2 : 0);
-  const size_t sums_at = c.take(dbias ? static_cast<size_t>(dz_partial_rows(m, n)) * n * 4 : 0);
+  const int64_t sum_rows = dz_partial_rows(m, n);
+  const size_t sums_at = c.take(dbias && sum_rows > 1 ? static_cast<size_t>(sum_rows) * n * 4 : 0);
   Input xi(a.x, m, k, a.ldx, dw, c), wi(a.w, n, k, a.ldw, dx, c);
   const Epilogue ep_dx = plain_epilogue(dx, a.lddx, m, k, dtype), ep_dw = plain_epilogue(dw, a.lddw, n, k, dtype);
   // the two products run one after the other and share the room for partial sums
@@ -157,7 +158,7 @@ oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
     d.dz = make_dz ? res.workspace + dz_at : nullptr;
     d.lddz = ld;
     d.dbias = dbias;
-    d.partial = reinterpret_cast<float*>(res.workspace + sums_at);
+    d.partial = sum_rows > 1 ? reinterpret_cast<float*>(res.workspace + sums_at) : nullptr;
     d.act = a.act;
     d.drop = drop;
     OZ2_TRY(launch_dz(d, dtype, st));

@@ -26,7 +26,6 @@ namespace {
 
 constexpr int kBK = 64;
 constexpr int kTileN = 128;  // rows of B per CTA
-constexpr int kThreads = 256;
 constexpr int kWBytes = kTileN * kBK * 2;
 
 template <int MP>
@@ -35,12 +34,14 @@ struct Few {
   static constexpr int STAGES = std::min(11, 196 * 1024 / (kWBytes + X_BYTES));
   static constexpr int SMEM = 1024 + STAGES * (kWBytes + X_BYTES) + 256;
   static constexpr int TMEM_COLS = MP < 32 ? 32 : MP;
+  static constexpr int THREADS = MP <= 32 ? 256 : 512;
   static_assert(MP * kTileN * 8 <= STAGES * (kWBytes + X_BYTES), "the partial sums and 16-bit outputs take the stages' place");
 };
 
 struct FewParams {
   Epilogue ep;
   int nkb, tiles_n;
+  int log_ranks;  // CTAs per cluster: 1 << log_ranks
   int* err;
 };
 
@@ -49,12 +50,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
 }
 
 __device__ __forceinline__ void load_cluster4(uint32_t addr, float* v) {
@@ -66,10 +61,11 @@ __device__ __forceinline__ void load_cluster4(uint32_t addr, float* v) {
 
 // X_ROWS, W_ROWS: A, B are [k][rows] (their rows contiguous in memory).
 template <typename T, int MP, bool X_ROWS, bool W_ROWS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Few<MP>::THREADS, 1)
     linear_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ FewParams p) {
   using F = Few<MP>;
+  constexpr int kThreads = F::THREADS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_w = smem;
@@ -81,11 +77,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
-  const int tile = static_cast<int>(blockIdx.x) / ranks;
+  const int ranks = 1 << p.log_ranks, rank = static_cast<int>(blockIdx.x) & (ranks - 1);
+  const int tile = static_cast<int>(blockIdx.x) >> p.log_ranks;
   const int row_x = tile / p.tiles_n * MP, row_w = tile % p.tiles_n * kTileN;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / ranks);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / ranks);
+  const int kb0 = p.nkb * rank >> p.log_ranks, kb1 = p.nkb * (rank + 1) >> p.log_ranks;  // nkb <= 2^25, 8 ranks at most
 
   auto load_stage = [&](int stage, int kb) {
     const uint32_t bar = smem_u32(&full[stage]), w = smem_u32(s_w + stage * kWBytes);
@@ -106,14 +101,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   const int ahead = min(F::STAGES, kb1 - kb0);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < F::STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), 1);
+  if (warp == 0) {
+    if (lane < F::STAGES) {
+      mbar_init(smem_u32(&full[lane]), 1);
+      mbar_init(smem_u32(&empty[lane]), 1);
     }
-    mbar_init(smem_u32(done), 1);
-    *abort_flag = 0;
+    if (lane == 0) {
+      mbar_init(smem_u32(done), 1);
+      *abort_flag = 0;
+    }
     fence_barrier_init();
+    __syncwarp();
+  } else if (warp == 2 && lane == 0) {
     prefetch_map(&map_x);
     prefetch_map(&map_w);
   }
@@ -132,6 +131,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+
+  // The outputs are finished in groups of eight columns, shared out among the
+  // ranks; what the first of this thread's groups needs is read ahead of the sums.
+  const int rows = static_cast<int>(min(p.ep.rows - row_x, static_cast<int64_t>(MP)));
+  const int items = rows * (kTileN / 8), per_rank = (items + ranks - 1) >> p.log_ranks;
+  const int begin = min(items, rank * per_rank), end = min(items, begin + per_rank);
+  int item = begin + static_cast<int>(threadIdx.x);
+  auto item_row = [&](int i) { return static_cast<int64_t>(row_x + i / (kTileN / 8)); };
+  auto item_col = [&](int i) { return static_cast<int64_t>(row_w + i % (kTileN / 8) * 8); };
+  uint4 bias = read_bias8<T>(p.ep, item < end ? item_col(item) : p.ep.cols);
+  uint4 residual = read_residual8<T>(p.ep, item < end ? item_row(item) : p.ep.rows, item_col(item));
 
   if (warp == 0) {
     if (lane == 0) {
@@ -184,9 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   let_successor_come();
   // every MMA and so every load is done: the sums take the stages' place, as [row of A][row of B]
   float* sums = reinterpret_cast<float*>(smem);
-  const int rows = static_cast<int>(min(p.ep.rows - row_x, static_cast<int64_t>(MP)));
 #pragma unroll 1
-  for (int c = warp / 4 * 32; c < rows; c += 64) {  // warp w: lanes 32 (w % 4) .., every other 32 columns
+  for (int c = warp / 4 * 32; c < rows; c += kThreads / 4) {  // warp w: lanes 32 (w % 4) .., 32 columns in turn
     uint32_t v[32];
     tmem_ld32(tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + c, v);
     tmem_wait_ld();
@@ -196,45 +205,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   if (ranks > 1) cluster_sync_all(); else __syncthreads();
-  // groups of eight columns, shared out among the ranks; a thread takes four at a time
-  const int items = rows * (kTileN / 8), per_rank = (items + ranks - 1) / ranks;
-  const int begin = min(items, rank * per_rank), end = min(items, begin + per_rank);
+  // This code runs once per CTA, from a cold instruction cache: it is kept short, not unrolled over groups.
   T* y_out = reinterpret_cast<T*>(smem + MP * kTileN * 4);  // for rows off 16-byte boundaries: y, then z
   T* z_out = y_out + MP * kTileN;
-  for (int i0 = begin + static_cast<int>(threadIdx.x); i0 < end; i0 += 4 * kThreads) {
-    uint4 bias[4], residual[4];
+#pragma unroll 1
+  for (; item < end; item += kThreads) {
+    const int64_t row = item_row(item), col = item_col(item), left = p.ep.cols - col;
+    const uint32_t at = smem_u32(sums + item * 8);
+    float v[8] = {};
+#pragma unroll 1
+    for (int s0 = 0; s0 < ranks; s0 += 4) {  // four ranks' sums in flight (past the last one: the last one's, not added)
+      float add[4][8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = min(i0 + u * kThreads, end - 1);
-      const int64_t row = row_x + i / (kTileN / 8), col = row_w + i % (kTileN / 8) * 8;
-      bias[u] = read_bias8<T>(p.ep, col);
-      residual[u] = read_residual8<T>(p.ep, row, col);
+      for (int s = 0; s < 4; ++s) {
+        const uint32_t from = map_to_rank(at, min(s0 + s, ranks - 1));
+        load_cluster4(from, add[s]);
+        load_cluster4(from + 16, add[s] + 4);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (s0 + s >= ranks) break;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += add[s][e];
+      }
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * kThreads;
-      if (i >= end) break;
-      const int64_t row = row_x + i / (kTileN / 8), col = row_w + i % (kTileN / 8) * 8, left = p.ep.cols - col;
-      const uint32_t at = smem_u32(sums + i * 8);
-      float v[8] = {};
-      for (int s = 0; s < ranks; ++s) {
-        const uint32_t from = map_to_rank(at, s);
-        float add[8];
-        load_cluster4(from, add);
-        load_cluster4(from + 16, add + 4);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += add[e];
-      }
-      const uint4 z = finish8<T>(p.ep, row, col, bias[u], residual[u], v);
-      if (p.ep.vec) {
-        if (left <= 0) continue;
-        const int n = left < 8 ? static_cast<int>(left) : 8;
-        if (p.ep.z) store8_raw(static_cast<T*>(p.ep.z) + row * p.ep.ldz + col, left >= 8, n, z);
-        store8_raw(static_cast<T*>(p.ep.y) + row * p.ep.ldy + col, left >= 8, n, pack8<T>(v));
-      } else {
-        reinterpret_cast<uint4*>(y_out)[i - begin] = pack8<T>(v);
-        reinterpret_cast<uint4*>(z_out)[i - begin] = z;
-      }
+    const uint4 z = finish8<T>(p.ep, row, col, bias, residual, v);
+    if (item + kThreads < end) {
+      bias = read_bias8<T>(p.ep, item_col(item + kThreads));
+      residual = read_residual8<T>(p.ep, item_row(item + kThreads), item_col(item + kThreads));
+    }
+    if (p.ep.vec) {
+      if (left <= 0) continue;
+      const int n = left < 8 ? static_cast<int>(left) : 8;
+      if (p.ep.z) store8_raw(static_cast<T*>(p.ep.z) + row * p.ep.ldz + col, left >= 8, n, z);
+      store8_raw(static_cast<T*>(p.ep.y) + row * p.ep.ldy + col, left >= 8, n, pack8<T>(v));
+    } else {
+      reinterpret_cast<uint4*>(y_out)[item - begin] = pack8<T>(v);
+      reinterpret_cast<uint4*>(z_out)[item - begin] = z;
     }
   }
   if (!p.ep.vec) {  // element by element, neighbouring threads neighbouring elements
@@ -259,7 +266,7 @@ cudaError_t launch_few_impl(const CUtensorMap& mx, const CUtensorMap& mw, const 
                             const DeviceResources& res, cudaStream_t st) {
   const cudaError_t e = allow_smem<linear_few_kernel<T, MP, X_ROWS, W_ROWS>>(Few<MP>::SMEM, res.device);
   if (e != cudaSuccess) return e;
-  return launch_kernel(linear_few_kernel<T, MP, X_ROWS, W_ROWS>, ctas, kThreads, Few<MP>::SMEM, ranks, st, mx, mw, p);
+  return launch_kernel(linear_few_kernel<T, MP, X_ROWS, W_ROWS>, ctas, Few<MP>::THREADS, Few<MP>::SMEM, ranks, st, mx, mw, p);
 }
 
 template <typename T, int MP>
@@ -272,6 +279,7 @@ cudaError_t launch_few_mp(const Operand& x, const Operand& w, int64_t k, FewPara
                         : !encode_map_2d(&mw, w.p, k, p.ep.cols, w.ld, kBK, kTileN))
     return cudaErrorInvalidValue;
   p.tiles_n = static_cast<int>(ceil_div(p.ep.cols, kTileN));
+  p.log_ranks = ranks == 8 ? 3 : ranks == 4 ? 2 : ranks - 1;
   const int64_t ctas = ceil_div(p.ep.rows, MP) * p.tiles_n * ranks;
   if constexpr (MP >= 64)
     if (x.rows_contiguous) return launch_few_impl<T, MP, true, true>(mx, mw, p, ctas, ranks, res, st);
@@ -299,8 +307,9 @@ FewPlan plan_few(bool x_rows, int64_t rows, int64_t cols, int nkb, int num_sms) 
   // CTAs per cluster: as many as the device has room for beside the tiles, each with two k blocks at least
   p.ranks = 1;
   while (p.ranks < 8 && tiles * p.ranks * 2 <= num_sms && nkb >= p.ranks * 4) p.ranks *= 2;
-  // a k block takes its operands' way from L2 (about 64 bytes per SM and cycle); the ends of a CTA 2.5 us and its outputs' share
-  const double block_us = (kWBytes + p.mp * kBK * 2) / 64.0 / 1900.0;
+  // a k block takes its operands' way from L2 (88 bytes per SM and cycle measured); the ends of a CTA 2.5 us and its
+  // outputs' share
+  const double block_us = (kWBytes + p.mp * kBK * 2) / 88.0 / 1900.0;
   const double waves = static_cast<double>(ceil_div(tiles * p.ranks, num_sms));
   p.us = 2.0 + waves * (2.5 + p.mp / 64.0 + ceil_div(nkb, p.ranks) * block_us);
   return p;

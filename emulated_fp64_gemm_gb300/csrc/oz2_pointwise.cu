@@ -148,7 +148,7 @@ cudaError_t launch_parts(const PackPart& a, const PackPart& b, cudaStream_t st) 
 // rows, warp w the rows w, w + 8, ..., two of them in flight; each thread keeps
 // its eight column sums in 32 bits.  The strip's sums go to one row of `partial`,
 // which column_sums_kernel adds up in order, so the result does not depend on
-// timing.  Bound by HBM: dy and z read, dz written once.
+// timing (with one strip of rows they go to dbias at once).  Bound by HBM: dy and z read, dz written once.
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzArgs a, bool aligned, int rows) {
   __shared__ float sums[8][256];
@@ -208,12 +208,16 @@ __global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzAr
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) s += sums[w][threadIdx.x];
-    a.partial[rb * a.n + c] = s;
+    if (a.partial)
+      a.partial[rb * a.n + c] = s;
+    else
+      static_cast<T*>(a.dbias)[c] = Elem<T>::down(s);
   }
 }
 
-// Rows per block: enough blocks to fill the device, then fewer partial rows.
-int dz_rows(int64_t m, int64_t n) { return ceil_div(n, 256) * ceil_div(m, 64) >= 608 ? 64 : 16; }
+// Rows per block: all of a short matrix, whose sums are then complete; else
+// enough blocks to fill the device, then fewer partial rows.
+int dz_rows(int64_t m, int64_t n) { return m <= 128 ? 128 : ceil_div(n, 256) * ceil_div(m, 64) >= 608 ? 64 : 16; }
 
 template <typename T>
 cudaError_t dz_impl(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
@@ -223,7 +227,7 @@ cudaError_t dz_impl(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
   static constexpr auto kernels = std::array{dz_kernel<T, OZ2_ACT_NONE>, dz_kernel<T, OZ2_ACT_RELU>, dz_kernel<T, OZ2_ACT_SILU>,
                                              dz_kernel<T, OZ2_ACT_GELU>, dz_kernel<T, OZ2_ACT_GELU_TANH>};
   const cudaError_t e = launch_kernel(kernels[a.act], blocks, 256, 0, 1, st, a, aligned, dz_rows(a.m, a.n));
-  if (e != cudaSuccess || !a.dbias) return e;
+  if (e != cudaSuccess || !a.dbias || !a.partial) return e;
   return launch_column_sums(a.partial, rows, a.n, dtype, a.dbias, st);
 }
 
