@@ -423,11 +423,13 @@ __device__ __forceinline__ uint4 read_residual8(const Epilogue& e, int64_t row, 
                    left < 8 ? static_cast<int>(left) : 8);
 }
 // Everything after the product, in 32 bits: v becomes y (to be rounded once), the return value is z, rounded.
+// act: e.act, or a constant that leaves the other activations' code out.
 template <typename T>
-__device__ __forceinline__ uint4 finish8(const Epilogue& e, int64_t row, int64_t col, uint4 bias, uint4 residual, float (&v)[8]) {
+__device__ __forceinline__ uint4 finish8(const Epilogue& e, int act, int64_t row, int64_t col, uint4 bias, uint4 residual,
+                                         float (&v)[8]) {
   if (e.bias) add8<T>(bias, v);
   const uint4 z = e.z ? pack8<T>(v) : make_uint4(0, 0, 0, 0);
-  activate8(e.act, v);
+  activate8(act, v);
   if (e.drop.threshold) drop8(e.drop, static_cast<uint32_t>(row), static_cast<uint32_t>(col >> 3), v);
   if (e.residual) add8<T>(residual, v);
   return z;
@@ -443,17 +445,6 @@ __device__ __forceinline__ void store8_raw(T* p, bool vec, int n, uint4 u) {
   for (int i = 0; i < 8; ++i)
     if (i < n) reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
 }
-// The whole epilogue of eight columns, row and col inside the output.
-template <typename T>
-__device__ __forceinline__ void epilogue8(const Epilogue& e, int64_t row, int64_t col, float (&v)[8]) {
-  const int64_t left = e.cols - col;
-  const bool vec = e.vec && left >= 8;
-  const int n = left < 8 ? static_cast<int>(left) : 8;
-  const uint4 z = finish8<T>(e, row, col, read_bias8<T>(e, col), read_residual8<T>(e, row, col), v);
-  if (e.z) store8_raw(static_cast<T*>(e.z) + row * e.ldz + col, vec, n, z);
-  store8_raw(static_cast<T*>(e.y) + row * e.ldy + col, vec, n, pack8<T>(v));
-}
-
 // ------------------------------------------------------------ launches
 // Every layer kernel is launched so that it may start while the kernel before
 // it on the stream ends (programmatic stream serialization).  It waits, before

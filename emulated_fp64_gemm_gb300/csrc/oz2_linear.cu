@@ -102,30 +102,51 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 
-// A 32 x 32 block of the epilogue at (row0, col0): lane l takes the eight columns
-// col0 + 8 (l % 4) of rows l / 4, l / 4 + 8, ...
-struct BlockReads {
-  uint4 bias, residual[4];
+// The epilogue of one warp's 32 rows x 128 columns goes in 16 steps of eight rows
+// x 32 columns: in step i lane l takes the eight columns 32 (i / 4) + 8 (l % 4) ..
+// of row 8 (i % 4) + l / 4.  The residual is read four steps ahead, in registers
+// that move up by one in each.  The code of a step is there once: unrolled, with
+// every activation in it, it ran out of the instruction caches and took 630 cycles
+// a step without doing more than rounding and storing.
+constexpr int kSteps = 16;
+struct Strip {
+  int64_t row0, col0;  // of the strip
+  __device__ __forceinline__ int64_t row(int i, int lane) const { return row0 + (i & 3) * 8 + (lane >> 2); }
+  __device__ __forceinline__ int64_t col(int i, int lane) const { return col0 + (i >> 2) * 32 + (lane & 3) * 8; }
 };
-template <typename T>
-__device__ __forceinline__ void read_block(const Epilogue& e, int lane, int64_t row0, int64_t col0, BlockReads& in) {
-  const int64_t col = col0 + (lane & 3) * 8;
-  in.bias = read_bias8<T>(e, col);
+struct ReadAhead {
+  uint4 bias, residual[4];  // the next block's bias; the residual of the next four steps
+  template <typename T>
+  __device__ __forceinline__ void start(const Epilogue& e, const Strip& s, int lane) {
+    bias = read_bias8<T>(e, s.col(0, lane));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) in.residual[i] = read_residual8<T>(e, row0 + i * 8 + (lane >> 2), col);
-}
-template <typename T>
-__device__ __forceinline__ void finish_block(const Epilogue& e, float* tile, int lane, int64_t row0, int64_t col0,
-                                             const BlockReads& in) {
+    for (int i = 0; i < 4; ++i) residual[i] = read_residual8<T>(e, s.row(i, lane), s.col(i, lane));
+  }
+  template <typename T>
+  __device__ __forceinline__ uint4 next_residual(const Epilogue& e, const Strip& s, int lane, int i) {
+    const uint4 now = residual[0];
+    if (!e.residual) return now;
+    residual[0] = residual[1];
+    residual[1] = residual[2];
+    residual[2] = residual[3];
+    if (i + 4 < kSteps) residual[3] = read_residual8<T>(e, s.row(i + 4, lane), s.col(i + 4, lane));
+    return now;
+  }
+};
+// Steps 4 b .. 4 b + 3: the block of 32 x 32 sums in `tile`.
+template <typename T, int ACT>
+__device__ __forceinline__ void finish_block(const Epilogue& e, float* tile, int lane, const Strip& s, int b, ReadAhead& in) {
   const int g = lane & 3;
-  const int64_t col = col0 + g * 8;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + (lane >> 2);
-    const int64_t row = row0 + r;
+  const uint4 bias = in.bias;
+  if (b < 3) in.bias = read_bias8<T>(e, s.col(4 * b + 4, lane));
+#pragma unroll 1
+  for (int i = 4 * b; i < 4 * b + 4; ++i) {
+    const int r = (i & 3) * 8 + (lane >> 2);
+    const int64_t row = s.row(i, lane), col = s.col(i, lane);
     float v[8];
     get_eight(tile, r, g, v);
-    const uint4 z = finish8<T>(e, row, col, in.bias, in.residual[i], v);
+    const uint4 residual = in.next_residual<T>(e, s, lane, i);
+    const uint4 z = finish8<T>(e, ACT, row, col, bias, residual, v);
     if (e.vec) {
       if (row < e.rows && col < e.cols) {
         const int64_t left = e.cols - col;
@@ -143,17 +164,18 @@ __device__ __forceinline__ void finish_block(const Epilogue& e, float* tile, int
   if (e.vec) return;
   __syncwarp();
   // and out element by element, a row's 64 bytes per instruction
-  if (col0 + lane >= e.cols) return;
-  for (int r = 0; r < 32 && row0 + r < e.rows; ++r) {
+  const int64_t col = s.col0 + b * 32 + lane;
+  if (col >= e.cols) return;
+  for (int r = 0; r < 32 && s.row0 + r < e.rows; ++r) {
     const T* from = reinterpret_cast<const T*>(tile + r * 32) + lane;
-    static_cast<T*>(e.y)[(row0 + r) * e.ldy + col0 + lane] = from[0];
-    if (e.z) static_cast<T*>(e.z)[(row0 + r) * e.ldz + col0 + lane] = from[32];
+    static_cast<T*>(e.y)[(s.row0 + r) * e.ldy + col] = from[0];
+    if (e.z) static_cast<T*>(e.z)[(s.row0 + r) * e.ldz + col] = from[32];
   }
 }
 
 // The block's sums as they are, into a partial tile.
 __device__ __forceinline__ void save_block(float* partial, const float* tile, int lane, int row0, int col0) {
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int r = i * 8 + (lane >> 2);
     float v[8];
@@ -162,7 +184,7 @@ __device__ __forceinline__ void save_block(float* partial, const float* tile, in
   }
 }
 
-template <typename T, bool A_ROWS, bool B_ROWS>
+template <typename T, bool A_ROWS, bool B_ROWS, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ GemmParams p) {
@@ -302,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit U = decode_unit(u, p);
       const int slot = n & 1;
       const int local_row = static_cast<int>(rank) * 128 + quad * 32;
-      const int64_t row0 = static_cast<int64_t>(U.tm) * 256 + local_row, col0 = static_cast<int64_t>(U.tn) * 256 + half * 128;
-      BlockReads next{};
-      if (U.slot < 0) read_block<T>(p.ep, lane, row0, col0, next);
+      const Strip strip{static_cast<int64_t>(U.tm) * 256 + local_row, static_cast<int64_t>(U.tn) * 256 + half * 128};
+      ReadAhead ahead{};
+      if (U.slot < 0) ahead.start<T>(p.ep, strip, lane);
       const bool got = mbar_wait_bounded(smem_u32(&acc_full[slot]), (n >> 1) & 1, abort_flag, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) {  // warp-uniform: the tensor-memory loads below are .aligned
         ok = false;
@@ -324,13 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         put_block(tile, lane, v);
         __syncwarp();
-        if (U.slot < 0) {
-          const BlockReads in = next;
-          if (cb < 3) read_block<T>(p.ep, lane, row0, col0 + cb * 32 + 32, next);
-          finish_block<T>(p.ep, tile, lane, row0, col0 + cb * 32, in);
-        } else {
+        if (U.slot < 0)
+          finish_block<T, ACT>(p.ep, tile, lane, strip, cb, ahead);
+        else
           save_block(p.partial + static_cast<int64_t>(U.slot) * kTileFloats, tile, lane, local_row, local_col);
-        }
         __syncwarp();
       }
     }
@@ -369,7 +388,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += add[i];
   }
-  const uint4 z = finish8<T>(e, r, c, bias, residual, v);
+  const uint4 z = finish8<T>(e, e.act, r, c, bias, residual, v);
   if (e.vec) {
     if (c >= e.cols) return;
     const int64_t left = e.cols - c;
@@ -435,23 +454,33 @@ GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms, double* us) {
   return p;
 }
 
-template <typename T, bool A_ROWS, bool B_ROWS>
+template <typename T, bool A_ROWS, bool B_ROWS, int ACT>
 cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p, const DeviceResources& res,
                            cudaStream_t st) {
-  const cudaError_t e = allow_smem<linear_gemm_kernel<T, A_ROWS, B_ROWS>>(kSmem, res.device);
+  const cudaError_t e = allow_smem<linear_gemm_kernel<T, A_ROWS, B_ROWS, ACT>>(kSmem, res.device);
   if (e != cudaSuccess) return e;
-  return launch_kernel(linear_gemm_kernel<T, A_ROWS, B_ROWS>, 2 * std::min(p.units, res.num_sms / 2), kThreads, kSmem, 2, st, ma,
-                       mb, p);
+  return launch_kernel(linear_gemm_kernel<T, A_ROWS, B_ROWS, ACT>, 2 * std::min(p.units, res.num_sms / 2), kThreads, kSmem, 2, st,
+                       ma, mb, p);
 }
 
 template <typename T>
 cudaError_t launch_typed(const Operand& a, const Operand& b, const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p,
                          const DeviceResources& res, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
-  if (p.units > 0)
-    e = a.rows_contiguous   ? launch_product<T, true, true>(ma, mb, p, res, st)
-        : b.rows_contiguous ? launch_product<T, false, true>(ma, mb, p, res, st)
-                            : launch_product<T, false, false>(ma, mb, p, res, st);
+  if (p.units > 0) {
+    // the backward products end in plain outputs
+    auto launch = a.rows_contiguous   ? launch_product<T, true, true, OZ2_ACT_NONE>
+                  : b.rows_contiguous ? launch_product<T, false, true, OZ2_ACT_NONE>
+                                      : launch_product<T, false, false, OZ2_ACT_NONE>;
+    switch (p.ep.act) {
+      case OZ2_ACT_RELU: launch = launch_product<T, false, false, OZ2_ACT_RELU>; break;
+      case OZ2_ACT_SILU: launch = launch_product<T, false, false, OZ2_ACT_SILU>; break;
+      case OZ2_ACT_GELU: launch = launch_product<T, false, false, OZ2_ACT_GELU>; break;
+      case OZ2_ACT_GELU_TANH: launch = launch_product<T, false, false, OZ2_ACT_GELU_TANH>; break;
+      default: break;
+    }
+    e = launch(ma, mb, p, res, st);
+  }
   const int join = p.tiles_m * p.tiles_n - p.full;
   if (e != cudaSuccess || join == 0) return e;
   return launch_kernel(linear_join_kernel<T>, join * 32, 256, 0, 1, st, p);

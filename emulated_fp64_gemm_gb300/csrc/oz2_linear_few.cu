@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(Few<MP>::THREADS, 1)
         for (int e = 0; e < 8; ++e) v[e] += add[s][e];
       }
     }
-    const uint4 z = finish8<T>(p.ep, row, col, bias, residual, v);
+    const uint4 z = finish8<T>(p.ep, p.ep.act, row, col, bias, residual, v);
     if (item + kThreads < end) {
       bias = read_bias8<T>(p.ep, item_col(item + kThreads));
       residual = read_residual8<T>(p.ep, item_row(item + kThreads), item_col(item + kThreads));
