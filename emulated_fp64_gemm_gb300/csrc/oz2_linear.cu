@@ -8,11 +8,11 @@
 //
 // Structure: a cluster of two CTAs on two SMs forms 256 x 256 tiles with
 // tcgen05.mma.cta_group::2, each CTA holding 128 rows of A and 128 of B's 256
-// rows in shared memory (six stages of 64 k) and 128 x 256 sums in tensor
+// rows in shared memory (five or six stages of 64 k) and 128 x 256 sums in tensor
 // memory, twice: while the epilogue warps empty one accumulator, the tensor
 // core fills the other.  Warp 0 loads by TMA, one lane of the leader's warp 1
-// issues the MMAs, warps 2-9 are the epilogue (two per tensor-memory lane
-// quadrant, 128 columns each).  The grid is persistent: one pair per two SMs,
+// issues the MMAs, the other 8 or 16 warps are the epilogue (two or four per
+// tensor-memory lane quadrant).  The grid is persistent: one pair per two SMs,
 // walking over the work units.
 //
 // Epilogue: a warp moves 32 x 32 sums at a time through 4 KB of shared memory
@@ -41,12 +41,21 @@ namespace oz2 {
 namespace {
 
 constexpr int kBK = 64;                        // k per stage: 128 bytes
-constexpr int kStages = 6;
 constexpr int kOperandBytes = 128 * kBK * 2;   // a CTA's share of one operand per stage
 constexpr int kStageTx = 4 * kOperandBytes;    // bytes landing per stage across the pair
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kSmem = 1024 + kStages * 2 * kOperandBytes + kEpiWarps * 4096 + 256;
+// Epilogue warps, each with 4 KB of shared memory; what they leave holds the
+// stages.  Sixteen warps finish a tile in 60 % of the time of eight (2048 x 1024 x
+// 4096 with gelu, dropout and residual: 27 instead of 34 us), which counts where a
+// pair has few k blocks to hide its epilogues behind; the sixth stage and fewer
+// warps are worth 1.5 % of a long product (8192 x 4096 x 16384).
+template <int WARPS>
+struct Shape {
+  static constexpr int THREADS = 64 + 32 * WARPS;
+  static constexpr int STAGES = WARPS == 8 ? 6 : 5;
+  static constexpr int COLS = 1024 / WARPS;    // of the tile, per warp
+  static constexpr int STEPS = COLS / 8;       // of eight rows x 32 columns
+  static constexpr int SMEM = 1024 + STAGES * 2 * kOperandBytes + WARPS * 4096 + 256;
+};
 constexpr int kTileFloats = 256 * 256;
 
 struct GemmParams {
@@ -56,6 +65,7 @@ struct GemmParams {
   int full;      // the first `full` tiles are whole units, the others `splits` units each
   int splits;
   int units;
+  bool lasting;  // many k blocks per pair: the form with more stages
   float* partial;  // [(tile - full) * splits + split][256][256]
   int* err;
 };
@@ -102,13 +112,12 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 
-// The epilogue of one warp's 32 rows x 128 columns goes in 16 steps of eight rows
-// x 32 columns: in step i lane l takes the eight columns 32 (i / 4) + 8 (l % 4) ..
+// The epilogue of one warp's strip of 32 rows goes in steps of eight rows x 32
+// columns: in step i lane l takes the eight columns 32 (i / 4) + 8 (l % 4) ..
 // of row 8 (i % 4) + l / 4.  The residual is read four steps ahead, in registers
 // that move up by one in each.  The code of a step is there once: unrolled, with
 // every activation in it, it ran out of the instruction caches and took 630 cycles
 // a step without doing more than rounding and storing.
-constexpr int kSteps = 16;
 struct Strip {
   int64_t row0, col0;  // of the strip
   __device__ __forceinline__ int64_t row(int i, int lane) const { return row0 + (i & 3) * 8 + (lane >> 2); }
@@ -122,30 +131,30 @@ struct ReadAhead {
 #pragma unroll
     for (int i = 0; i < 4; ++i) residual[i] = read_residual8<T>(e, s.row(i, lane), s.col(i, lane));
   }
-  template <typename T>
+  template <typename T, int STEPS>
   __device__ __forceinline__ uint4 next_residual(const Epilogue& e, const Strip& s, int lane, int i) {
     const uint4 now = residual[0];
     if (!e.residual) return now;
     residual[0] = residual[1];
     residual[1] = residual[2];
     residual[2] = residual[3];
-    if (i + 4 < kSteps) residual[3] = read_residual8<T>(e, s.row(i + 4, lane), s.col(i + 4, lane));
+    if (i + 4 < STEPS) residual[3] = read_residual8<T>(e, s.row(i + 4, lane), s.col(i + 4, lane));
     return now;
   }
 };
 // Steps 4 b .. 4 b + 3: the block of 32 x 32 sums in `tile`.
-template <typename T, int ACT>
+template <typename T, int ACT, int STEPS>
 __device__ __forceinline__ void finish_block(const Epilogue& e, float* tile, int lane, const Strip& s, int b, ReadAhead& in) {
   const int g = lane & 3;
   const uint4 bias = in.bias;
-  if (b < 3) in.bias = read_bias8<T>(e, s.col(4 * b + 4, lane));
+  if (4 * b + 4 < STEPS) in.bias = read_bias8<T>(e, s.col(4 * b + 4, lane));
 #pragma unroll 1
   for (int i = 4 * b; i < 4 * b + 4; ++i) {
     const int r = (i & 3) * 8 + (lane >> 2);
     const int64_t row = s.row(i, lane), col = s.col(i, lane);
     float v[8];
     get_eight(tile, r, g, v);
-    const uint4 residual = in.next_residual<T>(e, s, lane, i);
+    const uint4 residual = in.next_residual<T, STEPS>(e, s, lane, i);
     const uint4 z = finish8<T>(e, ACT, row, col, bias, residual, v);
     if (e.vec) {
       if (row < e.rows && col < e.cols) {
@@ -184,16 +193,18 @@ __device__ __forceinline__ void save_block(float* partial, const float* tile, in
   }
 }
 
-template <typename T, bool A_ROWS, bool B_ROWS, int ACT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, bool A_ROWS, bool B_ROWS, int ACT, int WARPS>
+__global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ GemmParams p) {
+  using S = Shape<WARPS>;
+  constexpr int kStages = S::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_a = smem;
   uint8_t* s_b = s_a + kStages * kOperandBytes;
   uint8_t* s_epi = s_b + kStages * kOperandBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_epi + kEpiWarps * 4096);  // [kStages] used in the leader only
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_epi + WARPS * 4096);  // [kStages] used in the leader only
   uint64_t* empty = full + kStages;                                        // [kStages] in both CTAs
   uint64_t* acc_full = empty + kStages;                                    // [2] in both CTAs
   uint64_t* acc_empty = acc_full + 2;                                      // [2] used in the leader only
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&acc_full[i]), 1);
-      mbar_init(smem_u32(&acc_empty[i]), 2 * kEpiWarps);  // one lane per epilogue warp, both CTAs
+      mbar_init(smem_u32(&acc_empty[i]), 2 * WARPS);  // one lane per epilogue warp, both CTAs
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    const int quad = warp & 3, half = (warp - 2) >> 2;  // the lanes this warp may read; its 128 columns
+    const int quad = warp & 3, part = (warp - 2) >> 2;  // the lanes this warp may read; its share of the columns
     float* tile = reinterpret_cast<float*>(s_epi + (warp - 2) * 4096);
     bool ok = true;
     int n = 0;
@@ -324,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit U = decode_unit(u, p);
       const int slot = n & 1;
       const int local_row = static_cast<int>(rank) * 128 + quad * 32;
-      const Strip strip{static_cast<int64_t>(U.tm) * 256 + local_row, static_cast<int64_t>(U.tn) * 256 + half * 128};
+      const Strip strip{static_cast<int64_t>(U.tm) * 256 + local_row, static_cast<int64_t>(U.tn) * 256 + part * S::COLS};
       ReadAhead ahead{};
       if (U.slot < 0) ahead.start<T>(p.ep, strip, lane);
       const bool got = mbar_wait_bounded(smem_u32(&acc_full[slot]), (n >> 1) & 1, abort_flag, kWaitLimitNs);
@@ -334,12 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
 #pragma unroll 1
-      for (int cb = 0; cb < 4; ++cb) {
+      for (int cb = 0; cb < S::COLS / 32; ++cb) {
         uint32_t v[32];
-        const int local_col = half * 128 + cb * 32;
+        const int local_col = part * S::COLS + cb * 32;
         tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + slot * 256 + local_col, v);
         tmem_wait_ld();
-        if (cb == 3) {
+        if (cb == S::COLS / 32 - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[slot]), 0));
@@ -347,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         put_block(tile, lane, v);
         __syncwarp();
         if (U.slot < 0)
-          finish_block<T, ACT>(p.ep, tile, lane, strip, cb, ahead);
+          finish_block<T, ACT, S::STEPS>(p.ep, tile, lane, strip, cb, ahead);
         else
           save_block(p.partial + static_cast<int64_t>(U.slot) * kTileFloats, tile, lane, local_row, local_col);
         __syncwarp();
@@ -451,16 +462,24 @@ GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms, double* us) {
   // 8 us: what a launch of one tile with one block takes, launch and epilogue included
   *us = 8.0 + 0.27 * plan_units(p.tiles_m * p.tiles_n, p.nkb, num_sms / 2, &p.full, &p.splits);
   p.units = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
+  p.lasting = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.nkb >= 256 * (num_sms / 2);
   return p;
 }
 
+template <typename T, bool A_ROWS, bool B_ROWS, int ACT, int WARPS>
+cudaError_t launch_shape(const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p, const DeviceResources& res,
+                         cudaStream_t st) {
+  using S = Shape<WARPS>;
+  const cudaError_t e = allow_smem<linear_gemm_kernel<T, A_ROWS, B_ROWS, ACT, WARPS>>(S::SMEM, res.device);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(linear_gemm_kernel<T, A_ROWS, B_ROWS, ACT, WARPS>, 2 * std::min(p.units, res.num_sms / 2), S::THREADS,
+                       S::SMEM, 2, st, ma, mb, p);
+}
 template <typename T, bool A_ROWS, bool B_ROWS, int ACT>
 cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p, const DeviceResources& res,
                            cudaStream_t st) {
-  const cudaError_t e = allow_smem<linear_gemm_kernel<T, A_ROWS, B_ROWS, ACT>>(kSmem, res.device);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(linear_gemm_kernel<T, A_ROWS, B_ROWS, ACT>, 2 * std::min(p.units, res.num_sms / 2), kThreads, kSmem, 2, st,
-                       ma, mb, p);
+  return p.lasting ? launch_shape<T, A_ROWS, B_ROWS, ACT, 8>(ma, mb, p, res, st)
+                   : launch_shape<T, A_ROWS, B_ROWS, ACT, 16>(ma, mb, p, res, st);
 }
 
 template <typename T>
