@@ -459,8 +459,8 @@ GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms, double* us) {
   // 32 MB of A per group: each of the two dies keeps its own copy in its half of the 129 MB L2.  At k = 4096 with
   // 16384 columns groups of 4, 8, 16 and 32 row tiles took 604, 572, 562 and 583 us.
   p.group = static_cast<int>(std::clamp<int64_t>((32 << 20) / (256 * 2 * std::max<int64_t>(k, 1)), 4, 16));
-  // 8 us: what a launch of one tile with one block takes, launch and epilogue included
-  *us = 8.0 + 0.27 * plan_units(p.tiles_m * p.tiles_n, p.nkb, num_sms / 2, &p.full, &p.splits);
+  // 9 us: what a launch takes beside its blocks, the exposed epilogue included
+  *us = 9.0 + 0.27 * plan_units(p.tiles_m * p.tiles_n, p.nkb, num_sms / 2, &p.full, &p.splits);
   p.units = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
   p.lasting = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.nkb >= 256 * (num_sms / 2);
   return p;

@@ -214,11 +214,12 @@ __global__ void __launch_bounds__(Few<MP>::THREADS, 1)
     const uint32_t at = smem_u32(sums + item * 8);
     float v[8] = {};
 #pragma unroll 1
-    for (int s0 = 0; s0 < ranks; s0 += 4) {  // four ranks' sums in flight (past the last one: the last one's, not added)
+    for (int s0 = 0; s0 < ranks; s0 += 4) {  // four ranks' sums in flight
       float add[4][8];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const uint32_t from = map_to_rank(at, min(s0 + s, ranks - 1));
+        if (s0 + s >= ranks) break;
+        const uint32_t from = map_to_rank(at, s0 + s);
         load_cluster4(from, add[s]);
         load_cluster4(from + 16, add[s] + 4);
       }
@@ -300,19 +301,22 @@ cudaError_t launch_few_typed(const FewPlan& plan, const Operand& x, const Operan
 
 }  // namespace
 
+// Times measured on the device for one wave of CTAs (launch, pipeline and
+// epilogue; a k block; joining 2, 4 or 8 ranks), from 1 x 512 x 512 to
+// 8192 x 512 x 512.  Clusters stay within a group of SMs, so fewer CTAs of large
+// ones run at once.
 FewPlan plan_few(bool x_rows, int64_t rows, int64_t cols, int nkb, int num_sms) {
-  FewPlan p{};
-  p.mp = x_rows ? (rows <= 64 ? 64 : 128) : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  const int64_t tiles = ceil_div(rows, p.mp) * ceil_div(cols, kTileN);
-  // CTAs per cluster: as many as the device has room for beside the tiles, each with two k blocks at least
-  p.ranks = 1;
-  while (p.ranks < 8 && tiles * p.ranks * 2 <= num_sms && nkb >= p.ranks * 4) p.ranks *= 2;
-  // a k block takes its operands' way from L2 (88 bytes per SM and cycle measured); the ends of a CTA 2.5 us and its
-  // outputs' share
-  const double block_us = (kWBytes + p.mp * kBK * 2) / 88.0 / 1900.0;
-  const double waves = static_cast<double>(ceil_div(tiles * p.ranks, num_sms));
-  p.us = 2.0 + waves * (2.5 + p.mp / 64.0 + ceil_div(nkb, p.ranks) * block_us);
-  return p;
+  const int mp = x_rows ? (rows <= 64 ? 64 : 128) : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int64_t tiles = ceil_div(rows, mp) * ceil_div(cols, kTileN);
+  const double share = mp / 128.0, base_us = mp == 128 ? 6.2 : 3.2 + 2.2 * share, block_us = 0.155 + 0.025 * share;
+  FewPlan best{mp, 1, 0.0};
+  for (int ranks = 1; ranks <= 8 && (ranks == 1 || nkb >= 2 * ranks); ranks *= 2) {
+    const int64_t room = ranks == 8 ? num_sms * 15 / 19 : ranks == 4 ? num_sms * 18 / 19 : num_sms;
+    const double join_us = ranks == 8 ? 2.0 + 2.0 * share : ranks == 4 ? 1.0 + share : ranks == 2 ? 0.5 : 0.0;
+    const double us = ceil_div(tiles * ranks, room) * (base_us + ceil_div(nkb, ranks) * block_us) + join_us;
+    if (ranks == 1 || us < best.us) best = FewPlan{mp, ranks, us};
+  }
+  return best;
 }
 
 cudaError_t launch_linear_few(const FewPlan& plan, const Operand& a, const Operand& b, int64_t k, const Epilogue& ep,
