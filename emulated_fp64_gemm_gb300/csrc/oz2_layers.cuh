@@ -132,8 +132,14 @@ struct DzArgs {
 };
 cudaError_t launch_dz(const DzArgs& a, oz2_dtype dtype, cudaStream_t st);
 
-// out[c] = the sum of partial[r][c] over the rows, in a fixed order.
-cudaError_t launch_column_sums(const float* partial, int64_t rows, int64_t cols, oz2_dtype dtype, void* out, cudaStream_t st);
+// out[c] = the sum of partial[r][c] over the rows, in a fixed order; of one
+// matrix or of two (null out: none).
+struct ColumnSums {
+  const float* partial;
+  int64_t rows;
+  void* out;
+};
+cudaError_t launch_column_sums(const ColumnSums& a, const ColumnSums& b, int64_t cols, oz2_dtype dtype, cudaStream_t st);
 
 cudaError_t launch_qk(const oz2_qk_args& a, const DeviceResources& res, cudaStream_t st);
 // Rows of dim floats that the backward pass needs in `partial` (null: the
@@ -460,7 +466,7 @@ namespace oz2 {
 
 // One launch; clusters of `cluster` CTAs.
 template <typename... P, typename... A>
-cudaError_t launch_kernel(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cluster, cudaStream_t st, A&&... args) {
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, A&&... args) {
   cudaLaunchAttribute attr[2]{};
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -468,7 +474,7 @@ cudaError_t launch_kernel(void (*kernel)(P...), int64_t grid, int threads, size_
   attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -476,6 +482,11 @@ cudaError_t launch_kernel(void (*kernel)(P...), int64_t grid, int threads, size_
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   count_launches(1);
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cluster, cudaStream_t st, A&&... args) {
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), threads, smem, cluster, st, std::forward<A>(args)...);
 }
 
 // Lets a kernel use `bytes` of shared memory, once per device (the attribute is the device's).

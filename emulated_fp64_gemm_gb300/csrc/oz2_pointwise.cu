@@ -228,34 +228,31 @@ cudaError_t dz_impl(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
                                              dz_kernel<T, OZ2_ACT_GELU>, dz_kernel<T, OZ2_ACT_GELU_TANH>};
   const cudaError_t e = launch_kernel(kernels[a.act], blocks, 256, 0, 1, st, a, aligned, dz_rows(a.m, a.n));
   if (e != cudaSuccess || !a.dbias || !a.partial) return e;
-  return launch_column_sums(a.partial, rows, a.n, dtype, a.dbias, st);
+  return launch_column_sums(ColumnSums{a.partial, rows, a.dbias}, ColumnSums{}, a.n, dtype, st);
 }
 
 // ------------------------------------------------------------------ column sums
-// A block of 8 warps per 32 columns: warp w adds the rows w, w + 8, ..., then the warps' sums are added.
+// A block of 8 warps per 32 columns: warp w adds the rows w, w + 8, ..., then the
+// warps' sums are added.  blockIdx.y: which of two matrices.
 template <typename T>
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* partial, int64_t rows, int64_t cols, T* out) {
+__global__ void __launch_bounds__(256) column_sums_kernel(const ColumnSums a, const ColumnSums b, int64_t cols) {
   __shared__ float sums[8][32];
   wait_for_predecessor();
   let_successor_come();
+  const ColumnSums& m = blockIdx.y == 0 ? a : b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int64_t r = warp; r < rows; r += 8) s += partial[r * cols + c];
+    for (int64_t r = warp; r < m.rows; r += 8) s += m.partial[r * cols + c];
   }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp || c >= cols) return;
+  if (warp || c >= cols || !m.out) return;
 #pragma unroll
   for (int w = 1; w < 8; ++w) s += sums[w][lane];
-  out[c] = Elem<T>::down(s);
-}
-
-template <typename T>
-cudaError_t column_sums_impl(const float* partial, int64_t rows, int64_t cols, void* out, cudaStream_t st) {
-  return launch_kernel(column_sums_kernel<T>, ceil_div(cols, 32), 256, 0, 1, st, partial, rows, cols, static_cast<T*>(out));
+  static_cast<T*>(m.out)[c] = Elem<T>::down(s);
 }
 
 }  // namespace
@@ -298,12 +295,11 @@ cudaError_t launch_dz(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
   return dtype == OZ2_BF16 ? dz_impl<__nv_bfloat16>(a, dtype, st) : dz_impl<__half>(a, dtype, st);
 }
 
-cudaError_t launch_column_sums(const float* partial, int64_t rows, int64_t cols, oz2_dtype dtype, void* out, cudaStream_t st) {
-  switch (dtype) {
-    case OZ2_BF16: return column_sums_impl<__nv_bfloat16>(partial, rows, cols, out, st);
-    case OZ2_F16: return column_sums_impl<__half>(partial, rows, cols, out, st);
-    default: return column_sums_impl<float>(partial, rows, cols, out, st);
-  }
+cudaError_t launch_column_sums(const ColumnSums& a, const ColumnSums& b, int64_t cols, oz2_dtype dtype, cudaStream_t st) {
+  auto kernel = dtype == OZ2_BF16  ? column_sums_kernel<__nv_bfloat16>
+                : dtype == OZ2_F16 ? column_sums_kernel<__half>
+                                   : column_sums_kernel<float>;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(ceil_div(cols, 32)), b.out ? 2 : 1), 256, 0, 1, st, a, b, cols);
 }
 
 }  // namespace oz2

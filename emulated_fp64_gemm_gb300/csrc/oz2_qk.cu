@@ -658,10 +658,9 @@ cudaError_t qk_backward_impl(const oz2_qk_args& a, int num_sms, float* partial, 
                       ? launch_kernel(backward_kernel<T>(lanes_for(a.dim), a.interleaved), b.q + b.k, kBlock, 0, 1, st, p, q_blocks)
                       : launch_kernel(a.interleaved ? qk_plain_backward_kernel<T, true> : qk_plain_backward_kernel<T, false>,
                                       b.q + b.k, kBlock, 0, 1, st, p, q_blocks);
-  const oz2_dtype t = static_cast<oz2_dtype>(a.dtype);
-  if (a.dq_weight && e == cudaSuccess) e = launch_column_sums(partial, b.q, a.dim, t, a.dq_weight, st);
-  if (a.dk_weight && e == cudaSuccess) e = launch_column_sums(partial + b.q * a.dim, b.k, a.dim, t, a.dk_weight, st);
-  return e;
+  if (e != cudaSuccess || !partial) return e;
+  return launch_column_sums(ColumnSums{partial, b.q, a.dq_weight}, ColumnSums{partial + b.q * a.dim, b.k, a.dk_weight}, a.dim,
+                            static_cast<oz2_dtype>(a.dtype), st);
 }
 
 }  // namespace

@@ -41,7 +41,6 @@ _LINEAR_BACKWARD_ARGS = struct.Struct("@qqqPqPqPqPqPqPqPQQdii")
 _DROPOUT_ARGS = struct.Struct("@qqPqPqPqQQdii")
 _HEADS = "Pqqq"
 _QK_ARGS = struct.Struct("@qqqqPPP" + 4 * _HEADS + "PP" + 2 * _HEADS + "PPdii")
-_NO_HEADS = (0, 0, 0, 0)
 
 _lib = None
 # the current stream's handle without the Stream object around it (0.1 instead of 3 us)
@@ -177,9 +176,14 @@ def linear(x, w, bias=None, *, activation="none", residual=None, dropout=0.0, se
     if residual is not None:
         residual, ldr = _rows(residual)
         r = residual.data_ptr()
-    y, ldy = (torch.empty((m, n), dtype=dtype, device=x.device), n) if out is None else (out, _ld(out))
+    if out is not None:
+        y, ldy = out, _ld(out)
+    else:
+        # like the residual where there is one: 0.7 us less on the Grace host
+        y = torch.empty_like(residual) if residual is not None and ldr == n else torch.empty((m, n), dtype=dtype, device=x.device)
+        ldy = n
     if save_preact:
-        preact = torch.empty((m, n), dtype=dtype, device=x.device)
+        preact = torch.empty((m, n), dtype=dtype, device=x.device) if out is not None else torch.empty_like(y)
         z = preact.data_ptr()
     code = _library().ozaki2_linear(
         _LINEAR_ARGS.pack(m, k, n, x.data_ptr(), ldx, w.data_ptr(), ldw, b, r, ldr, y.data_ptr(), ldy, z, n, seed & _MASK64,
@@ -258,7 +262,7 @@ def dropout(x, p, *, seed, offset=0, residual=None, out=None, stream=None):
     if residual is not None:
         residual, ldr = _rows(residual)
         r = residual.data_ptr()
-    y, ldy = (torch.empty(shape, dtype=dtype, device=x.device), cols) if out is None else (out, _ld(out))
+    y, ldy = (out, _ld(out)) if out is not None else (torch.empty_like(x) if ldx == cols else torch.empty(shape, dtype=dtype, device=x.device), cols)
     code = _library().ozaki2_dropout(
         _DROPOUT_ARGS.pack(rows, cols, x.data_ptr(), ldx, r, ldr, y.data_ptr(), ldy, seed & _MASK64, offset & _MASK64,
                            _probability(p), _FLOATS[dtype], 0), _stream_of(device))
@@ -274,7 +278,7 @@ def dropout_backward(dy, p, *, seed, offset=0, out=None, stream=None):
 
 def _neighbours(t):
     """t, or a copy where the features of a head are not neighbours in memory."""
-    return t if t.shape[2] <= 1 or t.stride(2) == 1 else t.contiguous()
+    return t if t.stride(2) == 1 or t.shape[2] <= 1 else t.contiguous()
 
 
 def _heads(t):
@@ -301,10 +305,11 @@ def _check_qk(q, k, q_weight, k_weight, cos, sin, positions, out):
     _check("k", k, dtype, device, (tokens, k.shape[1], dim))
     _check("q_weight", q_weight, dtype, device, (dim,))
     _check("k_weight", k_weight, dtype, device, (dim,))
-    if cos.dim() != 2 or 2 * cos.shape[1] > dim:
-        raise ValueError(f"cos must have shape (positions, rotated features / 2) with at most {dim} rotated, got {tuple(cos.shape)}")
-    _check("cos", cos, torch.float32, device, cos.shape)
-    _check("sin", sin, torch.float32, device, cos.shape)
+    table = cos.shape
+    if len(table) != 2 or 2 * table[1] > dim:
+        raise ValueError(f"cos must have shape (positions, rotated features / 2) with at most {dim} rotated, got {tuple(table)}")
+    _check("cos", cos, torch.float32, device, table)
+    _check("sin", sin, torch.float32, device, table)
     _check("positions", positions, torch.int64, device, (tokens,))
     if out is not None:
         _check_heads_out("out[0]", out[0], q)
@@ -312,12 +317,8 @@ def _check_qk(q, k, q_weight, k_weight, cos, sin, positions, out):
     return device
 
 
-def _qk_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out, k_out, dq_out, dk_out, dq_weight, dk_weight):
-    rows, half = cos.shape
-    return _QK_ARGS.pack(
-        q.shape[0], q.shape[2], 2 * half, rows, cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), *_heads(q), *_heads(k),
-        *_heads(q_out), *_heads(k_out), q_weight.data_ptr(), k_weight.data_ptr(), *dq_out, *dk_out, dq_weight, dk_weight, eps,
-        _FLOATS[q.dtype], bool(interleaved))
+def _contiguous(t):
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, interleaved=False, out=None, stream=None):
@@ -336,17 +337,24 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, int
         return _elsewhere(qk_norm_rope, device, stream, tensors, q, k, q_weight, k_weight, cos, sin, positions, eps=eps,
                           interleaved=interleaved, out=out)
 
+    tokens, nq, dim = q.shape
+    rows, half = cos.shape
+    dtype = q.dtype
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype, device=q.device))
-    q, k = _neighbours(q), _neighbours(k)
-    q_weight, k_weight, cos, sin, positions = (t if t.is_contiguous() else t.contiguous()
-                                               for t in (q_weight, k_weight, cos, sin, positions))
+        nk, where = k.shape[1], q.device
+        q_out = torch.empty((tokens, nq, dim), dtype=dtype, device=where)
+        k_out = torch.empty((tokens, nk, dim), dtype=dtype, device=where)
+    else:
+        q_out, k_out = out
+    q, k, cos, sin, positions = _neighbours(q), _neighbours(k), _contiguous(cos), _contiguous(sin), _contiguous(positions)
+    q_weight, k_weight = _contiguous(q_weight), _contiguous(k_weight)
     code = _library().ozaki2_qk_norm_rope(
-        _qk_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, *out, _NO_HEADS, _NO_HEADS, 0, 0),
-        _stream_of(device))
+        _QK_ARGS.pack(tokens, dim, 2 * half, rows, cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), *_heads(q), *_heads(k),
+                      *_heads(q_out), *_heads(k_out), q_weight.data_ptr(), k_weight.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, eps,
+                      _FLOATS[dtype], bool(interleaved)), _stream_of(device))
     if code:
         _fail(code, "ozaki2_qk_norm_rope")
-    return tuple(out)
+    return q_out, k_out
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, interleaved=False,
@@ -363,15 +371,23 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
         return _elsewhere(qk_norm_rope_backward, device, stream, tensors, dq_out, dk_out, q, k, q_weight, k_weight, cos, sin,
                           positions, eps=eps, interleaved=interleaved, out=out)
 
+    tokens, nq, dim = q.shape
+    rows, half = cos.shape
+    dtype, where = q.dtype, q.device
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype, device=q.device))
-    dwq, dwk = torch.empty(q_weight.shape, dtype=q.dtype, device=q.device), torch.empty(k_weight.shape, dtype=q.dtype, device=q.device)
+        dq = torch.empty((tokens, nq, dim), dtype=dtype, device=where)
+        dk = torch.empty((tokens, k.shape[1], dim), dtype=dtype, device=where)
+    else:
+        dq, dk = out
+    dwq = torch.empty((dim,), dtype=dtype, device=where)
+    dwk = torch.empty((dim,), dtype=dtype, device=where)
     q, k, dq_out, dk_out = _neighbours(q), _neighbours(k), _neighbours(dq_out), _neighbours(dk_out)
-    q_weight, k_weight, cos, sin, positions = (t if t.is_contiguous() else t.contiguous()
-                                               for t in (q_weight, k_weight, cos, sin, positions))
+    q_weight, k_weight, cos, sin, positions = (_contiguous(q_weight), _contiguous(k_weight), _contiguous(cos), _contiguous(sin),
+                                               _contiguous(positions))
     code = _library().ozaki2_qk_norm_rope_backward(
-        _qk_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, *out, _heads(dq_out), _heads(dk_out),
-                 dwq.data_ptr(), dwk.data_ptr()), _stream_of(device))
+        _QK_ARGS.pack(tokens, dim, 2 * half, rows, cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), *_heads(q), *_heads(k),
+                      *_heads(dq), *_heads(dk), q_weight.data_ptr(), k_weight.data_ptr(), *_heads(dq_out), *_heads(dk_out),
+                      dwq.data_ptr(), dwk.data_ptr(), eps, _FLOATS[dtype], bool(interleaved)), _stream_of(device))
     if code:
         _fail(code, "ozaki2_qk_norm_rope_backward")
-    return (*out, dwq, dwk)
+    return dq, dk, dwq, dwk
