@@ -99,6 +99,17 @@ def test_linear_long(oz2, m, k, n):
     check_backward(oz2, normal(m, n, dtype=BF16, seed=3), x, w)
 
 
+@pytest.mark.parametrize("n", [2560, 2555])
+def test_linear_split_tails(oz2, n):
+    # 100 tiles of 256 x 256: the last ones are split along k and joined
+    m, k = 2560, 4096
+    x, w, b = normal(m, k, dtype=F16), normal(n, k, dtype=F16, seed=1, scale=k**-0.5), normal(n, dtype=F16, seed=2)
+    r = normal(m, n, dtype=F16, seed=3)
+    y = check_linear(oz2, x, w, b, "gelu", r, 0.1, save=True)
+    assert torch.equal(y, oz2.linear(x, w, b, activation="gelu", residual=r, dropout=0.1, seed=SEED, offset=OFFSET))
+    check_backward(oz2, normal(m, n, dtype=F16, seed=4), x, w)
+
+
 @pytest.mark.parametrize("activation", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("m,n", [(4, 264), (300, 519)])
 def test_linear_activations_and_options(oz2, activation, m, n):
@@ -127,9 +138,10 @@ def test_linear_strides(oz2, m, k, n, pad, shift):
     check_linear(oz2, x.t().contiguous().t(), w.t().contiguous().t(), b, residual=r[:1].expand(m, n))
 
 
-def test_linear_in_place_on_the_residual(oz2):
-    for m in (5, 600):
-        x, w, r = normal(m, 96, dtype=BF16), normal(264, 96, dtype=BF16, seed=1), normal(m, 264, dtype=BF16, seed=2)
+@pytest.mark.parametrize("n", [264, 1027])
+def test_linear_in_place_on_the_residual(oz2, n):
+    for m in (5, 600, 5000):
+        x, w, r = normal(m, 96, dtype=BF16), normal(n, 96, dtype=BF16, seed=1), normal(m, n, dtype=BF16, seed=2)
         want = oz2.linear(x, w, residual=r)
         assert torch.equal(oz2.linear(x, w, residual=r, out=r), want)
 
@@ -475,6 +487,65 @@ def test_qk_backward_against_differences(oz2):
         diff = (loss(*up) - loss(*down)) / 2e-5
         # 32-bit gradients and a central difference with h = 1e-5: relative 1e-5 of the sum of magnitudes
         assert abs(float((g.double() * d).sum()) - diff) <= 1e-5 * float((g.double().abs() * d.abs()).sum())
+
+
+@pytest.mark.parametrize("t,hq,hkv,d,rot", [(700, 8, 8, 128, 128), (5000, 3, 1, 64, 64)])
+def test_qk_equal_positions_and_long_runs(oz2, t, hq, hkv, d, rot):
+    # all tokens at one position, more steps per warp than are in flight; against each token by itself
+    q, k, wq, wk, cos, sin, _ = qk_inputs(t, hq, hkv, d, rot, BF16)
+    pos = torch.full((t,), 77, device="cuda")
+    got = oz2.qk_norm_rope(q, k, wq, wk, cos, sin, pos)
+    for i in (0, 1, t // 2, t - 1):
+        one = oz2.qk_norm_rope(q[i:i + 1], k[i:i + 1], wq, wk, cos, sin, pos[:1])
+        assert torch.equal(got[0][i], one[0][0]) and torch.equal(got[1][i], one[1][0])
+
+
+# ------------------------------------------------------------------ together
+def test_block_example(oz2):
+    """The example's block: its gradients against 64-bit autograd of the same block, its training and its single tokens."""
+    import importlib.util
+    import os
+
+    from tests._util import ROOT
+
+    spec = importlib.util.spec_from_file_location("transformer_block", os.path.join(ROOT, "examples", "transformer_block.py"))
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    block = ex.Block(dim=256, heads=4, kv_heads=2, hidden=768)
+    t, p = 64, 0.1
+    x = normal(t, 256, dtype=BF16)
+    pos = torch.arange(t, device="cuda")
+    dy = normal(t, 256, dtype=BF16, seed=1)
+    y = block(x, pos, p, seed=SEED, step=3)
+    grads = torch.autograd.grad(y, list(block.w.values()), dy)
+
+    w = {n: v.detach().double().requires_grad_(True) for n, v in block.w.items()}
+    h, kv, d = block.heads, block.kv_heads, block.head_dim
+
+    def drop(v, i):
+        keep, scale = keep_mask(*v.shape, p, SEED, 4 * 3 + i)
+        return torch.where(keep.cuda(), v * scale, 0.0)
+
+    x0 = drop(x.double(), 0)
+    qkv = (x0 @ w["qkv"].t() + w["qkv_b"]).view(t, h + 2 * kv, d)
+    q = norm_rope(qkv[:, :h], w["wq"], block.cos[pos], block.sin[pos], 1e-6, False)
+    k = norm_rope(qkv[:, h:h + kv], w["wk"], block.cos[pos], block.sin[pos], 1e-6, False).repeat_interleave(h // kv, 1)
+    v = qkv[:, h + kv:].repeat_interleave(h // kv, 1)
+    s = torch.einsum("thd,shd->hts", q, k) * d**-0.5 + torch.full((t, t), float("-inf"), device="cuda").triu(1)
+    o = torch.einsum("hts,shd->thd", s.softmax(-1), v).flatten(1)
+    x1 = x0 + drop(o @ w["out"].t() + w["out_b"], 1)
+    want = x1 + drop(act(x1 @ w["up"].t() + w["up_b"], "gelu_tanh") @ w["down"].t() + w["down_b"], 2)
+    exact = torch.autograd.grad(want, list(w.values()), dy.double())
+    # a chain of about ten bfloat16 roundings of 2^-9 each: 2 % of the norm is four times their sum
+    for name, got, ref in (("y", y, want), *zip(w, grads, exact)):
+        got, ref = got.detach().double(), ref.detach()
+        assert float((got - ref).norm()) <= 0.02 * float(ref.norm()), name
+    losses = ex.train(block, tokens=64, steps=6)
+    assert losses[-1] < losses[0]
+    with torch.no_grad():
+        whole = block(x, pos)
+    single = ex.decode(block, x)
+    assert float((whole.double() - single.double()).norm()) <= 0.02 * float(whole.double().norm())
 
 
 # ------------------------------------------------------------------ refusals
