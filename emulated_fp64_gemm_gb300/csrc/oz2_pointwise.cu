@@ -150,7 +150,7 @@ cudaError_t launch_parts(const PackPart& a, const PackPart& b, cudaStream_t st) 
 // which column_sums_kernel adds up in order, so the result does not depend on
 // timing (with one strip of rows they go to dbias at once).  Bound by HBM: dy and z read, dz written once.
 template <typename T, int ACT>
-__global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzArgs a, bool aligned, int rows) {
+__global__ void __launch_bounds__(256, 4) dz_kernel(const __grid_constant__ DzArgs a, bool aligned, int rows) {
   __shared__ float sums[8][256];
   wait_for_predecessor();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -215,9 +215,10 @@ __global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzAr
   }
 }
 
-// Rows per block: all of a short matrix, whose sums are then complete; else
-// enough blocks to fill the device, then fewer partial rows.
-int dz_rows(int64_t m, int64_t n) { return m <= 128 ? 128 : ceil_div(n, 256) * ceil_div(m, 64) >= 608 ? 64 : 16; }
+// Rows per block: all of a short matrix, whose sums are then complete; 128 where
+// that fills the device (8192 x 16384 with gelu_tanh, sums only: 32, 64, 128 and
+// 256 rows took 128, 115, 93 and 95 us), else 16.
+int dz_rows(int64_t m, int64_t n) { return m <= 128 || ceil_div(n, 256) * ceil_div(m, 128) >= 608 ? 128 : 16; }
 
 template <typename T>
 cudaError_t dz_impl(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
