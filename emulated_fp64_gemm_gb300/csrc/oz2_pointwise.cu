@@ -132,11 +132,21 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackP
   p.groups.place(i, row, g);
   const int64_t col = static_cast<int64_t>(g) * 8;
   const uint16_t* x = p.x + row * p.ldx + col;
-  uint32_t v[8];
+  uint4 u;
+  if (col + 8 > p.groups.cols) {
+    uint32_t v[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = col + e < p.groups.cols ? x[e] : 0u;
-  *reinterpret_cast<uint4*>(p.out + row * p.ld_out + col) =
-      make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    for (int e = 0; e < 8; ++e) v[e] = col + e < p.groups.cols ? x[e] : 0u;
+    u = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  } else if (reinterpret_cast<uintptr_t>(x) % 4 == 0) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x + 1);
+    const uint32_t first = x[0], last = x[7];
+    u = make_uint4(first | w[0] << 16, w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | last << 16);
+  }
+  *reinterpret_cast<uint4*>(p.out + row * p.ld_out + col) = u;
 }
 cudaError_t launch_parts(const PackPart& a, const PackPart& b, cudaStream_t st) {
   const int64_t a_blocks = ceil_div(a.groups.count, 256), blocks = a_blocks + ceil_div(b.groups.count, 256);
@@ -233,11 +243,11 @@ cudaError_t dz_impl(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ column sums
-// A block of 8 warps per 32 columns: warp w adds the rows w, w + 8, ..., then the
+// A block of 32 warps per 32 columns: warp w adds the rows w, w + 32, ..., then the
 // warps' sums are added.  blockIdx.y: which of two matrices.
 template <typename T>
-__global__ void __launch_bounds__(256) column_sums_kernel(const ColumnSums a, const ColumnSums b, int64_t cols) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(1024) column_sums_kernel(const ColumnSums a, const ColumnSums b, int64_t cols) {
+  __shared__ float sums[32][32];
   wait_for_predecessor();
   let_successor_come();
   const ColumnSums& m = blockIdx.y == 0 ? a : b;
@@ -246,13 +256,13 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const ColumnSums a, co
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int64_t r = warp; r < m.rows; r += 8) s += m.partial[r * cols + c];
+    for (int64_t r = warp; r < m.rows; r += 32) s += m.partial[r * cols + c];
   }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp || c >= cols || !m.out) return;
 #pragma unroll
-  for (int w = 1; w < 8; ++w) s += sums[w][lane];
+  for (int w = 1; w < 32; ++w) s += sums[w][lane];
   static_cast<T*>(m.out)[c] = Elem<T>::down(s);
 }
 
@@ -300,7 +310,7 @@ cudaError_t launch_column_sums(const ColumnSums& a, const ColumnSums& b, int64_t
   auto kernel = dtype == OZ2_BF16  ? column_sums_kernel<__nv_bfloat16>
                 : dtype == OZ2_F16 ? column_sums_kernel<__half>
                                    : column_sums_kernel<float>;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(ceil_div(cols, 32)), b.out ? 2 : 1), 256, 0, 1, st, a, b, cols);
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(ceil_div(cols, 32)), b.out ? 2 : 1), 1024, 0, 1, st, a, b, cols);
 }
 
 }  // namespace oz2

@@ -99,6 +99,22 @@ def test_linear_long(oz2, m, k, n):
     check_backward(oz2, normal(m, n, dtype=BF16, seed=3), x, w)
 
 
+def test_linear_offsets_past_32_bits(oz2):
+    # 2^31 elements of y and of the backward pass's dz, and more: rows at the far end against the same rows by themselves
+    m, k, n = 70000, 64, 32768
+    x, w, b = normal(m, k, dtype=BF16), normal(n, k, dtype=BF16, seed=1, scale=k**-0.5), normal(n, dtype=BF16, seed=2)
+    y, z = oz2.linear(x, w, b, activation="silu", save_preact=True)
+    for rows in (slice(0, 200), slice(65500, 65700), slice(m - 200, m)):
+        want, want_z = oz2.linear(x[rows], w, b, activation="silu", save_preact=True)
+        assert torch.equal(y[rows], want) and torch.equal(z[rows], want_z)
+    dx, _, _ = oz2.linear_backward(y, x, w, preact=z, activation="silu", need_dw=False, need_dbias=False)
+    rows = slice(m - 300, m)
+    want, _, _ = oz2.linear_backward(y[rows], x[rows], w, preact=z[rows], activation="silu", need_dw=False, need_dbias=False)
+    # the two calls may split their sums of 32768 terms differently: both are within the bound of the exact sums
+    mag = y[rows].double().abs() @ w.double().abs() * 1.1
+    assert_within(dx[rows], want.double(), 2 * (UNIT[BF16] * want.double().abs() + n * ACC * mag) + TINY[BF16], "dx")
+
+
 @pytest.mark.parametrize("n", [2560, 2555])
 def test_linear_split_tails(oz2, n):
     # 100 tiles of 256 x 256: the last ones are split along k and joined
