@@ -111,12 +111,13 @@ def _ld(t):
     return s0 if s0 >= cols else 0
 
 
-def _rows(t):
-    """(a row-major tensor of the same values, its leading dimension)."""
+def _rows(t, cols):
+    """(a row-major tensor of the same values, its leading dimension); cols: t's."""
+    if t.is_contiguous():
+        return t, cols
     ld = _ld(t)
-    if ld == 0 and t.shape[1] > 0:
-        t = t.contiguous()
-        ld = t.shape[1]
+    if ld == 0 and cols > 0:
+        return t.contiguous(), cols
     return t, ld
 
 
@@ -166,21 +167,21 @@ def linear(x, w, bias=None, *, activation="none", residual=None, dropout=0.0, se
         return _elsewhere(linear, device, stream, (x, w, bias, residual, out), x, w, bias, activation=activation,
                           residual=residual, dropout=dropout, seed=seed, offset=offset, save_preact=save_preact, out=out)
 
-    x, ldx = _rows(x)
-    w, ldw = _rows(w)
+    x, ldx = _rows(x, k)
+    w, ldw = _rows(w, k)
     b = r = z = ldr = 0
     if bias is not None:
         if n > 1 and bias.stride(0) != 1:
             bias = bias.contiguous()
         b = bias.data_ptr()
     if residual is not None:
-        residual, ldr = _rows(residual)
+        residual, ldr = _rows(residual, n)
         r = residual.data_ptr()
     if out is not None:
         y, ldy = out, _ld(out)
     else:
         # like the residual where there is one: 0.7 us less on the Grace host
-        y = torch.empty_like(residual) if residual is not None and ldr == n else torch.empty((m, n), dtype=dtype, device=x.device)
+        y = torch.empty_like(residual) if r and residual.is_contiguous() else torch.empty((m, n), dtype=dtype, device=x.device)
         ldy = n
     if save_preact:
         preact = torch.empty((m, n), dtype=dtype, device=x.device) if out is not None else torch.empty_like(y)
@@ -220,16 +221,21 @@ def linear_backward(dy, x, w, *, preact=None, activation="none", dropout=0.0, se
         return _elsewhere(linear_backward, device, stream, (dy, x, w, preact), dy, x, w, preact=preact, activation=activation,
                           dropout=dropout, seed=seed, offset=offset, need_dx=need_dx, need_dw=need_dw, need_dbias=need_dbias)
 
-    dy, ldy = _rows(dy)
-    x, ldx = _rows(x)
-    w, ldw = _rows(w)
+    # outputs like the inputs they belong to where those are contiguous: 0.7 us less each on the Grace host
+    dx = dw = db = None
+    if need_dx:
+        dx = torch.empty_like(x) if x.is_contiguous() else torch.empty((m, k), dtype=dtype, device=x.device)
+    if need_dw:
+        dw = torch.empty_like(w) if w.is_contiguous() else torch.empty((n, k), dtype=dtype, device=x.device)
+    if need_dbias:
+        db = torch.empty((n,), dtype=dtype, device=x.device)
+    dy, ldy = _rows(dy, n)
+    x, ldx = _rows(x, k)
+    w, ldw = _rows(w, k)
     z = ldz = 0
     if preact is not None:
-        preact, ldz = _rows(preact)
+        preact, ldz = _rows(preact, n)
         z = preact.data_ptr()
-    dx = torch.empty((m, k), dtype=dtype, device=x.device) if need_dx else None
-    dw = torch.empty((n, k), dtype=dtype, device=x.device) if need_dw else None
-    db = torch.empty((n,), dtype=dtype, device=x.device) if need_dbias else None
     code = _library().ozaki2_linear_backward(
         _LINEAR_BACKWARD_ARGS.pack(m, k, n, dy.data_ptr(), ldy, x.data_ptr(), ldx, w.data_ptr(), ldw, z, ldz,
                                    dx.data_ptr() if need_dx else 0, k, dw.data_ptr() if need_dw else 0, k,
@@ -257,12 +263,16 @@ def dropout(x, p, *, seed, offset=0, residual=None, out=None, stream=None):
         return _elsewhere(dropout, device, stream, (x, residual, out), x, p, seed=seed, offset=offset, residual=residual, out=out)
 
     rows, cols = shape
-    x, ldx = _rows(x)
+    like = x.is_contiguous()
+    x, ldx = _rows(x, cols)
     r = ldr = 0
     if residual is not None:
-        residual, ldr = _rows(residual)
+        residual, ldr = _rows(residual, cols)
         r = residual.data_ptr()
-    y, ldy = (out, _ld(out)) if out is not None else (torch.empty_like(x) if ldx == cols else torch.empty(shape, dtype=dtype, device=x.device), cols)
+    if out is not None:
+        y, ldy = out, _ld(out)
+    else:
+        y, ldy = torch.empty_like(x) if like else torch.empty(shape, dtype=dtype, device=x.device), cols
     code = _library().ozaki2_dropout(
         _DROPOUT_ARGS.pack(rows, cols, x.data_ptr(), ldx, r, ldr, y.data_ptr(), ldy, seed & _MASK64, offset & _MASK64,
                            _probability(p), _FLOATS[dtype], 0), _stream_of(device))

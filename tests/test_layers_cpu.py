@@ -125,10 +125,10 @@ def test_no_gpu_means_a_loud_error(lib):
 def test_row_major_views_pass_through_and_others_are_copied():
     base = torch.arange(60.0).reshape(6, 10)
     for t, ld in ((base, 10), (base[1:4, 2:7], 10), (base[:1, :5], 5), (base[:, :1], 10), (base[:0], 10), (base.t()[:, :1][:1], 1)):
-        got, lead = layers._rows(t)
+        got, lead = layers._rows(t, t.shape[1])
         assert got is t and (lead == ld or t.shape[0] <= 1)
     for t in (base.t(), base[:, ::2], base[:1].expand(4, 10), base.flip(0).t()):
-        got, lead = layers._rows(t)
+        got, lead = layers._rows(t, t.shape[1])
         assert got is not t and torch.equal(got, t) and lead == t.shape[1]
 
 
