@@ -65,8 +65,9 @@ inline FastDiv make_fast_div(uint32_t d) {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t dtype_bytes(oz2_dtype t) { return t == OZ2_F32 ? 4 : 2; }
-inline bool aligned16(const void* p, int64_t ld, oz2_dtype t) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && static_cast<size_t>(ld) * dtype_bytes(t) % 16 == 0;
+// Whether groups of eight elements start on boundaries of their own size: 16 bytes, or 32 of 32-bit elements.
+inline bool groups_aligned(const void* p, int64_t ld, oz2_dtype t) {
+  return reinterpret_cast<uintptr_t>(p) % (8 * dtype_bytes(t)) == 0 && ld % 8 == 0;
 }
 
 // ------------------------------------------------------------ launchers
@@ -209,8 +210,9 @@ __device__ __forceinline__ void values8(const uint4* u, float* v, int stride = 1
   }
 }
 
-// Eight neighbouring elements of a row: whole vectors where `vec` (16-byte
-// aligned, all eight inside), else one by one, the first n (zeros after them).
+// Eight neighbouring elements of a row in global memory: one vector where `vec`
+// (a whole group on its boundary, so that 32-bit elements go by whole 32-byte
+// sectors too), else one by one, the first n (zeros after them).
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, bool vec, int n, float (&v)[8]) {
   if (vec) {
@@ -224,14 +226,10 @@ __device__ __forceinline__ void load8(const T* p, bool vec, int n, float (&v)[8]
         v[2 * i + 1] = f.y;
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 f = reinterpret_cast<const float4*>(p)[i];
-        v[4 * i] = f.x;
-        v[4 * i + 1] = f.y;
-        v[4 * i + 2] = f.z;
-        v[4 * i + 3] = f.w;
-      }
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                   : "l"(p)
+                   : "memory");
     }
   } else {
 #pragma unroll
@@ -246,8 +244,9 @@ __device__ __forceinline__ void store8(T* p, bool vec, int n, const float (&v)[8
       *reinterpret_cast<uint4*>(p) = make_uint4(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]),
                                                 Elem<T>::pack(v[4], v[5]), Elem<T>::pack(v[6], v[7]));
     } else {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                   "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                   : "memory");
     }
   } else {
 #pragma unroll

@@ -55,7 +55,7 @@ struct Input {
 
   Input(const void* p_, int64_t rows_, int64_t cols_, int64_t ld_, bool used, Carver& c)
       : p(p_), rows(rows_), cols(cols_), ld(rows_ > 1 ? ld_ : ceil_div(cols_, 8) * 8), copy(false), at(0) {
-    copy = used && rows > 0 && cols > 0 && !aligned16(p, ld, OZ2_BF16);
+    copy = used && rows > 0 && cols > 0 && !groups_aligned(p, ld, OZ2_BF16);
     if (copy) {
       ld = ceil_div(cols, 8) * 8;
       at = c.take(static_cast<size_t>(rows) * ld * 2);
@@ -88,8 +88,8 @@ oz2_status linear(const oz2_linear_args& a, cudaStream_t st) {
   ep.cols = a.n;
   ep.act = a.act;
   ep.drop = make_dropout(a.dropout, a.seed, a.offset);
-  ep.vec = aligned16(a.y, a.ldy, dtype) && (!a.bias || aligned16(a.bias, 0, dtype)) &&
-           (!a.residual || aligned16(a.residual, a.ldr, dtype)) && (!a.preact || aligned16(a.preact, a.ldz, dtype));
+  ep.vec = groups_aligned(a.y, a.ldy, dtype) && (!a.bias || groups_aligned(a.bias, 0, dtype)) &&
+           (!a.residual || groups_aligned(a.residual, a.ldr, dtype)) && (!a.preact || groups_aligned(a.preact, a.ldz, dtype));
   Carver c;
   Input xi(a.x, a.m, a.k, a.ldx, true, c), wi(a.w, a.n, a.k, a.ldw, true, c);
   const LinearPlan plan(Operand{xi.p, xi.ld, false}, a.k, ep, res.num_sms);
@@ -110,7 +110,7 @@ Epilogue plain_epilogue(void* out, int64_t ld, int64_t rows, int64_t cols, oz2_d
   ep.ldy = ld;
   ep.rows = rows;
   ep.cols = cols;
-  ep.vec = aligned16(out, ld, dtype);
+  ep.vec = groups_aligned(out, ld, dtype);
   return ep;
 }
 
@@ -132,7 +132,7 @@ oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
   if (k == 0) dx = dw = nullptr;
   // dz is dy itself where nothing follows the product and its rows are aligned
   const bool products = dx || dw;
-  const bool make_dz = products && (a.act != OZ2_ACT_NONE || drop.threshold != 0 || !aligned16(a.dy, a.lddy, dtype));
+  const bool make_dz = products && (a.act != OZ2_ACT_NONE || drop.threshold != 0 || !groups_aligned(a.dy, a.lddy, dtype));
   const int64_t ld = make_dz ? ceil_div(n, 8) * 8 : a.lddy;
   Carver c;
   const size_t dz_at = c.take(make_dz ? static_cast<size_t>(m) * ld * 2 : 0);

@@ -33,6 +33,23 @@ cudaError_t for_rows(int64_t rows, int64_t cols, F&& f) {
   return cudaSuccess;
 }
 
+// Eight neighbouring elements as they are in memory.
+template <typename T>
+struct Raw8 {
+  uint4 u;
+  __device__ __forceinline__ void read(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void values(float (&v)[8]) const { values8<T>(&u, v); }
+};
+template <>
+struct Raw8<float> {
+  float f[8];
+  __device__ __forceinline__ void read(const float* p) { load8(p, true, 8, f); }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f[i];
+  }
+};
+
 // ------------------------------------------------------------------ dropout
 // A thread takes U groups, 256 apart, and has all of their loads in flight at
 // once.  FLAT: the matrices are contiguous, with whole groups in every row, so a
@@ -44,18 +61,14 @@ __global__ void __launch_bounds__(256) dropout_kernel(const Groups groups, const
                                                       T* y, int64_t ldy, bool aligned, const Dropout drop) {
   wait_for_predecessor();
   const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
-  constexpr int kPieces = sizeof(T) / 2;
   if (FLAT) {
     const int64_t base = (groups.row0 * groups.per_row.d + first) * 8;
-    uint4 xs[U][kPieces], rs[U][kPieces];
+    Raw8<T> xs[U], rs[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (first + u * 256 >= groups.count) break;
-#pragma unroll
-      for (int k = 0; k < kPieces; ++k) {
-        xs[u][k] = reinterpret_cast<const uint4*>(x + base + u * 2048)[k];
-        if (residual) rs[u][k] = reinterpret_cast<const uint4*>(residual + base + u * 2048)[k];
-      }
+      xs[u].read(x + base + u * 2048);
+      if (residual) rs[u].read(residual + base + u * 2048);
     }
     let_successor_come();
 #pragma unroll
@@ -65,11 +78,11 @@ __global__ void __launch_bounds__(256) dropout_kernel(const Groups groups, const
       uint32_t g;
       groups.place(first + u * 256, row, g);
       float v[8];
-      values8<T>(xs[u], v);
+      xs[u].values(v);
       if (drop.threshold) drop8(drop, static_cast<uint32_t>(row), g, v);
       if (residual) {
         float add[8];
-        values8<T>(rs[u], add);
+        rs[u].values(add);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += add[e];
       }
@@ -232,7 +245,7 @@ int dz_rows(int64_t m, int64_t n) { return m <= 128 || ceil_div(n, 256) * ceil_d
 
 template <typename T>
 cudaError_t dz_impl(const DzArgs& a, oz2_dtype dtype, cudaStream_t st) {
-  const bool aligned = aligned16(a.dy, a.lddy, dtype) && (!a.preact || aligned16(a.preact, a.ldz, dtype));
+  const bool aligned = groups_aligned(a.dy, a.lddy, dtype) && (!a.preact || groups_aligned(a.preact, a.ldz, dtype));
   const int64_t rows = dz_partial_rows(a.m, a.n), blocks = ceil_div(a.n, 256) * rows;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   static constexpr auto kernels = std::array{dz_kernel<T, OZ2_ACT_NONE>, dz_kernel<T, OZ2_ACT_RELU>, dz_kernel<T, OZ2_ACT_SILU>,
@@ -272,7 +285,7 @@ int64_t dz_partial_rows(int64_t m, int64_t n) { return ceil_div(m, dz_rows(m, n)
 
 cudaError_t launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                            void* y, int64_t ldy, oz2_dtype dtype, const Dropout& drop, cudaStream_t st) {
-  const bool aligned = aligned16(x, ldx, dtype) && aligned16(y, ldy, dtype) && (!residual || aligned16(residual, ldr, dtype));
+  const bool aligned = groups_aligned(x, ldx, dtype) && groups_aligned(y, ldy, dtype) && (!residual || groups_aligned(residual, ldr, dtype));
   switch (dtype) {
     case OZ2_BF16: return dropout_impl<__nv_bfloat16>(rows, cols, x, ldx, residual, ldr, y, ldy, aligned, drop, st);
     case OZ2_F16: return dropout_impl<__half>(rows, cols, x, ldx, residual, ldr, y, ldy, aligned, drop, st);

@@ -44,6 +44,11 @@ constexpr int kChunk = sizeof(T) / 2;  // pieces of eight features
 // Steps in flight per warp.
 template <typename T>
 constexpr int kAhead = 8 / sizeof(T);
+// Shared memory of a block: the steps' slots, two tokens' angles and, forward, both weights.
+template <typename T>
+constexpr int kRing = (kAhead<T> * 2 * kChunk<T> + 2 * kAngles + 4 * kChunk<T>) * kPiece;
+template <typename T>
+constexpr int kBackRing = (kAhead<T> * 4 * kChunk<T> + 2 * kAngles) * kPiece;
 // Blocks per SM of one wave, by registers and shared memory.
 constexpr int kBlocks = 4;
 constexpr int kBackBlocks = 3;
@@ -136,7 +141,10 @@ struct Lane {
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < kChunk<T>; ++i)
-        copy16(to + (h * kChunk<T> + i) * kPiece, p + h * apart + i * (16 / static_cast<int>(sizeof(T))), on ? bytes[h] : 0);
+        if constexpr (sizeof(T) == 2)
+          copy16(to + h * kPiece, p + h * apart, on ? bytes[h] : 0);
+        else  // 16 of every 32 bytes: by way of L1, which has the other half when it is asked for
+          copy16_shared(to + (h * 2 + i) * kPiece, p + h * apart + i * 4, on ? bytes[h] : 0);
   }
   __device__ __forceinline__ void read_raw(const T* p, uint4 (&u)[2 * kChunk<T>], bool on) const {
 #pragma unroll
@@ -269,7 +277,7 @@ template <typename T, bool INTER, int LANES>
 __global__ void __launch_bounds__(kBlock, kBlocks) qk_kernel(const __grid_constant__ QkParams a) {
   using L = Lane<T, INTER, LANES>;
   constexpr int kHead = 2 * kChunk<T>;
-  __shared__ uint4 ring[(kAhead<T> * kHead + 2 * kAngles + 2 * kHead) * kBlock];
+  extern __shared__ uint4 ring[];
   wait_for_predecessor();
   const L l(a);
   const int nq = static_cast<int>(a.q.heads), nk = static_cast<int>(a.k.heads);
@@ -352,8 +360,8 @@ template <typename T, bool INTER, int LANES>
 __global__ void __launch_bounds__(kBlock, kBackBlocks) qk_backward_kernel(const __grid_constant__ QkParams a, int q_blocks) {
   using L = Lane<T, INTER, LANES>;
   constexpr int kHead = 2 * kChunk<T>;
-  __shared__ uint4 ring[(kAhead<T> * 2 * kHead + 2 * kAngles) * kBlock];
-  static_assert(sizeof(ring) >= kWarps * OZ2_HEAD_DIM_MAX * 4, "the warps' sums take the ring's place");
+  extern __shared__ uint4 ring[];
+  static_assert(kBackRing<T> >= kWarps * OZ2_HEAD_DIM_MAX * 4, "the warps' sums take the ring's place");
   wait_for_predecessor();
   const L l(a);
   const bool isq = static_cast<int>(blockIdx.x) < q_blocks;
@@ -555,19 +563,14 @@ __global__ void __launch_bounds__(kBlock) qk_plain_backward_kernel(const __grid_
 }
 
 // ------------------------------------------------------------------ host side
-bool side_aligned(const oz2_heads& h, oz2_dtype t) {
-  const size_t b = dtype_bytes(t);
-  return h.heads == 0 || (reinterpret_cast<uintptr_t>(h.data) % 16 == 0 && h.token_stride * b % 16 == 0 &&
-                          h.head_stride * b % 16 == 0);
-}
-
-// Whether the heads are made of aligned chunks of eight features.
+// Whether the heads are made of chunks of eight features on their own boundaries.
 bool chunked(const oz2_qk_args& a, bool backward) {
   const oz2_dtype t = static_cast<oz2_dtype>(a.dtype);
-  auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-  return a.dim % 8 == 0 && a.rot % 16 == 0 && side_aligned(a.q, t) && side_aligned(a.k, t) && side_aligned(a.q_out, t) &&
-         side_aligned(a.k_out, t) && (!backward || (side_aligned(a.dq_out, t) && side_aligned(a.dk_out, t))) &&
-         aligned(a.q_weight) && aligned(a.k_weight) && aligned(a.cos) && aligned(a.sin);
+  auto side = [&](const oz2_heads& h) { return h.heads == 0 || (groups_aligned(h.data, h.token_stride, t) && h.head_stride % 8 == 0); };
+  auto table = [](const float* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  return a.dim % 8 == 0 && a.rot % 16 == 0 && side(a.q) && side(a.k) && side(a.q_out) && side(a.k_out) &&
+         (!backward || (side(a.dq_out) && side(a.dk_out))) && groups_aligned(a.q_weight, 0, t) &&
+         groups_aligned(a.k_weight, 0, t) && table(a.cos) && table(a.sin);
 }
 // Lanes per head: 4, 8, 16 or 32, each with 16 features.
 int lanes_for(int64_t dim) {
@@ -576,22 +579,32 @@ int lanes_for(int64_t dim) {
   return lanes;
 }
 
+template <typename T, bool INTER, int LANES>
+cudaError_t launch_forward(const QkParams& p, int64_t blocks, const DeviceResources& res, cudaStream_t st) {
+  const cudaError_t e = allow_smem<qk_kernel<T, INTER, LANES>>(kRing<T>, res.device);
+  return e != cudaSuccess ? e : launch_kernel(qk_kernel<T, INTER, LANES>, blocks, kBlock, kRing<T>, 1, st, p);
+}
+template <typename T, bool INTER, int LANES>
+cudaError_t launch_back(const QkParams& p, int64_t blocks, int q_blocks, const DeviceResources& res, cudaStream_t st) {
+  const cudaError_t e = allow_smem<qk_backward_kernel<T, INTER, LANES>>(kBackRing<T>, res.device);
+  return e != cudaSuccess ? e : launch_kernel(qk_backward_kernel<T, INTER, LANES>, blocks, kBlock, kBackRing<T>, 1, st, p, q_blocks);
+}
 template <typename T>
-auto forward_kernel(int lanes, bool inter) {
+auto forward_launch(int lanes, bool inter) {
   switch (lanes) {
-    case 4: return inter ? qk_kernel<T, true, 4> : qk_kernel<T, false, 4>;
-    case 8: return inter ? qk_kernel<T, true, 8> : qk_kernel<T, false, 8>;
-    case 16: return inter ? qk_kernel<T, true, 16> : qk_kernel<T, false, 16>;
-    default: return inter ? qk_kernel<T, true, 32> : qk_kernel<T, false, 32>;
+    case 4: return inter ? launch_forward<T, true, 4> : launch_forward<T, false, 4>;
+    case 8: return inter ? launch_forward<T, true, 8> : launch_forward<T, false, 8>;
+    case 16: return inter ? launch_forward<T, true, 16> : launch_forward<T, false, 16>;
+    default: return inter ? launch_forward<T, true, 32> : launch_forward<T, false, 32>;
   }
 }
 template <typename T>
-auto backward_kernel(int lanes, bool inter) {
+auto back_launch(int lanes, bool inter) {
   switch (lanes) {
-    case 4: return inter ? qk_backward_kernel<T, true, 4> : qk_backward_kernel<T, false, 4>;
-    case 8: return inter ? qk_backward_kernel<T, true, 8> : qk_backward_kernel<T, false, 8>;
-    case 16: return inter ? qk_backward_kernel<T, true, 16> : qk_backward_kernel<T, false, 16>;
-    default: return inter ? qk_backward_kernel<T, true, 32> : qk_backward_kernel<T, false, 32>;
+    case 4: return inter ? launch_back<T, true, 4> : launch_back<T, false, 4>;
+    case 8: return inter ? launch_back<T, true, 8> : launch_back<T, false, 8>;
+    case 16: return inter ? launch_back<T, true, 16> : launch_back<T, false, 16>;
+    default: return inter ? launch_back<T, true, 32> : launch_back<T, false, 32>;
   }
 }
 
@@ -619,7 +632,7 @@ QkParams make_params(const oz2_qk_args& a, float* partial) {
 }
 
 template <typename T>
-cudaError_t qk_impl(const oz2_qk_args& a, int num_sms, cudaStream_t st) {
+cudaError_t qk_impl(const oz2_qk_args& a, const DeviceResources& res, cudaStream_t st) {
   const QkParams p = make_params(a, nullptr);
   if (!chunked(a, false)) {
     const int64_t blocks = ceil_div(a.tokens * (a.q.heads + a.k.heads), kWarps);
@@ -629,8 +642,8 @@ cudaError_t qk_impl(const oz2_qk_args& a, int num_sms, cudaStream_t st) {
   // a warp for each step, at most one wave
   const int lanes = lanes_for(a.dim), per_warp = 32 / lanes;
   const int64_t steps = a.tokens * (ceil_div(a.q.heads, per_warp) + ceil_div(a.k.heads, per_warp));
-  return launch_kernel(forward_kernel<T>(lanes, a.interleaved),
-                       std::min<int64_t>(ceil_div(steps, kWarps), static_cast<int64_t>(num_sms) * kBlocks), kBlock, 0, 1, st, p);
+  const int64_t blocks = std::min<int64_t>(ceil_div(steps, kWarps), static_cast<int64_t>(res.num_sms) * kBlocks);
+  return forward_launch<T>(lanes, a.interleaved)(p, blocks, res, st);
 }
 
 // Blocks for each side's steps: a warp for each step, at most the side's share
@@ -650,12 +663,12 @@ Blocks backward_blocks(const oz2_qk_args& a, int num_sms) {
 }
 
 template <typename T>
-cudaError_t qk_backward_impl(const oz2_qk_args& a, int num_sms, float* partial, cudaStream_t st) {
-  const Blocks b = backward_blocks(a, num_sms);
+cudaError_t qk_backward_impl(const oz2_qk_args& a, const DeviceResources& res, float* partial, cudaStream_t st) {
+  const Blocks b = backward_blocks(a, res.num_sms);
   const QkParams p = make_params(a, partial);
   const int q_blocks = static_cast<int>(b.q);
   cudaError_t e = chunked(a, true)
-                      ? launch_kernel(backward_kernel<T>(lanes_for(a.dim), a.interleaved), b.q + b.k, kBlock, 0, 1, st, p, q_blocks)
+                      ? back_launch<T>(lanes_for(a.dim), a.interleaved)(p, b.q + b.k, q_blocks, res, st)
                       : launch_kernel(a.interleaved ? qk_plain_backward_kernel<T, true> : qk_plain_backward_kernel<T, false>,
                                       b.q + b.k, kBlock, 0, 1, st, p, q_blocks);
   if (e != cudaSuccess || !partial) return e;
@@ -672,17 +685,17 @@ int64_t qk_partial_rows(const oz2_qk_args& a, int num_sms) {
 
 cudaError_t launch_qk(const oz2_qk_args& a, const DeviceResources& res, cudaStream_t st) {
   switch (a.dtype) {
-    case OZ2_BF16: return qk_impl<__nv_bfloat16>(a, res.num_sms, st);
-    case OZ2_F16: return qk_impl<__half>(a, res.num_sms, st);
-    default: return qk_impl<float>(a, res.num_sms, st);
+    case OZ2_BF16: return qk_impl<__nv_bfloat16>(a, res, st);
+    case OZ2_F16: return qk_impl<__half>(a, res, st);
+    default: return qk_impl<float>(a, res, st);
   }
 }
 
 cudaError_t launch_qk_backward(const oz2_qk_args& a, const DeviceResources& res, float* partial, cudaStream_t st) {
   switch (a.dtype) {
-    case OZ2_BF16: return qk_backward_impl<__nv_bfloat16>(a, res.num_sms, partial, st);
-    case OZ2_F16: return qk_backward_impl<__half>(a, res.num_sms, partial, st);
-    default: return qk_backward_impl<float>(a, res.num_sms, partial, st);
+    case OZ2_BF16: return qk_backward_impl<__nv_bfloat16>(a, res, partial, st);
+    case OZ2_F16: return qk_backward_impl<__half>(a, res, partial, st);
+    default: return qk_backward_impl<float>(a, res, partial, st);
   }
 }
 
