@@ -41,6 +41,7 @@ _LINEAR_BACKWARD_ARGS = struct.Struct("@qqqPqPqPqPqPqPqPQQdii")
 _DROPOUT_ARGS = struct.Struct("@qqPqPqPqQQdii")
 _HEADS = "Pqqq"
 _QK_ARGS = struct.Struct("@qqqqPPP" + 4 * _HEADS + "PP" + 2 * _HEADS + "PPdii")
+_QK_FORWARD_ARGS = struct.Struct("@qqqqPPP" + 4 * _HEADS + f"PP{struct.calcsize('@' + 2 * _HEADS + 'PP')}xdii")  # no gradients
 
 _lib = None
 # the current stream's handle without the Stream object around it (0.1 instead of 3 us)
@@ -286,15 +287,13 @@ def dropout_backward(dy, p, *, seed, offset=0, out=None, stream=None):
     return dropout(dy, p, seed=seed, offset=offset, out=out, stream=stream)
 
 
-def _neighbours(t):
-    """t, or a copy where the features of a head are not neighbours in memory."""
-    return t if t.stride(2) == 1 or t.shape[2] <= 1 else t.contiguous()
-
-
 def _heads(t):
-    """The C view of a (tokens, heads, dim) tensor."""
-    s0, s1, _ = t.stride()
-    return t.data_ptr(), t.shape[1], s0, s1
+    """(t, strides of its tokens and heads); a copy where the features of a head are not neighbours in memory."""
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and t.shape[2] > 1:
+        t = t.contiguous()
+        s0, s1, _ = t.stride()
+    return t, s0, s1
 
 
 def _check_heads_out(name, t, like):
@@ -309,26 +308,28 @@ def _check_qk(q, k, q_weight, k_weight, cos, sin, positions, out):
         _refuse("q", q, 3, _FLOATS)
     if k.dim() != 3:
         raise ValueError(f"k must have 3 dimensions, got shape {tuple(k.shape)}")
-    tokens, _, dim = q.shape
+    tokens, nq, dim = q.shape
+    nk = k.shape[1]
     if not 1 <= dim <= HEAD_DIM_MAX:
         raise ValueError(f"heads have 1 to {HEAD_DIM_MAX} features, got {dim}")
-    _check("k", k, dtype, device, (tokens, k.shape[1], dim))
+    _check("k", k, dtype, device, (tokens, nk, dim))
     _check("q_weight", q_weight, dtype, device, (dim,))
     _check("k_weight", k_weight, dtype, device, (dim,))
     table = cos.shape
-    if len(table) != 2 or 2 * table[1] > dim:
+    if cos.dim() != 2 or 2 * table[1] > dim:
         raise ValueError(f"cos must have shape (positions, rotated features / 2) with at most {dim} rotated, got {tuple(table)}")
+    rows, half = table
     _check("cos", cos, torch.float32, device, table)
     _check("sin", sin, torch.float32, device, table)
     _check("positions", positions, torch.int64, device, (tokens,))
     if out is not None:
         _check_heads_out("out[0]", out[0], q)
         _check_heads_out("out[1]", out[1], k)
-    return device
+    return dtype, device, tokens, nq, nk, dim, rows, half
 
 
-def _contiguous(t):
-    return t if t.is_contiguous() else t.contiguous()
+def _contiguous(*tensors):
+    return [t if t.is_contiguous() else t.contiguous() for t in tensors]
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, interleaved=False, out=None, stream=None):
@@ -341,27 +342,31 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, int
     pairs (i, i + rot / 2), or (2 i, 2 i + 1) if `interleaved`.  A position
     outside the tables gives NaN in that token's outputs.  `out`: a pair of
     tensors, q and k themselves for the operation in place."""
-    device = _check_qk(q, k, q_weight, k_weight, cos, sin, positions, out)
+    dtype, device, tokens, nq, nk, dim, rows, half = _check_qk(q, k, q_weight, k_weight, cos, sin, positions, out)
     if stream is not None or device != _current_device():
         tensors = (q, k, q_weight, k_weight, cos, sin, positions, *(out or ()))
         return _elsewhere(qk_norm_rope, device, stream, tensors, q, k, q_weight, k_weight, cos, sin, positions, eps=eps,
                           interleaved=interleaved, out=out)
 
-    tokens, nq, dim = q.shape
-    rows, half = cos.shape
-    dtype = q.dtype
     if out is None:
-        nk, where = k.shape[1], q.device
+        where = q.device
         q_out = torch.empty((tokens, nq, dim), dtype=dtype, device=where)
         k_out = torch.empty((tokens, nk, dim), dtype=dtype, device=where)
+        qo_token, ko_token, qo_head, ko_head = nq * dim, nk * dim, dim, dim
     else:
         q_out, k_out = out
-    q, k, cos, sin, positions = _neighbours(q), _neighbours(k), _contiguous(cos), _contiguous(sin), _contiguous(positions)
-    q_weight, k_weight = _contiguous(q_weight), _contiguous(k_weight)
+        qo_token, qo_head, _ = q_out.stride()
+        ko_token, ko_head, _ = k_out.stride()
+    q, q_token, q_head = _heads(q)
+    k, k_token, k_head = _heads(k)
+    if not (cos.is_contiguous() and sin.is_contiguous() and positions.is_contiguous() and q_weight.is_contiguous()
+            and k_weight.is_contiguous()):
+        cos, sin, positions, q_weight, k_weight = _contiguous(cos, sin, positions, q_weight, k_weight)
     code = _library().ozaki2_qk_norm_rope(
-        _QK_ARGS.pack(tokens, dim, 2 * half, rows, cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), *_heads(q), *_heads(k),
-                      *_heads(q_out), *_heads(k_out), q_weight.data_ptr(), k_weight.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, eps,
-                      _FLOATS[dtype], bool(interleaved)), _stream_of(device))
+        _QK_FORWARD_ARGS.pack(tokens, dim, 2 * half, rows, cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), q.data_ptr(), nq,
+                              q_token, q_head, k.data_ptr(), nk, k_token, k_head, q_out.data_ptr(), nq, qo_token, qo_head,
+                              k_out.data_ptr(), nk, ko_token, ko_head, q_weight.data_ptr(), k_weight.data_ptr(), eps,
+                              _FLOATS[dtype], 1 if interleaved else 0), _stream_of(device))
     if code:
         _fail(code, "ozaki2_qk_norm_rope")
     return q_out, k_out
@@ -373,31 +378,38 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
 
     The other arguments are the forward call's.  `out`: a pair of tensors for
     dq and dk, such as the slices of the joined projection's gradient."""
-    device = _check_qk(q, k, q_weight, k_weight, cos, sin, positions, out)
-    _check("dq_out", dq_out, q.dtype, device, q.shape)
-    _check("dk_out", dk_out, q.dtype, device, k.shape)
+    dtype, device, tokens, nq, nk, dim, rows, half = _check_qk(q, k, q_weight, k_weight, cos, sin, positions, out)
+    _check("dq_out", dq_out, dtype, device, (tokens, nq, dim))
+    _check("dk_out", dk_out, dtype, device, (tokens, nk, dim))
     if stream is not None or device != _current_device():
         tensors = (dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, *(out or ()))
         return _elsewhere(qk_norm_rope_backward, device, stream, tensors, dq_out, dk_out, q, k, q_weight, k_weight, cos, sin,
                           positions, eps=eps, interleaved=interleaved, out=out)
 
-    tokens, nq, dim = q.shape
-    rows, half = cos.shape
-    dtype, where = q.dtype, q.device
+    where = q.device
     if out is None:
         dq = torch.empty((tokens, nq, dim), dtype=dtype, device=where)
-        dk = torch.empty((tokens, k.shape[1], dim), dtype=dtype, device=where)
+        dk = torch.empty((tokens, nk, dim), dtype=dtype, device=where)
+        dq_token, dk_token, dq_head, dk_head = nq * dim, nk * dim, dim, dim
     else:
         dq, dk = out
+        dq_token, dq_head, _ = dq.stride()
+        dk_token, dk_head, _ = dk.stride()
     dwq = torch.empty((dim,), dtype=dtype, device=where)
     dwk = torch.empty((dim,), dtype=dtype, device=where)
-    q, k, dq_out, dk_out = _neighbours(q), _neighbours(k), _neighbours(dq_out), _neighbours(dk_out)
-    q_weight, k_weight, cos, sin, positions = (_contiguous(q_weight), _contiguous(k_weight), _contiguous(cos), _contiguous(sin),
-                                               _contiguous(positions))
+    q, q_token, q_head = _heads(q)
+    k, k_token, k_head = _heads(k)
+    dq_out, gq_token, gq_head = _heads(dq_out)
+    dk_out, gk_token, gk_head = _heads(dk_out)
+    if not (cos.is_contiguous() and sin.is_contiguous() and positions.is_contiguous() and q_weight.is_contiguous()
+            and k_weight.is_contiguous()):
+        cos, sin, positions, q_weight, k_weight = _contiguous(cos, sin, positions, q_weight, k_weight)
     code = _library().ozaki2_qk_norm_rope_backward(
-        _QK_ARGS.pack(tokens, dim, 2 * half, rows, cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), *_heads(q), *_heads(k),
-                      *_heads(dq), *_heads(dk), q_weight.data_ptr(), k_weight.data_ptr(), *_heads(dq_out), *_heads(dk_out),
-                      dwq.data_ptr(), dwk.data_ptr(), eps, _FLOATS[dtype], bool(interleaved)), _stream_of(device))
+        _QK_ARGS.pack(tokens, dim, 2 * half, rows, cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), q.data_ptr(), nq, q_token,
+                      q_head, k.data_ptr(), nk, k_token, k_head, dq.data_ptr(), nq, dq_token, dq_head, dk.data_ptr(), nk, dk_token,
+                      dk_head, q_weight.data_ptr(), k_weight.data_ptr(), dq_out.data_ptr(), nq, gq_token, gq_head,
+                      dk_out.data_ptr(), nk, gk_token, gk_head, dwq.data_ptr(), dwk.data_ptr(), eps, _FLOATS[dtype],
+                      1 if interleaved else 0), _stream_of(device))
     if code:
         _fail(code, "ozaki2_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
