@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
 
   let_successor_come();
   __syncthreads();
-  cluster_sync_all();  // the leader's MMAs are done with both CTAs' shared and tensor memory
+  cluster_sync_relaxed();  // the leader's MMAs are done with both CTAs' shared and tensor memory
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 

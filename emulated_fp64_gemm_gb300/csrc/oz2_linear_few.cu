@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(Few<MP>::THREADS, 1)
 #pragma unroll 1
   for (; item < end; item += kThreads) {
     const int64_t row = item_row(item), col = item_col(item), left = p.ep.cols - col;
+    if (left <= 0) continue;  // nothing is loaded from a peer that is not used before the last barrier
     const int group = item % (kTileN / 8) * 4;
     const uint32_t at = smem_u32(sums + item / (kTileN / 8) * kTileN), lo = at + group * 4, hi = at + 256 + (group ^ 16) * 4;
     float v[8] = {};
@@ -240,7 +241,6 @@ __global__ void __launch_bounds__(Few<MP>::THREADS, 1)
       residual = read_residual8<T>(p.ep, item_row(item + kThreads), item_col(item + kThreads));
     }
     if (p.ep.vec) {
-      if (left <= 0) continue;
       const int n = left < 8 ? static_cast<int>(left) : 8;
       if (p.ep.z) store8_raw(static_cast<T*>(p.ep.z) + row * p.ep.ldz + col, left >= 8, n, z);
       store8_raw(static_cast<T*>(p.ep.y) + row * p.ep.ldy + col, left >= 8, n, pack8<T>(v));
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(Few<MP>::THREADS, 1)
       if (p.ep.z) static_cast<T*>(p.ep.z)[row * p.ep.ldz + col] = z_out[e];
     }
   }
-  if (ranks > 1) cluster_sync_all(); else __syncthreads();  // the peers have read this CTA's sums
+  if (ranks > 1) cluster_sync_relaxed(); else __syncthreads();  // the peers have read this CTA's sums
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
