@@ -235,15 +235,17 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
     prefetch_map(&map_b);
   }
   wait_for_predecessor();
-  // both CTAs run before the collective allocation, and both have their barriers before any remote signal
-  __syncthreads();
+  // Both CTAs run, and have their barriers, before the collective allocation and
+  // before any remote signal.  The loads start then; the allocation goes on
+  // beside them, and the other warps wait for it in both CTAs.
+  __syncwarp();
   cluster_sync_all();
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
   tc_fence_before();
-  __syncthreads();
-  cluster_sync_all();
+  __syncwarp();
+  cluster_arrive();
+  if (warp != 0) cluster_wait();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads (both CTAs)
@@ -279,6 +281,7 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (leader only)
+    const uint32_t tmem = *tmem_slot;
     if (leader && elect_one()) {
       // kind::f16: 32-bit sums, both operands of type T, M = 256 (the pair), N = 256
       constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
@@ -329,6 +332,7 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int quad = warp & 3, part = (warp - 2) >> 2;  // the lanes this warp may read; its share of the columns
     float* tile = reinterpret_cast<float*>(s_epi + (warp - 2) * 4096);
+    const uint32_t tmem = *tmem_slot;
     bool ok = true;
     int n = 0;
     for (int u = pair; u < p.units; u += pairs, ++n) {
@@ -371,9 +375,10 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
   }
 
   let_successor_come();
-  __syncthreads();
+  __syncwarp();
+  if (warp == 0) cluster_wait();  // for the allocation, long done
   cluster_sync_relaxed();  // the leader's MMAs are done with both CTAs' shared and tensor memory
-  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (warp == 1) tmem_dealloc_pair(*tmem_slot, 512);
 }
 
 // Adds the partial sums of the split tiles in order and finishes them: one
