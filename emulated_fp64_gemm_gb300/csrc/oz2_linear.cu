@@ -44,8 +44,7 @@ constexpr int kBK = 64;                        // k per stage: 128 bytes
 constexpr int kOperandBytes = 128 * kBK * 2;   // a CTA's share of one operand per stage
 constexpr int kStageTx = 4 * kOperandBytes;    // bytes landing per stage across the pair
 // Epilogue warps, each with 4 KB of shared memory; what they leave holds the
-// stages.  Sixteen warps finish a tile in 60 % of the time of eight (2048 x 1024 x
-// 4096 with gelu, dropout and residual: 27 instead of 34 us), which counts where a
+// stages.  Sixteen warps finish a tile in 60 % of the time of eight, which counts where a
 // pair has few k blocks to hide its epilogues behind; the sixth stage and fewer
 // warps are worth 1.5 % of a long product (8192 x 4096 x 16384).
 template <int WARPS>
@@ -142,11 +141,62 @@ struct ReadAhead {
     return now;
   }
 };
-// Steps 4 b .. 4 b + 3: the block of 32 x 32 sums in `tile`.
+// Whether block b lies inside an output whose rows start on 16-byte boundaries.
+__device__ __forceinline__ bool whole_block(const Epilogue& e, const Strip& s, int b) {
+  return e.vec && s.row0 + 32 <= e.rows && s.col0 + 32 * (b + 1) <= e.cols;
+}
+// Steps 4 b .. 4 b + 3, the block of 32 x 32 sums in `tile`, where it is whole:
+// almost every block of an aligned layer.  The pointers run along, nothing is
+// tested per lane, and two steps are in the code, so that one's dependent chains
+// fill the other's waits.  A tile's epilogue by sixteen warps, in cycles: rounded
+// and stored 5900, with silu and residual 7800 (one step in the code 9300, four
+// 8100), with gelu, dropout and residual 13400 (15300, 13200); by finish_block,
+// which tests every lane in every step, 7100, 12300 and 19800.
+template <typename T, int ACT, int STEPS>
+__device__ __forceinline__ void finish_whole_block(const Epilogue& e, const float* tile, int lane, const Strip& s, int b,
+                                                   ReadAhead& in) {
+  const int64_t row0 = s.row(0, lane), col = s.col(4 * b, lane);
+  const uint4 bias = in.bias;
+  if (4 * b + 4 < STEPS) in.bias = read_bias8<T>(e, s.col(4 * b + 4, lane));
+  T* y = static_cast<T*>(e.y) + row0 * e.ldy + col;
+  T* z = static_cast<T*>(e.z) + row0 * e.ldz + col;
+  const T* ahead = static_cast<const T*>(e.residual) + row0 * e.ldr + col + 32;
+  const bool more = 4 * b + 4 < STEPS && whole_block(e, s, b + 1);  // else the next block reads its own
+  const int chunk = ((2 * (lane & 3)) ^ (lane >> 2)) << 2;          // as get_eight has it; r % 8 is lane / 4 in every step
+  const float* from = tile + (lane >> 2) * 32;
+  uint32_t row = static_cast<uint32_t>(row0);
+#pragma unroll 2
+  for (int i = 0; i < 4; ++i, row += 8, from += 8 * 32) {
+    const float4 lo = *reinterpret_cast<const float4*>(from + chunk), hi = *reinterpret_cast<const float4*>(from + (chunk ^ 4));
+    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (e.bias) add8<T>(bias, v);
+    if (e.z) {
+      *reinterpret_cast<uint4*>(z) = pack8<T>(v);
+      z += 8 * e.ldz;
+    }
+    activate8(ACT, v);
+    if (e.drop.threshold) drop8(e.drop, row, static_cast<uint32_t>(col >> 3), v);
+    if (e.residual) {
+      add8<T>(in.residual[0], v);
+      in.residual[0] = in.residual[1];
+      in.residual[1] = in.residual[2];
+      in.residual[2] = in.residual[3];
+      if (more) in.residual[3] = *reinterpret_cast<const uint4*>(ahead);
+      ahead += 8 * e.ldr;
+    }
+    *reinterpret_cast<uint4*>(y) = pack8<T>(v);
+    y += 8 * e.ldy;
+  }
+}
+// The same for any block.
 template <typename T, int ACT, int STEPS>
 __device__ __forceinline__ void finish_block(const Epilogue& e, float* tile, int lane, const Strip& s, int b, ReadAhead& in) {
   const int g = lane & 3;
   const uint4 bias = in.bias;
+  if (e.vec && b > 0) {  // the block before may have been a whole one, which did not read ahead
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) in.next_residual<T, STEPS>(e, s, lane, 4 * b + i - 4);
+  }
   if (4 * b + 4 < STEPS) in.bias = read_bias8<T>(e, s.col(4 * b + 4, lane));
 #pragma unroll 1
   for (int i = 4 * b; i < 4 * b + 4; ++i) {
@@ -361,10 +411,12 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
         }
         put_block(tile, lane, v);
         __syncwarp();
-        if (U.slot < 0)
-          finish_block<T, ACT, S::STEPS>(p.ep, tile, lane, strip, cb, ahead);
-        else
+        if (U.slot >= 0)
           save_block(p.partial + static_cast<int64_t>(U.slot) * kTileFloats, tile, lane, local_row, local_col);
+        else if (whole_block(p.ep, strip, cb))
+          finish_whole_block<T, ACT, S::STEPS>(p.ep, tile, lane, strip, cb, ahead);
+        else
+          finish_block<T, ACT, S::STEPS>(p.ep, tile, lane, strip, cb, ahead);
         __syncwarp();
       }
     }

