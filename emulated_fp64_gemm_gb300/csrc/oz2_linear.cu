@@ -151,7 +151,9 @@ __device__ __forceinline__ bool whole_block(const Epilogue& e, const Strip& s, i
 // fill the other's waits.  A tile's epilogue by sixteen warps, in cycles: rounded
 // and stored 5900, with silu and residual 7800 (one step in the code 9300, four
 // 8100), with gelu, dropout and residual 13400 (15300, 13200); by finish_block,
-// which tests every lane in every step, 7100, 12300 and 19800.
+// which tests every lane in every step, 7100, 12300 and 19800.  Eight warps, which
+// finish a tile behind the next one's product, do without it: there it cost dw of
+// 8192 x 4096 x 16384 two percent and dx half of one, and won one with a residual.
 template <typename T, int ACT, int STEPS>
 __device__ __forceinline__ void finish_whole_block(const Epilogue& e, const float* tile, int lane, const Strip& s, int b,
                                                    ReadAhead& in) {
@@ -193,7 +195,7 @@ template <typename T, int ACT, int STEPS>
 __device__ __forceinline__ void finish_block(const Epilogue& e, float* tile, int lane, const Strip& s, int b, ReadAhead& in) {
   const int g = lane & 3;
   const uint4 bias = in.bias;
-  if (e.vec && b > 0) {  // the block before may have been a whole one, which did not read ahead
+  if (e.residual && e.vec && b > 0) {  // the block before may have been a whole one, which did not read ahead
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) in.next_residual<T, STEPS>(e, s, lane, 4 * b + i - 4);
   }
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
         __syncwarp();
         if (U.slot >= 0)
           save_block(p.partial + static_cast<int64_t>(U.slot) * kTileFloats, tile, lane, local_row, local_col);
-        else if (whole_block(p.ep, strip, cb))
+        else if (WARPS == 16 && whole_block(p.ep, strip, cb))
           finish_whole_block<T, ACT, S::STEPS>(p.ep, tile, lane, strip, cb, ahead);
         else
           finish_block<T, ACT, S::STEPS>(p.ep, tile, lane, strip, cb, ahead);
