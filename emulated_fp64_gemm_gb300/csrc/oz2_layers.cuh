@@ -88,13 +88,18 @@ struct FewPlan {
 FewPlan plan_few(bool x_rows, int64_t rows, int64_t cols, int nkb, int num_sms);
 cudaError_t launch_linear_few(const FewPlan& plan, const Operand& a, const Operand& b, int64_t k, const Epilogue& ep,
                               oz2_dtype dtype, const DeviceResources& res, cudaStream_t st);
+// Both products of a layer's backward pass, of m x n gradients dz, in one launch; ranks 0 in the plan: not possible.
+FewPlan plan_few_pair(int64_t m, int64_t n, int64_t k, int num_sms);
+cudaError_t launch_few_pair(const FewPlan& plan, const Operand& dz, const Operand& w, const Operand& x, const Epilogue& ep_dx,
+                            const Epilogue& ep_dw, oz2_dtype dtype, const DeviceResources& res, cudaStream_t st);
 
 // How a product is run, and the bytes of `partial` that it needs.
 struct LinearPlan {
   FewPlan few;
   bool use_few;
   size_t partial_bytes;
-  LinearPlan() : few{}, use_few(false), partial_bytes(0) {}
+  double us;  // estimated
+  LinearPlan() : few{}, use_few(false), partial_bytes(0), us(0.0) {}
   LinearPlan(const Operand& a, int64_t k, const Epilogue& ep, int num_sms);
 };
 // B is rows_contiguous wherever A is.

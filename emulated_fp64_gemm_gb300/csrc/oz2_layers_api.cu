@@ -140,11 +140,14 @@ oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
   const size_t sums_at = c.take(dbias && sum_rows > 1 ? static_cast<size_t>(sum_rows) * n * 4 : 0);
   Input xi(a.x, m, k, a.ldx, dw, c), wi(a.w, n, k, a.ldw, dx, c);
   const Epilogue ep_dx = plain_epilogue(dx, a.lddx, m, k, dtype), ep_dw = plain_epilogue(dw, a.lddw, n, k, dtype);
-  // the two products run one after the other and share the room for partial sums
+  // the two products run side by side where they are small; else one after the other, and share the room for partial sums
   LinearPlan plan_dx, plan_dw;
+  FewPlan pair{};
   if (dx) plan_dx = LinearPlan(Operand{nullptr, ld, false}, n, ep_dx, res.num_sms);
   if (dw) plan_dw = LinearPlan(Operand{nullptr, ld, true}, m, ep_dw, res.num_sms);
-  const size_t partial_at = c.take(std::max(plan_dx.partial_bytes, plan_dw.partial_bytes));
+  if (dx && dw) pair = plan_few_pair(m, n, k, res.num_sms);
+  const bool together = pair.ranks > 0 && pair.us < plan_dx.us + plan_dw.us;
+  const size_t partial_at = c.take(together ? 0 : std::max(plan_dx.partial_bytes, plan_dw.partial_bytes));
   e = acquire_resources(st, c.used, &res);
   if (e != OZ2_OK) return e;
   if (make_dz || dbias) {
@@ -167,6 +170,11 @@ oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
   float* partial = reinterpret_cast<float*>(res.workspace + partial_at);
   const PackJob x_job = xi.place(res.workspace, a.ldx), w_job = wi.place(res.workspace, a.ldw);
   OZ2_TRY(launch_pack(x_job, w_job, st));
+  if (together) {
+    OZ2_TRY(launch_few_pair(pair, Operand{dz, ld, false}, Operand{wi.p, wi.ld, true}, Operand{xi.p, xi.ld, true}, ep_dx, ep_dw, dtype,
+                            res, st));
+    return OZ2_OK;
+  }
   if (dx) OZ2_TRY(launch_linear(plan_dx, Operand{dz, ld, false}, Operand{wi.p, wi.ld, true}, n, ep_dx, dtype, res, partial, st));
   if (dw) OZ2_TRY(launch_linear(plan_dw, Operand{dz, ld, true}, Operand{xi.p, xi.ld, true}, m, ep_dw, dtype, res, partial, st));
   return OZ2_OK;

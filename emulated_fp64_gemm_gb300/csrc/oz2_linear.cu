@@ -518,8 +518,8 @@ GemmParams make_params(int64_t k, const Epilogue& ep, int num_sms, double* us) {
   // 32 MB of A per group: each of the two dies keeps its own copy in its half of the 129 MB L2.  At k = 4096 with
   // 16384 columns groups of 4, 8, 16 and 32 row tiles took 604, 572, 562 and 583 us.
   p.group = static_cast<int>(std::clamp<int64_t>((32 << 20) / (256 * 2 * std::max<int64_t>(k, 1)), 4, 16));
-  // 9 us: what a launch takes beside its blocks, the exposed epilogue included
-  *us = 9.0 + 0.27 * plan_units(p.tiles_m * p.tiles_n, p.nkb, num_sms / 2, &p.full, &p.splits);
+  // 7.5 us: what a launch takes beside its blocks, the exposed epilogue included
+  *us = 7.5 + 0.27 * plan_units(p.tiles_m * p.tiles_n, p.nkb, num_sms / 2, &p.full, &p.splits);
   p.units = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
   p.lasting = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.nkb >= 256 * (num_sms / 2);
   return p;
@@ -569,12 +569,15 @@ cudaError_t launch_typed(const Operand& a, const Operand& b, const CUtensorMap& 
 LinearPlan::LinearPlan(const Operand& a, int64_t k, const Epilogue& ep, int num_sms)
     : few(plan_few(a.rows_contiguous, ep.rows, ep.cols, static_cast<int>(ceil_div(k, kBK)), num_sms)),
       use_few(k > 0 && ep.rows <= 64),
-      partial_bytes(0) {
+      partial_bytes(0),
+      us(few.us) {
   if (use_few) return;
   double gemm_us;
   const GemmParams p = make_params(k, ep, num_sms, &gemm_us);
   use_few = k > 0 && few.us < gemm_us;
-  if (!use_few) partial_bytes = static_cast<size_t>(p.tiles_m * p.tiles_n - p.full) * p.splits * kTileFloats * 4;
+  if (use_few) return;
+  us = gemm_us;
+  partial_bytes = static_cast<size_t>(p.tiles_m * p.tiles_n - p.full) * p.splits * kTileFloats * 4;
 }
 
 cudaError_t launch_linear(const LinearPlan& plan, const Operand& a, const Operand& b, int64_t k, const Epilogue& ep,

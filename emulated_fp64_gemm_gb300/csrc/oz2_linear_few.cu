@@ -59,11 +59,9 @@ __device__ __forceinline__ void load_cluster4(uint32_t addr, float* v) {
                : "memory");
 }
 
-// X_ROWS, W_ROWS: A, B are [k][rows] (their rows contiguous in memory).
+// CTA `cta` of a product.  X_ROWS, W_ROWS: A, B are [k][rows] (their rows contiguous in memory).
 template <typename T, int MP, bool X_ROWS, bool W_ROWS>
-__global__ void __launch_bounds__(Few<MP>::THREADS, 1)
-    linear_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                      const __grid_constant__ FewParams p) {
+__device__ __forceinline__ void few_cta(const CUtensorMap& map_x, const CUtensorMap& map_w, const FewParams& p, int cta) {
   using F = Few<MP>;
   constexpr int kThreads = F::THREADS;
   extern __shared__ uint8_t smem_raw[];
@@ -77,8 +75,8 @@ __global__ void __launch_bounds__(Few<MP>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ranks = 1 << p.log_ranks, rank = static_cast<int>(blockIdx.x) & (ranks - 1);
-  const int tile = static_cast<int>(blockIdx.x) >> p.log_ranks;
+  const int ranks = 1 << p.log_ranks, rank = cta & (ranks - 1);
+  const int tile = cta >> p.log_ranks;
   const int row_x = tile / p.tiles_n * MP, row_w = tile % p.tiles_n * kTileN;
   const int kb0 = p.nkb * rank >> p.log_ranks, kb1 = p.nkb * (rank + 1) >> p.log_ranks;  // nkb <= 2^25, 8 ranks at most
 
@@ -267,6 +265,30 @@ __global__ void __launch_bounds__(Few<MP>::THREADS, 1)
 }
 
 template <typename T, int MP, bool X_ROWS, bool W_ROWS>
+__global__ void __launch_bounds__(Few<MP>::THREADS, 1)
+    linear_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ FewParams p) {
+  few_cta<T, MP, X_ROWS, W_ROWS>(map_x, map_w, p, static_cast<int>(blockIdx.x));
+}
+
+// Both products of a small layer's backward pass, which need nothing of each
+// other: dx = dz w and dw = dz^T x side by side in one launch, the one of the
+// longer sums first.  Aligned 517 x 1024 x 1536: 14.5 us one after the other, 10.3
+// so; 1024 x 1024 x 1024: 14.3 and 9.0.
+template <typename T>
+__global__ void __launch_bounds__(Few<128>::THREADS, 1)
+    linear_few_pair_kernel(const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_w,
+                           const __grid_constant__ CUtensorMap map_dz_rows, const __grid_constant__ CUtensorMap map_x,
+                           const __grid_constant__ FewParams dx, const __grid_constant__ FewParams dw, int first_ctas, bool dx_first) {
+  const int cta = static_cast<int>(blockIdx.x);
+  const bool first = cta < first_ctas;
+  if (first == dx_first)
+    few_cta<T, 128, false, true>(map_dz, map_w, dx, first ? cta : cta - first_ctas);
+  else
+    few_cta<T, 128, true, true>(map_dz_rows, map_x, dw, first ? cta : cta - first_ctas);
+}
+
+template <typename T, int MP, bool X_ROWS, bool W_ROWS>
 cudaError_t launch_few_impl(const CUtensorMap& mx, const CUtensorMap& mw, const FewParams& p, int64_t ctas, int ranks,
                             const DeviceResources& res, cudaStream_t st) {
   const cudaError_t e = allow_smem<linear_few_kernel<T, MP, X_ROWS, W_ROWS>>(Few<MP>::SMEM, res.device);
@@ -274,17 +296,25 @@ cudaError_t launch_few_impl(const CUtensorMap& mx, const CUtensorMap& mw, const 
   return launch_kernel(linear_few_kernel<T, MP, X_ROWS, W_ROWS>, ctas, Few<MP>::THREADS, Few<MP>::SMEM, ranks, st, mx, mw, p);
 }
 
+// An operand's map, its boxes `box_rows` high where k is contiguous.
+bool make_map(CUtensorMap* map, const Operand& o, int64_t rows, int64_t k, int box_rows) {
+  return o.rows_contiguous ? encode_map_2d(map, o.p, rows, k, o.ld, 64, kBK) : encode_map_2d(map, o.p, k, rows, o.ld, kBK, box_rows);
+}
+FewParams make_params(const Epilogue& ep, int64_t k, int ranks, const DeviceResources& res) {
+  FewParams p{};
+  p.ep = ep;
+  p.nkb = static_cast<int>(ceil_div(k, kBK));
+  p.tiles_n = static_cast<int>(ceil_div(ep.cols, kTileN));
+  p.log_ranks = ranks == 8 ? 3 : ranks == 4 ? 2 : ranks - 1;
+  p.err = res.err;
+  return p;
+}
+
 template <typename T, int MP>
-cudaError_t launch_few_mp(const Operand& x, const Operand& w, int64_t k, FewParams& p, int ranks, const DeviceResources& res,
+cudaError_t launch_few_mp(const Operand& x, const Operand& w, int64_t k, const FewParams& p, int ranks, const DeviceResources& res,
                           cudaStream_t st) {
   CUtensorMap mx, mw;
-  if (x.rows_contiguous ? !encode_map_2d(&mx, x.p, p.ep.rows, k, x.ld, 64, kBK) : !encode_map_2d(&mx, x.p, k, p.ep.rows, x.ld, kBK, MP))
-    return cudaErrorInvalidValue;
-  if (w.rows_contiguous ? !encode_map_2d(&mw, w.p, p.ep.cols, k, w.ld, 64, kBK)
-                        : !encode_map_2d(&mw, w.p, k, p.ep.cols, w.ld, kBK, kTileN))
-    return cudaErrorInvalidValue;
-  p.tiles_n = static_cast<int>(ceil_div(p.ep.cols, kTileN));
-  p.log_ranks = ranks == 8 ? 3 : ranks == 4 ? 2 : ranks - 1;
+  if (!make_map(&mx, x, p.ep.rows, k, MP) || !make_map(&mw, w, p.ep.cols, k, kTileN)) return cudaErrorInvalidValue;
   const int64_t ctas = ceil_div(p.ep.rows, MP) * p.tiles_n * ranks;
   if constexpr (MP >= 64)
     if (x.rows_contiguous) return launch_few_impl<T, MP, true, true>(mx, mw, p, ctas, ranks, res, st);
@@ -293,7 +323,7 @@ cudaError_t launch_few_mp(const Operand& x, const Operand& w, int64_t k, FewPara
 }
 
 template <typename T>
-cudaError_t launch_few_typed(const FewPlan& plan, const Operand& x, const Operand& w, int64_t k, FewParams& p,
+cudaError_t launch_few_typed(const FewPlan& plan, const Operand& x, const Operand& w, int64_t k, const FewParams& p,
                              const DeviceResources& res, cudaStream_t st) {
   switch (plan.mp) {
     case 16: return launch_few_mp<T, 16>(x, w, k, p, plan.ranks, res, st);
@@ -303,34 +333,74 @@ cudaError_t launch_few_typed(const FewPlan& plan, const Operand& x, const Operan
   }
 }
 
+template <typename T>
+cudaError_t launch_pair_typed(const Operand& dz, const Operand& w, const Operand& x, const FewParams& dx, const FewParams& dw,
+                              int ranks, const DeviceResources& res, cudaStream_t st) {
+  const int64_t m = dx.ep.rows, n = dw.ep.rows;
+  const Operand dz_rows{dz.p, dz.ld, true};
+  CUtensorMap m_dz, m_w, m_dz_rows, m_x;
+  if (!make_map(&m_dz, dz, m, n, 128) || !make_map(&m_w, w, dx.ep.cols, n, kTileN) || !make_map(&m_dz_rows, dz_rows, n, m, 128) ||
+      !make_map(&m_x, x, dw.ep.cols, m, kTileN))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem<linear_few_pair_kernel<T>>(Few<128>::SMEM, res.device);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas_dx = ceil_div(m, 128) * dx.tiles_n * ranks, ctas_dw = ceil_div(n, 128) * dw.tiles_n * ranks;
+  const bool dx_first = dx.nkb >= dw.nkb;
+  return launch_kernel(linear_few_pair_kernel<T>, ctas_dx + ctas_dw, Few<128>::THREADS, Few<128>::SMEM, ranks, st, m_dz, m_w,
+                       m_dz_rows, m_x, dx, dw, static_cast<int>(dx_first ? ctas_dx : ctas_dw), dx_first);
+}
+
+// CTAs in clusters of `ranks` that run at once: clusters stay within a group of SMs, so fewer CTAs of large ones do.
+int64_t room_for(int ranks, int num_sms) { return ranks == 8 ? num_sms * 15 / 19 : ranks == 4 ? num_sms * 18 / 19 : num_sms; }
+// Joining the ranks' sums of MP = 128 share rows.
+double join_us(int ranks, double share) { return ranks == 8 ? 0.8 + 2.0 * share : ranks == 4 ? 0.5 + share : ranks == 2 ? 0.5 : 0.0; }
+
 }  // namespace
 
 // Times measured on the device for one wave of CTAs (launch, pipeline and
 // epilogue; a k block; joining 2, 4 or 8 ranks), from 1 x 512 x 512 to
-// 8192 x 512 x 512.  Clusters stay within a group of SMs, so fewer CTAs of large
-// ones run at once.
+// 8192 x 512 x 512.
 FewPlan plan_few(bool x_rows, int64_t rows, int64_t cols, int nkb, int num_sms) {
   const int mp = x_rows ? (rows <= 64 ? 64 : 128) : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   const int64_t tiles = ceil_div(rows, mp) * ceil_div(cols, kTileN);
-  const double share = mp / 128.0, base_us = mp == 128 ? 6.2 : 3.2 + 2.2 * share, block_us = 0.155 + 0.025 * share;
+  const double share = mp / 128.0, base_us = mp == 128 ? 5.3 : 3.2 + 2.2 * share, block_us = 0.155 + 0.045 * share;
   FewPlan best{mp, 1, 0.0};
   for (int ranks = 1; ranks <= 8 && (ranks == 1 || nkb >= 2 * ranks); ranks *= 2) {
-    const int64_t room = ranks == 8 ? num_sms * 15 / 19 : ranks == 4 ? num_sms * 18 / 19 : num_sms;
-    const double join_us = ranks == 8 ? 2.0 + 2.0 * share : ranks == 4 ? 1.0 + share : ranks == 2 ? 0.5 : 0.0;
-    const double us = ceil_div(tiles * ranks, room) * (base_us + ceil_div(nkb, ranks) * block_us) + join_us;
+    const double us = ceil_div(tiles * ranks, room_for(ranks, num_sms)) * (base_us + ceil_div(nkb, ranks) * block_us) + join_us(ranks, share);
     if (ranks == 1 || us < best.us) best = FewPlan{mp, ranks, us};
+  }
+  return best;
+}
+
+// The same for both products of a backward pass in one launch, where all their
+// CTAs run at once (ranks 0 elsewhere).  In more than one wave the long CTAs and
+// the short ones get in each other's way: 512 x 2048 x 2048 took 19.4 us side by
+// side, 17.4 one after the other.
+FewPlan plan_few_pair(int64_t m, int64_t n, int64_t k, int num_sms) {
+  FewPlan best{128, 0, 0.0};
+  if (m <= 64 || n <= 64) return best;
+  const int64_t tiles = (ceil_div(m, 128) + ceil_div(n, 128)) * ceil_div(k, kTileN);
+  const int64_t longest = ceil_div(std::max(m, n), kBK), shortest = ceil_div(std::min(m, n), kBK);
+  for (int ranks = 1; ranks <= 4 && (ranks == 1 || shortest >= 2 * ranks); ranks *= 2) {  // 16 tiles at least for eight: no room
+    if (tiles * ranks > room_for(ranks, num_sms)) break;
+    const double us = 5.3 + ceil_div(longest, ranks) * 0.2 + join_us(ranks, 1.0);
+    if (ranks == 1 || us < best.us) best = FewPlan{128, ranks, us};
   }
   return best;
 }
 
 cudaError_t launch_linear_few(const FewPlan& plan, const Operand& a, const Operand& b, int64_t k, const Epilogue& ep,
                               oz2_dtype dtype, const DeviceResources& res, cudaStream_t st) {
-  FewParams p{};
-  p.ep = ep;
-  p.nkb = static_cast<int>(ceil_div(k, kBK));
-  p.err = res.err;
+  const FewParams p = make_params(ep, k, plan.ranks, res);
   return dtype == OZ2_BF16 ? launch_few_typed<__nv_bfloat16>(plan, a, b, k, p, res, st)
                            : launch_few_typed<__half>(plan, a, b, k, p, res, st);
+}
+
+cudaError_t launch_few_pair(const FewPlan& plan, const Operand& dz, const Operand& w, const Operand& x, const Epilogue& ep_dx,
+                            const Epilogue& ep_dw, oz2_dtype dtype, const DeviceResources& res, cudaStream_t st) {
+  const FewParams dx = make_params(ep_dx, ep_dw.rows, plan.ranks, res), dw = make_params(ep_dw, ep_dx.rows, plan.ranks, res);
+  return dtype == OZ2_BF16 ? launch_pair_typed<__nv_bfloat16>(dz, w, x, dx, dw, plan.ranks, res, st)
+                           : launch_pair_typed<__half>(dz, w, x, dx, dw, plan.ranks, res, st);
 }
 
 }  // namespace oz2

@@ -89,8 +89,8 @@ oz2_status ozaki2_linear(const oz2_linear_args* args, void* stream);
  * Gradients of ozaki2_linear from dy [m][n]: with
  * dz = act'(preact) * keep * dy / (1 - p),
  *   dx [m][k] = dz w,  dw [n][k] = dz^T x,  dbias [n] = column sums of dz;
- * each of the three may be NULL.  preact is ozaki2_linear's, NULL for
- * OZ2_ACT_NONE.  The residual's gradient is dy itself.
+ * each of the three may be NULL, and they overlap nothing.  preact is
+ * ozaki2_linear's, NULL for OZ2_ACT_NONE.  The residual's gradient is dy itself.
  */
 typedef struct {
   int64_t m, k, n;

@@ -280,6 +280,19 @@ def test_backward_strides(oz2, pad, shift):
     check_backward(oz2, *t, "silu")
 
 
+# both products in one launch, the first or the second the one with the longer sums, k whole, in halves and in quarters
+@pytest.mark.parametrize("m,k,n", [(65, 64, 65), (70, 200, 130), (130, 200, 70), (517, 130, 1531), (1024, 40, 1024), (3000, 8, 600),
+                                   (600, 8, 3000), (129, 1000, 257)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_backward_products_side_by_side(oz2, m, k, n, dtype):
+    x, w = normal(m, k, dtype=dtype), normal(n, k, dtype=dtype, seed=1, scale=k**-0.5)
+    dy, z = normal(m, n, dtype=dtype, seed=2), normal(m, n, dtype=dtype, seed=3)
+    a = check_backward(oz2, dy, x, w)
+    b = oz2.linear_backward(dy, x, w)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    check_backward(oz2, dy, x, w, z, "silu", 0.25)
+
+
 def test_backward_parts_and_empty(oz2):
     m, k, n = 33, 72, 50
     dy, x, w = normal(m, n, dtype=BF16), normal(m, k, dtype=BF16, seed=1), normal(n, k, dtype=BF16, seed=2)
