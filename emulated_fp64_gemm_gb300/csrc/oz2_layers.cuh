@@ -284,8 +284,10 @@ __device__ __forceinline__ uint4 philox7(uint32_t c0, uint32_t c1, uint32_t c2, 
 // v <- keep * v * scale for the eight columns of group g (columns 8g .. 8g + 7)
 // of `row`; T > 0.  A dropped element becomes +0 whatever it was.  A high half's
 // draw is compared as the whole word: the bits below it cannot reach the next T.
-__device__ __forceinline__ void drop8(const Dropout& d, uint32_t row, uint32_t g, float (&v)[8]) {
-  const uint4 u = philox7(g, row, d.offset0, d.offset1, d.seed0, d.seed1);
+__device__ __forceinline__ uint4 draws8(const Dropout& d, uint32_t row, uint32_t g) {
+  return philox7(g, row, d.offset0, d.offset1, d.seed0, d.seed1);
+}
+__device__ __forceinline__ void drop8(const Dropout& d, const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -293,6 +295,8 @@ __device__ __forceinline__ void drop8(const Dropout& d, uint32_t row, uint32_t g
     v[2 * i + 1] = w[i] > d.limit ? v[2 * i + 1] * d.scale : 0.0f;
   }
 }
+
+__device__ __forceinline__ void drop8(const Dropout& d, uint32_t row, uint32_t g, float (&v)[8]) { drop8(d, draws8(d, row, g), v); }
 
 // ------------------------------------------------------------ activations
 // The results go to 16 bits, so the fast exponential and reciprocal (relative

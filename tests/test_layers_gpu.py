@@ -381,6 +381,37 @@ def test_dropout_strides_in_place_and_special_values(oz2):
     assert oz2.dropout(x[:0], 0.3, seed=1).shape == (0, 264) and oz2.dropout(x[:, :0], 0.3, seed=1).shape == (100, 0)
 
 
+@pytest.mark.parametrize("rows,cols,ld", [(37, 64, 65), (5, 256, 259), (9, 257, 257), (21, 261, 263), (33, 1001, 1001), (3, 2050, 2051),
+                                          (600, 5001, 5001), (2, 70001, 70003), (1, 1000, 1000)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_dropout_rows_off_boundaries(oz2, rows, cols, ld, dtype):
+    # matrices whose rows are alike off their boundaries, from each start, against the same call with rows that differ
+    x, r = normal(rows, cols, dtype=dtype), normal(rows, cols, dtype=dtype, seed=1)
+    want = oz2.dropout(x, 0.3, seed=SEED, offset=OFFSET, residual=r)
+    keep, scale = factor(rows, cols, 0.3)
+    exact = torch.where(keep, x.double() * scale, 0.0) + r.double()
+    assert_within(want, exact, (UNIT[dtype] + 2.0**-23) * exact.abs() + 2.0**-22 * (exact - r.double()).abs() + TINY[dtype])
+    plain = oz2.dropout(x, 0.3, seed=SEED, offset=OFFSET)
+    copied = oz2.dropout(x, 0.0, seed=SEED, residual=r)
+
+    def at(start, values=None):
+        buffer = torch.full((rows * ld + 16,), -7.0, dtype=dtype, device="cuda")
+        view = buffer.as_strided((rows, cols), (ld, 1), start)
+        if values is not None:
+            view.copy_(values)
+        return buffer, view
+
+    for start in range(8):
+        for y_start in (start, start + 3):
+            (buffer, y), xs, rs = at(y_start), at(start, x)[1], at(start, r)[1]
+            assert torch.equal(oz2.dropout(xs, 0.3, seed=SEED, offset=OFFSET, residual=rs, out=y), want)
+            y.fill_(-7.0)
+            assert bool((buffer == -7.0).all()), "nothing beside the rows is written"
+            assert torch.equal(oz2.dropout(xs, 0.3, seed=SEED, offset=OFFSET, out=y), plain)
+        assert torch.equal(oz2.dropout(xs, 0.0, seed=SEED, residual=rs, out=at(start)[1]), copied)
+        assert torch.equal(oz2.dropout(xs, 0.3, seed=SEED, offset=OFFSET, residual=rs, out=xs), want)
+
+
 def test_dropout_rate_and_row_numbers(oz2):
     # kept shares by row, by column within a group and in all, within six standard deviations
     x = torch.ones(4096, 2048, dtype=BF16, device="cuda")
