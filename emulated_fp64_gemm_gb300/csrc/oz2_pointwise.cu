@@ -128,11 +128,12 @@ __device__ __forceinline__ uint4 shifted_draws(const uint4& before, const uint4&
 // holds the end of one group of the mask and the start of the next, and has the
 // earlier group's draws from the lane before.  A warp goes along 32 U vectors of a
 // row and forms the draws ahead of its first one too.  Bound by
-// instructions (the draws' shuffles and shifts beside the generator): 8192 x 5001
-// takes 45 us in bfloat16 (3.7 TB/s) and 54 us in 32 bits, element by element, as
-// the general form has it, 92 and 90 us.
+// instructions (the draws' shuffles and shifts beside the generator: 190 per
+// vector, 97 in the aligned form) and registers: three blocks per SM take 8192 x
+// 5001 in bfloat16 in 38 us (4.3 TB/s), two in 45; 32 bits fit in two, 55 us.
+// Element by element, as the general form has it, 92 and 90 us.
 template <typename T, int U>
-__global__ void __launch_bounds__(256) dropout_shifted_kernel(const Groups runs, const T* x, int64_t ldx, const T* residual, int64_t ldr,
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) dropout_shifted_kernel(const Groups runs, const T* x, int64_t ldx, const T* residual, int64_t ldr,
                                                               T* y, int64_t ldy, const Dropout drop) {
   wait_for_predecessor();
   const int lane = threadIdx.x & 31;
@@ -211,7 +212,7 @@ bool alike(int64_t rows, size_t size, const void* x, int64_t ldx, const void* re
 template <typename T>
 cudaError_t dropout_impl(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                          void* y, int64_t ldy, bool aligned, const Dropout& drop, cudaStream_t st) {
-  // Short rows are mostly ends and idle lanes: 16384 rows of 257 take 11.8 us here and 12.3 in the general form, of 65 7.4 and 5.0.
+  // Short rows are mostly ends and idle lanes: 16384 rows of 257 take 10.6 us here and 12.3 in the general form, of 65 7.4 and 5.0.
   if (!aligned && cols >= 256 && alike(rows, sizeof(T), x, ldx, residual, ldr, y, ldy)) {
     const bool deep = rows * cols > 8 * 152 * 2048;
     const int64_t runs = ceil_div(ceil_div(cols + 7, 8), deep ? 128 : 32);
