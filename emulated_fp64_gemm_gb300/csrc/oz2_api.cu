@@ -18,6 +18,7 @@
 
 #include "oz2_internal.cuh"
 #include "oz2_layers.cuh"
+#include "oz2_workspace.h"
 
 namespace oz2 {
 namespace {
@@ -207,8 +208,7 @@ constexpr int kMaxParts = 4;   // column parts of its first (and, host entry poi
 constexpr int kMaxTasks = kMaxBlocks + 2 * kMaxParts;  // GEMM launches
 
 struct Workspace {
-  size_t bytes = 0;
-  uint8_t* base = nullptr;
+  WorkspaceMemory memory;
   // second stream and events of the overlapped schedule (created on first use)
   cudaStream_t aux = nullptr;
   // the overlapped schedule's GEMM launches, at the device's greatest stream
@@ -243,11 +243,22 @@ Profile g_prof;
 std::map<int, DeviceState> g_dev;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 
+// While any stream is captured in the global mode, calls that allocate are refused
+// unless the thread asks for the relaxed one.  What the library allocates is not
+// recorded, so a capture may go on beside it.
+struct RelaxedCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  RelaxedCapture(const RelaxedCapture&) = delete;
+};
+
 oz2_status device_state(DeviceState** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return OZ2_ERR_CUDA;
   auto it = g_dev.find(dev);
   if (it == g_dev.end()) {
+    RelaxedCapture relaxed;
     DeviceState ds;
     int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
@@ -309,6 +320,7 @@ Layout make_layout(int64_t p, int64_t q, int64_t r, int s, int64_t qp, bool stag
 
 oz2_status workspace_sync_objects(Workspace& w) {
   if (w.aux) return OZ2_OK;
+  RelaxedCapture relaxed;
   if (cudaStreamCreateWithFlags(&w.aux, cudaStreamNonBlocking) != cudaSuccess) return OZ2_ERR_CUDA;
   if (cudaStreamCreateWithFlags(&w.up, cudaStreamNonBlocking) != cudaSuccess) return OZ2_ERR_CUDA;
   int least = 0, greatest = 0;
@@ -346,27 +358,40 @@ void destroy_sync_objects(Workspace& w) {
   }
 }
 
+struct DeviceMemory {
+  uint8_t* allocate(size_t bytes) const {
+    if (std::getenv("OZ2_FAIL_ALLOC") != nullptr) return nullptr;  // host-side fault injection
+    RelaxedCapture relaxed;
+    uint8_t* p = nullptr;
+    if (cudaMalloc(&p, bytes) == cudaSuccess) return p;
+    cudaGetLastError();
+    return nullptr;
+  }
+  bool synchronize() const {
+    if (cudaDeviceSynchronize() == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+  }
+  void release(uint8_t* p) const {
+    RelaxedCapture relaxed;
+    cudaFree(p);
+  }
+};
+
+bool is_capturing(cudaStream_t st) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &status) == cudaSuccess) return status != cudaStreamCaptureStatusNone;
+  cudaGetLastError();  // the legacy stream beside a blocking stream's capture: its launches are refused
+  return true;
+}
+
 oz2_status get_workspace(cudaStream_t st, size_t bytes, uint8_t** base, Workspace** wout = nullptr) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return OZ2_ERR_CUDA;
   Workspace& w = g_ws[std::make_pair(dev, st)];
   if (wout) *wout = &w;
-  if (w.bytes < bytes) {
-    if (w.base) {
-      cudaDeviceSynchronize();
-      cudaFree(w.base);
-      w.base = nullptr;
-      w.bytes = 0;
-    }
-    if (std::getenv("OZ2_FAIL_ALLOC") != nullptr) return OZ2_ERR_NO_MEMORY;  // host-side fault injection
-    if (cudaMalloc(&w.base, bytes) != cudaSuccess) {
-      cudaGetLastError();
-      w.base = nullptr;
-      return OZ2_ERR_NO_MEMORY;
-    }
-    w.bytes = bytes;
-  }
-  *base = w.base;
+  if (!workspace_reserve(w.memory, bytes, is_capturing(st), DeviceMemory{})) return OZ2_ERR_NO_MEMORY;
+  *base = w.memory.base;
   return OZ2_OK;
 }
 
@@ -946,7 +971,7 @@ void ozaki2_workspace_release(void) {
   for (auto& kv : g_ws) {
     cudaSetDevice(kv.first.first);
     cudaDeviceSynchronize();
-    if (kv.second.base) cudaFree(kv.second.base);
+    workspace_free(kv.second.memory, DeviceMemory{});
     destroy_sync_objects(kv.second);  // the second, upload and GEMM streams and their events
   }
   g_ws.clear();

@@ -38,6 +38,16 @@
  * Calls on the same stream are ordered; calls that share a stream's
  * workspace must not run concurrently from several host threads.
  *
+ * Graphs: a call on a stream that is being captured records the addresses of
+ * that stream's workspace.  Memory that a capture has recorded is not freed
+ * when the workspace grows, only by ozaki2_workspace_release, after which the
+ * graph must not be replayed.  During a capture a workspace may be made or
+ * grown too, without synchronising; what it outgrows is kept as well.  A
+ * replay uses the workspace of the stream that it was captured on: it must
+ * not overlap in time with calls on that stream or with replays of other
+ * graphs captured on it.  Capture on streams of their own what is to run at
+ * the same time.
+ *
  * Preconditions: finite inputs (an Inf/NaN entry gives an unspecified
  * result in its row of C / column of C), 2 <= s <= 20, and the inner
  * dimension within its mode's limit below.  The INT32 condition q < 131072
@@ -220,7 +230,10 @@ int ozaki2_moduli(int s, int32_t* out);
  */
 oz2_status ozaki2_last_error(void);
 
-/* Frees every workspace of every device (synchronises each device first). */
+/*
+ * Frees every workspace of every device (synchronises each device first),
+ * those that captured graphs use among them.
+ */
 void ozaki2_workspace_release(void);
 
 /* Static text for a status code. */

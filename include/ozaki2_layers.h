@@ -17,8 +17,10 @@
  * on `stream` and return without synchronising, argument errors come back
  * before anything is enqueued, intermediates live in the library's workspace
  * of that (device, stream) pair, and ozaki2_last_error reports a wait that
- * gave up.  A first call of each shape may allocate; later ones do not, and
- * can then be captured in a CUDA graph.
+ * gave up.  A first call of each shape on a stream may allocate; later ones
+ * do not.  Calls can be captured in CUDA graphs, which stay valid when the
+ * workspace grows, until ozaki2_workspace_release (see ozaki2.h on graphs
+ * that run at the same time).
  *
  * Arithmetic: products, sums, statistics and activations are held in 32 bits
  * and every output is rounded to its type once.  One intermediate is rounded
