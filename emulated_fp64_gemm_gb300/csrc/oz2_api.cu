@@ -998,18 +998,26 @@ oz2_status ozaki2_selftest_wait_timeout(int limit_us) {
   DeviceState* ds = nullptr;
   oz2_status e = device_state(&ds);
   if (e != OZ2_OK) return e;
-  int* err = nullptr;
-  if (cudaMalloc(&err, sizeof(int)) != cudaSuccess) return OZ2_ERR_NO_MEMORY;
-  cudaMemset(err, 0, sizeof(int));
-  if (launch_wait_timeout_selftest(err, static_cast<long long>(limit_us) * 1000, nullptr) != cudaSuccess ||
-      cudaDeviceSynchronize() != cudaSuccess) {
-    cudaFree(err);
-    return OZ2_ERR_CUDA;
+  constexpr size_t kMatrices = 2 * kSelftestRows * kSelftestRows * 2;
+  uint8_t* memory = nullptr;  // two matrices, then the error word
+  if (cudaMalloc(&memory, kMatrices + sizeof(int)) != cudaSuccess) return OZ2_ERR_NO_MEMORY;
+  cudaMemset(memory, 0, kMatrices);
+  DeviceResources res{nullptr, reinterpret_cast<int*>(memory + kMatrices), ds->num_sms, 0};
+  const int64_t limit_ns = static_cast<int64_t>(limit_us) * 1000;
+  e = OZ2_ERR_DEVICE_TIMEOUT;
+  if (cudaGetDevice(&res.device) != cudaSuccess) e = OZ2_ERR_CUDA;
+  for (int kernel = 0; kernel < 3 && e == OZ2_ERR_DEVICE_TIMEOUT; ++kernel) {
+    int v = 0;
+    const bool ran = cudaMemset(res.err, 0, sizeof(int)) == cudaSuccess &&
+                     (kernel == 0   ? launch_wait_timeout_selftest(res.err, limit_ns, nullptr)
+                      : kernel == 1 ? launch_linear_timeout_selftest(memory, limit_ns, res)
+                                    : launch_few_timeout_selftest(memory, limit_ns, res)) == cudaSuccess &&
+                     cudaDeviceSynchronize() == cudaSuccess &&
+                     cudaMemcpy(&v, res.err, sizeof(int), cudaMemcpyDeviceToHost) == cudaSuccess;
+    e = !ran ? OZ2_ERR_CUDA : (v & kErrTimeout) ? OZ2_ERR_DEVICE_TIMEOUT : OZ2_OK;
   }
-  int v = 0;
-  cudaMemcpy(&v, err, sizeof(int), cudaMemcpyDeviceToHost);
-  cudaFree(err);
-  return (v & kErrTimeout) ? OZ2_ERR_DEVICE_TIMEOUT : OZ2_OK;
+  cudaFree(memory);
+  return e;
 }
 
 }  // extern "C"

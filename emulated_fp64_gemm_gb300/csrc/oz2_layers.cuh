@@ -106,6 +106,13 @@ struct LinearPlan {
 cudaError_t launch_linear(const LinearPlan& plan, const Operand& a, const Operand& b, int64_t k, const Epilogue& ep,
                           oz2_dtype dtype, const DeviceResources& res, float* partial, cudaStream_t st);
 
+// One product of each form with operands of which half of every stage never
+// comes: all their waits run out after limit_ns, and both set *res.err.
+// memory: 2 x kSelftestRows^2 16-bit elements.
+constexpr int kSelftestRows = 512;
+cudaError_t launch_linear_timeout_selftest(void* memory, int64_t limit_ns, const DeviceResources& res);
+cudaError_t launch_few_timeout_selftest(void* memory, int64_t limit_ns, const DeviceResources& res);
+
 // Copies of 16-bit matrices whose rows are ld_out (a multiple of 8) elements apart, in one launch; rows may be 0.
 struct PackJob {
   int64_t rows, cols;

@@ -26,7 +26,7 @@
 // them, so the result does not depend on timing.
 //
 // Every wait is bounded in time; a timeout sets the device error word and the
-// kernel winds down.
+// kernel winds down, once its copies and MMAs in flight are done.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -67,6 +67,7 @@ struct GemmParams {
   bool lasting;  // many k blocks per pair: the form with more stages
   float* partial;  // [(tile - full) * splits + split][256][256]
   int* err;
+  uint64_t wait_ns;  // limit of each wait
 };
 
 struct Unit {
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
   uint64_t* empty = full + kStages;                                        // [kStages] in both CTAs
   uint64_t* acc_full = empty + kStages;                                    // [2] in both CTAs
   uint64_t* acc_empty = acc_full + 2;                                      // [2] used in the leader only
-  uint64_t* drain = acc_empty + 2;                                         // leader
+  uint64_t* drain = acc_empty + 2;                                         // leader, after a wait that gave up
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -305,11 +306,25 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      // Waits until every stage's last phase on these barriers is complete.
+      auto last_phases = [&](uint64_t* bars, volatile int* stop, uint64_t limit_ns) {
+        int s = stage;
+        uint32_t parity = phase ^ 1;
+#pragma unroll 1
+        for (int i = 0; i < kStages; ++i) {
+          if (!mbar_wait_bounded(smem_u32(&bars[s]), parity, stop, limit_ns)) return false;
+          if (++s == kStages) {
+            s = 0;
+            parity ^= 1;
+          }
+        }
+        return true;
+      };
       for (int u = pair; u < p.units && ok; u += pairs) {
         const Unit U = decode_unit(u, p);
         const int row_a = U.tm * 256 + static_cast<int>(rank) * 128, row_b = U.tn * 256 + static_cast<int>(rank) * 128;
         for (int kb = U.kb0; kb < U.kb1; ++kb) {
-          if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, kWaitLimitNs)) {
+          if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.wait_ns)) {
             ok = false;
             break;
           }
@@ -323,12 +338,15 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
           }
         }
       }
+      // The MMAs of the last stages are done, and their arrivals, which come from the leader, have reached this
+      // CTA before it ends; so have its copies, which the MMAs waited for.
+      if (ok) ok = last_phases(empty, abort_flag, p.wait_ns);
       if (!ok) {
         *abort_flag = 1;
         atomicOr(p.err, kErrTimeout);
-        // copies in flight land before the block ends
+        // copies in flight land before the block ends; the peer's are counted by the leader's barriers
         volatile int never = 0;
-        if (leader) mbar_wait_bounded(smem_u32(&full[(stage + kStages - 1) % kStages]), stage ? phase : phase ^ 1, &never, kDrainLimitNs);
+        if (leader) last_phases(full, &never, kDrainLimitNs); else pause_ns(kDrainLimitNs);
       }
     }
   } else if (warp == 1) {
@@ -345,14 +363,14 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
       for (int u = pair; u < p.units && ok; u += pairs, ++n) {
         const Unit U = decode_unit(u, p);
         const int slot = n & 1;
-        if (!mbar_wait_bounded(smem_u32(&acc_empty[slot]), ((n >> 1) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
+        if (!mbar_wait_bounded(smem_u32(&acc_empty[slot]), ((n >> 1) & 1) ^ 1, abort_flag, p.wait_ns)) {
           ok = false;
           break;
         }
         tc_fence_after();
         bool ready = mbar_try_wait(smem_u32(&full[stage]), phase);
         for (int kb = U.kb0; kb < U.kb1; ++kb) {
-          if (!ready && !mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, kWaitLimitNs)) {
+          if (!ready && !mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.wait_ns)) {
             ok = false;
             break;
           }
@@ -373,12 +391,16 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
         }
         if (ok) mma_commit_pair(smem_u32(&acc_full[slot]));
       }
+      // both accumulators have been read, and the peer's arrivals have reached this CTA before it ends
+      for (int i = 0; i < 2 && ok; ++i, ++n)
+        ok = mbar_wait_bounded(smem_u32(&acc_empty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag, p.wait_ns);
       if (!ok) {
         *abort_flag = 1;
         atomicOr(p.err, kErrTimeout);
+        volatile int never = 0;
+        mma_commit_pair_here(smem_u32(drain));
+        mbar_wait_bounded(smem_u32(drain), 0, &never, kDrainLimitNs);
       }
-      mma_commit_pair(smem_u32(drain));
-      mbar_wait_bounded(smem_u32(drain), 0, abort_flag, kWaitLimitNs);
     }
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
@@ -394,7 +416,7 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
       const Strip strip{static_cast<int64_t>(U.tm) * 256 + local_row, static_cast<int64_t>(U.tn) * 256 + part * S::COLS};
       ReadAhead ahead{};
       if (U.slot < 0) ahead.start<T>(p.ep, strip, lane);
-      const bool got = mbar_wait_bounded(smem_u32(&acc_full[slot]), (n >> 1) & 1, abort_flag, kWaitLimitNs);
+      const bool got = mbar_wait_bounded(smem_u32(&acc_full[slot]), (n >> 1) & 1, abort_flag, p.wait_ns);
       if (!__all_sync(0xffffffffu, got)) {  // warp-uniform: the tensor-memory loads below are .aligned
         ok = false;
         break;
@@ -431,7 +453,7 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
   let_successor_come();
   __syncwarp();
   if (warp == 0) cluster_wait();  // for the allocation, long done
-  cluster_sync_relaxed();  // the leader's MMAs are done with both CTAs' shared and tensor memory
+  cluster_sync_relaxed();  // all MMAs, copies and arrivals are done with both CTAs' shared and tensor memory
   if (warp == 1) tmem_dealloc_pair(*tmem_slot, 512);
 }
 
@@ -588,10 +610,31 @@ cudaError_t launch_linear(const LinearPlan& plan, const Operand& a, const Operan
   GemmParams p = make_params(k, ep, res.num_sms, &us);
   p.partial = partial;
   p.err = res.err;
+  p.wait_ns = kWaitLimitNs;
   CUtensorMap ma{}, mb{};
   if (k > 0 && (!make_map(&ma, a, ep.rows, k) || !make_map(&mb, b, ep.cols, k))) return cudaErrorInvalidValue;
   return dtype == OZ2_BF16 ? launch_typed<__nv_bfloat16>(a, b, ma, mb, p, res, st)
                            : launch_typed<__half>(a, b, ma, mb, p, res, st);
+}
+
+cudaError_t launch_linear_timeout_selftest(void* memory, int64_t limit_ns, const DeviceResources& res) {
+  constexpr int kRows = kSelftestRows;
+  Epilogue ep{};
+  ep.y = static_cast<uint8_t*>(memory) + kRows * kRows * 2;
+  ep.ldy = ep.rows = ep.cols = kRows;
+  ep.vec = 1;
+  GemmParams p{};
+  p.ep = ep;
+  p.tiles_m = p.tiles_n = kRows / 256;
+  p.nkb = kRows / kBK;
+  p.group = 4;
+  p.full = p.units = p.tiles_m * p.tiles_n;
+  p.err = res.err;
+  p.wait_ns = static_cast<uint64_t>(limit_ns);
+  CUtensorMap whole, half;
+  if (!encode_map_2d(&whole, memory, kRows, kRows, kRows, kBK, 128) || !encode_map_2d(&half, memory, kRows, kRows, kRows, kBK, 64))
+    return cudaErrorInvalidValue;
+  return launch_shape<__nv_bfloat16, false, false, OZ2_ACT_NONE, 16>(half, whole, p, res, nullptr);
 }
 
 }  // namespace oz2

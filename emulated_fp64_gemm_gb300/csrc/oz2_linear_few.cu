@@ -13,7 +13,7 @@
 // launch, no workspace, and no result that depends on timing.
 //
 // Every wait is bounded in time; a timeout sets the device error word and the
-// kernel winds down.
+// kernel winds down, once its copies and MMAs in flight are done.
 #include <algorithm>
 #include <type_traits>
 
@@ -43,6 +43,7 @@ struct FewParams {
   int nkb, tiles_n;
   int log_ranks;  // CTAs per cluster: 1 << log_ranks
   int* err;
+  uint64_t wait_ns;  // limit of each wait
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -141,22 +142,17 @@ __device__ __forceinline__ void few_cta(const CUtensorMap& map_x, const CUtensor
   uint4 bias = read_bias8<T>(p.ep, item < end ? item_col(item) : p.ep.cols);
   uint4 residual = read_residual8<T>(p.ep, item < end ? item_row(item) : p.ep.rows, item_col(item));
 
+  int issued = ahead;  // stages, by thread 0
   if (warp == 0) {
     if (lane == 0) {
-      int issued = ahead;
       for (int kb = kb0 + ahead; kb < kb1; ++kb, ++issued) {
         const int stage = issued % F::STAGES;
-        if (!mbar_wait_bounded(smem_u32(&empty[stage]), (issued / F::STAGES - 1) & 1, abort_flag, kWaitLimitNs)) {
+        if (!mbar_wait_bounded(smem_u32(&empty[stage]), (issued / F::STAGES - 1) & 1, abort_flag, p.wait_ns)) {
           *abort_flag = 1;
           atomicOr(p.err, kErrTimeout);
           break;
         }
         load_stage(stage, kb);
-      }
-      if (*abort_flag) {  // copies in flight land before the block ends
-        volatile int never = 0;
-        for (int i = max(0, issued - F::STAGES); i < issued; ++i)
-          mbar_wait_bounded(smem_u32(&full[i % F::STAGES]), (i / F::STAGES) & 1, &never, kDrainLimitNs);
       }
     }
   } else if (warp == 1) {
@@ -167,7 +163,7 @@ __device__ __forceinline__ void few_cta(const CUtensorMap& map_x, const CUtensor
                                  (static_cast<uint32_t>(X_ROWS) << 16) | (static_cast<uint32_t>(MP >> 3) << 17) | ((128u >> 4) << 24);
       for (int i = 0; i < kb1 - kb0; ++i) {
         const int stage = i % F::STAGES;
-        if (!mbar_wait_bounded(smem_u32(&full[stage]), (i / F::STAGES) & 1, abort_flag, kWaitLimitNs)) {
+        if (!mbar_wait_bounded(smem_u32(&full[stage]), (i / F::STAGES) & 1, abort_flag, p.wait_ns)) {
           *abort_flag = 1;
           atomicOr(p.err, kErrTimeout);
           break;
@@ -177,17 +173,26 @@ __device__ __forceinline__ void few_cta(const CUtensorMap& map_x, const CUtensor
 #pragma unroll
         for (int s = 0; s < kBK / 16; ++s)
           mma_f16(tmem, operand_desc<W_ROWS>(w, s), operand_desc<X_ROWS>(x, s), idesc, i == 0 && s == 0 ? 0u : 1u);
-        mma_commit(smem_u32(&empty[stage]));
+        if (i + F::STAGES < kb1 - kb0) mma_commit(smem_u32(&empty[stage]));  // only where a load waits for it
       }
       mma_commit(smem_u32(done));
     }
   }
   __syncwarp();
-  if (!mbar_wait_bounded(smem_u32(done), 0, abort_flag, kWaitLimitNs)) {
+  if (!mbar_wait_bounded(smem_u32(done), 0, abort_flag, p.wait_ns)) {
     *abort_flag = 1;
     atomicOr(p.err, kErrTimeout);
   }
   __syncthreads();
+  if (*abort_flag) {  // a wait gave up: what is in flight lands before its place is used again
+    if (threadIdx.x == 0) {
+      volatile int never = 0;
+      bool landed = mbar_wait_bounded(smem_u32(done), 0, &never, kDrainLimitNs);
+      for (int i = max(0, issued - F::STAGES); i < issued && landed; ++i)
+        landed = mbar_wait_bounded(smem_u32(&full[i % F::STAGES]), (i / F::STAGES) & 1, &never, kDrainLimitNs);
+    }
+    __syncthreads();
+  }
   tc_fence_after();
   let_successor_come();
   // Every MMA and so every load is done: the sums take the stages' place, as [row of A][row of B].  A row's groups of
@@ -307,6 +312,7 @@ FewParams make_params(const Epilogue& ep, int64_t k, int ranks, const DeviceReso
   p.tiles_n = static_cast<int>(ceil_div(ep.cols, kTileN));
   p.log_ranks = ranks == 8 ? 3 : ranks == 4 ? 2 : ranks - 1;
   p.err = res.err;
+  p.wait_ns = kWaitLimitNs;
   return p;
 }
 
@@ -401,6 +407,21 @@ cudaError_t launch_few_pair(const FewPlan& plan, const Operand& dz, const Operan
   const FewParams dx = make_params(ep_dx, ep_dw.rows, plan.ranks, res), dw = make_params(ep_dw, ep_dx.rows, plan.ranks, res);
   return dtype == OZ2_BF16 ? launch_pair_typed<__nv_bfloat16>(dz, w, x, dx, dw, plan.ranks, res, st)
                            : launch_pair_typed<__half>(dz, w, x, dx, dw, plan.ranks, res, st);
+}
+
+cudaError_t launch_few_timeout_selftest(void* memory, int64_t limit_ns, const DeviceResources& res) {
+  constexpr int kRows = kSelftestRows, kRanks = 2;
+  Epilogue ep{};
+  ep.y = static_cast<uint8_t*>(memory) + kRows * kRows * 2;
+  ep.ldy = ep.cols = kRows;
+  ep.rows = 16;
+  ep.vec = 1;
+  FewParams p = make_params(ep, kRows, kRanks, res);
+  p.wait_ns = static_cast<uint64_t>(limit_ns);
+  CUtensorMap whole, half;
+  if (!encode_map_2d(&whole, memory, kRows, 16, kRows, kBK, 16) || !encode_map_2d(&half, memory, kRows, kRows, kRows, kBK, kTileN / 2))
+    return cudaErrorInvalidValue;
+  return launch_few_impl<__nv_bfloat16, 16, false, false>(whole, half, p, p.tiles_n * kRanks, kRanks, res, nullptr);
 }
 
 }  // namespace oz2

@@ -72,6 +72,17 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a, uint64
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
+// Arrives on this CTA's barrier once every MMA issued so far is done.
+__device__ __forceinline__ void mma_commit_pair_here(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Lets time pass, for what is in flight and no barrier of this CTA shows: after a wait that gave up.
+__device__ __forceinline__ void pause_ns(uint64_t ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < ns) __nanosleep(1000);
+}
+
 // Arrives on the barrier at this offset in both CTAs once every MMA issued so far is done.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
   asm volatile(

@@ -241,10 +241,11 @@ const char* ozaki2_status_string(oz2_status status);
 
 /*
  * Self-test of the bounded-wait machinery: launches one block that waits on
- * a barrier nothing completes, with a wait limit of about `limit_us`
- * microseconds (1..1000000).  It returns OZ2_ERR_DEVICE_TIMEOUT when the
- * wait gave up as designed and the kernel exited cleanly, OZ2_OK if it did
- * not (a bug), or OZ2_ERR_CUDA.  Synchronises the device.
+ * a barrier nothing completes, then one product of each form of
+ * ozaki2_linear whose operands never arrive whole, with wait limits of about
+ * `limit_us` microseconds (1..1000000).  It returns OZ2_ERR_DEVICE_TIMEOUT
+ * when every wait gave up as designed and the kernels exited cleanly, OZ2_OK
+ * if one did not (a bug), or OZ2_ERR_CUDA.  Synchronises the device.
  */
 oz2_status ozaki2_selftest_wait_timeout(int limit_us);
 
