@@ -211,6 +211,7 @@ __device__ __forceinline__ void few_cta(const CUtensorMap& map_x, const CUtensor
       if (c + i < rows) sums[(c + i) * kTileN + place] = __uint_as_float(v[i]);
   }
   tc_fence_before();
+  __syncwarp();
   if (ranks > 1) cluster_sync_all(); else __syncthreads();
   // This code runs once per CTA, from a cold instruction cache: it is kept short, not unrolled over groups.
   T* y_out = reinterpret_cast<T*>(smem + MP * kTileN * 4);  // for rows off 16-byte boundaries: y, then z
@@ -261,6 +262,7 @@ __device__ __forceinline__ void few_cta(const CUtensorMap& map_x, const CUtensor
       if (p.ep.z) static_cast<T*>(p.ep.z)[row * p.ep.ldz + col] = z_out[e];
     }
   }
+  __syncwarp();  // lanes leave the loops above at different times; the cluster barrier is a whole warp's
   if (ranks > 1) cluster_sync_relaxed(); else __syncthreads();  // the peers have read this CTA's sums
   if (warp == 1) {
     __syncwarp();
