@@ -45,7 +45,8 @@ struct Epilogue {
   int64_t ldr, ldy, ldz;
   int64_t rows, cols;
   int act;
-  int vec;  // rows of every matrix start on 16-byte boundaries (and bias does)
+  int vec;      // rows of every matrix start on 16-byte boundaries (and bias does)
+  float scale;  // of the sums, before anything else
   Dropout drop;
 };
 
@@ -126,9 +127,17 @@ cudaError_t launch_pack(const PackJob& a, const PackJob& b, cudaStream_t st);
 cudaError_t launch_dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                            void* y, int64_t ldy, oz2_dtype dtype, const Dropout& drop, cudaStream_t st);
 
-// dz = act'(preact) * keep * dy / (1 - p) into dz (null: not written) and its
-// column sums into dbias (null: not formed), through `partial`: dz_partial_rows
-// x n floats, null for one row.
+// dz = act'(preact) * keep * dy / (1 - p) is stored as an operand of two products
+// without its constant factor, which their epilogues apply to the sums (`scale`):
+// the dropout's 1 / (1 - p) and, in float16 for the activations whose slope passes 1
+// (1.129 at most), the inverse of 7/8.  So no finite float16 dy gives an infinite
+// operand.  It costs 0.1 to 0.4 us of a small layer's 15 (517 x 1024 x 1531).
+constexpr float dz_factor(int act, bool f16) {
+  return f16 && (act == OZ2_ACT_SILU || act == OZ2_ACT_GELU || act == OZ2_ACT_GELU_TANH) ? 0.875f : 1.0f;
+}
+
+// That form of dz into dz (null: not written), and dz's column sums into dbias
+// (null: not formed), through `partial`: dz_partial_rows x n floats, null for one row.
 int64_t dz_partial_rows(int64_t m, int64_t n);
 struct DzArgs {
   int64_t m, n;
@@ -141,6 +150,7 @@ struct DzArgs {
   void* dbias;
   float* partial;
   int act;
+  float scale;  // from the stored form to dz
   Dropout drop;
 };
 cudaError_t launch_dz(const DzArgs& a, oz2_dtype dtype, cudaStream_t st);
@@ -294,12 +304,13 @@ __device__ __forceinline__ uint4 philox7(uint32_t c0, uint32_t c1, uint32_t c2, 
 __device__ __forceinline__ uint4 draws8(const Dropout& d, uint32_t row, uint32_t g) {
   return philox7(g, row, d.offset0, d.offset1, d.seed0, d.seed1);
 }
+template <bool SCALED = true>
 __device__ __forceinline__ void drop8(const Dropout& d, const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = (w[i] << 16) > d.limit ? v[2 * i] * d.scale : 0.0f;
-    v[2 * i + 1] = w[i] > d.limit ? v[2 * i + 1] * d.scale : 0.0f;
+    v[2 * i] = (w[i] << 16) > d.limit ? (SCALED ? v[2 * i] * d.scale : v[2 * i]) : 0.0f;
+    v[2 * i + 1] = w[i] > d.limit ? (SCALED ? v[2 * i + 1] * d.scale : v[2 * i + 1]) : 0.0f;
   }
 }
 
@@ -423,6 +434,10 @@ __device__ __forceinline__ void add8(uint4 u, float (&v)[8]) {
     v[2 * i + 1] += f.y;
   }
 }
+__device__ __forceinline__ void scale8(float scale, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= scale;
+}
 template <typename T>
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]), Elem<T>::pack(v[4], v[5]), Elem<T>::pack(v[6], v[7]));
@@ -443,7 +458,7 @@ __device__ __forceinline__ uint4 read_residual8(const Epilogue& e, int64_t row, 
   return load8_raw(static_cast<const T*>(e.residual) + row * e.ldr + col, e.vec && left >= 8,
                    left < 8 ? static_cast<int>(left) : 8);
 }
-// Everything after the product, in 32 bits: v becomes y (to be rounded once), the return value is z, rounded.
+// Everything after the product, which has e.scale in it, in 32 bits: v becomes y (to be rounded once), the return value is z, rounded.
 // act: e.act, or a constant that leaves the other activations' code out.
 template <typename T>
 __device__ __forceinline__ uint4 finish8(const Epilogue& e, int act, int64_t row, int64_t col, uint4 bias, uint4 residual,

@@ -87,6 +87,7 @@ oz2_status linear(const oz2_linear_args& a, cudaStream_t st) {
   ep.rows = a.m;
   ep.cols = a.n;
   ep.act = a.act;
+  ep.scale = 1.0f;
   ep.drop = make_dropout(a.dropout, a.seed, a.offset);
   ep.vec = groups_aligned(a.y, a.ldy, dtype) && (!a.bias || groups_aligned(a.bias, 0, dtype)) &&
            (!a.residual || groups_aligned(a.residual, a.ldr, dtype)) && (!a.preact || groups_aligned(a.preact, a.ldz, dtype));
@@ -103,10 +104,11 @@ oz2_status linear(const oz2_linear_args& a, cudaStream_t st) {
   return OZ2_OK;
 }
 
-// A plain product into out (no bias, activation, dropout or residual).
-Epilogue plain_epilogue(void* out, int64_t ld, int64_t rows, int64_t cols, oz2_dtype dtype) {
+// A plain product, times scale, into out (no bias, activation, dropout or residual).
+Epilogue plain_epilogue(void* out, int64_t ld, int64_t rows, int64_t cols, float scale, oz2_dtype dtype) {
   Epilogue ep{};
   ep.y = out;
+  ep.scale = scale;
   ep.ldy = ld;
   ep.rows = rows;
   ep.cols = cols;
@@ -139,7 +141,8 @@ oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
   const int64_t sum_rows = dz_partial_rows(m, n);
   const size_t sums_at = c.take(dbias && sum_rows > 1 ? static_cast<size_t>(sum_rows) * n * 4 : 0);
   Input xi(a.x, m, k, a.ldx, dw, c), wi(a.w, n, k, a.ldw, dx, c);
-  const Epilogue ep_dx = plain_epilogue(dx, a.lddx, m, k, dtype), ep_dw = plain_epilogue(dw, a.lddw, n, k, dtype);
+  const float scale = drop.scale / dz_factor(a.act, dtype == OZ2_F16);  // 1 where dz is dy itself
+  const Epilogue ep_dx = plain_epilogue(dx, a.lddx, m, k, scale, dtype), ep_dw = plain_epilogue(dw, a.lddw, n, k, scale, dtype);
   // the two products run side by side where they are small; else one after the other, and share the room for partial sums
   LinearPlan plan_dx, plan_dw;
   FewPlan pair{};
@@ -163,6 +166,7 @@ oz2_status linear_backward(const oz2_linear_backward_args& a, cudaStream_t st) {
     d.dbias = dbias;
     d.partial = sum_rows > 1 ? reinterpret_cast<float*>(res.workspace + sums_at) : nullptr;
     d.act = a.act;
+    d.scale = scale;
     d.drop = drop;
     OZ2_TRY(launch_dz(d, dtype, st));
   }

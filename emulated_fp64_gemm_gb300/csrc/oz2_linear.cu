@@ -172,6 +172,7 @@ __device__ __forceinline__ void finish_whole_block(const Epilogue& e, const floa
   for (int i = 0; i < 4; ++i, row += 8, from += 8 * 32) {
     const float4 lo = *reinterpret_cast<const float4*>(from + chunk), hi = *reinterpret_cast<const float4*>(from + (chunk ^ 4));
     float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (e.scale != 1.0f) scale8(e.scale, v);
     if (e.bias) add8<T>(bias, v);
     if (e.z) {
       *reinterpret_cast<uint4*>(z) = pack8<T>(v);
@@ -208,6 +209,7 @@ __device__ __forceinline__ void finish_block(const Epilogue& e, float* tile, int
     float v[8];
     get_eight(tile, r, g, v);
     const uint4 residual = in.next_residual<T, STEPS>(e, s, lane, i);
+    if (e.scale != 1.0f) scale8(e.scale, v);
     const uint4 z = finish8<T>(e, ACT, row, col, bias, residual, v);
     if (e.vec) {
       if (row < e.rows && col < e.cols) {
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     float add[8];
     load8(at, true, 8, add);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += add[i];
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(add[i], e.scale, v[i]);
   }
   const uint4 z = finish8<T>(e, e.act, r, c, bias, residual, v);
   if (e.vec) {
@@ -623,6 +625,7 @@ cudaError_t launch_linear_timeout_selftest(void* memory, int64_t limit_ns, const
   ep.y = static_cast<uint8_t*>(memory) + kRows * kRows * 2;
   ep.ldy = ep.rows = ep.cols = kRows;
   ep.vec = 1;
+  ep.scale = 1.0f;
   GemmParams p{};
   p.ep = ep;
   p.tiles_m = p.tiles_n = kRows / 256;

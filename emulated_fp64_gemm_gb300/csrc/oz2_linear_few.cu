@@ -236,7 +236,7 @@ __device__ __forceinline__ void few_cta(const CUtensorMap& map_x, const CUtensor
       for (int s = 0; s < 4; ++s) {
         if (s0 + s >= ranks) break;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += add[s][e];
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(add[s][e], p.ep.scale, v[e]);
       }
     }
     const uint4 z = finish8<T>(p.ep, p.ep.act, row, col, bias, residual, v);
@@ -418,6 +418,7 @@ cudaError_t launch_few_timeout_selftest(void* memory, int64_t limit_ns, const De
   ep.ldy = ep.cols = kRows;
   ep.rows = 16;
   ep.vec = 1;
+  ep.scale = 1.0f;
   FewParams p = make_params(ep, kRows, kRanks, res);
   p.wait_ns = static_cast<uint64_t>(limit_ns);
   CUtensorMap whole, half;

@@ -4,6 +4,7 @@
 // vector of a 16-bit type and one call of the generator.
 #include <algorithm>
 #include <array>
+#include <type_traits>
 
 #include "oz2_layers.cuh"
 
@@ -282,6 +283,7 @@ cudaError_t launch_parts(const PackPart& a, const PackPart& b, cudaStream_t st) 
 // timing (with one strip of rows they go to dbias at once).  Bound by HBM: dy and z read, dz written once.
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256, 4) dz_kernel(const __grid_constant__ DzArgs a, bool aligned, int rows) {
+  constexpr float kFactor = dz_factor(ACT, std::is_same<T, __half>::value);
   __shared__ float sums[8][256];
   wait_for_predecessor();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -318,8 +320,9 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const __grid_constant__ DzAr
           float z[8];
           values8<T>(&zs[u], z);
           activate_grad8(ACT, z, g);
+          if (kFactor != 1.0f) scale8(kFactor, g);
         }
-        if (a.drop.threshold) drop8(a.drop, row + u * 8, static_cast<uint32_t>(col >> 3), g);
+        if (a.drop.threshold) drop8<false>(a.drop, draws8(a.drop, row + u * 8, static_cast<uint32_t>(col >> 3)), g);
         if (a.dz) {
           *reinterpret_cast<uint4*>(dz) = pack8<T>(g);
           dz += 8 * a.lddz;
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const __grid_constant__ DzAr
   let_successor_come();
   if (!a.dbias) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sums[warp][lane * 8 + e] = sum[e];
+  for (int e = 0; e < 8; ++e) sums[warp][lane * 8 + e] = sum[e] * a.scale;
   __syncthreads();
   const int64_t c = blockIdx.x % strips * 256 + threadIdx.x;
   if (c < a.n) {

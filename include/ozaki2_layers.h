@@ -25,7 +25,10 @@
  * Arithmetic: products, sums, statistics and activations are held in 32 bits
  * and every output is rounded to its type once.  One intermediate is rounded
  * to 16 bits: the gradient dz of linear_backward, as an operand of its two
- * tensor-core products.  No result depends on the order of atomics; equal
+ * tensor-core products.  It is rounded without the dropout's scale, and in
+ * float16 times a factor that keeps it below dy where the activation's slope
+ * passes 1; both are made up for in the products' 32-bit sums, so that a
+ * finite dy never overflows on the way.  No result depends on the order of atomics; equal
  * calls give equal bits.
  *
  * Dropout mask: never stored, a function of (row, column, seed, offset).

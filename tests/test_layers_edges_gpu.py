@@ -3,9 +3,11 @@ the types' ranges, activations' tails, positions out of range, and what autograd
 import pytest
 
 torch = pytest.importorskip("torch")
+from tests._layers_ref import TINY, UNIT, act, assert_within, keep_mask, slope  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+SEED, OFFSET = 0x1234567890ABCDEF, 0x0FEDCBA987654321
 
 
 @pytest.fixture(scope="module")
@@ -38,3 +40,54 @@ def test_product_kernels_wind_down_when_their_operands_never_come(oz2, limit_us)
     assert oz2.last_error() == 0
     for _ in range(3):
         assert torch.equal(oz2.linear(x, w), want) and torch.equal(oz2.linear(few, w), want_few)
+
+
+# ------------------------------------------------------------------ the ends of the types' ranges
+def check_backward(oz2, dy, x, w, z, activation, p, seed, offset):
+    """dx and dw against the 64-bit definition.
+
+    With u half an ulp of the type: dz is rounded to it once, without the
+    dropout's scale (relative u, and at most half the least subnormal times that
+    scale and the activations' common factor, together below 4 for these p); its
+    slope is off by 2^-17 (1 + |z|); sums of t products in 32 bits by (t + 8)
+    2^-23 of their magnitudes; the outputs are rounded once."""
+    dtype, u, tiny = dy.dtype, UNIT[dy.dtype], TINY[dy.dtype]
+    (m, n), k = dy.shape, x.shape[1]
+    dx, dw, db = oz2.linear_backward(dy, x, w, preact=z, activation=activation, dropout=p, seed=seed, offset=offset)
+    dz, err = dy.double(), torch.zeros(m, n, dtype=torch.float64, device="cuda")
+    if z is not None:
+        if activation != "relu":
+            err = dz.abs() * 2.0**-17 * (1 + z.double().abs())
+        dz = dz * slope(z.double(), activation)
+    if p:
+        keep, scale = keep_mask(m, n, p, seed, offset)
+        dz, err = (torch.where(keep.cuda(), v * scale, 0.0) for v in (dz, err))
+    err = err + (u + 2.0**-22) * (dz.abs() + err) + 4 * tiny
+    for name, got, a, e, b, terms in (("dx", dx, dz, err, w.double(), n), ("dw", dw, dz.t(), err.t(), x.double(), m)):
+        value, bound = a @ b, (e + (terms + 8) * 2.0**-23 * (a.abs() + e)) @ b.abs()
+        assert_within(got, value, bound + u * (value.abs() + bound) + tiny, name)
+    return dx, dw, db
+
+
+@pytest.mark.parametrize("m,k,n", [(40, 72, 96), (150, 136, 264), (700, 520, 1032)])
+@pytest.mark.parametrize("activation,p,top", [("none", 0.5, 6e4), ("relu", 0.75, 6e4), ("silu", 0.5, 6.5e4), ("gelu", 0.0, 6.55e4),
+                                              ("gelu_tanh", 0.1, 6.55e4)])
+def test_backward_of_gradients_near_the_largest_float16(oz2, m, k, n, activation, p, top):
+    # dz itself passes the largest float16 (by the dropout's scale, by the activation's slope up to 1.13), the gradients do not
+    dy = (torch.rand(m, n, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") * 0.05 + 0.95) * top
+    dy = (dy * torch.where(torch.arange(n, device="cuda") % 2 == 0, 1.0, -1.0)).to(F16)
+    z = (1.0 + normal(m, n, dtype=F32, seed=2).abs()).to(F16)  # slopes around their largest
+    x, w = normal(m, k, dtype=F16, seed=3, scale=2.0**-14), normal(n, k, dtype=F16, seed=4, scale=2.0**-10)
+    x[0, 0], w[0, 0] = 0.0, 0.0
+    dx, dw, db = check_backward(oz2, dy, x, w, None if activation == "none" else z, activation, p, SEED, OFFSET)
+    assert bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dw).all())
+    # (dbias passes the range in its own right: its sums are the definition's)
+
+
+@pytest.mark.parametrize("p", [0.0, 0.5])
+def test_backward_of_gradients_near_the_least_float16(oz2, p):
+    # dz of subnormal size: off by half the least subnormal where it is rounded, no more
+    m, k, n = 130, 64, 200
+    dy, z = normal(m, n, dtype=F16, scale=2.0**-17), normal(m, n, dtype=F16, seed=2)
+    x, w = normal(m, k, dtype=F16, seed=3, scale=64.0), normal(n, k, dtype=F16, seed=4, scale=64.0)
+    check_backward(oz2, dy, x, w, z, "silu", p, SEED, OFFSET)
