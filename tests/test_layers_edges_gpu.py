@@ -1,9 +1,11 @@
 """The layer operators where they leave the ordinary path: waits that run out, the ends of
 the types' ranges, activations' tails, positions out of range, and what autograd is told."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
-from tests._layers_ref import TINY, UNIT, act, assert_within, keep_mask, slope  # noqa: E402
+from tests._layers_ref import TINY, UNIT, assert_within, keep_mask, slope  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -91,3 +93,69 @@ def test_backward_of_gradients_near_the_least_float16(oz2, p):
     dy, z = normal(m, n, dtype=F16, scale=2.0**-17), normal(m, n, dtype=F16, seed=2)
     x, w = normal(m, k, dtype=F16, seed=3, scale=64.0), normal(n, k, dtype=F16, seed=4, scale=64.0)
     check_backward(oz2, dy, x, w, z, "silu", p, SEED, OFFSET)
+
+
+# ------------------------------------------------------------------ activations over every finite value
+C2, A3 = 2 * math.sqrt(2 / math.pi), 0.044715
+
+
+def every_value(dtype):
+    bits = torch.arange(-32768, 32768, device="cuda").to(torch.int16)
+    v = bits.view(dtype)
+    return v[torch.isfinite(v)].reshape(-1, 1)
+
+
+def exact_activation(z, name):
+    """act(z), act'(z), the size of the slope's terms, and the size of the exponent that their tails are made by.
+
+    All are free of cancellation in the tails.  For large z the factor is exactly
+    1 in 32 bits, so that the sizes stop growing there."""
+    if name == "relu":
+        return z.clamp(min=0), (z > 0).double(), torch.ones_like(z), torch.zeros_like(z)
+    if name == "gelu":
+        cdf = 0.5 * torch.special.erfc(-z * math.sqrt(0.5))
+        bell = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        return z * cdf, cdf + z * bell, cdf + z.abs() * bell, z.clamp(max=6)**2
+    if name == "silu":
+        s, near = torch.sigmoid(z), z.clamp(max=20)
+        return z * s, s + z * s * torch.sigmoid(-z), s * (1 + near.abs()), near.abs()
+    near = z.clamp(max=5.1)
+    argument, limited = C2 * (z + A3 * z**3), C2 * (near + A3 * near**3).abs()
+    s, g, g_near = torch.sigmoid(argument), C2 * (1 + 3 * A3 * z * z), C2 * (1 + 3 * A3 * near * near)
+    # far out g times sigmoid(-argument) would be infinity times zero
+    bend = torch.where(argument.abs() > 700, 0.0, z * s * torch.sigmoid(-argument) * g)
+    return z * s, s + bend, torch.where(argument < -700, 0.0, s * (1 + near.abs() * g_near)), limited
+
+
+@pytest.mark.parametrize("activation", ["relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_activations_relatively_over_every_finite_value(oz2, activation, dtype):
+    """A product with 1 is exact, so what is left is the activation and one rounding.
+
+    Its factor is off by at most 2^-18 relatively (a fit of 2^-20.3, a dozen
+    roundings of 2^-24, the approximate exponential and reciprocal of 2^-22),
+    and by the exponent's own roundings: at most eight of 2^-24 times its size.
+    Factors below the least normal number, 2^-126, come out as zero."""
+    u, tiny = UNIT[dtype], TINY[dtype]
+    x = every_value(dtype)
+    z = x.double()
+    want, rise, terms, exponent = exact_activation(z, activation)
+    rel = 0.0 if activation == "relu" else 2.0**-18 + exponent * 2.0**-21
+    one = torch.ones(1, 1, dtype=dtype, device="cuda")
+    y = oz2.linear(x, one, activation=activation)
+    assert_within(y, want, (rel + u * (1 + rel)) * want.abs() + tiny + z.abs() * 2.0**-126, "value")
+    # the slopes through dz and the product with 1: two roundings, the first of dz or of 7/8 of it
+    dx, _, _ = oz2.linear_backward(torch.ones_like(x), x, one, preact=x, activation=activation, need_dw=False, need_dbias=False)
+    err = rel * terms + (1 + z.abs() * C2 * (1 + 3 * A3 * z * z)).clamp(max=2.0**30) * 2.0**-126
+    assert_within(dx, rise, err + 2.1 * u * (rise.abs() + err) + 2.2 * tiny, "slope")
+
+
+def test_gelu_tail_relatively(oz2):
+    # 32-bit sums between the 16-bit values: z = x w, -12 to 12, against the distribution function's own tail
+    x = torch.linspace(-12, 12, 4001, device="cuda").to(BF16).reshape(-1, 1)
+    w = (1 + torch.arange(64, device="cuda") / 256.0).clamp(max=1.25).to(BF16).reshape(-1, 1)
+    z = x.double() @ w.double().t()
+    want, _, _, exponent = exact_activation(z, "gelu")
+    rel = 2.0**-18 + (exponent + 1) * 2.0**-21
+    # (the product is exact: both have eight significant bits)
+    assert_within(oz2.linear(x, w, activation="gelu"), want, (rel + UNIT[BF16] * (1 + rel)) * want.abs() + TINY[BF16] + z.abs() * 2.0**-126)
