@@ -154,7 +154,8 @@ __device__ __forceinline__ bool whole_block(const Epilogue& e, const Strip& s, i
 // 8100), with gelu, dropout and residual 13400 (15300, 13200); by finish_block,
 // which tests every lane in every step, 7100, 12300 and 19800.  Eight warps, which
 // finish a tile behind the next one's product, do without it: there it cost dw of
-// 8192 x 4096 x 16384 two percent and dx half of one, and won one with a residual.
+// 8192 x 4096 x 16384 two percent and dx half of one, and won one with a residual
+// (of which finish_block has won half by now, reading it once).
 template <typename T, int ACT, int STEPS>
 __device__ __forceinline__ void finish_whole_block(const Epilogue& e, const float* tile, int lane, const Strip& s, int b,
                                                    ReadAhead& in) {
@@ -193,13 +194,14 @@ __device__ __forceinline__ void finish_whole_block(const Epilogue& e, const floa
   }
 }
 // The same for any block.
-template <typename T, int ACT, int STEPS>
+template <typename T, int ACT, int WARPS>
 __device__ __forceinline__ void finish_block(const Epilogue& e, float* tile, int lane, const Strip& s, int b, ReadAhead& in) {
+  constexpr int STEPS = Shape<WARPS>::STEPS;
   const int g = lane & 3;
   const uint4 bias = in.bias;
-  if (e.residual && e.vec && b > 0) {  // the block before may have been a whole one, which did not read ahead
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) in.next_residual<T, STEPS>(e, s, lane, 4 * b + i - 4);
+  if (WARPS == 16 && e.residual && b > 0 && whole_block(e, s, b - 1)) {  // which did not read ahead
+#pragma unroll
+    for (int i = 0; i < 4; ++i) in.residual[i] = read_residual8<T>(e, s.row(4 * b + i, lane), s.col(4 * b + i, lane));
   }
   if (4 * b + 4 < STEPS) in.bias = read_bias8<T>(e, s.col(4 * b + 4, lane));
 #pragma unroll 1
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(Shape<WARPS>::THREADS, 1)
         else if (WARPS == 16 && whole_block(p.ep, strip, cb))
           finish_whole_block<T, ACT, S::STEPS>(p.ep, tile, lane, strip, cb, ahead);
         else
-          finish_block<T, ACT, S::STEPS>(p.ep, tile, lane, strip, cb, ahead);
+          finish_block<T, ACT, WARPS>(p.ep, tile, lane, strip, cb, ahead);
         __syncwarp();
       }
     }

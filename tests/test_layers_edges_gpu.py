@@ -159,3 +159,17 @@ def test_gelu_tail_relatively(oz2):
     rel = 2.0**-18 + (exponent + 1) * 2.0**-21
     # (the product is exact: both have eight significant bits)
     assert_within(oz2.linear(x, w, activation="gelu"), want, (rel + UNIT[BF16] * (1 + rel)) * want.abs() + TINY[BF16] + z.abs() * 2.0**-126)
+
+
+# ------------------------------------------------------------------ residuals of long products
+@pytest.mark.parametrize("m,n", [(4133, 4104), (4352, 4360), (700, 1032)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_residual_of_long_products_with_ragged_ends(oz2, m, n, in_place):
+    # more than 256 k blocks per pair of SMs (the form with fewer epilogue warps), and fewer; blocks past the rows' and columns' ends
+    k = 4352
+    x, w, r = normal(m, k), normal(n, k, seed=1, scale=k**-0.5), normal(m, n, seed=2)
+    z = x.double() @ w.double().t()
+    want = z.clamp(min=0) + r.double()
+    err = 1.2 * (k + 8) * 2.0**-23 * (x.double().abs() @ w.double().abs().t())
+    y = oz2.linear(x, w, activation="relu", residual=r, out=r if in_place else None)
+    assert_within(y, want, err + (UNIT[BF16] + 2.0**-23) * (want.abs() + err) + TINY[BF16])
