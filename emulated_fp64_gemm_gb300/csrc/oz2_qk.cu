@@ -403,6 +403,12 @@ __global__ void __launch_bounds__(kBlock, kBackBlocks) qk_backward_kernel(const 
         out.move(at, jump, dx, dx, l);
         const bool on = at.has(l.group, l.per_warp, heads, 0);
         float x[16], g[16];
+        if (bad) {  // the whole warp's token: NaN, and nothing of it in the weight's sums
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = __int_as_float(0x7fc00000);
+          l.store(out.p, x, on);
+          return;
+        }
         L::take(slot, x);
         L::take(slot + kHead * kPiece, g);
         if (turns) {
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(kBlock, kBackBlocks) qk_backward_kernel(const 
           }
         }
         const float inverse = l.inverse_rms(a, x);  // by all lanes: it exchanges sums
-        const float r = !on ? 0.0f : bad ? __int_as_float(0x7fc00000) : inverse;  // a group past the heads adds nothing
+        const float r = on ? inverse : 0.0f;  // a group past the heads adds nothing
         float d0 = 0.0f, d1 = 0.0f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -529,6 +535,12 @@ __global__ void __launch_bounds__(kBlock) qk_plain_backward_kernel(const __grid_
        i += static_cast<int64_t>(blocks) * kWarps) {
     const int64_t token = i / xs.heads, head = i % xs.heads, pos = position(a, token);
     float x[kItems][2], g[kItems][2];
+    if (!known(a, pos)) {  // NaN, and nothing of it in the weight's sums
+#pragma unroll
+      for (int t = 0; t < kItems; ++t) x[t][0] = x[t][1] = __int_as_float(0x7fc00000);
+      write_head<T, INTER>(a, head_ptr<T>(dx, token, head), x);
+      continue;
+    }
     read_head<T, INTER>(a, head_ptr<T>(xs, token, head), x);
     read_head<T, INTER>(a, head_ptr<T>(dy, token, head), g);
     rotate(a, pos, -1.0f, g);

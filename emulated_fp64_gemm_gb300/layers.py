@@ -376,7 +376,9 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
                           out=None, stream=None):
     """(dq, dk, dq_weight, dk_weight) of `qk_norm_rope` from the gradients of its outputs.
 
-    The other arguments are the forward call's.  `out`: a pair of tensors for
+    The other arguments are the forward call's.  A token whose position is
+    outside the tables gets NaN in dq and dk and adds nothing to the weights'
+    gradients.  `out`: a pair of tensors for
     dq and dk, such as the slices of the joined projection's gradient."""
     dtype, device, tokens, nq, nk, dim, rows, half = _check_qk(q, k, q_weight, k_weight, cos, sin, positions, out)
     _check("dq_out", dq_out, dtype, device, (tokens, nq, dim))

@@ -157,7 +157,9 @@ typedef struct {
  * Backward: dq_out, dk_out are the gradients of the outputs, q and k the
  * inputs; writes q_out, k_out (the inputs' gradients; either may be dq_out or
  * dk_out itself) and dq_weight [dim], dk_weight [dim] (sums over all tokens
- * and heads; may be NULL).  The forward call ignores these four.
+ * and heads; may be NULL).  A token whose position is outside the tables gets
+ * NaN in its inputs' gradients and adds nothing to the weights'.  The forward
+ * call ignores these four.
  */
 typedef struct {
   int64_t tokens, dim, rot, table_rows;

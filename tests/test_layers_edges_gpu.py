@@ -173,3 +173,28 @@ def test_residual_of_long_products_with_ragged_ends(oz2, m, n, in_place):
     err = 1.2 * (k + 8) * 2.0**-23 * (x.double().abs() @ w.double().abs().t())
     y = oz2.linear(x, w, activation="relu", residual=r, out=r if in_place else None)
     assert_within(y, want, err + (UNIT[BF16] + 2.0**-23) * (want.abs() + err) + TINY[BF16])
+
+
+# ------------------------------------------------------------------ positions out of range
+# the second of each: heads not made of aligned chunks, which take the plain kernels
+@pytest.mark.parametrize("t,hq,hk,d,rot", [(50, 6, 2, 64, 32), (50, 3, 2, 60, 24), (3000, 8, 2, 128, 128), (9, 1, 0, 96, 96)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_positions_out_of_range_stay_with_their_tokens(oz2, t, hq, hk, d, rot, dtype, interleaved):
+    q, k, dq, dk = (normal(t, h, d, dtype=dtype, seed=i) for i, h in enumerate((hq, hk, hq, hk)))
+    wq, wk = 1 + 0.1 * normal(d, dtype=dtype, seed=5), 1 + 0.1 * normal(d, dtype=dtype, seed=6)
+    angle = torch.arange(100, device="cuda")[:, None] * torch.linspace(0.01, 1, rot // 2, device="cuda")
+    pos = torch.arange(t, device="cuda") % 100
+    bad, lost = pos.clone(), [0, 3, t // 2, t - 1]
+    bad[lost] = torch.tensor([-1, 100, 2**40, -2**62], device="cuda")
+    ok = [i for i in range(t) if i not in lost]
+    for g in (dq, dk):  # gradients of zero add nothing
+        g[lost] = 0
+    want = oz2.qk_norm_rope_backward(dq, dk, q, k, wq, wk, angle.cos(), angle.sin(), pos, interleaved=interleaved)
+    for g in (dq, dk):
+        g[lost] = float("nan")
+    got = oz2.qk_norm_rope_backward(dq, dk, q, k, wq, wk, angle.cos(), angle.sin(), bad, interleaved=interleaved)
+    for a, b in zip(got[:2], want[:2]):
+        assert bool(a[lost].isnan().all()) and torch.equal(a[ok], b[ok])
+    assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
+    assert bool(torch.isfinite(got[2]).all())
