@@ -13,7 +13,9 @@ is passed as is, any other layout is first copied.  All calls are asynchronous
 on `stream` (default: the tensors' device's current stream).  With a `stream`
 given, outputs are allocated for it, and the tensors' memory is kept until its
 work is done; ordering it after the inputs' producers is the caller's, as
-for any torch operation.  Outputs carry no autograd history.
+for any torch operation.  Outputs carry no autograd history; a tensor given
+as `out` counts as modified, so that autograd refuses to use what was saved of
+it before.
 
 A call of a small layer is bound by the host, so the checks are written out
 and the arguments go over as one packed structure: 20 of them one by one
@@ -47,6 +49,8 @@ _lib = None
 # the current stream's handle without the Stream object around it (0.1 instead of 3 us)
 _stream_of = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+# autograd learns of a write to a caller's tensor by its version
+_written = torch.autograd.graph.increment_version
 
 
 def _library():
@@ -192,6 +196,8 @@ def linear(x, w, bias=None, *, activation="none", residual=None, dropout=0.0, se
                           offset & _MASK64, _probability(dropout), _HALVES[dtype], act), _stream_of(device))
     if code:
         _fail(code, "ozaki2_linear")
+    if out is not None:
+        _written(out)
     return (y, preact) if save_preact else y
 
 
@@ -279,6 +285,8 @@ def dropout(x, p, *, seed, offset=0, residual=None, out=None, stream=None):
                            _probability(p), _FLOATS[dtype], 0), _stream_of(device))
     if code:
         _fail(code, "ozaki2_dropout")
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -369,6 +377,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, int
                               _FLOATS[dtype], 1 if interleaved else 0), _stream_of(device))
     if code:
         _fail(code, "ozaki2_qk_norm_rope")
+    if out is not None:
+        _written(out)
     return q_out, k_out
 
 
@@ -414,4 +424,6 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
                       1 if interleaved else 0), _stream_of(device))
     if code:
         _fail(code, "ozaki2_qk_norm_rope_backward")
+    if out is not None:
+        _written(out)
     return dq, dk, dwq, dwk

@@ -198,3 +198,30 @@ def test_positions_out_of_range_stay_with_their_tokens(oz2, t, hq, hk, d, rot, d
         assert bool(a[lost].isnan().all()) and torch.equal(a[ok], b[ok])
     assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
     assert bool(torch.isfinite(got[2]).all())
+
+
+# ------------------------------------------------------------------ what autograd is told
+def test_autograd_notices_writes_to_out(oz2):
+    x, w, r = normal(8, 16), normal(24, 16, seed=1), normal(8, 24, seed=2)
+    q, k, g, h = normal(5, 2, 16), normal(5, 1, 16, seed=1), normal(5, 2, 16, seed=2), normal(5, 1, 16, seed=3)
+    angle, pos = torch.zeros(8, 8, device="cuda"), torch.zeros(5, dtype=torch.int64, device="cuda")
+    one = torch.ones(16, dtype=BF16, device="cuda")
+    stream = torch.cuda.current_stream()
+    for f, outs in ((lambda: oz2.linear(x, w, residual=r, out=r), (r,)), (lambda: oz2.linear(x, w, out=r, stream=stream), (r,)),
+                    (lambda: oz2.dropout(x, 0.5, seed=1, out=x), (x,)), (lambda: oz2.dropout_backward(x, 0.5, seed=1, out=x), (x,)),
+                    (lambda: oz2.qk_norm_rope(q, k, one, one, angle, angle, pos, out=(q, k)), (q, k)),
+                    (lambda: oz2.qk_norm_rope_backward(g, h, q, k, one, one, angle, angle, pos, out=(g, h)), (g, h))):
+        before = [t._version for t in outs]
+        f()
+        assert all(t._version > v for t, v in zip(outs, before))
+    # a saved tensor that a call overwrites is refused, not used
+    leaf = normal(8, 24, dtype=F32).requires_grad_(True)
+    saved = leaf.to(BF16) * 2
+    loss = (saved * saved).sum()
+    oz2.linear(x, w, out=saved.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # tensors made under inference mode have no version
+    with torch.inference_mode():
+        out = torch.empty(8, 24, dtype=BF16, device="cuda")
+        oz2.linear(x, w, out=out)
