@@ -239,12 +239,15 @@ bool qk_ok(const oz2_qk_args& a) {
          (a.rot == 0 || a.tokens == 0 || (a.cos && a.sin && a.positions));
 }
 
-// No exception leaves a C entry point; what can be thrown is the host's own lack of memory.
+// No exception leaves a C entry point; what can be thrown is the host's own lack of memory.  Nor does the runtime's
+// record of an error that the status reports: the next caller to ask for it, torch or dgemm, would take it for its own.
 template <typename F>
 oz2_status guarded(F&& f) {
   try {
     std::lock_guard<std::mutex> lk(library_mutex());
-    return f();
+    const oz2_status e = f();
+    if (e == OZ2_ERR_CUDA) cudaGetLastError();
+    return e;
   } catch (const std::bad_alloc&) {
     return OZ2_ERR_NO_MEMORY;
   } catch (...) {

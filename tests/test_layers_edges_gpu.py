@@ -1,5 +1,6 @@
 """The layer operators where they leave the ordinary path: waits that run out, the ends of
 the types' ranges, activations' tails, positions out of range, and what autograd is told."""
+import ctypes
 import math
 
 import pytest
@@ -225,3 +226,34 @@ def test_autograd_notices_writes_to_out(oz2):
     with torch.inference_mode():
         out = torch.empty(8, 24, dtype=BF16, device="cuda")
         oz2.linear(x, w, out=out)
+
+
+# ------------------------------------------------------------------ calls that fail on the host
+def test_a_failed_call_leaves_no_error_behind(oz2):
+    # a launch is refused on a stream whose capture was cut short; torch and the library's other calls share the
+    # runtime's record of the last error, and would report it as theirs
+    from emulated_fp64_gemm_gb300.layers import _library
+
+    runtime = _library()  # which links the shared CUDA runtime
+    x, w = normal(8, 16), normal(24, 16, seed=1)
+    a = torch.ones(64, 64, dtype=torch.float64, device="cuda")
+    want, out = oz2.linear(x, w), torch.empty(8, 24, dtype=BF16, device="cuda")
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    handle, graph = ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p()
+    assert runtime.cudaStreamBeginCapture(handle, 2) == 0
+    try:
+        assert runtime.cudaStreamSynchronize(handle) != 0  # not permitted: it ends the capture with an error
+        runtime.cudaGetLastError()
+        with torch.cuda.stream(stream), pytest.raises(oz2.Ozaki2Error):
+            oz2.linear(x, w, out=out)
+        left = runtime.cudaPeekAtLastError()
+    finally:
+        runtime.cudaStreamEndCapture(handle, ctypes.byref(graph))
+        runtime.cudaGetLastError()
+    assert left == 0
+    with torch.cuda.stream(stream):
+        oz2.linear(x, w, out=out)
+        oz2.dgemm(a, a, 8, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
