@@ -236,7 +236,7 @@ bool qk_ok(const oz2_qk_args& a) {
          dtype_ok(a.dtype) && side_ok(a.q, a.tokens, a.q.heads) && side_ok(a.k, a.tokens, a.k.heads) &&
          side_ok(a.q_out, a.tokens, a.q.heads) && side_ok(a.k_out, a.tokens, a.k.heads) &&
          (a.q_weight || a.q.heads == 0) && (a.k_weight || a.k.heads == 0) && a.eps >= 0.0 && a.table_rows >= 0 &&
-         (a.rot == 0 || a.tokens == 0 || (a.cos && a.sin && a.positions));
+         (a.rot == 0 || a.tokens == 0 || (a.positions && (a.table_rows == 0 || (a.cos && a.sin))));
 }
 
 // No exception leaves a C entry point; what can be thrown is the host's own lack of memory.  Nor does the runtime's

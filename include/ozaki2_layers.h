@@ -151,7 +151,8 @@ typedef struct {
  * (float tables [table_rows][rot / 2]); features past rot are only normed.
  * q -> q_out with q_weight [dim], k -> k_out with k_weight [dim]; a side with
  * zero heads is left out.  A position outside [0, table_rows) gives NaN in
- * that token's outputs.  An output may be its input itself.
+ * that token's outputs; with no rows every position is outside, and the
+ * tables may be NULL.  An output may be its input itself.
  * dtype: any, of heads and weights.  rot even, 0 <= rot <= dim <= OZ2_HEAD_DIM_MAX.
  *
  * Backward: dq_out, dk_out are the gradients of the outputs, q and k the

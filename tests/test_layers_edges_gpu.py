@@ -257,3 +257,15 @@ def test_a_failed_call_leaves_no_error_behind(oz2):
         oz2.dgemm(a, a, 8, stream=stream)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("d,rot", [(64, 32), (60, 24)])
+def test_tables_without_rows(oz2, d, rot):
+    # every position is outside them
+    q, k, one = normal(5, 2, d), normal(5, 1, d, seed=1), torch.ones(d, dtype=BF16, device="cuda")
+    empty, pos = torch.empty(0, rot // 2, device="cuda"), torch.zeros(5, dtype=torch.int64, device="cuda")
+    for t in oz2.qk_norm_rope(q, k, one, one, empty, empty, pos):
+        assert bool(t.isnan().all())
+    dq, dk, dwq, dwk = oz2.qk_norm_rope_backward(q, k, q, k, one, one, empty, empty, pos)
+    assert bool(dq.isnan().all()) and bool(dk.isnan().all()) and not dwq.any() and not dwk.any()
+    assert oz2.qk_norm_rope(q[:0], k[:0], one, one, empty, empty, pos[:0])[0].shape == (0, 2, d)
