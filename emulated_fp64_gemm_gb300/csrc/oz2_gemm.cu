@@ -694,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps2
   uint64_t* empty = bars + STAGES;        // [STAGES] in both CTAs
   uint64_t* accf = bars + 2 * STAGES;     // [2] in both CTAs
   uint64_t* acce = accf + 2;              // [2] used in the leader only
-  uint64_t* drain = acce + 2;             // [1] leader
+  uint64_t* drain = acce + 2;             // [1] in both CTAs: all MMAs are done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -937,6 +937,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps2
   }
 
   __syncthreads();
+  // the last of the leader's arrivals has reached the peer before it ends
+  if (!leader && threadIdx.x == 0) mbar_wait_bounded(smem_u32(drain), 0, abort_flag, kWaitLimitNs);
+  __syncwarp();
   cluster_sync_all();  // the leader's MMAs are done with both CTAs' shared and tensor memory
   if (warp == 1) {
     __syncwarp();
