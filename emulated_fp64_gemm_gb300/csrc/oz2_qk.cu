@@ -27,7 +27,8 @@
 //
 // Heads that are not made of aligned 16-byte chunks, or that rotate a number of
 // features that is no multiple of 16, take the plain kernels: a warp per head, a
-// feature at a time.
+// feature at a time (8192 tokens x 20 heads of 80, 20 rotated, in bfloat16: 127 us,
+// backwards 230; all 80 rotated, in chunks: 22 and 33).
 #include <algorithm>
 
 #include "oz2_layers.cuh"

@@ -28,7 +28,8 @@
  * tensor-core products.  It is rounded without the dropout's scale, and in
  * float16 times a factor that keeps it below dy where the activation's slope
  * passes 1; both are made up for in the products' 32-bit sums, so that a
- * finite dy never overflows on the way.  No result depends on the order of atomics; equal
+ * finite dy never overflows on the way.  dz lives in the workspace (2 m n
+ * bytes), which is kept like the rest of it.  No result depends on the order of atomics; equal
  * calls give equal bits.
  *
  * Dropout mask: never stored, a function of (row, column, seed, offset).
