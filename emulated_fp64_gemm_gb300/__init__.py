@@ -6,7 +6,9 @@ PyTorch supplies device memory and streams.  There is no CPU fallback: if
 the library is not built, loading it raises.
 
 The layer operators (``linear``, ``dropout``, ``qk_norm_rope`` and their
-gradients) are in ``layers.py``; they are row-major.
+gradients) are in ``layers.py``, the operators around them (``rms_norm``,
+``token_logprobs`` and their gradients, ``adamw``) in ``steps.py``; they are
+row-major.
 
 Matrices of the FP64 GEMM follow the library's column-major convention: a (p, q) tensor with
 strides (1, ld), ld >= p, is passed as is.  Any other layout (row-major,
@@ -20,11 +22,13 @@ import os
 
 _LAYERS = ("ACTIVATIONS", "linear", "linear_backward", "dropout", "dropout_backward", "qk_norm_rope",
            "qk_norm_rope_backward")  # layers.py
+_STEPS = ("TokenLogprobs", "AdamWState", "rms_norm", "rms_norm_backward", "token_logprobs", "token_logprobs_backward",
+          "adamw_state", "adamw")  # steps.py
 __all__ = [
     "FAST", "ACCU", "Ozaki2Error", "load_library", "library_path", "moduli", "dgemm",
     "dgemm_debug", "dgemm_stages", "dgemm_host", "last_error", "workspace_release",
     "selftest_wait_timeout", "STAGE_NAMES", "profile_begin", "profile_end", "launch_count",
-    *_LAYERS,
+    *_LAYERS, *_STEPS,
 ]
 
 FAST = 0
@@ -288,10 +292,11 @@ def selftest_wait_timeout(limit_us: int = 2000) -> int:
 
 
 def __getattr__(name):
-    # the layer operators are loaded on first use: their module imports torch
-    if name in _LAYERS:
-        from . import layers
+    # the layer and step operators are loaded on first use: their modules import torch
+    if name in _LAYERS or name in _STEPS:
+        from importlib import import_module
 
-        value = globals()[name] = getattr(layers, name)
+        module = import_module("." + ("layers" if name in _LAYERS else "steps"), __name__)
+        value = globals()[name] = getattr(module, name)
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

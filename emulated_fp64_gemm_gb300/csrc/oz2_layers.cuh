@@ -277,6 +277,28 @@ __device__ __forceinline__ void store8(T* p, bool vec, int n, const float (&v)[8
   }
 }
 
+// Eight neighbouring elements as they are in memory, on a boundary of their size.
+template <typename T>
+struct Raw8 {
+  uint4 u;
+  __device__ __forceinline__ void read(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void values(float (&v)[8]) const { values8<T>(&u, v); }
+};
+template <>
+struct Raw8<float> {
+  float f[8];
+  __device__ __forceinline__ void read(const float* p) { load8(p, true, 8, f); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f[i];
+  }
+};
+
 // ------------------------------------------------------------ dropout
 // One round of Philox4x32 (Salmon, Moraes, Dror, Shaw, SC 2011): two 32 x 32 ->
 // 64 bit products, their halves crossed with the other words and the key; the

@@ -2,24 +2,14 @@
 // kernels.
 #include <algorithm>
 #include <cmath>
-#include <new>
 
+#include "oz2_entry.cuh"
 #include "oz2_layers.cuh"
 
 namespace oz2 {
 namespace {
 
-#define OZ2_TRY(call)                                 \
-  do {                                                \
-    if ((call) != cudaSuccess) return OZ2_ERR_CUDA;   \
-  } while (0)
-
 bool is_16bit(int t) { return t == OZ2_BF16 || t == OZ2_F16; }
-bool size_ok(int64_t n) { return n >= 0 && n <= OZ2_LAYER_DIM_MAX; }
-// a matrix that a call reads or writes: present unless empty, rows that do not overlap
-bool matrix_ok(const void* p, int64_t rows, int64_t cols, int64_t ld) {
-  return ld >= cols && (p != nullptr || rows == 0 || cols == 0);
-}
 bool dropout_ok(double p) { return p >= 0.0 && p <= 1.0; }  // false for NaN
 
 Dropout make_dropout(double p, uint64_t seed, uint64_t offset) {
@@ -223,7 +213,6 @@ oz2_status qk_backward(const oz2_qk_args& a, cudaStream_t st) {
   return OZ2_OK;
 }
 
-bool dtype_ok(int t) { return t >= OZ2_BF16 && t <= OZ2_F32; }
 bool act_ok(int t) { return t >= OZ2_ACT_NONE && t <= OZ2_ACT_GELU_TANH; }
 
 bool side_ok(const oz2_heads& h, int64_t tokens, int64_t heads) {
@@ -237,22 +226,6 @@ bool qk_ok(const oz2_qk_args& a) {
          side_ok(a.q_out, a.tokens, a.q.heads) && side_ok(a.k_out, a.tokens, a.k.heads) &&
          (a.q_weight || a.q.heads == 0) && (a.k_weight || a.k.heads == 0) && a.eps >= 0.0 && a.table_rows >= 0 &&
          (a.rot == 0 || a.tokens == 0 || (a.positions && (a.table_rows == 0 || (a.cos && a.sin))));
-}
-
-// No exception leaves a C entry point; what can be thrown is the host's own lack of memory.  Nor does the runtime's
-// record of an error that the status reports: the next caller to ask for it, torch or dgemm, would take it for its own.
-template <typename F>
-oz2_status guarded(F&& f) {
-  try {
-    std::lock_guard<std::mutex> lk(library_mutex());
-    const oz2_status e = f();
-    if (e == OZ2_ERR_CUDA) cudaGetLastError();
-    return e;
-  } catch (const std::bad_alloc&) {
-    return OZ2_ERR_NO_MEMORY;
-  } catch (...) {
-    return OZ2_ERR_CUDA;
-  }
 }
 
 }  // namespace

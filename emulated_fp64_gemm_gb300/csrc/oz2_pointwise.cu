@@ -34,23 +34,6 @@ cudaError_t for_rows(int64_t rows, int64_t per_row, int64_t cols, F&& f) {
   return cudaSuccess;
 }
 
-// Eight neighbouring elements as they are in memory.
-template <typename T>
-struct Raw8 {
-  uint4 u;
-  __device__ __forceinline__ void read(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void values(float (&v)[8]) const { values8<T>(&u, v); }
-};
-template <>
-struct Raw8<float> {
-  float f[8];
-  __device__ __forceinline__ void read(const float* p) { load8(p, true, 8, f); }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f[i];
-  }
-};
-
 // ------------------------------------------------------------------ dropout
 // A thread takes U groups, 256 apart, and has all of their loads in flight at
 // once.  FLAT: the matrices are contiguous, with whole groups in every row, so a

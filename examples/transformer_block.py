@@ -37,7 +37,7 @@ class Linear(torch.autograd.Function):
         x, w, z = ctx.saved_tensors
         activation, (p, seed, offset), residual = ctx.rest
         dx, dw, db = oz2.linear_backward(dy, x, w, preact=z, activation=activation, dropout=p, seed=seed, offset=offset,
-                                         need_dx=ctx.needs_input_grad[0])
+                                         need_dx=ctx.needs_input_grad[0], need_dbias=ctx.needs_input_grad[2])
         return dx, dw, db, dy if residual else None, None, None
 
 
