@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBlock = OZ2_ADAMW_BLOCK;
+constexpr float kShortEps = 1e-12f;  // from here on a root of 2^-63 is nothing beside eps
 constexpr int kTurns = 4;  // of a CTA's warps in a long step: 8192 elements per CTA
 
 // The tensors of one launch.  A kernel's arguments may take 32764 bytes; few tensors get the short form, whose launch copies less.
@@ -68,30 +69,80 @@ __device__ __forceinline__ float2 unpack_e4m3(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-__device__ __forceinline__ float fourth(float k) {
-  const float q = __fmul_rn(k, k);  // exact
-  return __fmul_rn(q, q);
+__device__ __forceinline__ float2 fourth2(float2 k) {
+  const float2 q = mul2(k, k);  // exact
+  return mul2(q, q);
+}
+__device__ __forceinline__ float fourth(float k) { return fourth2(both(k)).x; }
+
+// 2^23 + byte i of a word, or + half i: a whole number as a float without a conversion.
+constexpr float kWhole = 8388608.0f;
+__device__ __forceinline__ float whole_byte(uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + i)); }
+__device__ __forceinline__ float fast_rsqrt(float t) {  // infinity for 0, 0 for infinity
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
 }
 
-// The code of t = v / scale, by its definition to the bit: the largest k with fl(k^4) <= t, by an approximate root
-// and two corrections, and up by the draw.
+// The code of t = v / scale by its definition: the largest k with fl(k^4) <= t, up by the draw.
 __device__ __forceinline__ uint32_t encode_fourth(float t, uint32_t draw) {
-  float root;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(t));
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(root));
-  float k = fminf(floorf(root), 255.0f);
-  float low = fourth(k), high = fourth(k + 1.0f);
-  if (low > t) {
-    k -= 1.0f;
-    high = low;
-    low = fourth(k);
-  } else if (high <= t && k < 255.0f) {
-    k += 1.0f;
-    low = high;
-    high = fourth(k + 1.0f);
-  }
-  const bool up = __fmul_rn(__fsub_rn(t, low), 65536.0f) > __fmul_rn(static_cast<float>(draw), __fsub_rn(high, low)) || (k == 0.0f && t > 0.0f);
+  float k = fminf(floorf(fast_rsqrt(fast_rsqrt(t))), 255.0f);
+  while (k > 0.0f && fourth(k) > t) k -= 1.0f;
+  while (k < 255.0f && fourth(k + 1.0f) <= t) k += 1.0f;
+  const float low = fourth(k), high = fourth(k + 1.0f);
+  const bool up = __fsub_rn(t, low) > __fmul_rn(static_cast<float>(draw) * 0x1p-16f, __fsub_rn(high, low)) || (k == 0.0f && t > 0.0f);
   return static_cast<uint32_t>(fminf(k + (up ? 1.0f : 0.0f), 255.0f));
+}
+
+// The codes of eight, in two words.  k is floor(t^(1/4)) of an approximate root that is never too large: off by one only
+// just above a step, where t is then at or above the step after k.  That, and 0 < t < 1, are left to the form above.  A t of
+// 255^4, the largest of a block, is taken for the number before it, which is rounded up to 255 by every draw.
+__device__ __forceinline__ uint2 encode_fourths(const float2 (&v)[4], float inverse, const uint4& draws) {
+  constexpr float kMost = 4228250368.0f;  // before fl(255^4)
+  const uint32_t d[4] = {draws.x, draws.y, draws.z, draws.w};
+  float2 t[4];
+  uint32_t code[8];
+  bool rare = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t[i] = mul2(v[i], both(inverse));
+    t[i] = make_float2(fminf(t[i].x, kMost), fminf(t[i].y, kMost));
+    // (an approximate reciprocal root is off by 2^-22, and the second one halves what the first has)
+    float2 k = make_float2(__fmaf_rd(fast_rsqrt(fast_rsqrt(t[i].x)), 1.0f - 0x1p-21f, kWhole),
+                           __fmaf_rd(fast_rsqrt(fast_rsqrt(t[i].y)), 1.0f - 0x1p-21f, kWhole));
+    const uint32_t k0 = __float_as_uint(k.x), k1 = __float_as_uint(k.y);
+    k = add2(k, both(-kWhole));
+    const float2 low = fourth2(k), high = fourth2(add2(k, both(1.0f)));
+    // draw / 2^16: 1 + it is the half in the fraction of a float
+    const float2 draw = add2(make_float2(__uint_as_float(0x3F800000u | (d[i] << 7 & 0x007FFF80u)), __uint_as_float(0x3F800000u | (d[i] >> 9 & 0x007FFF80u))),
+                             both(-1.0f));
+    const float2 above = sub_each(t[i], low), limit = mul2(draw, sub_each(high, low));
+    code[2 * i] = k0 + (above.x > limit.x);
+    code[2 * i + 1] = k1 + (above.y > limit.y);
+    rare = rare || t[i].x < 1.0f || t[i].y < 1.0f || high.x <= t[i].x || high.y <= t[i].y;
+  }
+  if (rare) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {  // one copy of the code; the element is picked from registers
+      float x = 0.0f;
+      uint32_t draw = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j == i) {
+          x = j & 1 ? t[j >> 1].y : t[j >> 1].x;
+          draw = d[j >> 1] >> (16 * (j & 1)) & 0xFFFFu;
+        }
+      const uint32_t c = encode_fourth(x, draw);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j == i) code[j] = c;
+    }
+  }
+  uint32_t out[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    out[h] = __byte_perm(__byte_perm(code[4 * h], code[4 * h + 1], 0x0040), __byte_perm(code[4 * h + 2], code[4 * h + 3], 0x0040), 0x5410);
+  return make_uint2(out[0], out[1]);
 }
 
 constexpr float kLeastScale = 1e-36f;
@@ -102,16 +153,39 @@ __device__ __forceinline__ float state_scale(float top, float unit) {
 }
 
 // ------------------------------------------------------------------ the step
-// Eight elements of a lane: n of them (8, or fewer at a tensor's end).
+// Eight elements of a lane as pairs: n of them (8, or fewer at a tensor's end, zeros after them).
 template <typename T>
-__device__ __forceinline__ void read8(const T* p, int n, float (&v)[8]) {
-  const bool vec = n == 8 && reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0;
-  load8(p, vec, n, v);
+__device__ __forceinline__ void read8(const T* p, int n, float2 (&v)[4]) {
+  float f[8];
+  load8(p, n == 8 && reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0, n, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
 }
 template <typename T>
-__device__ __forceinline__ void write8(T* p, int n, const float (&v)[8]) {
-  const bool vec = n == 8 && reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0;
-  store8(p, vec, n, v);
+__device__ __forceinline__ void write8(T* p, int n, const float2 (&v)[4]) {
+  const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+  store8(p, n == 8 && reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0, n, f);
+}
+
+// 1 / (sqrt(x) + eps).  TINY: eps is so small that a root below 2^-63, which the short form takes for 0, is to be seen beside it.
+template <bool TINY>
+__device__ __forceinline__ float inverse_root(float x, float eps) {
+  float root;
+  if (TINY) {
+    root = sqrtf(x);
+    return 1.0f / (root + eps);
+  }
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(x));
+  return fast_rcp(root + eps);
+}
+template <bool TINY>
+__device__ __forceinline__ void move(const StepFactors& f, float eps, const float2 (&m)[4], const float2 (&v)[4], float2 (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = mul2(v[i], both(f.root2));
+    const float2 by = make_float2(inverse_root<TINY>(x.x, eps), inverse_root<TINY>(x.y, eps));
+    w[i] = fma2(w[i], both(f.keep), mul2(mul2(m[i], both(-f.rate)), by));
+  }
 }
 
 template <typename P, typename G, int BITS, bool MASTER, int MOST>
@@ -128,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   const G* grad = static_cast<const G*>(tensors.grad[at]);
   const int64_t state_block = tensors.block[at];
   wait_for_predecessor();
+  let_successor_come();
   StepFactors f;
   {
     const int64_t t = p.step[0] + 1;
@@ -146,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const int64_t left = elements - e0;
     const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
     const int64_t s0 = (state_block + block) * kBlock + lane * 8;  // of the flat states, which start on boundaries of 256 bytes or are read one by one
-    float w[8], g[8], m[8], v[8];
+    float2 w[4], g[4], m[4], v[4];
     if (MASTER) read8(p.master + s0, n, w);
     else read8(param + e0, n, w);
     read8(grad + e0, n, g);
@@ -157,28 +232,31 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       // whole groups: the gaps behind a tensor's end are there to be read
       const uint2 qm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.exp_avg) + s0);
       const uint2 qv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.exp_avg_sq) + s0);
-      const float sm = p.exp_avg_scale[state_block + block], sv = p.exp_avg_sq_scale[state_block + block];
+      const float2 sm = both(p.exp_avg_scale[state_block + block]), sv = both(p.exp_avg_sq_scale[state_block + block]);
       const uint32_t um[2] = {qm.x, qm.y}, uv[2] = {qv.x, qv.y};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 d = unpack_e4m3(um[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
-        m[2 * i] = 2 * i < n ? __fmul_rn(d.x, sm) : 0.0f;
-        m[2 * i + 1] = 2 * i + 1 < n ? __fmul_rn(d.y, sm) : 0.0f;
+        m[i] = mul2(unpack_e4m3(um[i >> 1] >> (16 * (i & 1)) & 0xFFFFu), sm);
+        const float2 k = add2(make_float2(whole_byte(uv[i >> 1], 2 * (i & 1)), whole_byte(uv[i >> 1], 2 * (i & 1) + 1)), both(-kWhole));
+        v[i] = mul2(fourth2(k), sv);
       }
+      if (n < 8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = i < n ? __fmul_rn(fourth(static_cast<float>(uv[i >> 2] >> (8 * (i & 3)) & 0xFFu)), sv) : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          if (2 * i >= n) m[i].x = v[i].x = 0.0f;
+          if (2 * i + 1 >= n) m[i].y = v[i].y = 0.0f;
+        }
+      }
     }
+    // one rounding at a time: 8-bit states are defined to the bit
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      g[i] = __fmul_rn(g[i], f.grad_scale);
-      // one rounding at a time: 8-bit states are defined to the bit
-      m[i] = __fadd_rn(__fmul_rn(p.beta1, m[i]), __fmul_rn(p.rest1, g[i]));
-      v[i] = __fadd_rn(__fmul_rn(p.beta2, v[i]), __fmul_rn(p.rest2, __fmul_rn(g[i], g[i])));
-      float root;
-      asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[i] * f.root2));
-      w[i] = fmaf(w[i], f.keep, -f.rate * m[i] * fast_rcp(root + p.eps));
+    for (int i = 0; i < 4; ++i) {
+      g[i] = mul2(g[i], both(f.grad_scale));
+      m[i] = add_each(mul2(both(p.beta1), m[i]), mul2(both(p.rest1), g[i]));
+      v[i] = add_each(mul2(both(p.beta2), v[i]), mul2(both(p.rest2), mul2(g[i], g[i])));
     }
+    if (p.eps >= kShortEps) move<false>(f, p.eps, m, v, w);
+    else move<true>(f, p.eps, m, v, w);
     if (MASTER) write8(p.master + s0, n, w);
     write8(param + e0, n, w);
     if (BITS == 32) {
@@ -187,31 +265,34 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     } else {
       float top_m = 0.0f, top_v = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        top_m = max_nan(top_m, i < n ? fabsf(m[i]) : 0.0f);
-        top_v = max_nan(top_v, i < n ? v[i] : 0.0f);
+      for (int i = 0; i < 4; ++i) {
+        top_m = max_nan(top_m, max_nan(fabsf(m[i].x), fabsf(m[i].y)));
+        top_v = max_nan(top_v, max_nan(v[i].x, v[i].y));
       }
-      const float sm = state_scale(warp_max_nan(top_m), 1.0f / 448.0f), sv = state_scale(warp_max_nan(top_v), kFourth);
-      const float im = __frcp_rn(sm), iv = __frcp_rn(sv);
-      const uint64_t group = static_cast<uint64_t>(s0) >> 3;
-      const uint4 d = philox7(static_cast<uint32_t>(group), static_cast<uint32_t>(group >> 32), f.t0, f.t1, p.seed0, p.seed1);
-      const uint32_t draws[4] = {d.x, d.y, d.z, d.w};
-      uint32_t qm[2] = {0, 0}, qv[2] = {0, 0};
+      top_v = warp_max_nan(top_v);
+      const float sm = state_scale(warp_max_nan(top_m), 1.0f / 448.0f), sv = state_scale(top_v, kFourth);
+      const float2 im = both(__frcp_rn(sm));
+      uint32_t qm[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        qm[i >> 1] |= pack_e4m3(__fmul_rn(m[2 * i], im), __fmul_rn(m[2 * i + 1], im)) << (16 * (i & 1));
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        qv[i >> 2] |= encode_fourth(__fmul_rn(v[i], iv), draws[i >> 1] >> (16 * (i & 1)) & 0xFFFFu) << (8 * (i & 3));
+      for (int i = 0; i < 4; ++i) {
+        const float2 q = mul2(m[i], im);
+        qm[i >> 1] |= pack_e4m3(q.x, q.y) << (16 * (i & 1));
+      }
+      uint2 qv = make_uint2(0, 0);
+      if (top_v != 0.0f) {
+        const uint64_t group = static_cast<uint64_t>(s0) >> 3;
+        qv = encode_fourths(v, __frcp_rn(sv), philox7(static_cast<uint32_t>(group), static_cast<uint32_t>(group >> 32), f.t0, f.t1, p.seed0, p.seed1));
+      }
       uint8_t* out_m = static_cast<uint8_t*>(p.exp_avg) + s0;
       uint8_t* out_v = static_cast<uint8_t*>(p.exp_avg_sq) + s0;
       if (n == 8) {
         *reinterpret_cast<uint2*>(out_m) = make_uint2(qm[0], qm[1]);
-        *reinterpret_cast<uint2*>(out_v) = make_uint2(qv[0], qv[1]);
+        *reinterpret_cast<uint2*>(out_v) = qv;
       } else {
+        const uint32_t words[2] = {qv.x, qv.y};
         for (int i = 0; i < n; ++i) {
           out_m[i] = static_cast<uint8_t>(qm[i >> 2] >> (8 * (i & 3)));
-          out_v[i] = static_cast<uint8_t>(qv[i >> 2] >> (8 * (i & 3)));
+          out_v[i] = static_cast<uint8_t>(words[i >> 2] >> (8 * (i & 3)));
         }
       }
       if (lane == 0) {
@@ -220,7 +301,6 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       }
     }
   }
-  let_successor_come();
   if (!p.last) return;
   // the last CTA to arrive counts the step: all others have read its number by then
   __syncthreads();

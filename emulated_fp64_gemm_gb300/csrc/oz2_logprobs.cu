@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const __gri
     if ((tid & 31) == 0) sh.warp_top[tid >> 5] = m;
     __syncthreads();
     if (tid < 32) {
-      const float b = warp_max_nan<16>(sh.warp_top[tid & 15]);
+      const float b = warp_max_nan(sh.warp_top[tid & 15]);
       if (tid == 0) sh.top = b;
     }
   }

@@ -2,12 +2,12 @@
 // with scales, and its gradients.
 //
 // Both directions are one pass over their matrices and bound by HBM.  A row is
-// held in registers by the threads of one or a few warps: 256 neighbouring
-// columns (a span) at a time per warp, as eight neighbouring columns per lane
-// where rows start on the boundaries of such groups, else as single columns 32
-// apart.  Either way a span's two halves of 128 columns are halves of a warp or
-// of a lane's registers, so that a scale per 128 columns needs shuffles only.
+// worked on by the lanes of one or a few warps, 256 neighbouring columns (a span)
+// at a time per warp.  Rows of aligned pieces are copied ahead into shared memory;
+// other ones are read by single elements, and rows longer than a block's
+// registers in several passes.
 #include <algorithm>
+#include <type_traits>
 
 #include "oz2_steps.cuh"
 
@@ -15,21 +15,31 @@ namespace oz2 {
 namespace {
 
 // ------------------------------------------------------------------ a lane's eight elements of a span
-// VEC: columns 8 lane .. 8 lane + 7 of the span; else lane, lane + 32, ...
+// VEC: 16-byte pieces of neighbours, one of a 16-bit type (columns 8 lane .. of the span), or two of 32 bits, 128 columns
+// apart (4 lane .. and 128 + 4 lane ..).  Else single columns, lane, lane + 32, ...  A scale per 128 columns is that of
+// half a warp in the first case, of half of each lane's elements in the others.
+template <typename T>
+constexpr int kPieces = sizeof(T) / 2;
+template <typename T, bool VEC>
+constexpr bool kHalfWarps = VEC && sizeof(T) == 2;
+
 template <typename T, bool VEC>
 __device__ __forceinline__ int column(int span, int lane, int e) {
-  return span * 256 + (VEC ? lane * 8 + e : e * 32 + lane);
+  if (!VEC) return span * 256 + e * 32 + lane;
+  return sizeof(T) == 2 ? span * 256 + lane * 8 + e : span * 256 + (e >> 2) * 128 + lane * 4 + (e & 3);
 }
 
 template <typename T, bool VEC>
 struct Part {  // as they are in memory
-  Raw8<T> r;
+  uint4 u[kPieces<T>];
   __device__ __forceinline__ void read(const T* row, int span, int lane, int cols) {
-    const int c = column<T, VEC>(span, lane, 0);
-    if (c < cols) r.read(row + c);
-    else r.zero();
+#pragma unroll
+    for (int q = 0; q < kPieces<T>; ++q) {
+      const int c = column<T, VEC>(span, lane, 4 * q);
+      u[q] = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+    }
   }
-  __device__ __forceinline__ void values(float (&v)[8]) const { r.values(v); }
+  __device__ __forceinline__ void values(float (&v)[8]) const { values8<T>(u, v); }
 };
 template <typename T>
 struct Part<T, false> {
@@ -49,50 +59,96 @@ struct Part<T, false> {
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void write_part(T* row, int span, int lane, int cols, const float (&v)[8]) {
-  if (VEC) {
-    const int c = column<T, VEC>(span, lane, 0);
-    if (c < cols) store8(row + c, true, 8, v);
-  } else {
+  if constexpr (!VEC) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int c = column<T, VEC>(span, lane, e);
       if (c < cols) row[c] = Elem<T>::down(v[e]);
     }
+  } else if constexpr (sizeof(T) == 2) {
+    const int c = column<T, VEC>(span, lane, 0);
+    if (c < cols) *reinterpret_cast<uint4*>(row + c) = pack8<T>(v);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int c = column<T, VEC>(span, lane, 4 * q);
+      if (c < cols) *reinterpret_cast<float4*>(row + c) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    }
   }
 }
 
-// Eight e4m3 of a span; bytes8: rows of them start on 8-byte boundaries.
-template <bool VEC>
-__device__ __forceinline__ void write_e4m3(uint8_t* row, int span, int lane, int cols, bool bytes8, const float (&v)[8]) {
-  const uint32_t lo = pack_e4m3(v[0], v[1]) | pack_e4m3(v[2], v[3]) << 16, hi = pack_e4m3(v[4], v[5]) | pack_e4m3(v[6], v[7]) << 16;
-  const int c0 = column<float, VEC>(span, lane, 0);
-  if (VEC && bytes8) {
-    if (c0 < cols) *reinterpret_cast<uint2*>(row + c0) = make_uint2(lo, hi);
+// Eight e4m3 of a span; whole: rows of them start on boundaries of 8 bytes.
+template <typename T, bool VEC>
+__device__ __forceinline__ void write_e4m3(uint8_t* row, int span, int lane, int cols, bool whole, const float (&v)[8]) {
+  const uint32_t w[2] = {pack_e4m3(v[0], v[1]) | pack_e4m3(v[2], v[3]) << 16, pack_e4m3(v[4], v[5]) | pack_e4m3(v[6], v[7]) << 16};
+  if (VEC && whole) {
+    const int c = column<T, VEC>(span, lane, 0), c1 = column<T, VEC>(span, lane, 4);
+    if constexpr (sizeof(T) == 2) {
+      if (c < cols) *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+    } else {
+      if (c < cols) *reinterpret_cast<uint32_t*>(row + c) = w[0];
+      if (c1 < cols) *reinterpret_cast<uint32_t*>(row + c1) = w[1];
+    }
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int c = column<float, VEC>(span, lane, e);
-    if (c < cols) row[c] = static_cast<uint8_t>((e < 4 ? lo : hi) >> (8 * (e & 3)));
+    const int c = column<T, VEC>(span, lane, e);
+    if (c < cols) row[c] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
   }
+}
+
+// A lane's eight elements as pairs.
+using Pairs = float2[4];
+template <typename P>
+__device__ __forceinline__ void pairs_of(const P& part, Pairs& v) {
+  float f[8];
+  part.values(f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void singles(const Pairs& v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = v[i].x;
+    f[2 * i + 1] = v[i].y;
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void write_pairs(T* row, int span, int lane, int cols, const Pairs& v) {
+  float f[8];
+  singles(v, f);
+  write_part<T, VEC>(row, span, lane, cols, f);
+}
+__device__ __forceinline__ float max_magnitude(const Pairs& v, float top) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max_nan(top, max_nan(fabsf(v[i].x), fabsf(v[i].y)));
+  return top;
 }
 
 // ------------------------------------------------------------------ sums and maxima over a row's warps
 // A row belongs to `warps` warps: to one of several in the block, or to the whole block.  `room`: a float2 per warp; one
-// that is used again needs a barrier in between (callers alternate).
-template <bool SECOND_IS_MAX>
+// that is used again needs a barrier in between (callers alternate).  The second value is a sum, a maximum or none.
+enum Second { kNone, kSum, kMax };
+template <Second SECOND>
 __device__ __forceinline__ void row_reduce(float& a, float& b, int warps, float2* room) {
   a = warp_sum(a);
-  b = SECOND_IS_MAX ? warp_max_nan(b) : warp_sum(b);
+  if (SECOND == kSum) b = warp_sum(b);
+  if (SECOND == kMax) b = warp_max_nan(b);
   if (warps == 1) return;
   if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
-  a = b = 0.0f;
-  for (int i = 0; i < warps; ++i) {
-    const float2 v = room[i];
-    a += v.x;
-    b = SECOND_IS_MAX ? max_nan(b, v.y) : b + v.y;
+  // every warp adds the warps' sums in the same order
+  const int other_warp = threadIdx.x & 15;
+  const float2 v = other_warp < warps ? room[other_warp] : make_float2(0.0f, 0.0f);
+  a = v.x;
+  b = v.y;
+#pragma unroll
+  for (int i = 8; i; i >>= 1) {
+    a += __shfl_xor_sync(0xFFFFFFFFu, a, i);
+    if (SECOND == kSum) b += __shfl_xor_sync(0xFFFFFFFFu, b, i);
   }
+  if (SECOND == kMax) b = warp_max_nan(b);
 }
 
 // Whether a sum of squares has left the range where it can be used: overflowed (or not a number), or so small that its
@@ -126,7 +182,7 @@ struct NormParams {
   int64_t scales;  // per row
   int cols, warps;  // warps: per row
   int block;        // columns per scale: 128, or 0 for rows
-  int quantize, bytes8;
+  int quantize, whole;
   float eps;
 };
 
@@ -134,10 +190,11 @@ __device__ __forceinline__ float scale_of(float top) { return (top < 1e-30f ? 1e
 
 // The e4m3 of a span, and its scales where they are its own.  An element over the row's norm is t * r.  (Not t times
 // r / scale: the quotient overflows where a row of small elements has a scale at its floor.)
-template <bool VEC>
+template <typename T, bool VEC>
 __device__ __forceinline__ void quantize_span(const NormParams& p, int64_t row, int span, int lane, float r, float row_scale,
                                               float (&t)[8]) {
-  constexpr int HALVES = VEC ? 1 : 2;  // a lane's elements are of one block, or of two
+  constexpr bool HALF_WARPS = kHalfWarps<T, VEC>;
+  constexpr int HALVES = HALF_WARPS ? 1 : 2;  // a lane's elements are of one block, or of two
   float inv[HALVES];
 #pragma unroll
   for (int h = 0; h < HALVES; ++h) {
@@ -145,57 +202,206 @@ __device__ __forceinline__ void quantize_span(const NormParams& p, int64_t row, 
     if (p.block) {
       float top = 0.0f;
 #pragma unroll
-      for (int e = h * 4; e < (VEC ? 8 : h * 4 + 4); ++e) top = max_nan(top, fabsf(t[e]));
-      s = scale_of(warp_max_nan<VEC ? 16 : 32>(top) * r);
-      const int g = span * 2 + (VEC ? lane >> 4 : h);
-      if ((VEC ? lane & 15 : lane) == 0 && g < p.scales) p.scale[row * p.scales + g] = s;
+      for (int e = h * 4; e < (HALF_WARPS ? 8 : h * 4 + 4); ++e) top = max_nan(top, fabsf(t[e]));
+      s = scale_of((HALF_WARPS ? half_warp_max_nan(top) : warp_max_nan(top)) * r);
+      const int g = span * 2 + (HALF_WARPS ? lane >> 4 : h);
+      if ((HALF_WARPS ? lane & 15 : lane) == 0 && g < p.scales) p.scale[row * p.scales + g] = s;
     }
     inv[h] = fast_rcp(s);
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) t[e] = t[e] * r * inv[VEC ? 0 : e >> 2];
-  write_e4m3<VEC>(static_cast<uint8_t*>(p.y) + row * p.ldy, span, lane, p.cols, p.bytes8, t);
+  for (int e = 0; e < 8; ++e) t[e] = t[e] * r * inv[HALF_WARPS ? 0 : e >> 2];
+  write_e4m3<T, VEC>(static_cast<uint8_t*>(p.y) + row * p.ldy, span, lane, p.cols, p.whole, t);
 }
 
 // What becomes of a span's elements v (scaled as r is): y = v g r.
 template <typename T, bool VEC>
 __device__ __forceinline__ void finish_span(const NormParams& p, int64_t row, int span, int lane, float r, float row_scale,
-                                            const float (&g)[8], float (&v)[8]) {
+                                            const Pairs& g, const Pairs& v) {
+  Pairs y;
   if (p.quantize) {
+    float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= g[e];
-    quantize_span<VEC>(p, row, span, lane, r, row_scale, v);
+    for (int i = 0; i < 4; ++i) y[i] = mul2(v[i], g[i]);
+    singles(y, f);
+    quantize_span<T, VEC>(p, row, span, lane, r, row_scale, f);
   } else {  // not first by g: the product of two small ones would lose bits that r brings back
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= g[e] * r;
-    write_part<T, VEC>(static_cast<T*>(p.y) + row * p.ldy, span, lane, p.cols, v);
+    for (int i = 0; i < 4; ++i) y[i] = mul2(v[i], mul2(g[i], both(r)));
+    write_pairs<T, VEC>(static_cast<T*>(p.y) + row * p.ldy, span, lane, p.cols, y);
   }
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void read_sum(const NormParams& p, int64_t row, int span, int lane, float (&v)[8]) {
+__device__ __forceinline__ void read_sum(const NormParams& p, int64_t row, int span, int lane, Pairs& v) {
   Part<T, VEC> x, res;
   x.read(static_cast<const T*>(p.x) + row * p.ldx, span, lane, p.cols);
   if (p.residual) res.read(static_cast<const T*>(p.residual) + row * p.ldr, span, lane, p.cols);
-  x.values(v);
+  pairs_of(x, v);
   if (p.residual) {
-    float add[8];
-    res.values(add);
+    Pairs add;
+    pairs_of(res, add);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += add[e];
+    for (int i = 0; i < 4; ++i) v[i] = add2(v[i], add[i]);
   }
 }
 
+// ------------------------------------------------------------------ rows on their way
+// A team of warps takes every teams-th row.  Rows are copied ahead into shared memory, each lane its own elements, which
+// no other thread reads: no barrier belongs to it.  DEPTH - 1 rows per team are on their way while one is worked on.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+template <typename T, int N, int DEPTH>
+struct Ring {
+  uint32_t base;
+  int stride;  // of a piece of all threads
+  int arrays;
+  __device__ __forceinline__ Ring(void* smem, int arrays_) : base(smem_u32(smem) + threadIdx.x * 16), stride(blockDim.x * 16), arrays(arrays_) {}
+  __device__ __forceinline__ uint32_t at(int slot, int array, int j, int q) const {
+    return base + (((slot * arrays + array) * N + j) * kPieces<T> + q) * stride;
+  }
+  // The row's spans of one array, zeros past its end.
+  __device__ __forceinline__ void copy(int slot, int array, const T* row, int warps, int w, int lane, int cols) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int q = 0; q < kPieces<T>; ++q) {
+        const int c = column<T, true>(j * warps + w, lane, 4 * q);
+        copy16(at(slot, array, j, q), row + (c < cols ? c : 0), c < cols);
+      }
+  }
+  __device__ __forceinline__ void pairs(int slot, int array, int j, Pairs& v) const {
+    Part<T, true> part;
+#pragma unroll
+    for (int q = 0; q < kPieces<T>; ++q)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(part.u[q].x), "=r"(part.u[q].y), "=r"(part.u[q].z), "=r"(part.u[q].w) : "r"(at(slot, array, j, q)) : "memory");
+    pairs_of(part, v);
+  }
+};
+
 // ------------------------------------------------------------------ forward
-// N spans per warp, all of a row's loads in flight at once.  Bound by HBM: 4 to 8 bytes per element in 16 bits.
+// What follows once a row's s = x + residual is in registers.
 template <typename T, bool VEC, int N>
+__device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, int w, int lane, const Part<T, VEC> (&ws)[N], Pairs (&v)[N],
+                                         float2 (*room)[16]) {
+  const bool row_top = p.quantize && !p.block;
+  float top = 0.0f;
+  auto weighted_top = [&] {
+    top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      Pairs g;
+      pairs_of(ws[j], g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = mul2(v[j][i], g[i]);
+      top = max_magnitude(g, top);
+    }
+  };
+  auto squares = [&] {
+    float2 sum = both(0.0f);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum = fma2(v[j][i], v[j][i], sum);
+    return sum.x + sum.y;
+  };
+  float sum = squares();
+  if (row_top) {
+    weighted_top();
+    row_reduce<kMax>(sum, top, p.warps, room[0]);
+  } else {
+    row_reduce<kNone>(sum, top, p.warps, room[0]);
+  }
+  if (p.residual_out) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      write_pairs<T, VEC>(static_cast<T*>(p.residual_out) + row * p.ldo, j * p.warps + w, lane, p.cols, v[j]);
+  }
+  float f = 1.0f;
+  if (out_of_range(sum, p.eps)) {  // the same in all of the row's threads
+    float most = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) most = max_magnitude(v[j], most);
+    row_reduce<kMax>(sum, most, p.warps, room[1]);
+    f = range_factor(most);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], both(f));
+    sum = squares();
+    weighted_top();
+    row_reduce<kMax>(sum, top, p.warps, room[2]);
+  }
+  const float r = inverse_norm(sum, p.cols, p.eps, f);
+  const float row_scale = scale_of(top * r);
+  if (row_top && w == 0 && lane == 0) p.scale[row] = row_scale;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    Pairs g;
+    pairs_of(ws[j], g);
+    finish_span<T, VEC>(p, row, j * p.warps + w, lane, r, row_scale, g, v[j]);
+  }
+}
+
+// Rows of aligned pieces, N spans per warp.  Bound by HBM: 4 to 8 bytes per element in 16 bits.
+template <typename T, int N, int DEPTH>
 __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float2 room[2][16];
+  extern __shared__ uint4 ring_memory[];
+  __shared__ float2 room[2][3][16];
+  const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, w = in_block % p.warps, per_block = (blockDim.x >> 5) / p.warps;
+  const int64_t team = static_cast<int64_t>(blockIdx.x) * per_block + in_block / p.warps, teams = static_cast<int64_t>(gridDim.x) * per_block;
+  const Ring<T, N, DEPTH> ring(ring_memory, p.residual ? 2 : 1);
+  wait_for_predecessor();
+  auto copy = [&](int64_t row, int slot) {
+    if (row < p.rows) {
+      ring.copy(slot, 0, static_cast<const T*>(p.x) + row * p.ldx, p.warps, w, lane, p.cols);
+      if (p.residual) ring.copy(slot, 1, static_cast<const T*>(p.residual) + row * p.ldr, p.warps, w, lane, p.cols);
+    }
+    copies_end_group();
+  };
+  let_successor_come();  // its blocks take the places that this grid's leave
+#pragma unroll
+  for (int d = 0; d < DEPTH - 1; ++d) copy(team + d * teams, d);
+  Part<T, true> ws[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) ws[j].read(static_cast<const T*>(p.weight), j * p.warps + w, lane, p.cols);
+  int slot = 0, turn = 0;
+  for (int64_t row = team; row < p.rows; row += teams) {
+    copy(row + (DEPTH - 1) * teams, slot == 0 ? DEPTH - 1 : slot - 1);
+    copies_wait<DEPTH - 1>();
+    Pairs v[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      ring.pairs(slot, 0, j, v[j]);
+      if (p.residual) {
+        Pairs add;
+        ring.pairs(slot, 1, j, add);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], add[i]);
+      }
+    }
+    norm_row<T, true, N>(p, row, w, lane, ws, v, room[turn]);
+    if (++slot == DEPTH) slot = 0;
+    turn ^= 1;
+  }
+}
+
+// Rows off the boundaries of 16 bytes: a row per team, single elements.
+template <typename T, int N>
+__global__ void __launch_bounds__(512) rms_norm_ragged_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float2 room[3][16];
   const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, w = in_block % p.warps;
-  const int64_t row = p.warps == 1 ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + in_block : blockIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / p.warps) + in_block / p.warps;
   wait_for_predecessor();
   if (row >= p.rows) return;  // with one warp per row, where no barrier follows
-  Part<T, VEC> xs[N], rs[N], ws[N];
+  Part<T, false> xs[N], rs[N], ws[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     xs[j].read(static_cast<const T*>(p.x) + row * p.ldx, j * p.warps + w, lane, p.cols);
@@ -204,65 +410,18 @@ __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ N
 #pragma unroll
   for (int j = 0; j < N; ++j) ws[j].read(static_cast<const T*>(p.weight), j * p.warps + w, lane, p.cols);
   let_successor_come();
-  const bool row_top = p.quantize && !p.block;
-  float v[N][8], sum = 0.0f, top = 0.0f;
+  Pairs v[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    xs[j].values(v[j]);
+    pairs_of(xs[j], v[j]);
     if (p.residual) {
-      float add[8];
-      rs[j].values(add);
+      Pairs add;
+      pairs_of(rs[j], add);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] += add[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(v[j][e], v[j][e], sum);
-    if (row_top) {
-      float g[8];
-      ws[j].values(g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(v[j][e] * g[e]));
+      for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], add[i]);
     }
   }
-  row_reduce<true>(sum, top, p.warps, room[0]);
-  if (p.residual_out) {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      write_part<T, VEC>(static_cast<T*>(p.residual_out) + row * p.ldo, j * p.warps + w, lane, p.cols, v[j]);
-  }
-  float f = 1.0f;
-  if (out_of_range(sum, p.eps)) {  // the same in all of the row's threads
-    float most = 0.0f;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = max_nan(most, fabsf(v[j][e]));
-    sum = 0.0f;
-    row_reduce<true>(sum, most, p.warps, room[1]);
-    f = range_factor(most);
-    sum = top = 0.0f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      float g[8];
-      ws[j].values(g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[j][e] *= f;
-        sum = fmaf(v[j][e], v[j][e], sum);
-        top = max_nan(top, fabsf(v[j][e] * g[e]));
-      }
-    }
-    row_reduce<true>(sum, top, p.warps, room[0]);
-  }
-  const float r = inverse_norm(sum, p.cols, p.eps, f);
-  const float row_scale = scale_of(top * r);
-  if (row_top && w == 0 && lane == 0) p.scale[row] = row_scale;
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    float g[8];
-    ws[j].values(g);
-    finish_span<T, VEC>(p, row, j * p.warps + w, lane, r, row_scale, g, v[j]);
-  }
+  norm_row<T, false, N>(p, row, w, lane, ws, v, room);
 }
 
 // Rows longer than a block's registers: a block reads each of them twice (three times where its squares leave the
@@ -277,36 +436,36 @@ __global__ void __launch_bounds__(512) rms_norm_long_kernel(const __grid_constan
   const T* weight = static_cast<const T*>(p.weight);
   float f = 1.0f, sum = 0.0f, top = 0.0f;
   auto statistics = [&](bool with_weight) {  // of the elements times f
-    sum = top = 0.0f;
+    float2 squares = both(0.0f);
+    top = 0.0f;
 #pragma unroll 2
     for (int span = w; span < spans; span += p.warps) {
-      float v[8];
+      Pairs v, g;
       read_sum<T, VEC>(p, row, span, lane, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] *= f;
-        sum = fmaf(v[e], v[e], sum);
+      for (int i = 0; i < 4; ++i) {
+        v[i] = mul2(v[i], both(f));
+        squares = fma2(v[i], v[i], squares);
       }
       if (with_weight) {
         Part<T, VEC> ws;
-        float g[8];
         ws.read(weight, span, lane, p.cols);
-        ws.values(g);
+        pairs_of(ws, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= g[e];
+        for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], g[i]);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(v[e]));
+      top = max_magnitude(v, top);
     }
+    sum = squares.x + squares.y;
   };
   statistics(true);
-  row_reduce<true>(sum, top, p.warps, room[0]);
+  row_reduce<kMax>(sum, top, p.warps, room[0]);
   if (out_of_range(sum, p.eps)) {
     statistics(false);
-    row_reduce<true>(sum, top, p.warps, room[1]);
+    row_reduce<kMax>(sum, top, p.warps, room[1]);
     f = range_factor(top);
     statistics(true);
-    row_reduce<true>(sum, top, p.warps, room[2]);
+    row_reduce<kMax>(sum, top, p.warps, room[2]);
   }
   const float r = inverse_norm(sum, p.cols, p.eps, f);
   const float row_scale = scale_of(top * r);
@@ -314,14 +473,14 @@ __global__ void __launch_bounds__(512) rms_norm_long_kernel(const __grid_constan
   // (all reads of the row for its statistics are behind the last barrier: outputs may be inputs)
 #pragma unroll 2
   for (int span = w; span < spans; span += p.warps) {
-    float v[8], g[8];
+    Pairs v, g;
     Part<T, VEC> ws;
     ws.read(weight, span, lane, p.cols);
     read_sum<T, VEC>(p, row, span, lane, v);
-    if (p.residual_out) write_part<T, VEC>(static_cast<T*>(p.residual_out) + row * p.ldo, span, lane, p.cols, v);
-    ws.values(g);
+    if (p.residual_out) write_pairs<T, VEC>(static_cast<T*>(p.residual_out) + row * p.ldo, span, lane, p.cols, v);
+    pairs_of(ws, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= f;
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(f));
     finish_span<T, VEC>(p, row, span, lane, r, row_scale, g, v);
   }
 }
@@ -353,111 +512,161 @@ __device__ __forceinline__ RowTerms row_terms(float sum, float dot, int cols, fl
   return RowTerms{f, r, r * r * (dot / static_cast<float>(cols))};
 }
 
-// One team of warps (a warp, or the whole block) takes every teams-th row; the next row's loads are on their way while
-// this one's sums are joined (not with four spans, whose registers are all in use).  The weight's gradient is summed in
-// registers, a part per team.  Bound by HBM: 6 bytes per element in 16 bits, 8 with dresidual.
-template <typename T, bool VEC, int N>
-__global__ void __launch_bounds__(512) rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
-  constexpr bool AHEAD = N < 4;
-  __shared__ float2 room[4][16];
-  const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, w = in_block % p.warps;
-  const int per_block = (blockDim.x >> 5) / p.warps;
-  const int64_t team = static_cast<int64_t>(blockIdx.x) * per_block + in_block / p.warps, teams = static_cast<int64_t>(gridDim.x) * per_block;
-  wait_for_predecessor();
-  Part<T, VEC> ws[N], dys[N], xs[N], ds[N];
-  auto read = [&](int64_t row, Part<T, VEC>(&dy)[N], Part<T, VEC>(&x)[N], Part<T, VEC>(&d)[N]) {
+// A row's sums over u = x f, its terms, and what its elements become.  With four spans there is no room for the row's
+// elements in registers between the two: `dys`, `xs` give them again.
+template <typename T, bool VEC, int N, typename Dy, typename X, typename Residual>
+__device__ __forceinline__ void norm_row_backward(const NormBackwardParams& p, int64_t row, int w, int lane, const Part<T, VEC> (&ws)[N],
+                                                  Pairs (&acc)[N], float2 (*room)[16], Dy&& dys, X&& xs, Residual&& residual) {
+  constexpr bool KEEP = N < 4;
+  Pairs dy[KEEP ? N : 1], x[KEEP ? N : 1];
+  float f = 1.0f, sum, dot;
+  auto sums = [&] {
+    float2 squares = both(0.0f), products = both(0.0f);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int span = j * p.warps + w;
-      dy[j].read(static_cast<const T*>(p.dy) + row * p.lddy, span, lane, p.cols);
-      x[j].read(static_cast<const T*>(p.x) + row * p.ldx, span, lane, p.cols);
-      if (p.dresidual) d[j].read(static_cast<const T*>(p.dresidual) + row * p.ldd, span, lane, p.cols);
+      constexpr int M = KEEP ? N : 1;
+      Pairs g;
+      pairs_of(ws[j], g);
+      dys(j, dy[j % M]);
+      xs(j, x[j % M]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (f != 1.0f) x[j % M][i] = mul2(x[j % M][i], both(f));
+        squares = fma2(x[j % M][i], x[j % M][i], squares);
+        products = fma2(mul2(dy[j % M][i], g[i]), x[j % M][i], products);
+      }
     }
+    sum = squares.x + squares.y;
+    dot = products.x + products.y;
   };
-  float acc[N][8];
+  sums();
+  row_reduce<kSum>(sum, dot, p.warps, room[0]);
+  if (out_of_range(sum, p.eps)) {
+    float most = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      Pairs v;
+      xs(j, v);
+      most = max_magnitude(v, most);
+    }
+    row_reduce<kMax>(sum, most, p.warps, room[1]);
+    f = range_factor(most);
+    sums();
+    row_reduce<kSum>(sum, dot, p.warps, room[2]);
+  }
+  // dx = f r (g dy - u k) + dresidual
+  const RowTerms t = row_terms(sum, dot, p.cols, p.eps, f);
+  const float2 r = both(t.r), fr = both(t.f * t.r), frk = both(-t.f * t.r * t.k);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    constexpr int M = KEEP ? N : 1;
+    Pairs g, out;
+    pairs_of(ws[j], g);
+    if (!KEEP) {
+      dys(j, dy[j % M]);
+      xs(j, x[j % M]);
+      if (f != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[j % M][i] = mul2(x[j % M][i], both(f));
+      }
+    }
+    if (p.dresidual) residual(j, out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = x[j % M][i], d = dy[j % M][i];
+      acc[j][i] = fma2(mul2(d, r), u, acc[j][i]);
+      const float2 part = mul2(mul2(d, g[i]), fr);
+      out[i] = p.dresidual ? fma2(u, frk, add2(part, out[i])) : fma2(u, frk, part);
+    }
+    write_pairs<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx, j * p.warps + w, lane, p.cols, out);
+  }
+}
+
+// Rows of aligned pieces.  The weight's gradient is summed in registers, a part per team.  Bound by HBM: 6 bytes per
+// element in 16 bits, 8 with dresidual.
+template <typename T, int N, int DEPTH>
+__global__ void __launch_bounds__(512) rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
+  extern __shared__ uint4 ring_memory[];
+  __shared__ float2 room[2][3][16];
+  const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, w = in_block % p.warps, per_block = (blockDim.x >> 5) / p.warps;
+  const int64_t team = static_cast<int64_t>(blockIdx.x) * per_block + in_block / p.warps, teams = static_cast<int64_t>(gridDim.x) * per_block;
+  const Ring<T, N, DEPTH> ring(ring_memory, p.dresidual ? 3 : 2);
+  wait_for_predecessor();
+  auto copy = [&](int64_t row, int slot) {
+    if (row < p.rows) {
+      ring.copy(slot, 0, static_cast<const T*>(p.dy) + row * p.lddy, p.warps, w, lane, p.cols);
+      ring.copy(slot, 1, static_cast<const T*>(p.x) + row * p.ldx, p.warps, w, lane, p.cols);
+      if (p.dresidual) ring.copy(slot, 2, static_cast<const T*>(p.dresidual) + row * p.ldd, p.warps, w, lane, p.cols);
+    }
+    copies_end_group();
+  };
+  let_successor_come();  // its blocks take the places that this grid's leave
+#pragma unroll
+  for (int d = 0; d < DEPTH - 1; ++d) copy(team + d * teams, d);
+  Part<T, true> ws[N];
+  Pairs acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     ws[j].read(static_cast<const T*>(p.weight), j * p.warps + w, lane, p.cols);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[j][e] = 0.0f;
+    for (int i = 0; i < 4; ++i) acc[j][i] = both(0.0f);
   }
-  if (AHEAD && team < p.rows) read(team, dys, xs, ds);
+  int slot = 0, turn = 0;
+  for (int64_t row = team; row < p.rows; row += teams) {
+    copy(row + (DEPTH - 1) * teams, slot == 0 ? DEPTH - 1 : slot - 1);
+    copies_wait<DEPTH - 1>();
+    norm_row_backward<T, true, N>(
+        p, row, w, lane, ws, acc, room[turn], [&](int j, Pairs& v) { ring.pairs(slot, 0, j, v); },
+        [&](int j, Pairs& v) { ring.pairs(slot, 1, j, v); }, [&](int j, Pairs& v) { ring.pairs(slot, 2, j, v); });
+    if (++slot == DEPTH) slot = 0;
+    turn ^= 1;
+  }
+  if (!p.partial) return;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    float sums[8];
+    singles(acc[j], sums);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {  // four neighbours each
+      const int c = column<T, true>(j * p.warps + w, lane, 4 * q);
+      if (c < p.cols)
+        *reinterpret_cast<float4*>(p.partial + team * p.cols + c) = make_float4(sums[4 * q], sums[4 * q + 1], sums[4 * q + 2], sums[4 * q + 3]);
+    }
+  }
+}
+
+// The same for rows off the boundaries of 16 bytes, by single elements, which are read again after the sums.
+template <typename T, int N>
+__global__ void __launch_bounds__(512) rms_norm_ragged_backward_kernel(const __grid_constant__ NormBackwardParams p) {
+  __shared__ float2 room[2][3][16];
+  const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, w = in_block % p.warps, per_block = (blockDim.x >> 5) / p.warps;
+  const int64_t team = static_cast<int64_t>(blockIdx.x) * per_block + in_block / p.warps, teams = static_cast<int64_t>(gridDim.x) * per_block;
+  wait_for_predecessor();
+  Part<T, false> ws[N];
+  Pairs acc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    ws[j].read(static_cast<const T*>(p.weight), j * p.warps + w, lane, p.cols);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = both(0.0f);
+  }
   int turn = 0;
   for (int64_t row = team; row < p.rows; row += teams, turn ^= 1) {
-    Part<T, VEC> next_dy[N], next_x[N], next_d[N];
-    if (AHEAD) {
-      if (row + teams < p.rows) read(row + teams, next_dy, next_x, next_d);
-    } else {
-      read(row, dys, xs, ds);
-    }
-    float f = 1.0f, sum = 0.0f, dot = 0.0f;
-    auto statistics = [&] {
-      sum = dot = 0.0f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        float g[8], dy[8], x[8];
-        ws[j].values(g);
-        dys[j].values(dy);
-        xs[j].values(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] *= f;
-          sum = fmaf(x[e], x[e], sum);
-          dot = fmaf(dy[e] * g[e], x[e], dot);
-        }
-      }
-    };
-    statistics();
-    row_reduce<false>(sum, dot, p.warps, room[turn]);
-    if (out_of_range(sum, p.eps)) {
-      float most = 0.0f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        float x[8];
-        xs[j].values(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) most = max_nan(most, fabsf(x[e]));
-      }
-      float none = 0.0f;
-      if (p.warps > 1) __syncthreads();
-      row_reduce<true>(none, most, p.warps, room[2]);
-      f = range_factor(most);
-      statistics();
-      row_reduce<false>(sum, dot, p.warps, room[3]);
-    }
-    const RowTerms t = row_terms(sum, dot, p.cols, p.eps, f);
+    Part<T, false> dys[N], xs[N], ds[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      float g[8], dy[8], x[8];
-      ws[j].values(g);
-      dys[j].values(dy);
-      xs[j].values(x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = x[e] * f;
-        acc[j][e] = fmaf(dy[e] * t.r, u, acc[j][e]);
-        x[e] = (dy[e] * g[e] - u * t.k) * t.r * f;
-      }
-      if (p.dresidual) {
-        ds[j].values(dy);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += dy[e];
-      }
-      write_part<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx, j * p.warps + w, lane, p.cols, x);
+      dys[j].read(static_cast<const T*>(p.dy) + row * p.lddy, j * p.warps + w, lane, p.cols);
+      xs[j].read(static_cast<const T*>(p.x) + row * p.ldx, j * p.warps + w, lane, p.cols);
+      if (p.dresidual) ds[j].read(static_cast<const T*>(p.dresidual) + row * p.ldd, j * p.warps + w, lane, p.cols);
     }
-    if (AHEAD) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        dys[j] = next_dy[j];
-        xs[j] = next_x[j];
-        ds[j] = next_d[j];
-      }
-    }
+    norm_row_backward<T, false, N>(
+        p, row, w, lane, ws, acc, room[turn], [&](int j, Pairs& v) { pairs_of(dys[j], v); }, [&](int j, Pairs& v) { pairs_of(xs[j], v); },
+        [&](int j, Pairs& v) { pairs_of(ds[j], v); });
   }
   let_successor_come();
   if (!p.partial) return;
 #pragma unroll
-  for (int j = 0; j < N; ++j) write_part<float, VEC>(p.partial + team * p.cols, j * p.warps + w, lane, p.cols, acc[j]);
+  for (int j = 0; j < N; ++j) write_pairs<float, false>(p.partial + team * p.cols, j * p.warps + w, lane, p.cols, acc[j]);
 }
 
 // Rows longer than a block's registers, in three launches: the rows' terms; the weight's sums; dx, which may overwrite
@@ -492,13 +701,12 @@ __global__ void __launch_bounds__(512) rms_norm_long_stats_kernel(const __grid_c
     }
   };
   statistics();
-  row_reduce<false>(sum, dot, p.warps, room[0]);
+  row_reduce<kSum>(sum, dot, p.warps, room[0]);
   if (out_of_range(sum, p.eps)) {
-    float none = 0.0f;
-    row_reduce<true>(none, most, p.warps, room[1]);
+    row_reduce<kMax>(sum, most, p.warps, room[1]);
     f = range_factor(most);
     statistics();
-    row_reduce<false>(sum, dot, p.warps, room[2]);
+    row_reduce<kSum>(sum, dot, p.warps, room[2]);
   }
   const RowTerms t = row_terms(sum, dot, p.cols, p.eps, f);
   if (threadIdx.x == 0) p.stats[row] = make_float4(t.f, t.r, t.k, 0.0f);
@@ -565,83 +773,155 @@ __global__ void __launch_bounds__(512) rms_norm_long_dx_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ host side
-// Warps and spans per warp of a row: one span each up to 1024 columns, so that a row's loads spread over many lanes, then two,
-// four from 8192 on, where a block has its 16 warps.
-struct Shape {
-  int warps, spans;
+constexpr int64_t kLongSpans = 64;
+constexpr int64_t kRingMost = 224 * 1024;  // shared memory of an SM's rows on their way
+// Warps that an SM's registers hold, by the spans of each.
+struct ResidentWarps {
+  int one, two, four;
 };
-Shape row_shape(int64_t cols) {
+constexpr ResidentWarps kForward{32, 32, 16}, kBackward{24, 16, 16};
+// How rows are shared out: warps and spans per warp of a row, teams per block, blocks, rows on their way.
+struct Shape {
+  bool is_long;  // more than a block's registers, or than two of its rows in shared memory
+  int warps, spans, per_block, depth;
+  int64_t blocks;
+  int threads() const { return 32 * warps * per_block; }
+};
+// `element_bytes`: of all of a row's inputs together.  A row gets a warp of its
+// own where there are enough of them to fill the SMs and four spans hold it; else more warps, so that few rows are
+// spread over more lanes.
+Shape row_shape(int64_t rows, int64_t cols, int64_t element_bytes, bool vec, const ResidentWarps& warps, int num_sms) {
   const int64_t spans = ceil_div(cols, 256);
-  if (spans <= 4) return Shape{static_cast<int>(spans), 1};
-  if (spans <= 32) return Shape{static_cast<int>(ceil_div(spans, 2)), 2};
-  return Shape{static_cast<int>(std::min<int64_t>(ceil_div(spans, 4), 16)), 4};
+  Shape s{};
+  s.warps = 16;
+  s.is_long = spans > kLongSpans;
+  if (s.is_long) return s;
+  if (spans <= 4 && rows >= 16 * num_sms) {
+    s.warps = 1;
+    s.spans = spans == 3 ? 4 : static_cast<int>(spans);
+  } else if (spans <= 4) {
+    s.warps = static_cast<int>(spans);
+    s.spans = 1;
+  } else {
+    s.spans = spans <= 32 ? 2 : 4;
+    s.warps = static_cast<int>(ceil_div(spans, s.spans));
+  }
+  s.per_block = s.warps == 1 ? 4 : 1;
+  const int64_t slot = element_bytes * 256 * s.per_block * s.warps * s.spans;
+  s.is_long = vec && 2 * slot > kRingMost;
+  if (s.is_long) {
+    s.warps = 16;
+    return s;
+  }
+  // as many blocks as the registers hold, each with as many rows on their way as the shared memory then does
+  const int64_t by_registers = std::max(1, (s.spans == 1 ? warps.one : s.spans == 2 ? warps.two : warps.four) / (s.warps * s.per_block));
+  int64_t resident = by_registers;
+  if (vec) {
+    s.depth = 4;
+    while (s.depth > 2 && resident * (s.depth * slot + 1024) > kRingMost) --s.depth;
+    resident = std::max<int64_t>(1, std::min(resident, kRingMost / (s.depth * slot + 1024)));
+  }
+  s.blocks = std::min(ceil_div(rows, s.per_block), resident * num_sms);
+  return s;
 }
-// Rows per block of `warps` warps each: four where one warp has a row.
-int rows_per_block(const Shape& s) { return s.warps == 1 ? 4 : 1; }
+template <typename T>
+size_t ring_bytes(const Shape& s, int arrays) { return static_cast<size_t>(s.threads()) * s.depth * arrays * s.spans * kPieces<T> * 16; }
 
-// Blocks of the backward kernel: as many as run at once with its registers (about 100; 16 warps per SM, or one block of 16).
-int64_t backward_blocks(int64_t rows, const Shape& s, int num_sms) {
-  const int per_block = rows_per_block(s), warps = s.warps * per_block;
-  return std::min<int64_t>(ceil_div(rows, per_block), static_cast<int64_t>(num_sms) * std::max(1, 16 / warps));
-}
 int64_t weight_slices(const oz2_rms_norm_backward_args& a, int num_sms) {
   return std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.rows, 32), 4 * num_sms / std::max<int64_t>(1, ceil_div(a.cols, 256))));
 }
+bool pieces_aligned(const void* p, int64_t ld, oz2_dtype t) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<int64_t>(dtype_bytes(t)) % 16 == 0;
+}
+bool backward_vec(const oz2_rms_norm_backward_args& a) {
+  const oz2_dtype t = static_cast<oz2_dtype>(a.dtype);
+  return pieces_aligned(nullptr, a.cols, t) && pieces_aligned(a.dy, a.lddy, t) && pieces_aligned(a.x, a.ldx, t) &&
+         pieces_aligned(a.weight, 0, t) && pieces_aligned(a.dx, a.lddx, t) && (!a.dresidual || pieces_aligned(a.dresidual, a.ldd, t));
+}
+Shape backward_shape(const oz2_rms_norm_backward_args& a, int num_sms) {
+  // (as for three inputs, with or without dresidual: the weight's sums are then the same)
+  return row_shape(a.rows, a.cols, dtype_bytes(static_cast<oz2_dtype>(a.dtype)) * 3, backward_vec(a), kBackward, num_sms);
+}
 int64_t partial_rows(const oz2_rms_norm_backward_args& a, int num_sms) {
   if (!a.dweight) return 0;
-  if (a.cols > kNormRegisterCols) return weight_slices(a, num_sms);
-  const Shape s = row_shape(a.cols);
-  return backward_blocks(a.rows, s, num_sms) * rows_per_block(s);
+  const Shape s = backward_shape(a, num_sms);
+  return s.is_long ? weight_slices(a, num_sms) : s.blocks * s.per_block;
 }
-size_t stats_bytes(const oz2_rms_norm_backward_args& a) {
-  return a.cols > kNormRegisterCols ? static_cast<size_t>(a.rows) * sizeof(float4) : 0;
+size_t stats_bytes(const oz2_rms_norm_backward_args& a, int num_sms) {
+  return backward_shape(a, num_sms).is_long ? static_cast<size_t>(a.rows) * sizeof(float4) : 0;
+}
+
+// Calls f with the kernel's spans per warp and depth as constants.
+template <typename F>
+cudaError_t with_spans(int spans, F&& f) {
+  switch (spans) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    default: return f(std::integral_constant<int, 4>());
+  }
+}
+template <typename F>
+cudaError_t with_depth(int depth, F&& f) {
+  switch (depth) {
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    default: return f(std::integral_constant<int, 4>());
+  }
+}
+
+template <typename T>
+cudaError_t forward(NormParams& p, bool vec, const DeviceResources& res, cudaStream_t st) {
+  const int arrays = p.residual ? 2 : 1;
+  const Shape s = row_shape(p.rows, p.cols, sizeof(T) * arrays, vec, kForward, res.num_sms);
+  p.warps = s.warps;
+  if (s.is_long) {
+    return vec ? launch_kernel(rms_norm_long_kernel<T, true>, p.rows, 512, 0, 1, st, p)
+               : launch_kernel(rms_norm_long_kernel<T, false>, p.rows, 512, 0, 1, st, p);
+  }
+  return with_spans(s.spans, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    if (!vec) return launch_kernel(rms_norm_ragged_kernel<T, N>, ceil_div(p.rows, s.per_block), s.threads(), 0, 1, st, p);
+    return with_depth(s.depth, [&](auto d) {
+      constexpr auto kernel = rms_norm_kernel<T, N, decltype(d)::value>;
+      const size_t smem = ring_bytes<T>(s, arrays);
+      const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
+      return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), smem, 1, st, p) : e;
+    });
+  });
 }
 
 template <typename T, bool VEC>
-cudaError_t forward(const NormParams& p, cudaStream_t st) {
-  if (p.cols > kNormRegisterCols) return launch_kernel(rms_norm_long_kernel<T, VEC>, p.rows, 32 * p.warps, 0, 1, st, p);
-  const Shape s = row_shape(p.cols);
-  const int per_block = rows_per_block(s), threads = 32 * s.warps * per_block;
-  const int64_t blocks = ceil_div(p.rows, per_block);
-  switch (s.spans) {
-    case 1: return launch_kernel(rms_norm_kernel<T, VEC, 1>, blocks, threads, 0, 1, st, p);
-    case 2: return launch_kernel(rms_norm_kernel<T, VEC, 2>, blocks, threads, 0, 1, st, p);
-    default: return launch_kernel(rms_norm_kernel<T, VEC, 4>, blocks, threads, 0, 1, st, p);
-  }
+cudaError_t backward_long(const NormBackwardParams& p, int64_t slices, cudaStream_t st) {
+  cudaError_t e = launch_kernel(rms_norm_long_stats_kernel<T, VEC>, p.rows, 512, 0, 1, st, p);
+  if (e == cudaSuccess && p.partial)
+    e = launch_kernel(rms_norm_long_weight_kernel<T, VEC>, dim3(static_cast<unsigned>(ceil_div(p.cols, 256)), static_cast<unsigned>(slices)), 256, 0,
+                      1, st, p);
+  return e == cudaSuccess ? launch_kernel(rms_norm_long_dx_kernel<T, VEC>, p.rows, 512, 0, 1, st, p) : e;
 }
 template <typename T>
-cudaError_t forward(const NormParams& p, bool vec, cudaStream_t st) {
-  return vec ? forward<T, true>(p, st) : forward<T, false>(p, st);
-}
-
-template <typename T, bool VEC>
-cudaError_t backward(const NormBackwardParams& p, const oz2_rms_norm_backward_args& a, int num_sms, cudaStream_t st) {
-  if (a.cols > kNormRegisterCols) {
-    cudaError_t e = launch_kernel(rms_norm_long_stats_kernel<T, VEC>, p.rows, 32 * p.warps, 0, 1, st, p);
-    if (e == cudaSuccess && p.partial)
-      e = launch_kernel(rms_norm_long_weight_kernel<T, VEC>,
-                        dim3(static_cast<unsigned>(ceil_div(a.cols, 256)), static_cast<unsigned>(weight_slices(a, num_sms))), 256, 0, 1, st, p);
-    return e == cudaSuccess ? launch_kernel(rms_norm_long_dx_kernel<T, VEC>, p.rows, 32 * p.warps, 0, 1, st, p) : e;
+cudaError_t backward(NormBackwardParams& p, const oz2_rms_norm_backward_args& a, const DeviceResources& res, cudaStream_t st) {
+  const bool vec = backward_vec(a);
+  const Shape s = backward_shape(a, res.num_sms);
+  p.warps = s.warps;
+  if (s.is_long) {
+    const int64_t slices = weight_slices(a, res.num_sms);
+    return vec ? backward_long<T, true>(p, slices, st) : backward_long<T, false>(p, slices, st);
   }
-  const Shape s = row_shape(a.cols);
-  const int threads = 32 * s.warps * rows_per_block(s);
-  const int64_t blocks = backward_blocks(a.rows, s, num_sms);
-  switch (s.spans) {
-    case 1: return launch_kernel(rms_norm_backward_kernel<T, VEC, 1>, blocks, threads, 0, 1, st, p);
-    case 2: return launch_kernel(rms_norm_backward_kernel<T, VEC, 2>, blocks, threads, 0, 1, st, p);
-    default: return launch_kernel(rms_norm_backward_kernel<T, VEC, 4>, blocks, threads, 0, 1, st, p);
-  }
+  return with_spans(s.spans, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    if (!vec) return launch_kernel(rms_norm_ragged_backward_kernel<T, N>, s.blocks, s.threads(), 0, 1, st, p);
+    return with_depth(s.depth, [&](auto d) {
+      constexpr auto kernel = rms_norm_backward_kernel<T, N, decltype(d)::value>;
+      const size_t smem = ring_bytes<T>(s, a.dresidual ? 3 : 2);
+      const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
+      return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), smem, 1, st, p) : e;
+    });
+  });
 }
-template <typename T>
-cudaError_t backward(const NormBackwardParams& p, const oz2_rms_norm_backward_args& a, bool vec, int num_sms, cudaStream_t st) {
-  return vec ? backward<T, true>(p, a, num_sms, st) : backward<T, false>(p, a, num_sms, st);
-}
-
-int warps_of(int64_t cols) { return cols > kNormRegisterCols ? 16 : row_shape(cols).warps; }
 
 }  // namespace
 
-cudaError_t launch_rms_norm(const oz2_rms_norm_args& a, cudaStream_t st) {
+cudaError_t launch_rms_norm(const oz2_rms_norm_args& a, const DeviceResources& res, cudaStream_t st) {
   const oz2_dtype t = static_cast<oz2_dtype>(a.dtype);
   NormParams p{};
   p.rows = a.rows;
@@ -657,23 +937,22 @@ cudaError_t launch_rms_norm(const oz2_rms_norm_args& a, cudaStream_t st) {
   p.scale = a.scale;
   p.scales = a.block ? ceil_div(a.cols, a.block) : 1;
   p.cols = static_cast<int>(a.cols);
-  p.warps = warps_of(a.cols);
   p.block = static_cast<int>(a.block);
   p.quantize = a.quantize;
-  p.bytes8 = reinterpret_cast<uintptr_t>(a.y) % 8 == 0 && a.ldy % 8 == 0;
+  p.whole = reinterpret_cast<uintptr_t>(a.y) % 8 == 0 && a.ldy % 8 == 0;
   p.eps = static_cast<float>(a.eps);
-  const bool vec = a.cols % 8 == 0 && groups_aligned(a.x, a.ldx, t) && groups_aligned(a.weight, 0, t) &&
-                   (!a.residual || groups_aligned(a.residual, a.ldr, t)) && (!a.residual_out || groups_aligned(a.residual_out, a.ldo, t)) &&
-                   (a.quantize || groups_aligned(a.y, a.ldy, t));
+  const bool vec = pieces_aligned(nullptr, a.cols, t) && pieces_aligned(a.x, a.ldx, t) && pieces_aligned(a.weight, 0, t) &&
+                   (!a.residual || pieces_aligned(a.residual, a.ldr, t)) && (!a.residual_out || pieces_aligned(a.residual_out, a.ldo, t)) &&
+                   (a.quantize || pieces_aligned(a.y, a.ldy, t));
   switch (t) {
-    case OZ2_BF16: return forward<__nv_bfloat16>(p, vec, st);
-    case OZ2_F16: return forward<__half>(p, vec, st);
-    default: return forward<float>(p, vec, st);
+    case OZ2_BF16: return forward<__nv_bfloat16>(p, vec, res, st);
+    case OZ2_F16: return forward<__half>(p, vec, res, st);
+    default: return forward<float>(p, vec, res, st);
   }
 }
 
 size_t rms_norm_backward_bytes(const oz2_rms_norm_backward_args& a, int num_sms) {
-  return stats_bytes(a) + static_cast<size_t>(partial_rows(a, num_sms)) * a.cols * 4;
+  return stats_bytes(a, num_sms) + static_cast<size_t>(partial_rows(a, num_sms)) * a.cols * 4;
 }
 
 cudaError_t launch_rms_norm_backward(const oz2_rms_norm_backward_args& a, const DeviceResources& res, cudaStream_t st) {
@@ -690,17 +969,14 @@ cudaError_t launch_rms_norm_backward(const oz2_rms_norm_backward_args& a, const 
   p.dx = a.dx;
   p.lddx = a.lddx;
   p.stats = reinterpret_cast<float4*>(res.workspace);
-  p.partial = a.dweight ? reinterpret_cast<float*>(res.workspace + stats_bytes(a)) : nullptr;
+  p.partial = a.dweight ? reinterpret_cast<float*>(res.workspace + stats_bytes(a, res.num_sms)) : nullptr;
   p.cols = static_cast<int>(a.cols);
-  p.warps = warps_of(a.cols);
   p.eps = static_cast<float>(a.eps);
-  const bool vec = a.cols % 8 == 0 && groups_aligned(a.dy, a.lddy, t) && groups_aligned(a.x, a.ldx, t) && groups_aligned(a.weight, 0, t) &&
-                   groups_aligned(a.dx, a.lddx, t) && (!a.dresidual || groups_aligned(a.dresidual, a.ldd, t));
   cudaError_t e;
   switch (t) {
-    case OZ2_BF16: e = backward<__nv_bfloat16>(p, a, vec, res.num_sms, st); break;
-    case OZ2_F16: e = backward<__half>(p, a, vec, res.num_sms, st); break;
-    default: e = backward<float>(p, a, vec, res.num_sms, st); break;
+    case OZ2_BF16: e = backward<__nv_bfloat16>(p, a, res, st); break;
+    case OZ2_F16: e = backward<__half>(p, a, res, st); break;
+    default: e = backward<float>(p, a, res, st); break;
   }
   if (e != cudaSuccess || !a.dweight) return e;
   return launch_column_sums(ColumnSums{p.partial, partial_rows(a, res.num_sms), a.dweight}, ColumnSums{}, a.cols, t, st);

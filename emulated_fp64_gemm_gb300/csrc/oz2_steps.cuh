@@ -7,9 +7,7 @@
 
 namespace oz2 {
 
-// The largest number of columns of a row that a block of the norm kernels keeps in registers; longer rows are read again.
-constexpr int64_t kNormRegisterCols = 16384;
-cudaError_t launch_rms_norm(const oz2_rms_norm_args& a, cudaStream_t st);
+cudaError_t launch_rms_norm(const oz2_rms_norm_args& a, const DeviceResources& res, cudaStream_t st);
 // Bytes of workspace that the backward pass needs.
 size_t rms_norm_backward_bytes(const oz2_rms_norm_backward_args& a, int num_sms);
 cudaError_t launch_rms_norm_backward(const oz2_rms_norm_backward_args& a, const DeviceResources& res, cudaStream_t st);
@@ -36,13 +34,48 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int i = 16; i; i >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, i);
   return v;
 }
-// Over the lanes whose numbers differ in the bits of `WIDTH` - 1.
-template <int WIDTH = 32>
 __device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float half_warp_max_nan(float v) {
 #pragma unroll
-  for (int i = WIDTH / 2; i; i >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, i));
+  for (int i = 8; i; i >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, i));
   return v;
 }
+
+// Two 32-bit operations in one instruction, each rounded to nearest.  The compiler joins a product and a sum of these into
+// one rounding; where results are defined to the bit, sums of products are taken one by one.
+__device__ __forceinline__ uint64_t pair_bits(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 bits_pair(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+// One by one, never joined with the product before.
+__device__ __forceinline__ float2 add_each(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 sub_each(float2 a, float2 b) { return make_float2(__fsub_rn(a.x, b.x), __fsub_rn(a.y, b.y)); }
 
 // Two values as e4m3, the first in the low byte; past 448 saturated, NaN stays.
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {

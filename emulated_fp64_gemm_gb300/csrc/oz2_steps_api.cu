@@ -17,7 +17,7 @@ oz2_status rms_norm(const oz2_rms_norm_args& a, cudaStream_t st) {
   DeviceResources res;
   const oz2_status e = acquire_resources(st, 0, &res);
   if (e != OZ2_OK) return e;
-  OZ2_TRY(launch_rms_norm(a, st));
+  OZ2_TRY(launch_rms_norm(a, res, st));
   return OZ2_OK;
 }
 
