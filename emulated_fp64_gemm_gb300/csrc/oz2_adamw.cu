@@ -13,7 +13,9 @@
 // 1 - beta2 of itself, far less than that, so it is rounded up or down at random, to
 // its own value on average; its draws are the dropout mask's generator over the
 // element's place and the step's number.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "oz2_steps.cuh"
 
@@ -23,7 +25,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBlock = OZ2_ADAMW_BLOCK;
 constexpr float kShortEps = 1e-12f;  // from here on a root of 2^-63 is nothing beside eps
-constexpr int kTurns = 4;  // of a CTA's warps in a long step: 8192 elements per CTA
+constexpr int kTurns = 16;  // of a CTA's warps in a long step: 32768 elements per CTA
 
 // The tensors of one launch.  A kernel's arguments may take 32764 bytes; few tensors get the short form, whose launch copies less.
 template <int MOST>
@@ -54,7 +56,7 @@ struct AdamwParams {
   int last;   // the call's last launch: counts the step
 };
 
-// What all elements of a launch share.
+// What all elements of a launch share; formed by one thread of each CTA.
 struct StepFactors {
   float keep;     // 1 - lr weight_decay
   float rate;     // lr / (1 - beta1^t)
@@ -77,7 +79,8 @@ __device__ __forceinline__ float fourth(float k) { return fourth2(both(k)).x; }
 
 // 2^23 + byte i of a word, or + half i: a whole number as a float without a conversion.
 constexpr float kWhole = 8388608.0f;
-__device__ __forceinline__ float whole_byte(uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + i)); }
+__device__ __forceinline__ float whole_byte(uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 + i)); }
+__device__ __forceinline__ float whole_half(uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4B000000u, i ? 0x7632 : 0x7610)); }
 __device__ __forceinline__ float fast_rsqrt(float t) {  // infinity for 0, 0 for infinity
   float r;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
@@ -94,34 +97,33 @@ __device__ __forceinline__ uint32_t encode_fourth(float t, uint32_t draw) {
   return static_cast<uint32_t>(fminf(k + (up ? 1.0f : 0.0f), 255.0f));
 }
 
-// The codes of eight, in two words.  k is floor(t^(1/4)) of an approximate root that is never too large: off by one only
-// just above a step, where t is then at or above the step after k.  That, and 0 < t < 1, are left to the form above.  A t of
+// The codes of eight, in two words: k is the whole number next to an approximate root, or the one before where its fourth
+// power is above t (just above a step is where a step of the optimiser leaves many elements, so no approximation decides
+// there); the step it belongs to ends at the neighbour on the other side.  0 < t < 1 is left to the form above.  A t of
 // 255^4, the largest of a block, is taken for the number before it, which is rounded up to 255 by every draw.
 __device__ __forceinline__ uint2 encode_fourths(const float2 (&v)[4], float inverse, const uint4& draws) {
   constexpr float kMost = 4228250368.0f;  // before fl(255^4)
   const uint32_t d[4] = {draws.x, draws.y, draws.z, draws.w};
   float2 t[4];
   uint32_t code[8];
-  bool rare = false;
+  float least = 1.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     t[i] = mul2(v[i], both(inverse));
     t[i] = make_float2(fminf(t[i].x, kMost), fminf(t[i].y, kMost));
-    // (an approximate reciprocal root is off by 2^-22, and the second one halves what the first has)
-    float2 k = make_float2(__fmaf_rd(fast_rsqrt(fast_rsqrt(t[i].x)), 1.0f - 0x1p-21f, kWhole),
-                           __fmaf_rd(fast_rsqrt(fast_rsqrt(t[i].y)), 1.0f - 0x1p-21f, kWhole));
+    float2 k = add2(make_float2(fast_rsqrt(fast_rsqrt(t[i].x)), fast_rsqrt(fast_rsqrt(t[i].y))), both(kWhole));
     const uint32_t k0 = __float_as_uint(k.x), k1 = __float_as_uint(k.y);
     k = add2(k, both(-kWhole));
-    const float2 low = fourth2(k), high = fourth2(add2(k, both(1.0f)));
-    // draw / 2^16: 1 + it is the half in the fraction of a float
-    const float2 draw = add2(make_float2(__uint_as_float(0x3F800000u | (d[i] << 7 & 0x007FFF80u)), __uint_as_float(0x3F800000u | (d[i] >> 9 & 0x007FFF80u))),
-                             both(-1.0f));
-    const float2 above = sub_each(t[i], low), limit = mul2(draw, sub_each(high, low));
-    code[2 * i] = k0 + (above.x > limit.x);
-    code[2 * i + 1] = k1 + (above.y > limit.y);
-    rare = rare || t[i].x < 1.0f || t[i].y < 1.0f || high.x <= t[i].x || high.y <= t[i].y;
+    const float2 near = fourth2(k);
+    const bool b0 = near.x > t[i].x, b1 = near.y > t[i].y;
+    const float2 far = fourth2(add2(k, make_float2(b0 ? -1.0f : 1.0f, b1 ? -1.0f : 1.0f)));
+    // draw / 2^16
+    const float2 draw = fma2(make_float2(whole_half(d[i], 0), whole_half(d[i], 1)), both(0x1p-16f), both(-kWhole * 0x1p-16f));
+    code[2 * i] = k0 - b0 + (__fsub_rn(t[i].x, fminf(near.x, far.x)) > __fmul_rn(draw.x, fabsf(__fsub_rn(near.x, far.x))));
+    code[2 * i + 1] = k1 - b1 + (__fsub_rn(t[i].y, fminf(near.y, far.y)) > __fmul_rn(draw.y, fabsf(__fsub_rn(near.y, far.y))));
+    least = fminf(least, fminf(t[i].x, t[i].y));
   }
-  if (rare) {
+  if (least < 1.0f) {
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {  // one copy of the code; the element is picked from registers
       float x = 0.0f;
@@ -153,19 +155,82 @@ __device__ __forceinline__ float state_scale(float top, float unit) {
 }
 
 // ------------------------------------------------------------------ the step
-// Eight elements of a lane as pairs: n of them (8, or fewer at a tensor's end, zeros after them).
+// Eight elements of a lane: n of them (8, or fewer at a tensor's end, zeros after them); vec: whole ones lie on boundaries
+// of their size.
 template <typename T>
-__device__ __forceinline__ void read8(const T* p, int n, float2 (&v)[4]) {
+__device__ __forceinline__ void read8(const T* p, bool vec, int n, Raw8<T>& raw) {
+  if (vec && n == 8) {
+    raw.read(p);
+  } else {
+    T* out = reinterpret_cast<T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = i < n ? p[i] : Elem<T>::down(0.0f);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void values(const Raw8<T>& raw, float2 (&v)[4]) {
   float f[8];
-  load8(p, n == 8 && reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0, n, f);
+  raw.values(f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
 }
 template <typename T>
-__device__ __forceinline__ void write8(T* p, int n, const float2 (&v)[4]) {
+__device__ __forceinline__ void write8(T* p, bool vec, int n, const float2 (&v)[4]) {
   const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-  store8(p, n == 8 && reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0, n, f);
+  store8(p, vec && n == 8, n, f);
 }
+template <typename T>
+__device__ __forceinline__ bool on_boundary(const T* p) { return reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0; }
+
+// What a lane reads of a block of 256 elements.
+template <typename P, typename G, int BITS, bool MASTER>
+struct Block {
+  Raw8<std::conditional_t<MASTER, float, P>> w;
+  Raw8<G> g;
+  Raw8<float> m, v;   // 32 bits
+  uint2 qm, qv;       // 8 bits
+  float sm, sv;
+  int n;
+  __device__ __forceinline__ void read(const AdamwParams& p, const P* param, const G* grad, int64_t elements, int64_t block, int64_t state_block,
+                                       int lane, bool vec_param, bool vec_grad, bool vec_state) {
+    const int64_t e0 = block * kBlock + lane * 8, s0 = (state_block + block) * kBlock + lane * 8, left = elements - e0;
+    n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+    if constexpr (MASTER) read8(p.master + s0, vec_state, n, w);
+    else read8(param + e0, vec_param, n, w);
+    read8(grad + e0, vec_grad, n, g);
+    if constexpr (BITS == 32) {
+      read8(static_cast<const float*>(p.exp_avg) + s0, vec_state, n, m);
+      read8(static_cast<const float*>(p.exp_avg_sq) + s0, vec_state, n, v);
+    } else {
+      // whole groups: the gaps behind a tensor's end are there to be read
+      qm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.exp_avg) + s0);
+      qv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.exp_avg_sq) + s0);
+      sm = p.exp_avg_scale[state_block + block];
+      sv = p.exp_avg_sq_scale[state_block + block];
+    }
+  }
+  __device__ __forceinline__ void moments(float2 (&mv)[4], float2 (&vv)[4]) const {
+    if constexpr (BITS == 32) {
+      values(m, mv);
+      values(v, vv);
+    } else {
+      const uint32_t um[2] = {qm.x, qm.y}, uv[2] = {qv.x, qv.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mv[i] = mul2(unpack_e4m3(um[i >> 1] >> (16 * (i & 1)) & 0xFFFFu), both(sm));
+        const float2 k = add2(make_float2(whole_byte(uv[i >> 1], 2 * (i & 1)), whole_byte(uv[i >> 1], 2 * (i & 1) + 1)), both(-kWhole));
+        vv[i] = mul2(fourth2(k), both(sv));
+      }
+      if (n < 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (2 * i >= n) mv[i].x = vv[i].x = 0.0f;
+          if (2 * i + 1 >= n) mv[i].y = vv[i].y = 0.0f;
+        }
+      }
+    }
+  }
+};
 
 // 1 / (sqrt(x) + eps).  TINY: eps is so small that a root below 2^-63, which the short form takes for 0, is to be seen beside it.
 template <bool TINY>
@@ -188,8 +253,11 @@ __device__ __forceinline__ void move(const StepFactors& f, float eps, const floa
   }
 }
 
+// With 8-bit states a warp has its next block on its way while it works on one: there is enough to do in between.
 template <typename P, typename G, int BITS, bool MASTER, int MOST>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Tensors<MOST> tensors, const __grid_constant__ AdamwParams p) {
+  __shared__ StepFactors factors;
+  __shared__ int done;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // the tensor whose chunks this CTA's number is among: the last one that starts at it or before
   int at = 0;
@@ -197,57 +265,48 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   for (int step = MOST <= 32 ? 16 : 512; step; step >>= 1)
     if (at + step < p.count && tensors.chunk[at + step] <= static_cast<int>(blockIdx.x)) at += step;
   const int64_t elements = tensors.elements[at];
-  const int64_t first = static_cast<int64_t>(blockIdx.x - tensors.chunk[at]) * (p.turns * kWarps);
   P* param = static_cast<P*>(tensors.param[at]);
   const G* grad = static_cast<const G*>(tensors.grad[at]);
   const int64_t state_block = tensors.block[at];
+  const bool vec_param = on_boundary(param), vec_grad = on_boundary(grad);
+  const bool vec_state = (BITS == 8 || (on_boundary(static_cast<float*>(p.exp_avg)) && on_boundary(static_cast<float*>(p.exp_avg_sq)))) &&
+                         (!MASTER || on_boundary(p.master));
+  int64_t block = static_cast<int64_t>(blockIdx.x - tensors.chunk[at]) * (p.turns * kWarps) + warp;
+  const int64_t end = min(block - warp + p.turns * kWarps, (elements + kBlock - 1) / kBlock);
   wait_for_predecessor();
   let_successor_come();
-  StepFactors f;
-  {
+  Block<P, G, BITS, MASTER> next;
+  if (BITS == 8 && block < end) next.read(p, param, grad, elements, block, state_block, lane, vec_param, vec_grad, vec_state);
+  if (threadIdx.x == 0) {
     const int64_t t = p.step[0] + 1;
     const float lr = p.lr_device ? *p.lr_device : p.lr;
+    StepFactors f;
     f.keep = 1.0f - lr * p.weight_decay;
     f.rate = lr / -expm1f(static_cast<float>(t) * p.log_beta1);
     f.root2 = 1.0f / -expm1f(static_cast<float>(t) * p.log_beta2);
     f.grad_scale = p.grad_scale_device ? *p.grad_scale_device : p.grad_scale;
     f.t0 = static_cast<uint32_t>(t);
     f.t1 = static_cast<uint32_t>(static_cast<uint64_t>(t) >> 32);
+    factors = f;
+    done = 0;
   }
+  __syncthreads();
+  const StepFactors f = factors;
 #pragma unroll 1
-  for (int turn = 0; turn < p.turns; ++turn) {
-    const int64_t block = first + turn * kWarps + warp, e0 = block * kBlock + lane * 8;
-    if (block * kBlock >= elements) break;
-    const int64_t left = elements - e0;
-    const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
-    const int64_t s0 = (state_block + block) * kBlock + lane * 8;  // of the flat states, which start on boundaries of 256 bytes or are read one by one
-    float2 w[4], g[4], m[4], v[4];
-    if (MASTER) read8(p.master + s0, n, w);
-    else read8(param + e0, n, w);
-    read8(grad + e0, n, g);
-    if (BITS == 32) {
-      read8(static_cast<const float*>(p.exp_avg) + s0, n, m);
-      read8(static_cast<const float*>(p.exp_avg_sq) + s0, n, v);
+  for (; block < end; block += kWarps) {
+    Block<P, G, BITS, MASTER> now;
+    if (BITS == 8) {
+      now = next;
+      if (block + kWarps < end) next.read(p, param, grad, elements, block + kWarps, state_block, lane, vec_param, vec_grad, vec_state);
     } else {
-      // whole groups: the gaps behind a tensor's end are there to be read
-      const uint2 qm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.exp_avg) + s0);
-      const uint2 qv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.exp_avg_sq) + s0);
-      const float2 sm = both(p.exp_avg_scale[state_block + block]), sv = both(p.exp_avg_sq_scale[state_block + block]);
-      const uint32_t um[2] = {qm.x, qm.y}, uv[2] = {qv.x, qv.y};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        m[i] = mul2(unpack_e4m3(um[i >> 1] >> (16 * (i & 1)) & 0xFFFFu), sm);
-        const float2 k = add2(make_float2(whole_byte(uv[i >> 1], 2 * (i & 1)), whole_byte(uv[i >> 1], 2 * (i & 1) + 1)), both(-kWhole));
-        v[i] = mul2(fourth2(k), sv);
-      }
-      if (n < 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (2 * i >= n) m[i].x = v[i].x = 0.0f;
-          if (2 * i + 1 >= n) m[i].y = v[i].y = 0.0f;
-        }
-      }
+      now.read(p, param, grad, elements, block, state_block, lane, vec_param, vec_grad, vec_state);
     }
+    const int n = now.n;
+    const int64_t e0 = block * kBlock + lane * 8, s0 = (state_block + block) * kBlock + lane * 8;
+    float2 w[4], g[4], m[4], v[4];
+    values(now.w, w);
+    values(now.g, g);
+    now.moments(m, v);
     // one rounding at a time: 8-bit states are defined to the bit
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -257,17 +316,17 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     }
     if (p.eps >= kShortEps) move<false>(f, p.eps, m, v, w);
     else move<true>(f, p.eps, m, v, w);
-    if (MASTER) write8(p.master + s0, n, w);
-    write8(param + e0, n, w);
+    if (MASTER) write8(p.master + s0, vec_state, n, w);
+    write8(param + e0, vec_param, n, w);
     if (BITS == 32) {
-      write8(static_cast<float*>(p.exp_avg) + s0, n, m);
-      write8(static_cast<float*>(p.exp_avg_sq) + s0, n, v);
+      write8(static_cast<float*>(p.exp_avg) + s0, vec_state, n, m);
+      write8(static_cast<float*>(p.exp_avg_sq) + s0, vec_state, n, v);
     } else {
       float top_m = 0.0f, top_v = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        top_m = max_nan(top_m, max_nan(fabsf(m[i].x), fabsf(m[i].y)));
-        top_v = max_nan(top_v, max_nan(v[i].x, v[i].y));
+        top_m = max_abs_nan(top_m, m[i].x, m[i].y);
+        top_v = max_nan(top_v, v[i].x, v[i].y);
       }
       top_v = warp_max_nan(top_v);
       const float sm = state_scale(warp_max_nan(top_m), 1.0f / 448.0f), sv = state_scale(top_v, kFourth);
@@ -302,13 +361,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     }
   }
   if (!p.last) return;
-  // the last CTA to arrive counts the step: all others have read its number by then
-  __syncthreads();
-  if (threadIdx.x) return;
-  __threadfence();
-  if (atomicAdd(reinterpret_cast<unsigned long long*>(p.step + 1), 1ull) + 1 == gridDim.x) {
-    p.step[1] = 0;
-    p.step[0] += 1;
+  // the last warp of the last CTA counts the step: all others have read its number by then
+  if (lane == 0 && atomicAdd(&done, 1) == kWarps - 1) {
+    __threadfence();
+    if (atomicAdd(reinterpret_cast<unsigned long long*>(p.step + 1), 1ull) + 1 == gridDim.x) {
+      p.step[1] = 0;
+      p.step[0] += 1;
+    }
   }
 }
 
@@ -378,7 +437,7 @@ cudaError_t launch_adamw(const oz2_adamw_args& a, const DeviceResources& res, cu
   // one turn per warp until the CTAs fill the SMs several times over
   int64_t elements = 0;
   for (int64_t i = 0; i < a.count; ++i) elements += a.tensors[i].elements;
-  p.turns = elements >= static_cast<int64_t>(res.num_sms) * 16 * kBlock * kWarps * kTurns ? kTurns : 1;
+  p.turns = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kTurns, elements / (static_cast<int64_t>(res.num_sms) * 8 * kBlock * kWarps))));
   p.exp_avg = a.exp_avg;
   p.exp_avg_sq = a.exp_avg_sq;
   p.exp_avg_scale = a.exp_avg_scale;

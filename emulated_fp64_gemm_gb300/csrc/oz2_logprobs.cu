@@ -3,14 +3,14 @@
 //
 // Forward: one pass over the logits.  Each thread keeps the running maximum m of
 // its elements, s = sum 2^d and t = sum 2^d d with d = c x - fl(c m), c = log2(e) /
-// temperature: one FFMA, one EX2 and one or two sums per element, and what was
-// summed before is rescaled where the maximum grows (seldom after a thread's first
-// elements).  A row belongs to one block, or with few rows to a cluster of up to
-// eight, which join their parts through distributed shared memory.
+// temperature: per pair of elements one packed FFMA, two EX2 and one or two packed
+// sums, and what was summed before is rescaled where the maximum grows (seldom after a
+// thread's first elements).  A row belongs to one block, or with few rows to a
+// cluster of up to eight, which join their parts through distributed shared memory.
 //
 // Everything past the pass uses that a thread's elements can be found again:
-//  * the k-th largest of the maxima of groups of eight threads is a lower bound of the
-//    k-th largest logit, so that only threads whose own maximum reaches it can hold
+//  * the k-th largest of the maxima of groups of threads is a lower bound of the k-th
+//    largest logit, so that only threads whose own maximum reaches it can hold
 //    alternatives: a few dozen, whose elements are read again (from L2);
 //  * where one token has almost all of the probability, its log p is -log1p of the others'
 //    sum, which 32 bits have lost beside it: the elements of the thread that holds the
@@ -19,7 +19,8 @@
 // Bound by HBM, and not far from it by the exponential unit: 16 per SM and cycle are
 // 4.7e12 per second, 2-byte logits at the measured copy rate 3.4e12.
 #include <algorithm>
-#include <cmath>
+#include <cstring>
+#include <type_traits>
 
 #include "oz2_pair.cuh"
 #include "oz2_steps.cuh"
@@ -27,11 +28,7 @@
 namespace oz2 {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kVectors = 4;         // of eight elements, in flight per thread
-constexpr int kGroups = 64;         // of eight threads
-constexpr int kCandidates = 2304;   // past the elements of a slice that has fewer vectors than 32 groups have threads
-constexpr int kJobs = 128;
 constexpr float kExtreme = 1e30f;   // |x| c from here on: c x may overflow, the row is summed as (x - max) c
 constexpr float kLeast = -150.0f;   // 2^d is zero below (and at) it, and its product with d stays zero for d = -inf
 constexpr float kLn2 = 0.6931471805599453f;
@@ -43,6 +40,7 @@ struct LogprobParams {
   float *logprobs, *z_max, *log_sum, *entropy, *top_logprobs;
   int64_t* top_ids;
   float inv_t, c, low;  // low = -kExtreme / c
+  uint32_t floor2;      // low as two bfloat16, towards zero: c times it is finite, and 2^ of that 0
   int top, ranks;
 };
 
@@ -74,8 +72,8 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(
 __device__ __forceinline__ uint64_t place_key(uint32_t key, uint32_t column) { return static_cast<uint64_t>(key) << 32 | (0xFFFFFFFFu - column); }
 
 // A block's part of a row: `lead` single elements up to a boundary of groups of eight, groups, single ones behind them.
-// The single ones are threads 0 .. 7's and 8 .. 15's; group v0 + i is thread i % kThreads'.
-template <typename T>
+// The single ones are threads 0 .. 7's and 8 .. 15's; group v0 + i is thread i % THREADS'.
+template <typename T, int THREADS>
 struct Slice {
   const T* row;
   const T* groups;
@@ -105,7 +103,7 @@ struct Slice {
   template <typename F>
   __device__ __forceinline__ void again(int t, int lane, int lanes, F&& f) const {
     const int base = static_cast<int>(groups - row);
-    for (int64_t v = v0 + t + static_cast<int64_t>(lane) * kThreads; v < v1; v += static_cast<int64_t>(lanes) * kThreads) {
+    for (int64_t v = v0 + t + static_cast<int64_t>(lane) * THREADS; v < v1; v += static_cast<int64_t>(lanes) * THREADS) {
       Raw8<T> raw;
       float x[8];
       raw.read(groups + v * 8);
@@ -118,44 +116,63 @@ struct Slice {
   }
 };
 
-// A thread's running statistics: mc = fl(c m), 0 while there is no element but -inf.
-template <bool ENTROPY>
+// A thread's running statistics: mc = fl(c m), 0 while there is no element but -inf; s and t in two halves each.
+template <typename T, bool ENTROPY>
 struct Running {
-  float m = -infinity(), mc = 0.0f, s = 0.0f, t = 0.0f;
+  float m = -infinity(), mc = 0.0f;
+  float2 s = make_float2(0.0f, 0.0f), t = make_float2(0.0f, 0.0f);
   __device__ __forceinline__ void raise(float top, const LogprobParams& p) {
     if (top <= m || m != m) return;  // a NaN comes in, and stays
     const float mc_new = top * p.c;
     if (m < p.low) {  // nothing before counts (and its sums may be lost)
-      s = t = 0.0f;
+      s = t = both(0.0f);
     } else {
-      const float f = fast_exp2(mc - mc_new);
-      if (ENTROPY) t = f * fmaf(s, fmaxf(mc - mc_new, kLeast), t);
-      s *= f;
+      const float2 f = both(fast_exp2(mc - mc_new));
+      if (ENTROPY) t = mul2(f, fma2(s, both(fmaxf(mc - mc_new, kLeast)), t));
+      s = mul2(s, f);
     }
     m = top;
     mc = mc_new;
   }
-  __device__ __forceinline__ void add(float x, float c) {
-    float d = fmaf(x, c, -mc);
-    if (ENTROPY) d = fmaxf(d, kLeast);
-    const float e = fast_exp2(d);
-    s += e;
-    if (ENTROPY) t = fmaf(e, d, t);
+  // d = -inf must not meet the product with 2^d = 0: it is limited, in bfloat16 already in x, two at a time (see floor2)
+  static constexpr bool LIMITED = sizeof(T) == 2 && std::is_same_v<T, __nv_bfloat16>;
+  __device__ __forceinline__ void add(float2 x, float c) {
+    float2 d = fma2(x, both(c), both(-mc));
+    if (ENTROPY && !LIMITED) d = make_float2(fmaxf(d.x, kLeast), fmaxf(d.y, kLeast));
+    const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+    s = add2(s, e);
+    if (ENTROPY) t = fma2(e, d, t);
   }
-  template <typename T, int N>
-  __device__ __forceinline__ void add_groups(const Raw8<T> (&raw)[N], const LogprobParams& p) {
+  __device__ __forceinline__ void add_single(float x, const LogprobParams& p) {
+    raise(x, p);
+    float d = fmaf(x, p.c, -mc);
+    d = fmaxf(d, kLeast);
+    const float e = fast_exp2(d);
+    s.x += e;
+    if (ENTROPY) t.x = fmaf(e, d, t.x);
+  }
+  template <int N>
+  __device__ __forceinline__ void add_groups(Raw8<T> (&raw)[N], const LogprobParams& p) {
     float top = top8(raw[0]);
 #pragma unroll
     for (int i = 1; i < N; ++i) top = max_nan(top, top8(raw[i]));
     raise(top, p);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+      if constexpr (ENTROPY && LIMITED) {
+        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw[i].u);
+        const __nv_bfloat162 least = *reinterpret_cast<const __nv_bfloat162*>(&p.floor2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = __hmax2(h[j], least);
+      }
       float x[8];
       raw[i].values(x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) add(x[e], p.c);
+      for (int j = 0; j < 4; ++j) add(make_float2(x[2 * j], x[2 * j + 1]), p.c);
     }
   }
+  __device__ __forceinline__ float sum() const { return s.x + s.y; }
+  __device__ __forceinline__ float bent() const { return t.x + t.y; }
 };
 
 // What the elements of a thread, a block or a row are beside their row's maximum: how many are equal to it, the sum of
@@ -164,20 +181,27 @@ struct Parts {
   float equal, rest, bent;
 };
 
+template <int THREADS>
 struct Shared {
+  static constexpr int kWarps = THREADS / 32;
+  static constexpr int kGroups = THREADS < 64 ? THREADS : 64;
+  // candidates: past the elements of a slice that reaches fewer than 32 groups (their threads have one vector each)
+  static constexpr int kCandidates = THREADS == 32 ? 512 : 6 * THREADS;
+  static constexpr int kJobs = THREADS < 64 ? THREADS : 64;
   uint64_t candidates[kCandidates];
-  uint64_t list[OZ2_TOP_MAX];       // the block's alternatives, in order
+  uint64_t list[OZ2_TOP_MAX];  // the block's alternatives, in order
   uint64_t merged[8 * OZ2_TOP_MAX];
   uint32_t group_top[kGroups];
-  uint16_t jobs[kThreads];
-  float warp_top[kWarps];
+  uint16_t jobs[THREADS];
+  float warp_top[32];
   Parts warp_parts[kWarps];
   uint32_t warp_counts[kWarps];
-  float top;      // of the block
-  Parts parts;    // of the block
+  float top;    // of the block
+  Parts parts;  // of the block, relative to it
   uint32_t threshold, count, job_count;
   uint64_t best;
 };
+static_assert(Shared<32>::kCandidates >= 31 * 8 + 15 && Shared<128>::kCandidates >= 63 * 8 + 15 && Shared<256>::kCandidates >= 127 * 8 + 15, "");
 
 __device__ __forceinline__ float load_cluster(const float* mine, int rank) {
   float v;
@@ -189,39 +213,30 @@ __device__ __forceinline__ uint64_t load_cluster(const uint64_t* mine, int rank)
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to_rank(smem_u32(mine), rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ void row_sync(int ranks) {
-  if (ranks > 1) cluster_sync_all();
-  else __syncthreads();
-}
 
-// Every thread's parts summed over the block, in a fixed order, into sh.parts (to be read behind a barrier).
-__device__ __forceinline__ void sum_parts(Shared& sh, Parts v) {
+__device__ __forceinline__ Parts warp_parts_sum(Parts v) {
   v.equal = warp_sum(v.equal);
   v.rest = warp_sum(v.rest);
   v.bent = warp_sum(v.bent);
+  return v;
+}
+// Every thread's parts summed over the block, in a fixed order.  sh.warp_parts is free again behind the next barrier.
+template <int THREADS>
+__device__ __forceinline__ Parts sum_parts(Shared<THREADS>& sh, Parts v) {
+  v = warp_parts_sum(v);
+  if (THREADS == 32) return v;
   if ((threadIdx.x & 31) == 0) sh.warp_parts[threadIdx.x >> 5] = v;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    Parts a = sh.warp_parts[0];
-    for (int i = 1; i < kWarps; ++i) {
-      a.equal += sh.warp_parts[i].equal;
-      a.rest += sh.warp_parts[i].rest;
-      a.bent += sh.warp_parts[i].bent;
-    }
-    sh.parts = a;
+  v = sh.warp_parts[0];
+#pragma unroll
+  for (int i = 1; i < THREADS / 32; ++i) {
+    v.equal += sh.warp_parts[i].equal;
+    v.rest += sh.warp_parts[i].rest;
+    v.bent += sh.warp_parts[i].bent;
   }
+  return v;
 }
-__device__ __forceinline__ Parts row_parts(const Shared& sh, int ranks) {
-  if (ranks == 1) return sh.parts;
-  Parts a{0.0f, 0.0f, 0.0f};
-  for (int i = 0; i < ranks; ++i) {
-    a.equal += load_cluster(&sh.parts.equal, i);
-    a.rest += load_cluster(&sh.parts.rest, i);
-    a.bent += load_cluster(&sh.parts.bent, i);
-  }
-  return a;
-}
-// An element's part relative to the row's maximum, free of cancellation.
+// An element's part relative to the maximum, free of cancellation.
 __device__ __forceinline__ void add_exactly(Parts& a, float x, float top, float c) {
   if (x == top) {
     a.equal += 1.0f;
@@ -231,29 +246,35 @@ __device__ __forceinline__ void add_exactly(Parts& a, float x, float top, float 
     a.bent = fmaf(e, d, a.bent);
   }
 }
+// Parts relative to `from` as parts relative to a larger maximum.
+__device__ __forceinline__ Parts relative_to(float top, float from, Parts v, float c) {
+  if (from == top || !(from > -infinity())) return v;
+  const float d = fmaxf((from - top) * c, kLeast), e = fast_exp2(d), all = v.equal + v.rest;
+  return Parts{0.0f, e * all, e * fmaf(d, all, v.bent)};
+}
 
 // ------------------------------------------------------------------ alternatives
-// The block's `top` largest place keys into sh.list, in order (0: there are fewer).  m: the thread's largest element.
-template <typename T>
-__device__ __forceinline__ void collect_at_least(Shared& sh, const Slice<T>& s, uint32_t least) {
+// The block's `top` largest place keys go into sh.list, in order (0: there are fewer).
+template <typename T, int THREADS>
+__device__ __forceinline__ void collect_at_least(Shared<THREADS>& sh, const Slice<T, THREADS>& s, uint32_t least) {
   const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
-  for (uint32_t j = half; j < sh.job_count; j += kThreads / 16)
+  for (uint32_t j = half; j < sh.job_count; j += THREADS / 16)
     s.again(sh.jobs[j], lane, 16, [&](float x, int column) {
       const uint32_t k = order_key(x);
       if (k < least) return;
       const uint32_t at = atomicAdd(&sh.count, 1u);  // the order is made up for by the sorting
-      if (at < kCandidates) sh.candidates[at] = place_key(k, column);
+      if (at < Shared<THREADS>::kCandidates) sh.candidates[at] = place_key(k, column);
     });
 }
 
 // The elements equal to the threshold, from the lowest place on, until there are `top` candidates.
-template <typename T>
-__device__ __forceinline__ void collect_equal(Shared& sh, const Slice<T>& s, int top) {
+template <typename T, int THREADS>
+__device__ __forceinline__ void collect_equal(Shared<THREADS>& sh, const Slice<T, THREADS>& s, int top) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, end = s.last_column();
   uint32_t have = sh.count;
   const uint32_t key = sh.threshold, want = static_cast<uint32_t>(top);
   __syncthreads();
-  for (int64_t c0 = s.first_column(); c0 < end && have < want; c0 += 8 * kThreads) {
+  for (int64_t c0 = s.first_column(); c0 < end && have < want; c0 += 8 * THREADS) {
     uint32_t equal = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -268,7 +289,7 @@ __device__ __forceinline__ void collect_equal(Shared& sh, const Slice<T>& s, int
     if (lane == 31) sh.warp_counts[warp] = before;
     __syncthreads();
     uint32_t at = have + before - __popc(equal), all = 0;
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < THREADS / 32; ++i) {
       if (i < warp) at += sh.warp_counts[i];
       all += sh.warp_counts[i];
     }
@@ -286,8 +307,8 @@ __device__ __forceinline__ void collect_equal(Shared& sh, const Slice<T>& s, int
 
 // One alternative after the other, each the largest below the one before: for rows where more elements than there is
 // room for reach the threshold (many large logits in a few threads' elements).  Reads the slice `top` times.
-template <typename T>
-__device__ __forceinline__ void collect_in_turn(Shared& sh, const Slice<T>& s, int top) {
+template <typename T, int THREADS>
+__device__ __forceinline__ void collect_in_turn(Shared<THREADS>& sh, const Slice<T, THREADS>& s, int top) {
   uint64_t limit = ~uint64_t(0);
   for (int i = 0; i < top; ++i) {
     uint64_t best = 0;
@@ -310,59 +331,72 @@ __device__ __forceinline__ void collect_in_turn(Shared& sh, const Slice<T>& s, i
   if (threadIdx.x == 0) sh.count = top;
 }
 
-template <typename T>
-__device__ __forceinline__ void find_alternatives(Shared& sh, const Slice<T>& s, float m, int top) {
+// m: the thread's largest element.
+template <typename T, int THREADS>
+__device__ __forceinline__ void find_alternatives(Shared<THREADS>& sh, const Slice<T, THREADS>& s, float m, int top) {
+  using S = Shared<THREADS>;
   const int tid = threadIdx.x;
   const uint32_t mine = s.has(tid) ? order_key(m) : 0u;
   uint32_t k = mine;
 #pragma unroll
-  for (int i = 1; i < 8; i <<= 1) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, i));
-  if ((tid & 7) == 0) sh.group_top[tid >> 3] = k;
+  for (int i = 1; i < THREADS / S::kGroups; i <<= 1) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, i));
+  if (tid % (THREADS / S::kGroups) == 0) sh.group_top[tid / (THREADS / S::kGroups)] = k;
   if (tid < OZ2_TOP_MAX) sh.list[tid] = 0;
   if (tid == 0) sh.count = sh.job_count = 0;
   __syncthreads();
-  if (tid < kGroups) {
+  if (tid < S::kGroups) {
     k = sh.group_top[tid];
     int above = 0;
-    for (int i = 0; i < kGroups; ++i) above += sh.group_top[i] > k || (sh.group_top[i] == k && i < tid);
+#pragma unroll 8
+    for (int i = 0; i < S::kGroups; ++i) above += sh.group_top[i] > k || (sh.group_top[i] == k && i < tid);
     if (above == top - 1) sh.threshold = k;
   }
   __syncthreads();
+  // threads that hold elements at the threshold or above
   const uint32_t threshold = sh.threshold;
-  // threads that hold elements at the threshold or above; where these are many (masked rows, whose threshold is -inf), only
-  // those above, and the lowest places at the threshold by a search in order
-  const int reach = __syncthreads_count(mine && mine >= threshold);
-  const uint32_t least = reach <= kJobs ? max(threshold, 1u) : threshold + 1;  // (no key is 0xFFFFFFFF + 1: see below)
-  const bool all_nan = threshold == 0xFFFFFFFFu && reach > kJobs;               // nothing is above NaN
-  if (mine >= least && !all_nan && mine) sh.jobs[atomicAdd(&sh.job_count, 1u)] = static_cast<uint16_t>(tid);
+  if (mine && mine >= threshold) sh.jobs[atomicAdd(&sh.job_count, 1u)] = static_cast<uint16_t>(tid);
   __syncthreads();
-  collect_at_least(sh, s, least);
+  const bool many = sh.job_count > S::kJobs;
+  if (many) {
+    // (masked rows, whose threshold is -inf, or constant ones): only those above it, and then the lowest places at it by a
+    // search in order
+    __syncthreads();
+    if (tid == 0) sh.job_count = 0;
+    __syncthreads();
+    if (mine > threshold) sh.jobs[atomicAdd(&sh.job_count, 1u)] = static_cast<uint16_t>(tid);
+    __syncthreads();
+  }
+  // (nothing is above the largest key, that of NaN, and no thread has a job then)
+  collect_at_least(sh, s, many ? threshold + 1 : max(threshold, 1u));
   __syncthreads();
-  if (sh.count > kCandidates) {
+  if (sh.count > S::kCandidates) {
     __syncthreads();
     collect_in_turn(sh, s, top);
-  } else if (reach > kJobs && sh.count < static_cast<uint32_t>(top)) {
+    __syncthreads();
+  } else if (many && sh.count < static_cast<uint32_t>(top)) {
     collect_equal(sh, s, top);
+    __syncthreads();
   }
-  __syncthreads();
   const int n = static_cast<int>(sh.count);
-  for (int i = tid; i < n; i += kThreads) {
+  for (int i = tid; i < n; i += THREADS) {
     const uint64_t key = sh.candidates[i];
     int above = 0;
-    for (int j = 0; j < n && above < top; ++j) above += sh.candidates[j] > key;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) above += sh.candidates[j] > key;
     if (above < top) sh.list[above] = key;
   }
 }
 
 // ------------------------------------------------------------------ forward
-template <typename T, bool ENTROPY>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const __grid_constant__ LogprobParams p) {
-  __shared__ Shared sh;
-  const int tid = threadIdx.x, ranks = p.ranks;
+template <typename T, bool ENTROPY, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel(const __grid_constant__ LogprobParams p) {
+  __shared__ Shared<THREADS> sh;
+  const int tid = threadIdx.x, lane = tid & 31, ranks = p.ranks;
   const int64_t row = blockIdx.x / ranks;
   const int rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   wait_for_predecessor();
-  const Slice<T> s(p, row, rank);
+  let_successor_come();
+  const Slice<T, THREADS> s(p, row, rank);
   int64_t target = 0;
   float target_logit = 0.0f;
   if (rank == 0 && tid == 0) {
@@ -370,134 +404,142 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const __gri
     if (target >= 0 && target < p.vocab) target_logit = Elem<T>::up(s.row[target]);
   }
 
-  Running<ENTROPY> a;
+  Running<T, ENTROPY> a;
   {
     int64_t v = s.v0 + tid;
 #pragma unroll 1
-    for (; v + (kVectors - 1) * kThreads < s.v1; v += kVectors * kThreads) {
+    for (; v + (kVectors - 1) * THREADS < s.v1; v += kVectors * THREADS) {
       Raw8<T> raw[kVectors];
 #pragma unroll
-      for (int u = 0; u < kVectors; ++u) raw[u].read(s.groups + (v + u * kThreads) * 8);
+      for (int u = 0; u < kVectors; ++u) raw[u].read(s.groups + (v + u * THREADS) * 8);
       a.add_groups(raw, p);
     }
 #pragma unroll 1
-    for (; v < s.v1; v += kThreads) {
+    for (; v < s.v1; v += THREADS) {
       Raw8<T> raw[1];
       raw[0].read(s.groups + v * 8);
       a.add_groups(raw, p);
     }
     const int c = s.single(tid);
-    if (c >= 0) {
-      const float x = Elem<T>::up(s.row[c]);
-      a.raise(x, p);
-      a.add(x, p.c);
-    }
+    if (c >= 0) a.add_single(Elem<T>::up(s.row[c]), p);
   }
-  let_successor_come();
 
-  // the row's maximum
-  {
-    const float m = warp_max_nan(a.m);
-    if ((tid & 31) == 0) sh.warp_top[tid >> 5] = m;
+  // the block's maximum
+  float top = warp_max_nan(a.m);
+  if (THREADS > 32) {
+    if (lane == 0) sh.warp_top[tid >> 5] = top;
     __syncthreads();
-    if (tid < 32) {
-      const float b = warp_max_nan(sh.warp_top[tid & 15]);
-      if (tid == 0) sh.top = b;
-    }
+    top = warp_max_nan(sh.warp_top[lane % (THREADS / 32)]);
   }
-  row_sync(ranks);
-  float top = sh.top;
-  if (ranks > 1)
-    for (int i = 0; i < ranks; ++i) top = max_nan(top, load_cluster(&sh.top, i));
-
-  Parts row_sum{1.0f, 0.0f, 0.0f};
-  const float z_max = top * p.inv_t;
-  if (fabsf(z_max) < infinity()) {  // there is a distribution
+  Parts sum{0.0f, 0.0f, 0.0f};
+  if (fabsf(top) < infinity()) {
     Parts mine{0.0f, 0.0f, 0.0f};
     const float mc = top * p.c;
-    if (fabsf(mc) < kExtreme) {
-      // every sum is relative to fl(c m), which is off the maximum by `delta`
-      const float delta = fmaf(top, p.c, -mc), back = fast_exp2(-delta);
-      if (a.m >= p.low) {
-        const float by = fmaxf(a.mc - mc, kLeast), f = fast_exp2(by) * back, all = a.s * f;
-        mine.bent = fmaf(f, fmaf(a.s, by, a.t), -delta * all);
-        mine.equal = a.m == top ? 1.0f : 0.0f;
-        mine.rest = all - mine.equal;
-      }
-    } else {
+    const bool extreme = !(fabsf(mc) < kExtreme);
+    if (extreme) {
       s.again(tid, 0, 1, [&](float x, int) { add_exactly(mine, x, top, p.c); });
+    } else if (a.m >= p.low) {
+      // every sum is relative to fl(c m), which is off the maximum by `delta`
+      const float delta = fmaf(top, p.c, -mc), by = fmaxf(a.mc - mc, kLeast), f = fast_exp2(by) * fast_exp2(-delta), all = a.sum() * f;
+      mine.bent = fmaf(f, fmaf(a.sum(), by, a.bent()), -delta * all);
+      mine.equal = a.m == top ? 1.0f : 0.0f;
+      mine.rest = all - mine.equal;
     }
-    sum_parts(sh, mine);
-    row_sync(ranks);
-    row_sum = row_parts(sh, ranks);
-    if (row_sum.equal + row_sum.rest < 1.0625f && fabsf(mc) < kExtreme) {  // the same in all of the row's threads
+    sum = sum_parts(sh, mine);
+    if (sum.equal + sum.rest < 1.0625f && !extreme) {  // the same in all of the block's threads
       const uint32_t owners = __ballot_sync(0xFFFFFFFFu, a.m == top);
-      if (owners) {  // one thread of the row: a second one would make the sum 2
-        const int owner = __ffs(owners) - 1, lane = tid & 31;
-        Parts again{0.0f, 0.0f, 0.0f};
-        s.again((tid & ~31) + owner, lane, 32, [&](float x, int) { add_exactly(again, x, top, p.c); });
-        again.equal = warp_sum(again.equal);
-        again.rest = warp_sum(again.rest);
-        again.bent = warp_sum(again.bent);
-        if (lane == owner) mine = again;
+      if (owners) {  // one thread of the block: a second one would make the sum 2
+        const int owner = __ffs(owners) - 1;
+        Parts exactly{0.0f, 0.0f, 0.0f};
+        s.again((tid & ~31) + owner, lane, 32, [&](float x, int) { add_exactly(exactly, x, top, p.c); });
+        exactly = warp_parts_sum(exactly);
+        if (lane == owner) mine = exactly;
       }
-      row_sync(ranks);  // the parts have been read
-      sum_parts(sh, mine);
-      row_sync(ranks);
-      row_sum = row_parts(sh, ranks);
-    }
-  }
-
-  if (p.top) {
-    __syncthreads();
-    find_alternatives(sh, s, a.m, p.top);
-    row_sync(ranks);
-    if (rank == 0) {
-      const int n = ranks * p.top;
-      if (tid < n) sh.merged[tid] = ranks > 1 ? load_cluster(&sh.list[tid % p.top], tid / p.top) : sh.list[tid];
       __syncthreads();
-      if (tid < n) {
-        const uint64_t key = sh.merged[tid];
-        int above = 0;
-        for (int i = 0; i < n; ++i) above += sh.merged[i] > key;
-        if (key && above < p.top) {
-          const float x = key_value(static_cast<uint32_t>(key >> 32));
-          float v = fmaf(x - top, p.inv_t, -log1pf(row_sum.equal - 1.0f + row_sum.rest));
-          if (z_max == -infinity()) v = z_max;
-          if (!(z_max < infinity())) v = __int_as_float(0x7FFFFFFF);
-          p.top_logprobs[row * p.top + above] = v;
-          p.top_ids[row * p.top + above] = 0xFFFFFFFFu - static_cast<uint32_t>(key);
-        }
-      }
+      sum = sum_parts(sh, mine);
     }
   }
-  if (rank == 0 && tid == 0) {
-    const float others = row_sum.equal - 1.0f + row_sum.rest, nan = __int_as_float(0x7FFFFFFF);
-    const bool none = z_max == -infinity(), bad = !(z_max < infinity());
-    const float log_sum = bad ? nan : log1pf(others);
+  if (p.top) find_alternatives(sh, s, a.m, p.top);
+
+  // the row's, by its first block
+  if (ranks > 1) {
+    if (tid == 0) {
+      sh.top = top;
+      sh.parts = sum;
+    }
+    __syncwarp();
+    cluster_sync_all();
+    if (rank) {
+      cluster_sync_all();  // nobody's shared memory goes while it is read
+      return;
+    }
+    float other = -infinity();
+    Parts part{0.0f, 0.0f, 0.0f};
+    if (lane < ranks) {
+      other = load_cluster(&sh.top, lane);
+      part.equal = load_cluster(&sh.parts.equal, lane);
+      part.rest = load_cluster(&sh.parts.rest, lane);
+      part.bent = load_cluster(&sh.parts.bent, lane);
+    }
+    top = warp_max_nan(other);
+    sum = warp_parts_sum(relative_to(top, other, part, p.c));
+  } else {
+    __syncthreads();
+  }
+  const float z_max = top * p.inv_t, others = sum.equal - 1.0f + sum.rest, nan = __int_as_float(0x7FFFFFFF);
+  const bool none = z_max == -infinity(), bad = !(z_max < infinity());
+  const float log_sum = bad ? nan : none ? 0.0f : log1pf(others);
+  if (p.top) {
+    const int n = ranks * p.top;
+    for (int i = tid; i < n; i += THREADS) sh.merged[i] = ranks > 1 ? load_cluster(&sh.list[i % p.top], i / p.top) : sh.list[i];
+    __syncthreads();
+    if (ranks > 1) cluster_arrive();
+    for (int i = tid; i < n; i += THREADS) {
+      const uint64_t key = sh.merged[i];
+      int above = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) above += sh.merged[j] > key;
+      if (key && above < p.top) {
+        const float x = key_value(static_cast<uint32_t>(key >> 32));
+        p.top_logprobs[row * p.top + above] = bad ? nan : none ? z_max : fmaf(x - top, p.inv_t, -log_sum);
+        p.top_ids[row * p.top + above] = 0xFFFFFFFFu - static_cast<uint32_t>(key);
+      }
+    }
+  } else if (ranks > 1) {
+    cluster_arrive();
+  }
+  if (tid == 0) {
     float logprob = none ? z_max : fmaf(target_logit - top, p.inv_t, -log_sum);
-    if (target < 0 || target >= p.vocab) logprob = nan;
+    if (target < 0 || target >= p.vocab || bad) logprob = nan;
     if (target == p.ignore_index) logprob = 0.0f;
     p.logprobs[row] = logprob;
     p.z_max[row] = bad ? nan : z_max;
     p.log_sum[row] = log_sum;
-    if (ENTROPY) p.entropy[row] = bad ? nan : none ? 0.0f : log_sum - kLn2 * row_sum.bent / (1.0f + others);
+    if (ENTROPY) p.entropy[row] = bad ? nan : none ? 0.0f : log_sum - kLn2 * sum.bent / (1.0f + others);
   }
-  if (ranks > 1) cluster_sync_all();  // nobody's shared memory goes while it is read
+  __syncwarp();
+  if (ranks > 1) cluster_wait();
 }
 
-// Blocks per row: as many of 1, 2, 4 and 8 as fill the SMs twice, but none with less than a pass of its threads.
+// Blocks per row: as many of 1, 2, 4 and 8 as keep every SM busy, but none with less than two passes of its threads.
 int ranks_for(int64_t rows, int64_t vocab, int num_sms) {
   int ranks = 1;
-  while (ranks < 8 && rows * ranks * 2 <= 2 * num_sms && vocab / (ranks * 2) >= 8 * kThreads) ranks *= 2;
+  while (ranks < 8 && rows * ranks * 2 <= 4 * num_sms && vocab / (ranks * 2) >= 4096) ranks *= 2;
   return ranks;
 }
 
-template <typename T>
+// Few threads for short rows, whose work behind the pass would else be most of it.
+template <typename T, int THREADS>
 cudaError_t forward(const LogprobParams& p, int64_t rows, cudaStream_t st) {
   const int64_t blocks = rows * p.ranks;
-  return p.entropy ? launch_kernel(token_logprobs_kernel<T, true>, blocks, kThreads, 0, p.ranks, st, p)
-                   : launch_kernel(token_logprobs_kernel<T, false>, blocks, kThreads, 0, p.ranks, st, p);
+  return p.entropy ? launch_kernel(token_logprobs_kernel<T, true, THREADS>, blocks, THREADS, 0, p.ranks, st, p)
+                   : launch_kernel(token_logprobs_kernel<T, false, THREADS>, blocks, THREADS, 0, p.ranks, st, p);
+}
+template <typename T>
+cudaError_t forward(const LogprobParams& p, int64_t rows, cudaStream_t st) {
+  if (p.vocab <= 1024) return forward<T, 32>(p, rows, st);
+  if (p.vocab < 8192) return forward<T, 128>(p, rows, st);
+  return forward<T, 256>(p, rows, st);
 }
 
 // ------------------------------------------------------------------ backward
@@ -514,8 +556,7 @@ struct LogprobBackwardParams {
   int segments;  // blocks per row
 };
 
-constexpr int kBackThreads = 256, kBackVectors = 4;
-constexpr int kSegment = kBackThreads * kBackVectors * 8;  // elements of a block
+constexpr int kBackThreads = 256, kBackVectors = 4;  // at most
 
 // What a row's elements share.
 struct RowGradient {
@@ -544,12 +585,12 @@ __global__ void __launch_bounds__(kBackThreads) token_logprobs_backward_kernel(c
   const int vocab = static_cast<int>(p.vocab);
   const int past = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) & 7);
   const int lead = min((8 - past) & 7, vocab), vectors = (vocab - lead) / 8;
-  const int v0 = segment * (kBackThreads * kBackVectors) + tid;
+  const int threads = blockDim.x, v0 = segment * threads * kBackVectors + tid;
   const bool alike = reinterpret_cast<uintptr_t>(out + lead) % (8 * sizeof(T)) == 0;
   Raw8<T> raw[kBackVectors];
 #pragma unroll
   for (int u = 0; u < kBackVectors; ++u)
-    if (v0 + u * kBackThreads < vectors) raw[u].read(x + lead + static_cast<int64_t>(v0 + u * kBackThreads) * 8);
+    if (v0 + u * threads < vectors) raw[u].read(x + lead + static_cast<int64_t>(v0 + u * threads) * 8);
 
   RowGradient r;
   const int64_t target = p.targets[row];
@@ -578,7 +619,7 @@ __global__ void __launch_bounds__(kBackThreads) token_logprobs_backward_kernel(c
 
 #pragma unroll
   for (int u = 0; u < kBackVectors; ++u) {
-    const int v = v0 + u * kBackThreads;
+    const int v = v0 + u * threads;
     if (v >= vectors) break;
     const int column = lead + v * 8;
     float y[8];
@@ -601,10 +642,13 @@ __global__ void __launch_bounds__(kBackThreads) token_logprobs_backward_kernel(c
 }
 
 template <typename T>
-cudaError_t backward(const LogprobBackwardParams& p, int64_t rows, cudaStream_t st) {
+cudaError_t backward(LogprobBackwardParams& p, int64_t rows, cudaStream_t st) {
+  // a block has no more threads than four vectors each of a short row need
+  const int threads = static_cast<int>(std::min<int64_t>(kBackThreads, ceil_div(p.vocab, 32 * 8 * kBackVectors) * 32));
+  p.segments = static_cast<int>(ceil_div(p.vocab, threads * kBackVectors * 8));
   const int64_t blocks = rows * p.segments;
-  return p.dentropy ? launch_kernel(token_logprobs_backward_kernel<T, true>, blocks, kBackThreads, 0, 1, st, p)
-                    : launch_kernel(token_logprobs_backward_kernel<T, false>, blocks, kBackThreads, 0, 1, st, p);
+  return p.dentropy ? launch_kernel(token_logprobs_backward_kernel<T, true>, blocks, threads, 0, 1, st, p)
+                    : launch_kernel(token_logprobs_backward_kernel<T, false>, blocks, threads, 0, 1, st, p);
 }
 
 constexpr double kLog2eDouble = 1.4426950408889634074;
@@ -627,6 +671,9 @@ cudaError_t launch_token_logprobs(const oz2_token_logprobs_args& a, const Device
   p.inv_t = static_cast<float>(1.0 / a.temperature);
   p.c = static_cast<float>(kLog2eDouble / a.temperature);
   p.low = -kExtreme / p.c;
+  uint32_t bits;
+  std::memcpy(&bits, &p.low, 4);
+  p.floor2 = (bits & 0xFFFF0000u) | bits >> 16;
   p.top = a.top;
   p.ranks = ranks_for(a.rows, a.vocab, res.num_sms);
   switch (a.dtype) {
@@ -653,7 +700,6 @@ cudaError_t launch_token_logprobs_backward(const oz2_token_logprobs_backward_arg
   p.ldd = a.ldd;
   p.inv_t = static_cast<float>(1.0 / a.temperature);
   p.c = static_cast<float>(kLog2eDouble / a.temperature);
-  p.segments = static_cast<int>(ceil_div(a.vocab, kSegment));
   switch (a.dtype) {
     case OZ2_BF16: return backward<__nv_bfloat16>(p, a.rows, st);
     case OZ2_F16: return backward<__half>(p, a.rows, st);

@@ -122,7 +122,7 @@ __device__ __forceinline__ void write_pairs(T* row, int span, int lane, int cols
 }
 __device__ __forceinline__ float max_magnitude(const Pairs& v, float top) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = max_nan(top, max_nan(fabsf(v[i].x), fabsf(v[i].y)));
+  for (int i = 0; i < 4; ++i) top = max_abs_nan(top, v[i].x, v[i].y);
   return top;
 }
 
