@@ -22,10 +22,13 @@
 namespace oz2 {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBlock = OZ2_ADAMW_BLOCK;
 constexpr float kShortEps = 1e-12f;  // from here on a root of 2^-63 is nothing beside eps
-constexpr int kTurns = 16;  // of a CTA's warps in a long step: 32768 elements per CTA
+// A CTA is one warp, which takes up to this many blocks of 256 elements.  Warps that share a CTA keep its place until the
+// last of them is done, and they end far apart: 2^29 elements in 8 bits by CTAs of 8, 4, 2 and 1 warps 1350, 1207, 1199 and
+// 1084 us.
+constexpr int kTurns = 16;
+constexpr int kResident = 24;  // CTAs per SM, with the registers they take
 
 // The tensors of one launch.  A kernel's arguments may take 32764 bytes; few tensors get the short form, whose launch copies less.
 template <int MOST>
@@ -33,8 +36,8 @@ struct Tensors {
   void* param[MOST];
   const void* grad[MOST];
   int64_t elements[MOST];
-  int64_t block[MOST];    // of its states
-  int chunk[MOST];        // its first CTA
+  int64_t block[MOST];  // of its states
+  int chunk[MOST];      // its first CTA
 };
 constexpr int kFew = 24, kMany = 880;
 
@@ -50,13 +53,14 @@ struct AdamwParams {
   float lr, beta1, beta2, rest1, rest2;  // rest: 1 - beta
   float log_beta1, log_beta2;            // natural logarithms
   float eps, weight_decay, grad_scale;
+  float one, minus_one;                  // see add_exact
   uint32_t seed0, seed1;
   int count;
   int turns;  // blocks of 256 elements per warp
   int last;   // the call's last launch: counts the step
 };
 
-// What all elements of a launch share; formed by one thread of each CTA.
+// What all elements of a launch share.
 struct StepFactors {
   float keep;     // 1 - lr weight_decay
   float rate;     // lr / (1 - beta1^t)
@@ -101,7 +105,7 @@ __device__ __forceinline__ uint32_t encode_fourth(float t, uint32_t draw) {
 // power is above t (just above a step is where a step of the optimiser leaves many elements, so no approximation decides
 // there); the step it belongs to ends at the neighbour on the other side.  0 < t < 1 is left to the form above.  A t of
 // 255^4, the largest of a block, is taken for the number before it, which is rounded up to 255 by every draw.
-__device__ __forceinline__ uint2 encode_fourths(const float2 (&v)[4], float inverse, const uint4& draws) {
+__device__ __forceinline__ uint2 encode_fourths(const float2 (&v)[4], float inverse, const uint4& draws, float minus_one) {
   constexpr float kMost = 4228250368.0f;  // before fl(255^4)
   const uint32_t d[4] = {draws.x, draws.y, draws.z, draws.w};
   float2 t[4];
@@ -111,16 +115,19 @@ __device__ __forceinline__ uint2 encode_fourths(const float2 (&v)[4], float inve
   for (int i = 0; i < 4; ++i) {
     t[i] = mul2(v[i], both(inverse));
     t[i] = make_float2(fminf(t[i].x, kMost), fminf(t[i].y, kMost));
-    float2 k = add2(make_float2(fast_rsqrt(fast_rsqrt(t[i].x)), fast_rsqrt(fast_rsqrt(t[i].y))), both(kWhole));
-    const uint32_t k0 = __float_as_uint(k.x), k1 = __float_as_uint(k.y);
-    k = add2(k, both(-kWhole));
-    const float2 near = fourth2(k);
+    // whole numbers k as 2^23 + k, whose last byte they are
+    const float2 near_whole = add2(make_float2(fast_rsqrt(fast_rsqrt(t[i].x)), fast_rsqrt(fast_rsqrt(t[i].y))), both(kWhole));
+    const float2 near = fourth2(add2(near_whole, both(-kWhole)));
     const bool b0 = near.x > t[i].x, b1 = near.y > t[i].y;
-    const float2 far = fourth2(add2(k, make_float2(b0 ? -1.0f : 1.0f, b1 ? -1.0f : 1.0f)));
+    const float2 far_whole = add2(near_whole, make_float2(b0 ? -1.0f : 1.0f, b1 ? -1.0f : 1.0f));
+    const float2 far = fourth2(add2(far_whole, both(-kWhole)));
     // draw / 2^16
     const float2 draw = fma2(make_float2(whole_half(d[i], 0), whole_half(d[i], 1)), both(0x1p-16f), both(-kWhole * 0x1p-16f));
-    code[2 * i] = k0 - b0 + (__fsub_rn(t[i].x, fminf(near.x, far.x)) > __fmul_rn(draw.x, fabsf(__fsub_rn(near.x, far.x))));
-    code[2 * i + 1] = k1 - b1 + (__fsub_rn(t[i].y, fminf(near.y, far.y)) > __fmul_rn(draw.y, fabsf(__fsub_rn(near.y, far.y))));
+    const float2 above = sub_exact(t[i], make_float2(fminf(near.x, far.x), fminf(near.y, far.y)), minus_one), step = sub_exact(far, near, minus_one);
+    // up from near is far, and up from far, where that is below, is near
+    const bool u0 = above.x > __fmul_rn(draw.x, fabsf(step.x)), u1 = above.y > __fmul_rn(draw.y, fabsf(step.y));
+    code[2 * i] = __float_as_uint(u0 != b0 ? far_whole.x : near_whole.x);
+    code[2 * i + 1] = __float_as_uint(u1 != b1 ? far_whole.y : near_whole.y);
     least = fminf(least, fminf(t[i].x, t[i].y));
   }
   if (least < 1.0f) {
@@ -182,7 +189,19 @@ __device__ __forceinline__ void write8(T* p, bool vec, int n, const float2 (&v)[
 template <typename T>
 __device__ __forceinline__ bool on_boundary(const T* p) { return reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0; }
 
-// What a lane reads of a block of 256 elements.
+// A CTA's chunk of a tensor: its pointers, the same in all lanes, and how many elements it has.
+template <typename P, typename G>
+struct Chunk {
+  P* param;
+  const G* grad;
+  float* master;
+  uint8_t *m, *v;  // bytes, or floats
+  float *sm, *sv;
+  int elements;
+  bool vec_param, vec_grad, vec_state;
+};
+
+// What a lane reads of a block of 256 elements, `at`: its first one's place in the chunk.
 template <typename P, typename G, int BITS, bool MASTER>
 struct Block {
   Raw8<std::conditional_t<MASTER, float, P>> w;
@@ -190,26 +209,22 @@ struct Block {
   Raw8<float> m, v;   // 32 bits
   uint2 qm, qv;       // 8 bits
   float sm, sv;
-  int n;
-  __device__ __forceinline__ void read(const AdamwParams& p, const P* param, const G* grad, int64_t elements, int64_t block, int64_t state_block,
-                                       int lane, bool vec_param, bool vec_grad, bool vec_state) {
-    const int64_t e0 = block * kBlock + lane * 8, s0 = (state_block + block) * kBlock + lane * 8, left = elements - e0;
-    n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
-    if constexpr (MASTER) read8(p.master + s0, vec_state, n, w);
-    else read8(param + e0, vec_param, n, w);
-    read8(grad + e0, vec_grad, n, g);
+  __device__ __forceinline__ void read(const Chunk<P, G>& c, uint32_t at, int n) {
+    if constexpr (MASTER) read8(c.master + at, c.vec_state, n, w);
+    else read8(c.param + at, c.vec_param, n, w);
+    read8(c.grad + at, c.vec_grad, n, g);
     if constexpr (BITS == 32) {
-      read8(static_cast<const float*>(p.exp_avg) + s0, vec_state, n, m);
-      read8(static_cast<const float*>(p.exp_avg_sq) + s0, vec_state, n, v);
+      read8(reinterpret_cast<const float*>(c.m) + at, c.vec_state, n, m);
+      read8(reinterpret_cast<const float*>(c.v) + at, c.vec_state, n, v);
     } else {
       // whole groups: the gaps behind a tensor's end are there to be read
-      qm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.exp_avg) + s0);
-      qv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.exp_avg_sq) + s0);
-      sm = p.exp_avg_scale[state_block + block];
-      sv = p.exp_avg_sq_scale[state_block + block];
+      qm = *reinterpret_cast<const uint2*>(c.m + at);
+      qv = *reinterpret_cast<const uint2*>(c.v + at);
+      sm = c.sm[at / kBlock];
+      sv = c.sv[at / kBlock];
     }
   }
-  __device__ __forceinline__ void moments(float2 (&mv)[4], float2 (&vv)[4]) const {
+  __device__ __forceinline__ void moments(int n, float2 (&mv)[4], float2 (&vv)[4]) const {
     if constexpr (BITS == 32) {
       values(m, mv);
       values(v, vv);
@@ -253,121 +268,126 @@ __device__ __forceinline__ void move(const StepFactors& f, float eps, const floa
   }
 }
 
+// One step of a lane's eight elements.
+template <typename P, typename G, int BITS, bool MASTER>
+__device__ __forceinline__ void step_block(const AdamwParams& p, const StepFactors& f, const Chunk<P, G>& c, const Block<P, G, BITS, MASTER>& now,
+                                           uint32_t at, int n, int lane, uint64_t group) {
+  float2 w[4], g[4], m[4], v[4];
+  values(now.w, w);
+  values(now.g, g);
+  now.moments(n, m, v);
+  // one rounding at a time: 8-bit states are defined to the bit
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    g[i] = mul2(g[i], both(f.grad_scale));
+    m[i] = add_exact(mul2(both(p.beta1), m[i]), mul2(both(p.rest1), g[i]), p.one);
+    v[i] = add_exact(mul2(both(p.beta2), v[i]), mul2(both(p.rest2), mul2(g[i], g[i])), p.one);
+  }
+  if (p.eps >= kShortEps) move<false>(f, p.eps, m, v, w);
+  else move<true>(f, p.eps, m, v, w);
+  if (MASTER) write8(c.master + at, c.vec_state, n, w);
+  write8(c.param + at, c.vec_param, n, w);
+  if (BITS == 32) {
+    write8(reinterpret_cast<float*>(c.m) + at, c.vec_state, n, m);
+    write8(reinterpret_cast<float*>(c.v) + at, c.vec_state, n, v);
+    return;
+  }
+  float top_m = 0.0f, top_v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top_m = max_abs_nan(top_m, m[i].x, m[i].y);
+    top_v = max_nan(top_v, v[i].x, v[i].y);
+  }
+  top_v = warp_max_nan(top_v);
+  const float sm = state_scale(warp_max_nan(top_m), 1.0f / 448.0f), sv = state_scale(top_v, kFourth);
+  const float2 im = both(__frcp_rn(sm));
+  uint32_t qm[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 q = mul2(m[i], im);
+    qm[i >> 1] |= pack_e4m3(q.x, q.y) << (16 * (i & 1));
+  }
+  uint2 qv = make_uint2(0, 0);
+  if (top_v != 0.0f)
+    qv = encode_fourths(v, __frcp_rn(sv), philox7(static_cast<uint32_t>(group), static_cast<uint32_t>(group >> 32), f.t0, f.t1, p.seed0, p.seed1),
+                        p.minus_one);
+  if (n == 8) {
+    *reinterpret_cast<uint2*>(c.m + at) = make_uint2(qm[0], qm[1]);
+    *reinterpret_cast<uint2*>(c.v + at) = qv;
+  } else {
+    const uint32_t words[2] = {qv.x, qv.y};
+    for (int i = 0; i < n; ++i) {
+      c.m[at + i] = static_cast<uint8_t>(qm[i >> 2] >> (8 * (i & 3)));
+      c.v[at + i] = static_cast<uint8_t>(words[i >> 2] >> (8 * (i & 3)));
+    }
+  }
+  if (lane == 0) {
+    c.sm[at / kBlock] = sm;
+    c.sv[at / kBlock] = sv;
+  }
+}
+
 // With 8-bit states a warp has its next block on its way while it works on one: there is enough to do in between.
 template <typename P, typename G, int BITS, bool MASTER, int MOST>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Tensors<MOST> tensors, const __grid_constant__ AdamwParams p) {
-  __shared__ StepFactors factors;
-  __shared__ int done;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(32) adamw_kernel(const __grid_constant__ Tensors<MOST> tensors, const __grid_constant__ AdamwParams p) {
+  const int lane = threadIdx.x;
   // the tensor whose chunks this CTA's number is among: the last one that starts at it or before
-  int at = 0;
+  int which = 0;
 #pragma unroll
   for (int step = MOST <= 32 ? 16 : 512; step; step >>= 1)
-    if (at + step < p.count && tensors.chunk[at + step] <= static_cast<int>(blockIdx.x)) at += step;
-  const int64_t elements = tensors.elements[at];
-  P* param = static_cast<P*>(tensors.param[at]);
-  const G* grad = static_cast<const G*>(tensors.grad[at]);
-  const int64_t state_block = tensors.block[at];
-  const bool vec_param = on_boundary(param), vec_grad = on_boundary(grad);
-  const bool vec_state = (BITS == 8 || (on_boundary(static_cast<float*>(p.exp_avg)) && on_boundary(static_cast<float*>(p.exp_avg_sq)))) &&
-                         (!MASTER || on_boundary(p.master));
-  int64_t block = static_cast<int64_t>(blockIdx.x - tensors.chunk[at]) * (p.turns * kWarps) + warp;
-  const int64_t end = min(block - warp + p.turns * kWarps, (elements + kBlock - 1) / kBlock);
+    if (which + step < p.count && tensors.chunk[which + step] <= static_cast<int>(blockIdx.x)) which += step;
+  constexpr int STATE = BITS == 8 ? 1 : 4;
+  const int64_t first_block = static_cast<int64_t>(blockIdx.x - tensors.chunk[which]) * p.turns, first = first_block * kBlock;
+  const int64_t state_block = tensors.block[which] + first_block, state = state_block * kBlock;
+  Chunk<P, G> c;
+  c.param = static_cast<P*>(tensors.param[which]) + first;
+  c.grad = static_cast<const G*>(tensors.grad[which]) + first;
+  c.master = MASTER ? p.master + state : nullptr;
+  c.m = static_cast<uint8_t*>(p.exp_avg) + state * STATE;
+  c.v = static_cast<uint8_t*>(p.exp_avg_sq) + state * STATE;
+  c.sm = p.exp_avg_scale + state_block;
+  c.sv = p.exp_avg_sq_scale + state_block;
+  c.elements = static_cast<int>(min(tensors.elements[which] - first, static_cast<int64_t>(p.turns) * kBlock));
+  c.vec_param = on_boundary(c.param);
+  c.vec_grad = on_boundary(c.grad);
+  c.vec_state = (BITS == 8 || (on_boundary(reinterpret_cast<float*>(c.m)) && on_boundary(reinterpret_cast<float*>(c.v)))) && (!MASTER || on_boundary(c.master));
+  auto left = [&](uint32_t at) { return max(0, min(8, c.elements - static_cast<int>(at))); };
+  uint32_t at = lane * 8;
+  const uint32_t end = (c.elements + kBlock - 1) / kBlock * kBlock;  // whole blocks
   wait_for_predecessor();
   let_successor_come();
+  constexpr bool AHEAD = BITS == 8;
   Block<P, G, BITS, MASTER> next;
-  if (BITS == 8 && block < end) next.read(p, param, grad, elements, block, state_block, lane, vec_param, vec_grad, vec_state);
-  if (threadIdx.x == 0) {
+  if (AHEAD && at < end) next.read(c, at, left(at));
+  StepFactors f;
+  {
     const int64_t t = p.step[0] + 1;
     const float lr = p.lr_device ? *p.lr_device : p.lr;
-    StepFactors f;
     f.keep = 1.0f - lr * p.weight_decay;
     f.rate = lr / -expm1f(static_cast<float>(t) * p.log_beta1);
     f.root2 = 1.0f / -expm1f(static_cast<float>(t) * p.log_beta2);
     f.grad_scale = p.grad_scale_device ? *p.grad_scale_device : p.grad_scale;
     f.t0 = static_cast<uint32_t>(t);
     f.t1 = static_cast<uint32_t>(static_cast<uint64_t>(t) >> 32);
-    factors = f;
-    done = 0;
   }
-  __syncthreads();
-  const StepFactors f = factors;
+  const uint64_t group = static_cast<uint64_t>(state) >> 3;
 #pragma unroll 1
-  for (; block < end; block += kWarps) {
+  for (; at < end; at += kBlock) {
     Block<P, G, BITS, MASTER> now;
-    if (BITS == 8) {
+    if (AHEAD) {
       now = next;
-      if (block + kWarps < end) next.read(p, param, grad, elements, block + kWarps, state_block, lane, vec_param, vec_grad, vec_state);
+      if (at + kBlock < end) next.read(c, at + kBlock, left(at + kBlock));
     } else {
-      now.read(p, param, grad, elements, block, state_block, lane, vec_param, vec_grad, vec_state);
+      now.read(c, at, left(at));
     }
-    const int n = now.n;
-    const int64_t e0 = block * kBlock + lane * 8, s0 = (state_block + block) * kBlock + lane * 8;
-    float2 w[4], g[4], m[4], v[4];
-    values(now.w, w);
-    values(now.g, g);
-    now.moments(m, v);
-    // one rounding at a time: 8-bit states are defined to the bit
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      g[i] = mul2(g[i], both(f.grad_scale));
-      m[i] = add_each(mul2(both(p.beta1), m[i]), mul2(both(p.rest1), g[i]));
-      v[i] = add_each(mul2(both(p.beta2), v[i]), mul2(both(p.rest2), mul2(g[i], g[i])));
-    }
-    if (p.eps >= kShortEps) move<false>(f, p.eps, m, v, w);
-    else move<true>(f, p.eps, m, v, w);
-    if (MASTER) write8(p.master + s0, vec_state, n, w);
-    write8(param + e0, vec_param, n, w);
-    if (BITS == 32) {
-      write8(static_cast<float*>(p.exp_avg) + s0, vec_state, n, m);
-      write8(static_cast<float*>(p.exp_avg_sq) + s0, vec_state, n, v);
-    } else {
-      float top_m = 0.0f, top_v = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        top_m = max_abs_nan(top_m, m[i].x, m[i].y);
-        top_v = max_nan(top_v, v[i].x, v[i].y);
-      }
-      top_v = warp_max_nan(top_v);
-      const float sm = state_scale(warp_max_nan(top_m), 1.0f / 448.0f), sv = state_scale(top_v, kFourth);
-      const float2 im = both(__frcp_rn(sm));
-      uint32_t qm[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 q = mul2(m[i], im);
-        qm[i >> 1] |= pack_e4m3(q.x, q.y) << (16 * (i & 1));
-      }
-      uint2 qv = make_uint2(0, 0);
-      if (top_v != 0.0f) {
-        const uint64_t group = static_cast<uint64_t>(s0) >> 3;
-        qv = encode_fourths(v, __frcp_rn(sv), philox7(static_cast<uint32_t>(group), static_cast<uint32_t>(group >> 32), f.t0, f.t1, p.seed0, p.seed1));
-      }
-      uint8_t* out_m = static_cast<uint8_t*>(p.exp_avg) + s0;
-      uint8_t* out_v = static_cast<uint8_t*>(p.exp_avg_sq) + s0;
-      if (n == 8) {
-        *reinterpret_cast<uint2*>(out_m) = make_uint2(qm[0], qm[1]);
-        *reinterpret_cast<uint2*>(out_v) = qv;
-      } else {
-        const uint32_t words[2] = {qv.x, qv.y};
-        for (int i = 0; i < n; ++i) {
-          out_m[i] = static_cast<uint8_t>(qm[i >> 2] >> (8 * (i & 3)));
-          out_v[i] = static_cast<uint8_t>(words[i >> 2] >> (8 * (i & 3)));
-        }
-      }
-      if (lane == 0) {
-        p.exp_avg_scale[state_block + block] = sm;
-        p.exp_avg_sq_scale[state_block + block] = sv;
-      }
-    }
+    step_block(p, f, c, now, at, left(at), lane, group + (at >> 3));
   }
-  if (!p.last) return;
-  // the last warp of the last CTA counts the step: all others have read its number by then
-  if (lane == 0 && atomicAdd(&done, 1) == kWarps - 1) {
-    __threadfence();
-    if (atomicAdd(reinterpret_cast<unsigned long long*>(p.step + 1), 1ull) + 1 == gridDim.x) {
-      p.step[1] = 0;
-      p.step[0] += 1;
-    }
+  // the last CTA counts the step: all others have the number in use by then (no fence: nothing else is handed over, and one
+  // per CTA took 6 % of a long step)
+  if (!p.last || lane) return;
+  if (atomicAdd(reinterpret_cast<unsigned long long*>(p.step + 1), 1ull) + 1 == gridDim.x) {
+    p.step[1] = 0;
+    p.step[0] += 1;
   }
 }
 
@@ -390,9 +410,9 @@ cudaError_t launch_part(const oz2_adamw_args& a, AdamwParams p, int64_t from, in
       t.chunk[p.count++] = static_cast<int>(chunks);
     }
     block += ceil_div(x.elements, kBlock);
-    chunks += ceil_div(x.elements, kBlock * kWarps * p.turns);
+    chunks += ceil_div(x.elements, kBlock * p.turns);
   }
-  return launch_kernel(adamw_kernel<P, G, BITS, MASTER, MOST>, chunks ? chunks : 1, kThreads, 0, 1, st, t, p);
+  return launch_kernel(adamw_kernel<P, G, BITS, MASTER, MOST>, chunks ? chunks : 1, 32, 0, 1, st, t, p);
 }
 
 // As many launches as the tensors need: kMany of them at a time, and at most 2^30 CTAs or one tensor's.
@@ -404,7 +424,7 @@ cudaError_t launch_all(const oz2_adamw_args& a, AdamwParams p, cudaStream_t st) 
   do {
     int64_t to = from, some = 0, chunks = 0, blocks = 0;
     for (; to < end; ++to) {
-      const int64_t n = a.tensors[to].elements, c = ceil_div(n, kBlock * kWarps * p.turns);
+      const int64_t n = a.tensors[to].elements, c = ceil_div(n, kBlock * p.turns);
       if (some && (some + (n > 0) > kMany || chunks + c > (int64_t(1) << 30))) break;
       some += n > 0;
       chunks += c;
@@ -434,10 +454,10 @@ cudaError_t launch_half(const oz2_adamw_args& a, const AdamwParams& p, cudaStrea
 
 cudaError_t launch_adamw(const oz2_adamw_args& a, const DeviceResources& res, cudaStream_t st) {
   AdamwParams p{};
-  // one turn per warp until the CTAs fill the SMs several times over
-  int64_t elements = 0;
-  for (int64_t i = 0; i < a.count; ++i) elements += a.tensors[i].elements;
-  p.turns = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kTurns, elements / (static_cast<int64_t>(res.num_sms) * 8 * kBlock * kWarps))));
+  // as few turns as let all CTAs run at once, up to those of a long step
+  int64_t blocks = 0;
+  for (int64_t i = 0; i < a.count; ++i) blocks += ceil_div(a.tensors[i].elements, kBlock);
+  p.turns = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kTurns, ceil_div(blocks, static_cast<int64_t>(res.num_sms) * kResident))));
   p.exp_avg = a.exp_avg;
   p.exp_avg_sq = a.exp_avg_sq;
   p.exp_avg_scale = a.exp_avg_scale;
@@ -456,6 +476,8 @@ cudaError_t launch_adamw(const oz2_adamw_args& a, const DeviceResources& res, cu
   p.eps = static_cast<float>(a.eps);
   p.weight_decay = static_cast<float>(a.weight_decay);
   p.grad_scale = static_cast<float>(a.grad_scale);
+  p.one = 1.0f;
+  p.minus_one = -1.0f;
   p.seed0 = static_cast<uint32_t>(a.seed);
   p.seed1 = static_cast<uint32_t>(a.seed >> 32);
   switch (a.dtype) {

@@ -56,7 +56,7 @@ __device__ __forceinline__ float half_warp_max_nan(float v) {
 }
 
 // Two 32-bit operations in one instruction, each rounded to nearest.  The compiler joins a product and a sum of these into
-// one rounding; where results are defined to the bit, sums of products are taken one by one.
+// one rounding.  Where results are defined to the bit the sum is an FFMA with a factor of one that the compiler does not know.
 __device__ __forceinline__ uint64_t pair_bits(float2 a) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
@@ -83,9 +83,8 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
   return bits_pair(r);
 }
-// One by one, never joined with the product before.
-__device__ __forceinline__ float2 add_each(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
-__device__ __forceinline__ float2 sub_each(float2 a, float2 b) { return make_float2(__fsub_rn(a.x, b.x), __fsub_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 add_exact(float2 a, float2 b, float one) { return fma2(a, both(one), b); }
+__device__ __forceinline__ float2 sub_exact(float2 a, float2 b, float minus_one) { return fma2(b, both(minus_one), a); }
 
 // Two values as e4m3, the first in the low byte; past 448 saturated, NaN stays.
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
