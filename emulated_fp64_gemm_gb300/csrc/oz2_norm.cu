@@ -1,10 +1,14 @@
 // RMS norm with the residual stream's addition, in the input's type or in 8 bits
 // with scales, and its gradients.
 //
-// Both directions are one pass over their matrices and bound by HBM.  A row is
-// worked on by the lanes of one or a few warps, 256 neighbouring columns (a span)
-// at a time per warp.  Rows of aligned pieces are copied ahead into shared memory;
-// other ones are read by single elements, and rows longer than a block's
+// Both directions are one pass over their matrices and bound by HBM, if only just:
+// at 8 bytes per element the SMs have 30 instructions for each of them, so that
+// addresses are kept, pairs of elements share an instruction and a lane has as many
+// elements of a row as its registers hold.
+//
+// A row is worked on by the lanes of one or a few warps, 256 neighbouring columns (a
+// span) at a time per warp.  Rows of aligned pieces are copied ahead into shared
+// memory; other ones are read by single elements, and rows longer than a block's
 // registers in several passes.
 #include <algorithm>
 #include <type_traits>
@@ -23,103 +27,94 @@ constexpr int kPieces = sizeof(T) / 2;
 template <typename T, bool VEC>
 constexpr bool kHalfWarps = VEC && sizeof(T) == 2;
 
+// Of element e of a lane: its distance from the lane's first one.
 template <typename T, bool VEC>
-__device__ __forceinline__ int column(int span, int lane, int e) {
-  if (!VEC) return span * 256 + e * 32 + lane;
-  return sizeof(T) == 2 ? span * 256 + lane * 8 + e : span * 256 + (e >> 2) * 128 + lane * 4 + (e & 3);
+__host__ __device__ constexpr int distance(int e) {
+  return !VEC ? e * 32 : sizeof(T) == 2 ? e : (e >> 2) * 128 + (e & 3);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ int first_column(int span, int lane) {
+  return span * 256 + (!VEC ? lane : sizeof(T) == 2 ? lane * 8 : lane * 4);
 }
 
+using Pairs = float2[4];
+
+// As they are in memory.  p: the lane's first element of its first span, `left`: how many columns there are from it on;
+// j: the span.
 template <typename T, bool VEC>
-struct Part {  // as they are in memory
+struct Part {
   uint4 u[kPieces<T>];
-  __device__ __forceinline__ void read(const T* row, int span, int lane, int cols) {
+  __device__ __forceinline__ void read(const T* p, int left, int j) {
 #pragma unroll
     for (int q = 0; q < kPieces<T>; ++q) {
-      const int c = column<T, VEC>(span, lane, 4 * q);
-      u[q] = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+      const int d = j * 256 + distance<T, VEC>(4 * q);
+      u[q] = d < left ? *reinterpret_cast<const uint4*>(p + d) : make_uint4(0, 0, 0, 0);
     }
   }
-  __device__ __forceinline__ void values(float (&v)[8]) const { values8<T>(u, v); }
+  __device__ __forceinline__ void pairs(Pairs& v) const {
+    float f[8];
+    values8<T>(u, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  }
 };
 template <typename T>
 struct Part<T, false> {
   T r[8];
-  __device__ __forceinline__ void read(const T* row, int span, int lane, int cols) {
+  __device__ __forceinline__ void read(const T* p, int left, int j) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = column<T, false>(span, lane, e);
-      r[e] = c < cols ? row[c] : Elem<T>::down(0.0f);
+      const int d = j * 256 + distance<T, false>(e);
+      r[e] = d < left ? p[d] : Elem<T>::down(0.0f);
     }
   }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
+  __device__ __forceinline__ void pairs(Pairs& v) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = Elem<T>::up(r[e]);
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(Elem<T>::up(r[2 * i]), Elem<T>::up(r[2 * i + 1]));
   }
 };
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void write_part(T* row, int span, int lane, int cols, const float (&v)[8]) {
+__device__ __forceinline__ void write_span(T* p, int left, int j, const Pairs& v) {
+  const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
   if constexpr (!VEC) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = column<T, VEC>(span, lane, e);
-      if (c < cols) row[c] = Elem<T>::down(v[e]);
+      const int d = j * 256 + distance<T, VEC>(e);
+      if (d < left) p[d] = Elem<T>::down(f[e]);
     }
   } else if constexpr (sizeof(T) == 2) {
-    const int c = column<T, VEC>(span, lane, 0);
-    if (c < cols) *reinterpret_cast<uint4*>(row + c) = pack8<T>(v);
+    if (j * 256 < left) *reinterpret_cast<uint4*>(p + j * 256) = pack8<T>(f);
   } else {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int c = column<T, VEC>(span, lane, 4 * q);
-      if (c < cols) *reinterpret_cast<float4*>(row + c) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      const int d = j * 256 + distance<T, VEC>(4 * q);
+      if (d < left) *reinterpret_cast<float4*>(p + d) = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
     }
   }
 }
 
-// Eight e4m3 of a span; whole: rows of them start on boundaries of 8 bytes.
+// Eight e4m3; whole: rows of them start on boundaries of 8 bytes.
 template <typename T, bool VEC>
-__device__ __forceinline__ void write_e4m3(uint8_t* row, int span, int lane, int cols, bool whole, const float (&v)[8]) {
-  const uint32_t w[2] = {pack_e4m3(v[0], v[1]) | pack_e4m3(v[2], v[3]) << 16, pack_e4m3(v[4], v[5]) | pack_e4m3(v[6], v[7]) << 16};
+__device__ __forceinline__ void write_e4m3(uint8_t* p, int left, int j, bool whole, const Pairs& v) {
+  const uint32_t w[2] = {pack_e4m3(v[0].x, v[0].y) | pack_e4m3(v[1].x, v[1].y) << 16, pack_e4m3(v[2].x, v[2].y) | pack_e4m3(v[3].x, v[3].y) << 16};
   if (VEC && whole) {
-    const int c = column<T, VEC>(span, lane, 0), c1 = column<T, VEC>(span, lane, 4);
     if constexpr (sizeof(T) == 2) {
-      if (c < cols) *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+      if (j * 256 < left) *reinterpret_cast<uint2*>(p + j * 256) = make_uint2(w[0], w[1]);
     } else {
-      if (c < cols) *reinterpret_cast<uint32_t*>(row + c) = w[0];
-      if (c1 < cols) *reinterpret_cast<uint32_t*>(row + c1) = w[1];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (j * 256 + q * 128 < left) *reinterpret_cast<uint32_t*>(p + j * 256 + q * 128) = w[q];
     }
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int c = column<T, VEC>(span, lane, e);
-    if (c < cols) row[c] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
+    const int d = j * 256 + distance<T, VEC>(e);
+    if (d < left) p[d] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
   }
 }
 
-// A lane's eight elements as pairs.
-using Pairs = float2[4];
-template <typename P>
-__device__ __forceinline__ void pairs_of(const P& part, Pairs& v) {
-  float f[8];
-  part.values(f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
-}
-__device__ __forceinline__ void singles(const Pairs& v, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = v[i].x;
-    f[2 * i + 1] = v[i].y;
-  }
-}
-template <typename T, bool VEC>
-__device__ __forceinline__ void write_pairs(T* row, int span, int lane, int cols, const Pairs& v) {
-  float f[8];
-  singles(v, f);
-  write_part<T, VEC>(row, span, lane, cols, f);
-}
 __device__ __forceinline__ float max_magnitude(const Pairs& v, float top) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) top = max_abs_nan(top, v[i].x, v[i].y);
@@ -161,12 +156,75 @@ __device__ __forceinline__ float range_factor(float top) {
   return exp2f(-static_cast<float>(max(ilogbf(top), -126)));
 }
 // 1 / sqrt(mean + eps f^2), `sum` being of the squares of elements times f; 0 where it is infinite.
-__device__ __forceinline__ float inverse_norm(float sum, int cols, float eps, float f) {
-  const float mean = sum / static_cast<float>(cols);
+__device__ __forceinline__ float inverse_norm(float sum, float inv_cols, float eps, float f) {
+  const float mean = sum * inv_cols;
   return f == 1.0f ? rsqrtf(mean + eps) : static_cast<float>(1.0 / sqrt(static_cast<double>(mean) + static_cast<double>(eps) * f * f));
 }
 
-// ------------------------------------------------------------------ 8 bits
+// ------------------------------------------------------------------ rows on their way
+// A team of warps takes every teams-th row.  Rows are copied ahead into shared memory, each lane its own elements, which
+// no other thread reads: no barrier belongs to it.  depth - 1 rows per team are on their way while one is worked on.
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until the oldest of `depth` groups is there.
+__device__ __forceinline__ void copies_wait(int depth) {
+  if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+
+// A warp's slots: `arrays` times N spans of 256 elements each.
+template <typename T, int N>
+struct Ring {
+  static constexpr int ARRAY = N * kPieces<T> * 512;  // bytes
+  uint32_t base;
+  int slot_bytes, left;
+  __device__ __forceinline__ Ring(void* smem, int arrays, int depth, int left_) : slot_bytes(arrays * ARRAY), left(left_) {
+    base = smem_u32(smem) + (threadIdx.x >> 5) * depth * slot_bytes + (threadIdx.x & 31) * 16;
+    // what lies past the row's end is never copied, and stays zero
+    if (left <= (N - 1) * 256 + distance<T, true>(4 * (kPieces<T> - 1)))
+      for (int i = 0; i < depth * slot_bytes; i += 512) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + i), "r"(0) : "memory");
+  }
+  __device__ __forceinline__ uint32_t slot(int i) const { return base + i * slot_bytes; }
+  // p: the row's first element of the lane.
+  __device__ __forceinline__ void copy(uint32_t slot, int array, const T* p) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int q = 0; q < kPieces<T>; ++q) {
+        const int d = j * 256 + distance<T, true>(4 * q);
+        if (d < left)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + array * ARRAY + (j * kPieces<T> + q) * 512), "l"(p + d) : "memory");
+      }
+  }
+  __device__ __forceinline__ void pairs(uint32_t slot, int array, int j, Pairs& v) const {
+    Part<T, true> part;
+#pragma unroll
+    for (int q = 0; q < kPieces<T>; ++q)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(part.u[q].x), "=r"(part.u[q].y), "=r"(part.u[q].z), "=r"(part.u[q].w)
+                   : "r"(slot + array * ARRAY + (j * kPieces<T> + q) * 512)
+                   : "memory");
+    part.pairs(v);
+  }
+};
+
+// Which row's elements a thread has: w, of the row's warps; c0, its first column.
+template <typename T, bool VEC, int N>
+struct Place {
+  int lane, w, c0, left;
+  int64_t team, teams;
+  __device__ __forceinline__ Place(int warps, int cols) {
+    const int in_block = threadIdx.x >> 5, per_block = warps == 1 ? blockDim.x >> 5 : 1;
+    lane = threadIdx.x & 31;
+    w = warps == 1 ? 0 : in_block;
+    c0 = first_column<T, VEC>(w * N, lane);
+    left = cols - c0;
+    team = warps == 1 ? static_cast<int64_t>(blockIdx.x) * per_block + in_block : blockIdx.x;
+    teams = static_cast<int64_t>(gridDim.x) * per_block;
+  }
+};
+
+// ------------------------------------------------------------------ forward
 struct NormParams {
   int64_t rows;
   const void* x;
@@ -180,10 +238,10 @@ struct NormParams {
   int64_t ldo;
   float* scale;
   int64_t scales;  // per row
-  int cols, warps;  // warps: per row
-  int block;        // columns per scale: 128, or 0 for rows
+  int cols, warps, depth;  // warps: per row
+  int block;               // columns per scale: 128, or 0 for rows
   int quantize, whole;
-  float eps;
+  float eps, inv_cols;
 };
 
 __device__ __forceinline__ float scale_of(float top) { return (top < 1e-30f ? 1e-30f : top) * (1.0f / 448.0f); }  // NaN stays
@@ -191,10 +249,11 @@ __device__ __forceinline__ float scale_of(float top) { return (top < 1e-30f ? 1e
 // The e4m3 of a span, and its scales where they are its own.  An element over the row's norm is t * r.  (Not t times
 // r / scale: the quotient overflows where a row of small elements has a scale at its floor.)
 template <typename T, bool VEC>
-__device__ __forceinline__ void quantize_span(const NormParams& p, int64_t row, int span, int lane, float r, float row_scale,
-                                              float (&t)[8]) {
+__device__ __forceinline__ void quantize_span(const NormParams& p, int64_t row, uint8_t* y, int left, int first_span, int j, float r,
+                                              float row_scale, Pairs& t) {
   constexpr bool HALF_WARPS = kHalfWarps<T, VEC>;
   constexpr int HALVES = HALF_WARPS ? 1 : 2;  // a lane's elements are of one block, or of two
+  const int lane = threadIdx.x & 31;
   float inv[HALVES];
 #pragma unroll
   for (int h = 0; h < HALVES; ++h) {
@@ -202,94 +261,37 @@ __device__ __forceinline__ void quantize_span(const NormParams& p, int64_t row, 
     if (p.block) {
       float top = 0.0f;
 #pragma unroll
-      for (int e = h * 4; e < (HALF_WARPS ? 8 : h * 4 + 4); ++e) top = max_nan(top, fabsf(t[e]));
+      for (int i = h * 2; i < (HALF_WARPS ? 4 : h * 2 + 2); ++i) top = max_abs_nan(top, t[i].x, t[i].y);
       s = scale_of((HALF_WARPS ? half_warp_max_nan(top) : warp_max_nan(top)) * r);
-      const int g = span * 2 + (HALF_WARPS ? lane >> 4 : h);
+      const int g = (first_span + j) * 2 + (HALF_WARPS ? lane >> 4 : h);
       if ((HALF_WARPS ? lane & 15 : lane) == 0 && g < p.scales) p.scale[row * p.scales + g] = s;
     }
     inv[h] = fast_rcp(s);
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) t[e] = t[e] * r * inv[HALF_WARPS ? 0 : e >> 2];
-  write_e4m3<T, VEC>(static_cast<uint8_t*>(p.y) + row * p.ldy, span, lane, p.cols, p.whole, t);
+  for (int i = 0; i < 4; ++i) t[i] = mul2(mul2(t[i], both(r)), both(inv[HALF_WARPS ? 0 : i >> 1]));
+  write_e4m3<T, VEC>(y, left, j, p.whole, t);
 }
 
 // What becomes of a span's elements v (scaled as r is): y = v g r.
 template <typename T, bool VEC>
-__device__ __forceinline__ void finish_span(const NormParams& p, int64_t row, int span, int lane, float r, float row_scale,
+__device__ __forceinline__ void finish_span(const NormParams& p, int64_t row, int c0, int left, int first_span, int j, float r, float row_scale,
                                             const Pairs& g, const Pairs& v) {
   Pairs y;
   if (p.quantize) {
-    float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = mul2(v[i], g[i]);
-    singles(y, f);
-    quantize_span<T, VEC>(p, row, span, lane, r, row_scale, f);
+    quantize_span<T, VEC>(p, row, static_cast<uint8_t*>(p.y) + row * p.ldy + c0, left, first_span, j, r, row_scale, y);
   } else {  // not first by g: the product of two small ones would lose bits that r brings back
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = mul2(v[i], mul2(g[i], both(r)));
-    write_pairs<T, VEC>(static_cast<T*>(p.y) + row * p.ldy, span, lane, p.cols, y);
+    write_span<T, VEC>(static_cast<T*>(p.y) + row * p.ldy + c0, left, j, y);
   }
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void read_sum(const NormParams& p, int64_t row, int span, int lane, Pairs& v) {
-  Part<T, VEC> x, res;
-  x.read(static_cast<const T*>(p.x) + row * p.ldx, span, lane, p.cols);
-  if (p.residual) res.read(static_cast<const T*>(p.residual) + row * p.ldr, span, lane, p.cols);
-  pairs_of(x, v);
-  if (p.residual) {
-    Pairs add;
-    pairs_of(res, add);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = add2(v[i], add[i]);
-  }
-}
-
-// ------------------------------------------------------------------ rows on their way
-// A team of warps takes every teams-th row.  Rows are copied ahead into shared memory, each lane its own elements, which
-// no other thread reads: no barrier belongs to it.  DEPTH - 1 rows per team are on their way while one is worked on.
-__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool some) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
-}
-
-template <typename T, int N, int DEPTH>
-struct Ring {
-  uint32_t base;
-  int stride;  // of a piece of all threads
-  int arrays;
-  __device__ __forceinline__ Ring(void* smem, int arrays_) : base(smem_u32(smem) + threadIdx.x * 16), stride(blockDim.x * 16), arrays(arrays_) {}
-  __device__ __forceinline__ uint32_t at(int slot, int array, int j, int q) const {
-    return base + (((slot * arrays + array) * N + j) * kPieces<T> + q) * stride;
-  }
-  // The row's spans of one array, zeros past its end.
-  __device__ __forceinline__ void copy(int slot, int array, const T* row, int warps, int w, int lane, int cols) const {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int q = 0; q < kPieces<T>; ++q) {
-        const int c = column<T, true>(j * warps + w, lane, 4 * q);
-        copy16(at(slot, array, j, q), row + (c < cols ? c : 0), c < cols);
-      }
-  }
-  __device__ __forceinline__ void pairs(int slot, int array, int j, Pairs& v) const {
-    Part<T, true> part;
-#pragma unroll
-    for (int q = 0; q < kPieces<T>; ++q)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(part.u[q].x), "=r"(part.u[q].y), "=r"(part.u[q].z), "=r"(part.u[q].w) : "r"(at(slot, array, j, q)) : "memory");
-    pairs_of(part, v);
-  }
-};
-
-// ------------------------------------------------------------------ forward
 // What follows once a row's s = x + residual is in registers.
 template <typename T, bool VEC, int N>
-__device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, int w, int lane, const Part<T, VEC> (&ws)[N], Pairs (&v)[N],
+__device__ __forceinline__ void norm_row(const NormParams& p, const Place<T, VEC, N>& at, int64_t row, const Part<T, VEC> (&ws)[N], Pairs (&v)[N],
                                          float2 (*room)[16]) {
   const bool row_top = p.quantize && !p.block;
   float top = 0.0f;
@@ -298,7 +300,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, int w
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       Pairs g;
-      pairs_of(ws[j], g);
+      ws[j].pairs(g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) g[i] = mul2(v[j][i], g[i]);
       top = max_magnitude(g, top);
@@ -313,16 +315,15 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, int w
     return sum.x + sum.y;
   };
   float sum = squares();
+  if (p.residual_out) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) write_span<T, VEC>(static_cast<T*>(p.residual_out) + row * p.ldo + at.c0, at.left, j, v[j]);
+  }
   if (row_top) {
     weighted_top();
     row_reduce<kMax>(sum, top, p.warps, room[0]);
   } else {
     row_reduce<kNone>(sum, top, p.warps, room[0]);
-  }
-  if (p.residual_out) {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      write_pairs<T, VEC>(static_cast<T*>(p.residual_out) + row * p.ldo, j * p.warps + w, lane, p.cols, v[j]);
   }
   float f = 1.0f;
   if (out_of_range(sum, p.eps)) {  // the same in all of the row's threads
@@ -339,56 +340,65 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, int w
     weighted_top();
     row_reduce<kMax>(sum, top, p.warps, room[2]);
   }
-  const float r = inverse_norm(sum, p.cols, p.eps, f);
-  const float row_scale = scale_of(top * r);
-  if (row_top && w == 0 && lane == 0) p.scale[row] = row_scale;
+  const float r = inverse_norm(sum, p.inv_cols, p.eps, f);
+  float row_scale = 0.0f;
+  if (row_top) {
+    row_scale = scale_of(top * r);
+    if (at.w == 0 && at.lane == 0) p.scale[row] = row_scale;
+  }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     Pairs g;
-    pairs_of(ws[j], g);
-    finish_span<T, VEC>(p, row, j * p.warps + w, lane, r, row_scale, g, v[j]);
+    ws[j].pairs(g);
+    finish_span<T, VEC>(p, row, at.c0, at.left, at.w * N, j, r, row_scale, g, v[j]);
   }
 }
 
-// Rows of aligned pieces, N spans per warp.  Bound by HBM: 4 to 8 bytes per element in 16 bits.
-template <typename T, int N, int DEPTH>
+// Rows of aligned pieces, N spans per warp.
+template <typename T, int N>
 __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ uint4 ring_memory[];
   __shared__ float2 room[2][3][16];
-  const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, w = in_block % p.warps, per_block = (blockDim.x >> 5) / p.warps;
-  const int64_t team = static_cast<int64_t>(blockIdx.x) * per_block + in_block / p.warps, teams = static_cast<int64_t>(gridDim.x) * per_block;
-  const Ring<T, N, DEPTH> ring(ring_memory, p.residual ? 2 : 1);
+  const Place<T, true, N> at(p.warps, p.cols);
+  const Ring<T, N> ring(ring_memory, p.residual ? 2 : 1, p.depth, at.left);
   wait_for_predecessor();
-  auto copy = [&](int64_t row, int slot) {
-    if (row < p.rows) {
-      ring.copy(slot, 0, static_cast<const T*>(p.x) + row * p.ldx, p.warps, w, lane, p.cols);
-      if (p.residual) ring.copy(slot, 1, static_cast<const T*>(p.residual) + row * p.ldr, p.warps, w, lane, p.cols);
+  let_successor_come();  // its blocks take the places that this grid's leave
+  const T* x = static_cast<const T*>(p.x) + at.team * p.ldx + at.c0;
+  const T* residual = static_cast<const T*>(p.residual) + at.team * p.ldr + at.c0;
+  const int64_t x_step = at.teams * p.ldx, r_step = at.teams * p.ldr;
+  int64_t copied = at.team;
+  auto copy = [&](int slot) {  // the next row on its way
+    if (copied < p.rows) {
+      ring.copy(ring.slot(slot), 0, x);
+      if (p.residual) ring.copy(ring.slot(slot), 1, residual);
+      copied += at.teams;
+      x += x_step;
+      residual += r_step;
     }
     copies_end_group();
   };
-  let_successor_come();  // its blocks take the places that this grid's leave
-#pragma unroll
-  for (int d = 0; d < DEPTH - 1; ++d) copy(team + d * teams, d);
+  for (int d = 0; d < p.depth - 1; ++d) copy(d);
   Part<T, true> ws[N];
 #pragma unroll
-  for (int j = 0; j < N; ++j) ws[j].read(static_cast<const T*>(p.weight), j * p.warps + w, lane, p.cols);
+  for (int j = 0; j < N; ++j) ws[j].read(static_cast<const T*>(p.weight) + at.c0, at.left, j);
   int slot = 0, turn = 0;
-  for (int64_t row = team; row < p.rows; row += teams) {
-    copy(row + (DEPTH - 1) * teams, slot == 0 ? DEPTH - 1 : slot - 1);
-    copies_wait<DEPTH - 1>();
+  for (int64_t row = at.team; row < p.rows; row += at.teams) {
+    copy(slot == 0 ? p.depth - 1 : slot - 1);
+    copies_wait(p.depth);
     Pairs v[N];
+    const uint32_t from = ring.slot(slot);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      ring.pairs(slot, 0, j, v[j]);
+      ring.pairs(from, 0, j, v[j]);
       if (p.residual) {
         Pairs add;
-        ring.pairs(slot, 1, j, add);
+        ring.pairs(from, 1, j, add);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], add[i]);
       }
     }
-    norm_row<T, true, N>(p, row, w, lane, ws, v, room[turn]);
-    if (++slot == DEPTH) slot = 0;
+    norm_row<T, true, N>(p, at, row, ws, v, room[turn]);
+    if (++slot == p.depth) slot = 0;
     turn ^= 1;
   }
 }
@@ -397,35 +407,49 @@ __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ N
 template <typename T, int N>
 __global__ void __launch_bounds__(512) rms_norm_ragged_kernel(const __grid_constant__ NormParams p) {
   __shared__ float2 room[3][16];
-  const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, w = in_block % p.warps;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / p.warps) + in_block / p.warps;
+  const Place<T, false, N> at(p.warps, p.cols);
+  const int64_t row = at.team;
   wait_for_predecessor();
   if (row >= p.rows) return;  // with one warp per row, where no barrier follows
   Part<T, false> xs[N], rs[N], ws[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    xs[j].read(static_cast<const T*>(p.x) + row * p.ldx, j * p.warps + w, lane, p.cols);
-    if (p.residual) rs[j].read(static_cast<const T*>(p.residual) + row * p.ldr, j * p.warps + w, lane, p.cols);
+    xs[j].read(static_cast<const T*>(p.x) + row * p.ldx + at.c0, at.left, j);
+    if (p.residual) rs[j].read(static_cast<const T*>(p.residual) + row * p.ldr + at.c0, at.left, j);
   }
 #pragma unroll
-  for (int j = 0; j < N; ++j) ws[j].read(static_cast<const T*>(p.weight), j * p.warps + w, lane, p.cols);
+  for (int j = 0; j < N; ++j) ws[j].read(static_cast<const T*>(p.weight) + at.c0, at.left, j);
   let_successor_come();
   Pairs v[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    pairs_of(xs[j], v[j]);
+    xs[j].pairs(v[j]);
     if (p.residual) {
       Pairs add;
-      pairs_of(rs[j], add);
+      rs[j].pairs(add);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], add[i]);
     }
   }
-  norm_row<T, false, N>(p, row, w, lane, ws, v, room);
+  norm_row<T, false, N>(p, at, row, ws, v, room);
 }
 
 // Rows longer than a block's registers: a block reads each of them twice (three times where its squares leave the
 // range), the second time mostly from L2.
+template <typename T, bool VEC>
+__device__ __forceinline__ void read_sum(const NormParams& p, int64_t row, int c0, Pairs& v) {
+  Part<T, VEC> x, res;
+  x.read(static_cast<const T*>(p.x) + row * p.ldx + c0, p.cols - c0, 0);
+  if (p.residual) res.read(static_cast<const T*>(p.residual) + row * p.ldr + c0, p.cols - c0, 0);
+  x.pairs(v);
+  if (p.residual) {
+    Pairs add;
+    res.pairs(add);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = add2(v[i], add[i]);
+  }
+}
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512) rms_norm_long_kernel(const __grid_constant__ NormParams p) {
   __shared__ float2 room[3][16];
@@ -441,7 +465,8 @@ __global__ void __launch_bounds__(512) rms_norm_long_kernel(const __grid_constan
 #pragma unroll 2
     for (int span = w; span < spans; span += p.warps) {
       Pairs v, g;
-      read_sum<T, VEC>(p, row, span, lane, v);
+      const int c0 = first_column<T, VEC>(span, lane);
+      read_sum<T, VEC>(p, row, c0, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = mul2(v[i], both(f));
@@ -449,8 +474,8 @@ __global__ void __launch_bounds__(512) rms_norm_long_kernel(const __grid_constan
       }
       if (with_weight) {
         Part<T, VEC> ws;
-        ws.read(weight, span, lane, p.cols);
-        pairs_of(ws, g);
+        ws.read(weight + c0, p.cols - c0, 0);
+        ws.pairs(g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], g[i]);
       }
@@ -467,7 +492,7 @@ __global__ void __launch_bounds__(512) rms_norm_long_kernel(const __grid_constan
     statistics(true);
     row_reduce<kMax>(sum, top, p.warps, room[2]);
   }
-  const float r = inverse_norm(sum, p.cols, p.eps, f);
+  const float r = inverse_norm(sum, p.inv_cols, p.eps, f);
   const float row_scale = scale_of(top * r);
   if (p.quantize && !p.block && threadIdx.x == 0) p.scale[row] = row_scale;
   // (all reads of the row for its statistics are behind the last barrier: outputs may be inputs)
@@ -475,13 +500,14 @@ __global__ void __launch_bounds__(512) rms_norm_long_kernel(const __grid_constan
   for (int span = w; span < spans; span += p.warps) {
     Pairs v, g;
     Part<T, VEC> ws;
-    ws.read(weight, span, lane, p.cols);
-    read_sum<T, VEC>(p, row, span, lane, v);
-    if (p.residual_out) write_pairs<T, VEC>(static_cast<T*>(p.residual_out) + row * p.ldo, span, lane, p.cols, v);
-    pairs_of(ws, g);
+    const int c0 = first_column<T, VEC>(span, lane), left = p.cols - c0;
+    ws.read(weight + c0, left, 0);
+    read_sum<T, VEC>(p, row, c0, v);
+    if (p.residual_out) write_span<T, VEC>(static_cast<T*>(p.residual_out) + row * p.ldo + c0, left, 0, v);
+    ws.pairs(g);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(f));
-    finish_span<T, VEC>(p, row, span, lane, r, row_scale, g, v);
+    finish_span<T, VEC>(p, row, c0, left, span, 0, r, row_scale, g, v);
   }
 }
 
@@ -499,34 +525,34 @@ struct NormBackwardParams {
   int64_t lddx;
   float* partial;  // [teams][cols], sums for dweight; null: not formed
   float4* stats;   // long rows: [rows] of (f, r, r^2 mean(g u))
-  int cols, warps;
-  float eps;
+  int cols, warps, depth;
+  float eps, inv_cols;
 };
 
-// What the gradient needs of a row, from sums over u = x f: dx = f r (g - u k), the weight's part dy u r.
+// What the gradient needs of a row, from sums over u = x f: dx = f r (g dy - u k), the weight's part dy u r.
 struct RowTerms {
   float f, r, k;
 };
-__device__ __forceinline__ RowTerms row_terms(float sum, float dot, int cols, float eps, float f) {
-  const float r = inverse_norm(sum, cols, eps, f);
-  return RowTerms{f, r, r * r * (dot / static_cast<float>(cols))};
+__device__ __forceinline__ RowTerms row_terms(float sum, float dot, float inv_cols, float eps, float f) {
+  const float r = inverse_norm(sum, inv_cols, eps, f);
+  return RowTerms{f, r, r * r * (dot * inv_cols)};
 }
 
 // A row's sums over u = x f, its terms, and what its elements become.  With four spans there is no room for the row's
 // elements in registers between the two: `dys`, `xs` give them again.
 template <typename T, bool VEC, int N, typename Dy, typename X, typename Residual>
-__device__ __forceinline__ void norm_row_backward(const NormBackwardParams& p, int64_t row, int w, int lane, const Part<T, VEC> (&ws)[N],
+__device__ __forceinline__ void norm_row_backward(const NormBackwardParams& p, const Place<T, VEC, N>& at, int64_t row, const Part<T, VEC> (&ws)[N],
                                                   Pairs (&acc)[N], float2 (*room)[16], Dy&& dys, X&& xs, Residual&& residual) {
   constexpr bool KEEP = N < 4;
-  Pairs dy[KEEP ? N : 1], x[KEEP ? N : 1];
+  constexpr int M = KEEP ? N : 1;
+  Pairs dy[M], x[M];
   float f = 1.0f, sum, dot;
   auto sums = [&] {
     float2 squares = both(0.0f), products = both(0.0f);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      constexpr int M = KEEP ? N : 1;
       Pairs g;
-      pairs_of(ws[j], g);
+      ws[j].pairs(g);
       dys(j, dy[j % M]);
       xs(j, x[j % M]);
 #pragma unroll
@@ -555,13 +581,12 @@ __device__ __forceinline__ void norm_row_backward(const NormBackwardParams& p, i
     row_reduce<kSum>(sum, dot, p.warps, room[2]);
   }
   // dx = f r (g dy - u k) + dresidual
-  const RowTerms t = row_terms(sum, dot, p.cols, p.eps, f);
+  const RowTerms t = row_terms(sum, dot, p.inv_cols, p.eps, f);
   const float2 r = both(t.r), fr = both(t.f * t.r), frk = both(-t.f * t.r * t.k);
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    constexpr int M = KEEP ? N : 1;
     Pairs g, out;
-    pairs_of(ws[j], g);
+    ws[j].pairs(g);
     if (!KEEP) {
       dys(j, dy[j % M]);
       xs(j, x[j % M]);
@@ -575,98 +600,111 @@ __device__ __forceinline__ void norm_row_backward(const NormBackwardParams& p, i
     for (int i = 0; i < 4; ++i) {
       const float2 u = x[j % M][i], d = dy[j % M][i];
       acc[j][i] = fma2(mul2(d, r), u, acc[j][i]);
-      const float2 part = mul2(mul2(d, g[i]), fr);
-      out[i] = p.dresidual ? fma2(u, frk, add2(part, out[i])) : fma2(u, frk, part);
+      const float2 gd = mul2(d, g[i]);
+      out[i] = fma2(u, frk, p.dresidual ? fma2(gd, fr, out[i]) : mul2(gd, fr));
     }
-    write_pairs<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx, j * p.warps + w, lane, p.cols, out);
+    write_span<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx + at.c0, at.left, j, out);
   }
 }
 
-// Rows of aligned pieces.  The weight's gradient is summed in registers, a part per team.  Bound by HBM: 6 bytes per
-// element in 16 bits, 8 with dresidual.
-template <typename T, int N, int DEPTH>
+template <typename T, bool VEC, int N>
+__device__ __forceinline__ void write_partial(const NormBackwardParams& p, const Place<T, VEC, N>& at, const Pairs (&acc)[N]) {
+  if (!p.partial) return;
+  float* out = p.partial + at.team * p.cols + at.c0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if constexpr (kHalfWarps<T, VEC>) {  // eight neighbours: two pieces of a row of floats
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (j * 256 < at.left)
+          *reinterpret_cast<float4*>(out + j * 256 + 4 * q) = make_float4(acc[j][2 * q].x, acc[j][2 * q].y, acc[j][2 * q + 1].x, acc[j][2 * q + 1].y);
+    } else {
+      write_span<float, VEC>(out, at.left, j, acc[j]);
+    }
+  }
+}
+
+// Rows of aligned pieces.  The weight's gradient is summed in registers, a part per team.
+template <typename T, int N>
 __global__ void __launch_bounds__(512) rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
   extern __shared__ uint4 ring_memory[];
   __shared__ float2 room[2][3][16];
-  const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, w = in_block % p.warps, per_block = (blockDim.x >> 5) / p.warps;
-  const int64_t team = static_cast<int64_t>(blockIdx.x) * per_block + in_block / p.warps, teams = static_cast<int64_t>(gridDim.x) * per_block;
-  const Ring<T, N, DEPTH> ring(ring_memory, p.dresidual ? 3 : 2);
+  const Place<T, true, N> at(p.warps, p.cols);
+  const Ring<T, N> ring(ring_memory, p.dresidual ? 3 : 2, p.depth, at.left);
   wait_for_predecessor();
-  auto copy = [&](int64_t row, int slot) {
-    if (row < p.rows) {
-      ring.copy(slot, 0, static_cast<const T*>(p.dy) + row * p.lddy, p.warps, w, lane, p.cols);
-      ring.copy(slot, 1, static_cast<const T*>(p.x) + row * p.ldx, p.warps, w, lane, p.cols);
-      if (p.dresidual) ring.copy(slot, 2, static_cast<const T*>(p.dresidual) + row * p.ldd, p.warps, w, lane, p.cols);
+  let_successor_come();
+  const T* dy = static_cast<const T*>(p.dy) + at.team * p.lddy + at.c0;
+  const T* x = static_cast<const T*>(p.x) + at.team * p.ldx + at.c0;
+  const T* d = static_cast<const T*>(p.dresidual) + at.team * p.ldd + at.c0;
+  const int64_t dy_step = at.teams * p.lddy, x_step = at.teams * p.ldx, d_step = at.teams * p.ldd;
+  int64_t copied = at.team;
+  auto copy = [&](int slot) {
+    if (copied < p.rows) {
+      ring.copy(ring.slot(slot), 0, dy);
+      ring.copy(ring.slot(slot), 1, x);
+      if (p.dresidual) ring.copy(ring.slot(slot), 2, d);
+      copied += at.teams;
+      dy += dy_step;
+      x += x_step;
+      d += d_step;
     }
     copies_end_group();
   };
-  let_successor_come();  // its blocks take the places that this grid's leave
-#pragma unroll
-  for (int d = 0; d < DEPTH - 1; ++d) copy(team + d * teams, d);
+  for (int i = 0; i < p.depth - 1; ++i) copy(i);
   Part<T, true> ws[N];
   Pairs acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    ws[j].read(static_cast<const T*>(p.weight), j * p.warps + w, lane, p.cols);
+    ws[j].read(static_cast<const T*>(p.weight) + at.c0, at.left, j);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = both(0.0f);
   }
   int slot = 0, turn = 0;
-  for (int64_t row = team; row < p.rows; row += teams) {
-    copy(row + (DEPTH - 1) * teams, slot == 0 ? DEPTH - 1 : slot - 1);
-    copies_wait<DEPTH - 1>();
+  for (int64_t row = at.team; row < p.rows; row += at.teams) {
+    copy(slot == 0 ? p.depth - 1 : slot - 1);
+    copies_wait(p.depth);
+    const uint32_t from = ring.slot(slot);
     norm_row_backward<T, true, N>(
-        p, row, w, lane, ws, acc, room[turn], [&](int j, Pairs& v) { ring.pairs(slot, 0, j, v); },
-        [&](int j, Pairs& v) { ring.pairs(slot, 1, j, v); }, [&](int j, Pairs& v) { ring.pairs(slot, 2, j, v); });
-    if (++slot == DEPTH) slot = 0;
+        p, at, row, ws, acc, room[turn], [&](int j, Pairs& v) { ring.pairs(from, 0, j, v); }, [&](int j, Pairs& v) { ring.pairs(from, 1, j, v); },
+        [&](int j, Pairs& v) { ring.pairs(from, 2, j, v); });
+    if (++slot == p.depth) slot = 0;
     turn ^= 1;
   }
-  if (!p.partial) return;
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    float sums[8];
-    singles(acc[j], sums);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {  // four neighbours each
-      const int c = column<T, true>(j * p.warps + w, lane, 4 * q);
-      if (c < p.cols)
-        *reinterpret_cast<float4*>(p.partial + team * p.cols + c) = make_float4(sums[4 * q], sums[4 * q + 1], sums[4 * q + 2], sums[4 * q + 3]);
-    }
-  }
+  write_partial<T, true, N>(p, at, acc);
 }
 
-// The same for rows off the boundaries of 16 bytes, by single elements, which are read again after the sums.
+// The same for rows off the boundaries of 16 bytes, by single elements.
 template <typename T, int N>
 __global__ void __launch_bounds__(512) rms_norm_ragged_backward_kernel(const __grid_constant__ NormBackwardParams p) {
   __shared__ float2 room[2][3][16];
-  const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5, w = in_block % p.warps, per_block = (blockDim.x >> 5) / p.warps;
-  const int64_t team = static_cast<int64_t>(blockIdx.x) * per_block + in_block / p.warps, teams = static_cast<int64_t>(gridDim.x) * per_block;
+  const Place<T, false, N> at(p.warps, p.cols);
   wait_for_predecessor();
+  let_successor_come();
   Part<T, false> ws[N];
   Pairs acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    ws[j].read(static_cast<const T*>(p.weight), j * p.warps + w, lane, p.cols);
+    ws[j].read(static_cast<const T*>(p.weight) + at.c0, at.left, j);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = both(0.0f);
   }
   int turn = 0;
-  for (int64_t row = team; row < p.rows; row += teams, turn ^= 1) {
+  for (int64_t row = at.team; row < p.rows; row += at.teams, turn ^= 1) {
+    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy + at.c0;
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx + at.c0;
+    const T* d = static_cast<const T*>(p.dresidual) + row * p.ldd + at.c0;
     Part<T, false> dys[N], xs[N], ds[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      dys[j].read(static_cast<const T*>(p.dy) + row * p.lddy, j * p.warps + w, lane, p.cols);
-      xs[j].read(static_cast<const T*>(p.x) + row * p.ldx, j * p.warps + w, lane, p.cols);
-      if (p.dresidual) ds[j].read(static_cast<const T*>(p.dresidual) + row * p.ldd, j * p.warps + w, lane, p.cols);
+      dys[j].read(dy, at.left, j);
+      xs[j].read(x, at.left, j);
+      if (p.dresidual) ds[j].read(d, at.left, j);
     }
     norm_row_backward<T, false, N>(
-        p, row, w, lane, ws, acc, room[turn], [&](int j, Pairs& v) { pairs_of(dys[j], v); }, [&](int j, Pairs& v) { pairs_of(xs[j], v); },
-        [&](int j, Pairs& v) { pairs_of(ds[j], v); });
+        p, at, row, ws, acc, room[turn], [&](int j, Pairs& v) { dys[j].pairs(v); }, [&](int j, Pairs& v) { xs[j].pairs(v); },
+        [&](int j, Pairs& v) { ds[j].pairs(v); });
   }
-  let_successor_come();
-  if (!p.partial) return;
-#pragma unroll
-  for (int j = 0; j < N; ++j) write_pairs<float, false>(p.partial + team * p.cols, j * p.warps + w, lane, p.cols, acc[j]);
+  write_partial<T, false, N>(p, at, acc);
 }
 
 // Rows longer than a block's registers, in three launches: the rows' terms; the weight's sums; dx, which may overwrite
@@ -680,25 +718,29 @@ __global__ void __launch_bounds__(512) rms_norm_long_stats_kernel(const __grid_c
   let_successor_come();
   float f = 1.0f, sum, dot, most;
   auto statistics = [&] {
-    sum = dot = most = 0.0f;
+    float2 squares = both(0.0f), products = both(0.0f);
+    most = 0.0f;
 #pragma unroll 2
     for (int span = w; span < spans; span += p.warps) {
       Part<T, VEC> ws, dys, xs;
-      float g[8], dy[8], x[8];
-      ws.read(static_cast<const T*>(p.weight), span, lane, p.cols);
-      dys.read(static_cast<const T*>(p.dy) + row * p.lddy, span, lane, p.cols);
-      xs.read(static_cast<const T*>(p.x) + row * p.ldx, span, lane, p.cols);
-      ws.values(g);
-      dys.values(dy);
-      xs.values(x);
+      Pairs g, dy, x;
+      const int c0 = first_column<T, VEC>(span, lane), left = p.cols - c0;
+      ws.read(static_cast<const T*>(p.weight) + c0, left, 0);
+      dys.read(static_cast<const T*>(p.dy) + row * p.lddy + c0, left, 0);
+      xs.read(static_cast<const T*>(p.x) + row * p.ldx + c0, left, 0);
+      ws.pairs(g);
+      dys.pairs(dy);
+      xs.pairs(x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] *= f;
-        most = max_nan(most, fabsf(x[e]));
-        sum = fmaf(x[e], x[e], sum);
-        dot = fmaf(dy[e] * g[e], x[e], dot);
+      for (int i = 0; i < 4; ++i) {
+        x[i] = mul2(x[i], both(f));
+        squares = fma2(x[i], x[i], squares);
+        products = fma2(mul2(dy[i], g[i]), x[i], products);
       }
+      most = max_magnitude(x, most);
     }
+    sum = squares.x + squares.y;
+    dot = products.x + products.y;
   };
   statistics();
   row_reduce<kSum>(sum, dot, p.warps, room[0]);
@@ -708,7 +750,7 @@ __global__ void __launch_bounds__(512) rms_norm_long_stats_kernel(const __grid_c
     statistics();
     row_reduce<kSum>(sum, dot, p.warps, room[2]);
   }
-  const RowTerms t = row_terms(sum, dot, p.cols, p.eps, f);
+  const RowTerms t = row_terms(sum, dot, p.inv_cols, p.eps, f);
   if (threadIdx.x == 0) p.stats[row] = make_float4(t.f, t.r, t.k, 0.0f);
 }
 
@@ -717,24 +759,30 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) rms_norm_long_weight_kernel(const __grid_constant__ NormBackwardParams p) {
   __shared__ float joined[8][256];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, span = blockIdx.x;
+  const int c0 = first_column<T, VEC>(span, lane), left = p.cols - c0;
   const int64_t from = p.rows * blockIdx.y / gridDim.y, to = p.rows * (blockIdx.y + 1) / gridDim.y;
   wait_for_predecessor();
   let_successor_come();
-  float acc[8] = {};
+  Pairs acc;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = both(0.0f);
 #pragma unroll 4
   for (int64_t row = from + w; row < to; row += 8) {
     Part<T, VEC> dys, xs;
-    float dy[8], x[8];
-    dys.read(static_cast<const T*>(p.dy) + row * p.lddy, span, lane, p.cols);
-    xs.read(static_cast<const T*>(p.x) + row * p.ldx, span, lane, p.cols);
+    Pairs dy, x;
+    dys.read(static_cast<const T*>(p.dy) + row * p.lddy + c0, left, 0);
+    xs.read(static_cast<const T*>(p.x) + row * p.ldx + c0, left, 0);
     const float4 t = p.stats[row];
-    dys.values(dy);
-    xs.values(x);
+    dys.pairs(dy);
+    xs.pairs(x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = fmaf(dy[e] * t.y, x[e] * t.x, acc[e]);
+    for (int i = 0; i < 4; ++i) acc[i] = fma2(mul2(dy[i], both(t.y)), mul2(x[i], both(t.x)), acc[i]);
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) joined[w][column<T, VEC>(0, lane, e)] = acc[e];
+  for (int i = 0; i < 4; ++i) {
+    joined[w][first_column<T, VEC>(0, lane) + distance<T, VEC>(2 * i)] = acc[i].x;
+    joined[w][first_column<T, VEC>(0, lane) + distance<T, VEC>(2 * i + 1)] = acc[i].y;
+  }
   __syncthreads();
   float sum = 0.0f;
 #pragma unroll
@@ -750,25 +798,26 @@ __global__ void __launch_bounds__(512) rms_norm_long_dx_kernel(const __grid_cons
   wait_for_predecessor();
   let_successor_come();
   const float4 t = p.stats[row];
+  const float2 fr = both(t.x * t.y), frk = both(-t.x * t.y * t.z);
 #pragma unroll 2
   for (int span = w; span < spans; span += p.warps) {
     Part<T, VEC> ws, dys, xs, ds;
-    float g[8], dy[8], x[8];
-    ws.read(static_cast<const T*>(p.weight), span, lane, p.cols);
-    dys.read(static_cast<const T*>(p.dy) + row * p.lddy, span, lane, p.cols);
-    xs.read(static_cast<const T*>(p.x) + row * p.ldx, span, lane, p.cols);
-    if (p.dresidual) ds.read(static_cast<const T*>(p.dresidual) + row * p.ldd, span, lane, p.cols);
-    ws.values(g);
-    dys.values(dy);
-    xs.values(x);
+    Pairs g, dy, x, out;
+    const int c0 = first_column<T, VEC>(span, lane), left = p.cols - c0;
+    ws.read(static_cast<const T*>(p.weight) + c0, left, 0);
+    dys.read(static_cast<const T*>(p.dy) + row * p.lddy + c0, left, 0);
+    xs.read(static_cast<const T*>(p.x) + row * p.ldx + c0, left, 0);
+    if (p.dresidual) ds.read(static_cast<const T*>(p.dresidual) + row * p.ldd + c0, left, 0);
+    ws.pairs(g);
+    dys.pairs(dy);
+    xs.pairs(x);
+    if (p.dresidual) ds.pairs(out);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (dy[e] * g[e] - x[e] * t.x * t.z) * t.y * t.x;
-    if (p.dresidual) {
-      ds.values(dy);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] += dy[e];
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = mul2(x[i], both(t.x)), gd = mul2(dy[i], g[i]);
+      out[i] = fma2(u, frk, p.dresidual ? fma2(gd, fr, out[i]) : mul2(gd, fr));
     }
-    write_part<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx, span, lane, p.cols, x);
+    write_span<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx + c0, left, 0, out);
   }
 }
 
@@ -787,25 +836,18 @@ struct Shape {
   int64_t blocks;
   int threads() const { return 32 * warps * per_block; }
 };
-// `element_bytes`: of all of a row's inputs together.  A row gets a warp of its
-// own where there are enough of them to fill the SMs and four spans hold it; else more warps, so that few rows are
-// spread over more lanes.
-Shape row_shape(int64_t rows, int64_t cols, int64_t element_bytes, bool vec, const ResidentWarps& warps, int num_sms) {
+// `element_bytes`: of all of a row's inputs together; `wide`: the most spans per warp where there are rows enough to fill
+// the SMs.  Few rows are spread over more warps each.
+Shape row_shape(int64_t rows, int64_t cols, int64_t element_bytes, bool vec, int wide, const ResidentWarps& warps, int num_sms) {
   const int64_t spans = ceil_div(cols, 256);
   Shape s{};
   s.warps = 16;
   s.is_long = spans > kLongSpans;
   if (s.is_long) return s;
-  if (spans <= 4 && rows >= 16 * num_sms) {
-    s.warps = 1;
-    s.spans = spans == 3 ? 4 : static_cast<int>(spans);
-  } else if (spans <= 4) {
-    s.warps = static_cast<int>(spans);
-    s.spans = 1;
-  } else {
-    s.spans = spans <= 32 ? 2 : 4;
-    s.warps = static_cast<int>(ceil_div(spans, s.spans));
-  }
+  const bool many = rows >= 4 * num_sms;
+  s.spans = spans <= 4 && !many ? 1 : spans <= 32 ? 2 : 4;
+  if (many && (spans <= 4 || wide == 4)) s.spans = spans == 1 ? 1 : spans == 2 ? 2 : 4;
+  s.warps = static_cast<int>(ceil_div(spans, s.spans));
   s.per_block = s.warps == 1 ? 4 : 1;
   const int64_t slot = element_bytes * 256 * s.per_block * s.warps * s.spans;
   s.is_long = vec && 2 * slot > kRingMost;
@@ -814,8 +856,7 @@ Shape row_shape(int64_t rows, int64_t cols, int64_t element_bytes, bool vec, con
     return s;
   }
   // as many blocks as the registers hold, each with as many rows on their way as the shared memory then does
-  const int64_t by_registers = std::max(1, (s.spans == 1 ? warps.one : s.spans == 2 ? warps.two : warps.four) / (s.warps * s.per_block));
-  int64_t resident = by_registers;
+  int64_t resident = std::max(1, (s.spans == 1 ? warps.one : s.spans == 2 ? warps.two : warps.four) / (s.warps * s.per_block));
   if (vec) {
     s.depth = 4;
     while (s.depth > 2 && resident * (s.depth * slot + 1024) > kRingMost) --s.depth;
@@ -840,7 +881,7 @@ bool backward_vec(const oz2_rms_norm_backward_args& a) {
 }
 Shape backward_shape(const oz2_rms_norm_backward_args& a, int num_sms) {
   // (as for three inputs, with or without dresidual: the weight's sums are then the same)
-  return row_shape(a.rows, a.cols, dtype_bytes(static_cast<oz2_dtype>(a.dtype)) * 3, backward_vec(a), kBackward, num_sms);
+  return row_shape(a.rows, a.cols, dtype_bytes(static_cast<oz2_dtype>(a.dtype)) * 3, backward_vec(a), 2, kBackward, num_sms);
 }
 int64_t partial_rows(const oz2_rms_norm_backward_args& a, int num_sms) {
   if (!a.dweight) return 0;
@@ -851,7 +892,7 @@ size_t stats_bytes(const oz2_rms_norm_backward_args& a, int num_sms) {
   return backward_shape(a, num_sms).is_long ? static_cast<size_t>(a.rows) * sizeof(float4) : 0;
 }
 
-// Calls f with the kernel's spans per warp and depth as constants.
+// Calls f with the kernel's spans per warp as a constant.
 template <typename F>
 cudaError_t with_spans(int spans, F&& f) {
   switch (spans) {
@@ -860,20 +901,13 @@ cudaError_t with_spans(int spans, F&& f) {
     default: return f(std::integral_constant<int, 4>());
   }
 }
-template <typename F>
-cudaError_t with_depth(int depth, F&& f) {
-  switch (depth) {
-    case 2: return f(std::integral_constant<int, 2>());
-    case 3: return f(std::integral_constant<int, 3>());
-    default: return f(std::integral_constant<int, 4>());
-  }
-}
 
 template <typename T>
 cudaError_t forward(NormParams& p, bool vec, const DeviceResources& res, cudaStream_t st) {
   const int arrays = p.residual ? 2 : 1;
-  const Shape s = row_shape(p.rows, p.cols, sizeof(T) * arrays, vec, kForward, res.num_sms);
+  const Shape s = row_shape(p.rows, p.cols, sizeof(T) * arrays, vec, vec ? 4 : 2, kForward, res.num_sms);
   p.warps = s.warps;
+  p.depth = s.depth;
   if (s.is_long) {
     return vec ? launch_kernel(rms_norm_long_kernel<T, true>, p.rows, 512, 0, 1, st, p)
                : launch_kernel(rms_norm_long_kernel<T, false>, p.rows, 512, 0, 1, st, p);
@@ -881,12 +915,9 @@ cudaError_t forward(NormParams& p, bool vec, const DeviceResources& res, cudaStr
   return with_spans(s.spans, [&](auto n) {
     constexpr int N = decltype(n)::value;
     if (!vec) return launch_kernel(rms_norm_ragged_kernel<T, N>, ceil_div(p.rows, s.per_block), s.threads(), 0, 1, st, p);
-    return with_depth(s.depth, [&](auto d) {
-      constexpr auto kernel = rms_norm_kernel<T, N, decltype(d)::value>;
-      const size_t smem = ring_bytes<T>(s, arrays);
-      const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
-      return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), smem, 1, st, p) : e;
-    });
+    constexpr auto kernel = rms_norm_kernel<T, N>;
+    const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
+    return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), ring_bytes<T>(s, arrays), 1, st, p) : e;
   });
 }
 
@@ -903,6 +934,7 @@ cudaError_t backward(NormBackwardParams& p, const oz2_rms_norm_backward_args& a,
   const bool vec = backward_vec(a);
   const Shape s = backward_shape(a, res.num_sms);
   p.warps = s.warps;
+  p.depth = s.depth;
   if (s.is_long) {
     const int64_t slices = weight_slices(a, res.num_sms);
     return vec ? backward_long<T, true>(p, slices, st) : backward_long<T, false>(p, slices, st);
@@ -910,12 +942,9 @@ cudaError_t backward(NormBackwardParams& p, const oz2_rms_norm_backward_args& a,
   return with_spans(s.spans, [&](auto n) {
     constexpr int N = decltype(n)::value;
     if (!vec) return launch_kernel(rms_norm_ragged_backward_kernel<T, N>, s.blocks, s.threads(), 0, 1, st, p);
-    return with_depth(s.depth, [&](auto d) {
-      constexpr auto kernel = rms_norm_backward_kernel<T, N, decltype(d)::value>;
-      const size_t smem = ring_bytes<T>(s, a.dresidual ? 3 : 2);
-      const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
-      return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), smem, 1, st, p) : e;
-    });
+    constexpr auto kernel = rms_norm_backward_kernel<T, N>;
+    const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
+    return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), ring_bytes<T>(s, a.dresidual ? 3 : 2), 1, st, p) : e;
   });
 }
 
@@ -941,6 +970,7 @@ cudaError_t launch_rms_norm(const oz2_rms_norm_args& a, const DeviceResources& r
   p.quantize = a.quantize;
   p.whole = reinterpret_cast<uintptr_t>(a.y) % 8 == 0 && a.ldy % 8 == 0;
   p.eps = static_cast<float>(a.eps);
+  p.inv_cols = static_cast<float>(1.0 / static_cast<double>(a.cols));
   const bool vec = pieces_aligned(nullptr, a.cols, t) && pieces_aligned(a.x, a.ldx, t) && pieces_aligned(a.weight, 0, t) &&
                    (!a.residual || pieces_aligned(a.residual, a.ldr, t)) && (!a.residual_out || pieces_aligned(a.residual_out, a.ldo, t)) &&
                    (a.quantize || pieces_aligned(a.y, a.ldy, t));
@@ -972,6 +1002,7 @@ cudaError_t launch_rms_norm_backward(const oz2_rms_norm_backward_args& a, const 
   p.partial = a.dweight ? reinterpret_cast<float*>(res.workspace + stats_bytes(a, res.num_sms)) : nullptr;
   p.cols = static_cast<int>(a.cols);
   p.eps = static_cast<float>(a.eps);
+  p.inv_cols = static_cast<float>(1.0 / static_cast<double>(a.cols));
   cudaError_t e;
   switch (t) {
     case OZ2_BF16: e = backward<__nv_bfloat16>(p, a, res, st); break;
