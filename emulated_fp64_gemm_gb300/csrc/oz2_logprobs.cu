@@ -10,8 +10,10 @@
 //
 // Everything past the pass uses that a thread's elements can be found again:
 //  * the k-th largest of the maxima of groups of threads is a lower bound of the k-th
-//    largest logit, so that only threads whose own maximum reaches it can hold
-//    alternatives: a few dozen, whose elements are read again (from L2);
+//    largest logit.  Each thread has noted the maxima of its passes in shared memory, so
+//    that only passes (of 32 elements, mostly) that reach the bound can hold
+//    alternatives: a few dozen, which are read again (whole threads' elements, sixteen times
+//    as many, cost 4096 x 131072 with 20 alternatives 75 us instead of NEW);
 //  * where one token has almost all of the probability, its log p is -log1p of the others'
 //    sum, which 32 bits have lost beside it: the elements of the thread that holds the
 //    maximum are summed again without it.
@@ -79,6 +81,7 @@ struct Slice {
   const T* groups;
   int vocab, lead, tail, v0, v1;
   int64_t tail_at;
+  int shift;  // a thread's n-th group is noted in slot n >> shift
   __device__ __forceinline__ Slice(const LogprobParams& p, int64_t r, int rank) {
     row = static_cast<const T*>(p.logits) + r * p.ld;
     vocab = static_cast<int>(p.vocab);
@@ -90,6 +93,8 @@ struct Slice {
     tail = rank == p.ranks - 1 ? static_cast<int>(vocab - tail_at) : 0;
     v0 = static_cast<int>(static_cast<int64_t>(vectors) * rank / p.ranks);
     v1 = static_cast<int>(static_cast<int64_t>(vectors) * (rank + 1) / p.ranks);
+    shift = 2;
+    while (((v1 - v0 + THREADS - 1) / THREADS - 1) >> shift >= 16) ++shift;
   }
   __device__ __forceinline__ int first_column() const { return lead ? 0 : static_cast<int>(groups - row) + 8 * v0; }
   __device__ __forceinline__ int last_column() const { return tail ? vocab : static_cast<int>(groups - row) + 8 * v1; }
@@ -151,8 +156,9 @@ struct Running {
     s.x += e;
     if (ENTROPY) t.x = fmaf(e, d, t.x);
   }
+  // The largest element is returned.
   template <int N>
-  __device__ __forceinline__ void add_groups(Raw8<T> (&raw)[N], const LogprobParams& p) {
+  __device__ __forceinline__ float add_groups(Raw8<T> (&raw)[N], const LogprobParams& p) {
     float top = top8(raw[0]);
 #pragma unroll
     for (int i = 1; i < N; ++i) top = max_nan(top, top8(raw[i]));
@@ -170,6 +176,7 @@ struct Running {
 #pragma unroll
       for (int j = 0; j < 4; ++j) add(make_float2(x[2 * j], x[2 * j + 1]), p.c);
     }
+    return top;
   }
   __device__ __forceinline__ float sum() const { return s.x + s.y; }
   __device__ __forceinline__ float bent() const { return t.x + t.y; }
@@ -187,12 +194,15 @@ struct Shared {
   static constexpr int kGroups = THREADS < 64 ? THREADS : 64;
   // candidates: past the elements of a slice that reaches fewer than 32 groups (their threads have one vector each)
   static constexpr int kCandidates = THREADS == 32 ? 512 : 6 * THREADS;
-  static constexpr int kJobs = THREADS < 64 ? THREADS : 64;
+  static constexpr int kSlots = 16;    // in which a thread notes its maxima
+  static constexpr int kFewJobs = 96;  // more are looked at more closely
+  static constexpr int kJobs = 512;
   uint64_t candidates[kCandidates];
+  float noted[kSlots][THREADS];
   uint64_t list[OZ2_TOP_MAX];  // the block's alternatives, in order
   uint64_t merged[8 * OZ2_TOP_MAX];
-  uint32_t group_top[kGroups];
-  uint16_t jobs[THREADS];
+  alignas(16) uint32_t group_top[kGroups];
+  uint16_t jobs[kJobs];  // slot * THREADS + thread
   float warp_top[32];
   Parts warp_parts[kWarps];
   uint32_t warp_counts[kWarps];
@@ -255,16 +265,33 @@ __device__ __forceinline__ Parts relative_to(float top, float from, Parts v, flo
 
 // ------------------------------------------------------------------ alternatives
 // The block's `top` largest place keys go into sh.list, in order (0: there are fewer).
+template <int THREADS>
+__device__ __forceinline__ void take(Shared<THREADS>& sh, float x, int column, uint32_t least) {
+  const uint32_t k = order_key(x);
+  if (k < least) return;
+  const uint32_t at = atomicAdd(&sh.count, 1u);  // the order is made up for by the sorting
+  if (at < Shared<THREADS>::kCandidates) sh.candidates[at] = place_key(k, column);
+}
+
+// Of what the jobs name, the elements whose key is at least `least`; four lanes to a job.
 template <typename T, int THREADS>
 __device__ __forceinline__ void collect_at_least(Shared<THREADS>& sh, const Slice<T, THREADS>& s, uint32_t least) {
-  const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
-  for (uint32_t j = half; j < sh.job_count; j += THREADS / 16)
-    s.again(sh.jobs[j], lane, 16, [&](float x, int column) {
-      const uint32_t k = order_key(x);
-      if (k < least) return;
-      const uint32_t at = atomicAdd(&sh.count, 1u);  // the order is made up for by the sorting
-      if (at < Shared<THREADS>::kCandidates) sh.candidates[at] = place_key(k, column);
-    });
+  const int lane = threadIdx.x & 3, base = static_cast<int>(s.groups - s.row), jobs = min(sh.job_count, static_cast<uint32_t>(Shared<THREADS>::kJobs));
+  for (int j = threadIdx.x >> 2; j < jobs; j += THREADS / 4) {
+    const int job = sh.jobs[j], t = job % THREADS, slot = job / THREADS;
+#pragma unroll 1
+    for (int n = lane; n < 1 << s.shift; n += 4) {
+      const int64_t v = s.v0 + t + ((static_cast<int64_t>(slot) << s.shift) + n) * THREADS;
+      if (v >= s.v1) break;
+      Raw8<T> raw;
+      raw.read(s.groups + v * 8);
+      if (order_key(top8(raw)) < least) continue;
+      float x[8];
+      raw.values(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) take(sh, x[e], static_cast<int>(base + v * 8 + e), least);
+    }
+  }
 }
 
 // The elements equal to the threshold, from the lowest place on, until there are `top` candidates.
@@ -347,29 +374,48 @@ __device__ __forceinline__ void find_alternatives(Shared<THREADS>& sh, const Sli
   if (tid < S::kGroups) {
     k = sh.group_top[tid];
     int above = 0;
-#pragma unroll 8
-    for (int i = 0; i < S::kGroups; ++i) above += sh.group_top[i] > k || (sh.group_top[i] == k && i < tid);
+    const uint4* four = reinterpret_cast<const uint4*>(sh.group_top);
+#pragma unroll
+    for (int i = 0; i < S::kGroups / 4; ++i) {
+      const uint4 g = four[i];
+      above += (g.x > k || (g.x == k && 4 * i < tid)) + (g.y > k || (g.y == k && 4 * i + 1 < tid)) +
+               (g.z > k || (g.z == k && 4 * i + 2 < tid)) + (g.w > k || (g.w == k && 4 * i + 3 < tid));
+    }
     if (above == top - 1) sh.threshold = k;
   }
   __syncthreads();
-  // threads that hold elements at the threshold or above
+  // the passes that hold elements at the threshold or above, and the thread's single element
   const uint32_t threshold = sh.threshold;
-  if (mine && mine >= threshold) sh.jobs[atomicAdd(&sh.job_count, 1u)] = static_cast<uint16_t>(tid);
+  const int column = s.single(tid), slots = s.v0 + tid < s.v1 ? (((s.v1 - s.v0 - tid - 1) / THREADS) >> s.shift) + 1 : 0;
+  auto name_jobs = [&](uint32_t least) {
+    if (mine < least || !mine) return;
+    for (int i = 0; i < slots; ++i)
+      if (order_key(sh.noted[i][tid]) >= least) {
+        const uint32_t at = atomicAdd(&sh.job_count, 1u);
+        if (at < S::kJobs) sh.jobs[at] = static_cast<uint16_t>(i * THREADS + tid);
+      }
+  };
+  uint32_t least = max(threshold, 1u);
+  name_jobs(least);
   __syncthreads();
-  const bool many = sh.job_count > S::kJobs;
+  const bool many = sh.job_count > S::kFewJobs;
+  bool crowded = false;
   if (many) {
     // (masked rows, whose threshold is -inf, or constant ones): only those above it, and then the lowest places at it by a
-    // search in order
+    // search in order.  Nothing is above the largest key, that of NaN.
     __syncthreads();
     if (tid == 0) sh.job_count = 0;
     __syncthreads();
-    if (mine > threshold) sh.jobs[atomicAdd(&sh.job_count, 1u)] = static_cast<uint16_t>(tid);
+    if (threshold != 0xFFFFFFFFu) name_jobs(least = threshold + 1);
     __syncthreads();
+    crowded = sh.job_count > S::kJobs;
   }
-  // (nothing is above the largest key, that of NaN, and no thread has a job then)
-  collect_at_least(sh, s, many ? threshold + 1 : max(threshold, 1u));
+  if (!crowded && !(many && threshold == 0xFFFFFFFFu)) {
+    collect_at_least(sh, s, least);
+    if (column >= 0) take(sh, Elem<T>::up(s.row[column]), column, least);
+  }
   __syncthreads();
-  if (sh.count > S::kCandidates) {
+  if (crowded || sh.count > S::kCandidates) {
     __syncthreads();
     collect_in_turn(sh, s, top);
     __syncthreads();
@@ -407,18 +453,27 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel
   Running<T, ENTROPY> a;
   {
     int64_t v = s.v0 + tid;
+    int n = 0;
+    auto note = [&](float most) {  // of the groups from the n-th on
+      float& slot = sh.noted[n >> s.shift][tid];
+      slot = n & ((1 << s.shift) - 1) ? max_nan(slot, most) : most;
+    };
 #pragma unroll 1
     for (; v + (kVectors - 1) * THREADS < s.v1; v += kVectors * THREADS) {
       Raw8<T> raw[kVectors];
 #pragma unroll
       for (int u = 0; u < kVectors; ++u) raw[u].read(s.groups + (v + u * THREADS) * 8);
-      a.add_groups(raw, p);
+      const float most = a.add_groups(raw, p);
+      if (p.top) note(most);
+      n += kVectors;
     }
 #pragma unroll 1
     for (; v < s.v1; v += THREADS) {
       Raw8<T> raw[1];
       raw[0].read(s.groups + v * 8);
-      a.add_groups(raw, p);
+      const float most = a.add_groups(raw, p);
+      if (p.top) note(most);
+      ++n;
     }
     const int c = s.single(tid);
     if (c >= 0) a.add_single(Elem<T>::up(s.row[c]), p);
@@ -496,9 +551,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel
     if (ranks > 1) cluster_arrive();
     for (int i = tid; i < n; i += THREADS) {
       const uint64_t key = sh.merged[i];
-      int above = 0;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) above += sh.merged[j] > key;
+      const int mine = i / p.top;
+      int above = i % p.top;  // the lists are in order: of each other one, how many are above
+      for (int r = 0; r < ranks; ++r) {
+        if (r == mine) continue;
+        int from = 0;
+#pragma unroll
+        for (int step = OZ2_TOP_MAX; step; step >>= 1)
+          if (from + step <= p.top && sh.merged[r * p.top + from + step - 1] > key) from += step;
+        above += from;
+      }
       if (key && above < p.top) {
         const float x = key_value(static_cast<uint32_t>(key >> 32));
         p.top_logprobs[row * p.top + above] = bad ? nan : none ? z_max : fmaf(x - top, p.inv_t, -log_sum);

@@ -162,8 +162,8 @@ __device__ __forceinline__ float inverse_norm(float sum, float inv_cols, float e
 }
 
 // ------------------------------------------------------------------ rows on their way
-// A team of warps takes every teams-th row.  Rows are copied ahead into shared memory, each lane its own elements, which
-// no other thread reads: no barrier belongs to it.  depth - 1 rows per team are on their way while one is worked on.
+// Rows are copied ahead into shared memory, each lane its own elements, which no other thread reads: no barrier belongs to
+// it.  depth - 1 rows per team of warps are on their way while one is worked on.
 __device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until the oldest of `depth` groups is there.
 __device__ __forceinline__ void copies_wait(int depth) {
@@ -238,8 +238,8 @@ struct NormParams {
   int64_t ldo;
   float* scale;
   int64_t scales;  // per row
-  int cols, warps, depth;  // warps: per row
-  int block;               // columns per scale: 128, or 0 for rows
+  int cols, warps, depth, run;  // warps: per row; run: rows of a team
+  int block;                    // columns per scale: 128, or 0 for rows
   int quantize, whole;
   float eps, inv_cols;
 };
@@ -354,7 +354,9 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const Place<T, VEC
   }
 }
 
-// Rows of aligned pieces, N spans per warp.
+// Rows of aligned pieces, N spans per warp, a run of a few neighbouring rows per team.  Blocks that take rows from the whole
+// matrix until all are done drift apart, and the memory serves them worse: 8192 x 8192 to 8 bits 80 us that way, 73 in runs
+// of four; 8192 x 4096 with residual 44 and 41.7.
 template <typename T, int N>
 __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ uint4 ring_memory[];
@@ -363,17 +365,17 @@ __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ N
   const Ring<T, N> ring(ring_memory, p.residual ? 2 : 1, p.depth, at.left);
   wait_for_predecessor();
   let_successor_come();  // its blocks take the places that this grid's leave
-  const T* x = static_cast<const T*>(p.x) + at.team * p.ldx + at.c0;
-  const T* residual = static_cast<const T*>(p.residual) + at.team * p.ldr + at.c0;
-  const int64_t x_step = at.teams * p.ldx, r_step = at.teams * p.ldr;
-  int64_t copied = at.team;
+  const int64_t first = at.team * p.run, end = min(first + p.run, p.rows);
+  const T* x = static_cast<const T*>(p.x) + first * p.ldx + at.c0;
+  const T* residual = static_cast<const T*>(p.residual) + first * p.ldr + at.c0;
+  int64_t copied = first;
   auto copy = [&](int slot) {  // the next row on its way
-    if (copied < p.rows) {
+    if (copied < end) {
       ring.copy(ring.slot(slot), 0, x);
       if (p.residual) ring.copy(ring.slot(slot), 1, residual);
-      copied += at.teams;
-      x += x_step;
-      residual += r_step;
+      ++copied;
+      x += p.ldx;
+      residual += p.ldr;
     }
     copies_end_group();
   };
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ N
 #pragma unroll
   for (int j = 0; j < N; ++j) ws[j].read(static_cast<const T*>(p.weight) + at.c0, at.left, j);
   int slot = 0, turn = 0;
-  for (int64_t row = at.team; row < p.rows; row += at.teams) {
+  for (int64_t row = first; row < end; ++row) {
     copy(slot == 0 ? p.depth - 1 : slot - 1);
     copies_wait(p.depth);
     Pairs v[N];
@@ -673,7 +675,8 @@ __global__ void __launch_bounds__(512) rms_norm_backward_kernel(const __grid_con
   write_partial<T, true, N>(p, at, acc);
 }
 
-// The same for rows off the boundaries of 16 bytes, by single elements.
+// The same for rows off the boundaries of 16 bytes, by single elements.  Bound by latency: 8192 x 5001 takes 147 us (read a
+// second time after the sums instead of kept, with more warps, 221).
 template <typename T, int N>
 __global__ void __launch_bounds__(512) rms_norm_ragged_backward_kernel(const __grid_constant__ NormBackwardParams p) {
   __shared__ float2 room[2][3][16];
@@ -855,18 +858,20 @@ Shape row_shape(int64_t rows, int64_t cols, int64_t element_bytes, bool vec, int
     s.warps = 16;
     return s;
   }
-  // as many blocks as the registers hold, each with as many rows on their way as the shared memory then does
+  // as many blocks as the registers hold, with up to 50 KB per SM on their way, and 100 where rows are long (more is served
+  // worse: the gradient of 16384 x 4096 with 49, 98 and 147 KB 84.0, 82.9 and 88.8 us, of 65536 x 512 47, 50 and 53)
   int64_t resident = std::max(1, (s.spans == 1 ? warps.one : s.spans == 2 ? warps.two : warps.four) / (s.warps * s.per_block));
   if (vec) {
+    const int64_t most = s.per_block == 1 ? 100 * 1024 : 50 * 1024;
     s.depth = 4;
-    while (s.depth > 2 && resident * (s.depth * slot + 1024) > kRingMost) --s.depth;
+    while (s.depth > 2 && (resident * (s.depth * slot + 1024) > kRingMost || resident * (s.depth - 1) * slot > most)) --s.depth;
     resident = std::max<int64_t>(1, std::min(resident, kRingMost / (s.depth * slot + 1024)));
   }
   s.blocks = std::min(ceil_div(rows, s.per_block), resident * num_sms);
   return s;
 }
 template <typename T>
-size_t ring_bytes(const Shape& s, int arrays) { return static_cast<size_t>(s.threads()) * s.depth * arrays * s.spans * kPieces<T> * 16; }
+size_t ring_bytes(const Shape& s, int arrays, int depth) { return static_cast<size_t>(s.threads()) * depth * arrays * s.spans * kPieces<T> * 16; }
 
 int64_t weight_slices(const oz2_rms_norm_backward_args& a, int num_sms) {
   return std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.rows, 32), 4 * num_sms / std::max<int64_t>(1, ceil_div(a.cols, 256))));
@@ -907,7 +912,9 @@ cudaError_t forward(NormParams& p, bool vec, const DeviceResources& res, cudaStr
   const int arrays = p.residual ? 2 : 1;
   const Shape s = row_shape(p.rows, p.cols, sizeof(T) * arrays, vec, vec ? 4 : 2, kForward, res.num_sms);
   p.warps = s.warps;
-  p.depth = s.depth;
+  p.depth = std::min(s.depth, 2);
+  // four rows per team, 16 where the rows have one input (8192 x 4096: 22.7 us, in fours 24.6), but no fewer blocks than run at once
+  p.run = static_cast<int>(std::min<int64_t>(p.residual ? 4 : 16, ceil_div(p.rows, s.blocks * s.per_block)));
   if (s.is_long) {
     return vec ? launch_kernel(rms_norm_long_kernel<T, true>, p.rows, 512, 0, 1, st, p)
                : launch_kernel(rms_norm_long_kernel<T, false>, p.rows, 512, 0, 1, st, p);
@@ -917,7 +924,7 @@ cudaError_t forward(NormParams& p, bool vec, const DeviceResources& res, cudaStr
     if (!vec) return launch_kernel(rms_norm_ragged_kernel<T, N>, ceil_div(p.rows, s.per_block), s.threads(), 0, 1, st, p);
     constexpr auto kernel = rms_norm_kernel<T, N>;
     const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
-    return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), ring_bytes<T>(s, arrays), 1, st, p) : e;
+    return e == cudaSuccess ? launch_kernel(kernel, ceil_div(p.rows, s.per_block * p.run), s.threads(), ring_bytes<T>(s, arrays, p.depth), 1, st, p) : e;
   });
 }
 
@@ -944,7 +951,7 @@ cudaError_t backward(NormBackwardParams& p, const oz2_rms_norm_backward_args& a,
     if (!vec) return launch_kernel(rms_norm_ragged_backward_kernel<T, N>, s.blocks, s.threads(), 0, 1, st, p);
     constexpr auto kernel = rms_norm_backward_kernel<T, N>;
     const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
-    return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), ring_bytes<T>(s, a.dresidual ? 3 : 2), 1, st, p) : e;
+    return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), ring_bytes<T>(s, a.dresidual ? 3 : 2, s.depth), 1, st, p) : e;
   });
 }
 
