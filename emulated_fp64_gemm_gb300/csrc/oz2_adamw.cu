@@ -401,16 +401,16 @@ cudaError_t launch_part(const oz2_adamw_args& a, AdamwParams p, int64_t from, in
   int64_t chunks = 0;
   p.count = 0;
   for (int64_t i = from; i < to; ++i) {
-    const oz2_adamw_tensor& x = a.tensors[i];
-    if (x.elements) {
-      t.param[p.count] = x.param;
-      t.grad[p.count] = x.grad;
-      t.elements[p.count] = x.elements;
+    const int64_t n = a.elements[i];
+    if (n) {
+      t.param[p.count] = a.params[i];
+      t.grad[p.count] = a.grads[i];
+      t.elements[p.count] = n;
       t.block[p.count] = block;
       t.chunk[p.count++] = static_cast<int>(chunks);
     }
-    block += ceil_div(x.elements, kBlock);
-    chunks += ceil_div(x.elements, kBlock * p.turns);
+    block += ceil_div(n, kBlock);
+    chunks += ceil_div(n, kBlock * p.turns);
   }
   return launch_kernel(adamw_kernel<P, G, BITS, MASTER, MOST>, chunks ? chunks : 1, 32, 0, 1, st, t, p);
 }
@@ -419,12 +419,12 @@ cudaError_t launch_part(const oz2_adamw_args& a, AdamwParams p, int64_t from, in
 template <typename P, typename G, int BITS, bool MASTER>
 cudaError_t launch_all(const oz2_adamw_args& a, AdamwParams p, cudaStream_t st) {
   int64_t end = a.count;  // behind the last tensor that is not empty
-  while (end > 0 && a.tensors[end - 1].elements == 0) --end;
+  while (end > 0 && a.elements[end - 1] == 0) --end;
   int64_t block = 0, from = 0;
   do {
     int64_t to = from, some = 0, chunks = 0, blocks = 0;
     for (; to < end; ++to) {
-      const int64_t n = a.tensors[to].elements, c = ceil_div(n, kBlock * p.turns);
+      const int64_t n = a.elements[to], c = ceil_div(n, kBlock * p.turns);
       if (some && (some + (n > 0) > kMany || chunks + c > (int64_t(1) << 30))) break;
       some += n > 0;
       chunks += c;
@@ -456,7 +456,7 @@ cudaError_t launch_adamw(const oz2_adamw_args& a, const DeviceResources& res, cu
   AdamwParams p{};
   // as few turns as let all CTAs run at once, up to those of a long step
   int64_t blocks = 0;
-  for (int64_t i = 0; i < a.count; ++i) blocks += ceil_div(a.tensors[i].elements, kBlock);
+  for (int64_t i = 0; i < a.count; ++i) blocks += ceil_div(a.elements[i], kBlock);
   p.turns = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kTurns, ceil_div(blocks, static_cast<int64_t>(res.num_sms) * kResident))));
   p.exp_avg = a.exp_avg;
   p.exp_avg_sq = a.exp_avg_sq;

@@ -63,9 +63,9 @@ oz2_status adamw(const oz2_adamw_args& a, cudaStream_t st) {
   spans.reserve(static_cast<size_t>(a.count));
   const size_t size = dtype_bytes(static_cast<oz2_dtype>(a.dtype));
   for (int64_t i = 0; i < a.count; ++i)
-    if (a.tensors[i].elements) {
-      const uintptr_t at = reinterpret_cast<uintptr_t>(a.tensors[i].param);
-      spans.emplace_back(at, at + static_cast<size_t>(a.tensors[i].elements) * size);
+    if (a.elements[i]) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(a.params[i]);
+      spans.emplace_back(at, at + static_cast<size_t>(a.elements[i]) * size);
     }
   if (!std::is_sorted(spans.begin(), spans.end())) std::sort(spans.begin(), spans.end());
   for (size_t i = 1; i < spans.size(); ++i)
@@ -111,16 +111,16 @@ bool token_logprobs_backward_ok(const oz2_token_logprobs_backward_args& a) {
 bool finite(double v) { return std::isfinite(v) && std::fabs(v) <= 1e30; }
 
 bool adamw_ok(const oz2_adamw_args& a) {
-  if (!(a.count >= 0 && a.count <= (1 << 24) && (a.tensors || a.count == 0) && dtype_ok(a.dtype) &&
+  if (!(a.count >= 0 && a.count <= (1 << 24) && ((a.params && a.grads && a.elements) || a.count == 0) && dtype_ok(a.dtype) &&
         (a.grad_dtype == a.dtype || a.grad_dtype == OZ2_F32) && (a.bits == 8 || a.bits == 32) && a.reserved == 0 && a.step &&
         a.beta1 >= 0.0 && a.beta1 < 1.0 && a.beta2 >= 0.0 && a.beta2 < 1.0 && eps_ok(a.eps) && finite(a.lr) && finite(a.weight_decay) &&
         finite(a.grad_scale) && (!a.master || a.dtype != OZ2_F32)))
     return false;
   int64_t elements = 0;
   for (int64_t i = 0; i < a.count; ++i) {
-    const oz2_adamw_tensor& t = a.tensors[i];
-    if (t.elements < 0 || t.elements > (int64_t(1) << 40) || (t.elements > 0 && (!t.param || !t.grad))) return false;
-    elements += t.elements;
+    const int64_t n = a.elements[i];
+    if (n < 0 || n > (int64_t(1) << 40) || (n > 0 && (!a.params[i] || !a.grads[i]))) return false;
+    elements += n;
     if (elements > (int64_t(1) << 40)) return false;
   }
   if (elements == 0) return true;

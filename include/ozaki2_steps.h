@@ -155,15 +155,10 @@ oz2_status ozaki2_token_logprobs_backward(const oz2_token_logprobs_backward_args
 /* Elements that share a scale in 8 bits; each tensor's states start at a multiple of it. */
 #define OZ2_ADAMW_BLOCK 256
 
-typedef struct {
-  void* param;
-  const void* grad;
-  int64_t elements;
-} oz2_adamw_tensor;
-
 /*
- * One step of AdamW over `count` tensors (a host array, read before the call
- * returns), each contiguous: with g = grad * grad_scale and t = step[0] + 1,
+ * One step of AdamW over `count` tensors, each contiguous: params, grads and
+ * elements are host arrays, read before the call returns.  With g = grad *
+ * grad_scale and t = step[0] + 1,
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
  *   param = param (1 - lr weight_decay)
  *           - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps),
@@ -203,7 +198,9 @@ typedef struct {
  */
 typedef struct {
   int64_t count;
-  const oz2_adamw_tensor* tensors;
+  void* const* params;
+  const void* const* grads;
+  const int64_t* elements;
   void* exp_avg;
   void* exp_avg_sq;
   float* exp_avg_scale;

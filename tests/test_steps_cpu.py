@@ -49,10 +49,10 @@ def fields(name):
         line = " ".join(line.split())
         if not line:
             continue
-        kind, names = re.match(r"((?:const )?\w+) ?(.*)", line).groups()
+        kind, names = re.match(r"((?:const )?\w+(?:\* const)?) ?(.*)", line).groups()
         for n in names.split(","):
             n = n.strip()
-            code = "P" if n.startswith("*") else {"int64_t": "q", "uint64_t": "Q", "double": "d", "int32_t": "i"}.get(kind, "P")
+            code = "P" if n.startswith("*") or "*" in kind else {"int64_t": "q", "uint64_t": "Q", "double": "d", "int32_t": "i"}.get(kind, "P")
             out.append((n.lstrip("* "), code))
     return out
 
@@ -87,14 +87,16 @@ def logprobs_backward(lib, **kw):
 
 
 def tensors(*entries):
-    return np.array(entries, dtype=np.int64)
+    """Columns of (param, grad, elements), each contiguous."""
+    return np.ascontiguousarray(np.array(entries, dtype=np.int64).T)
 
 
 def adamw(lib, table=None, **kw):
     t = tensors((1 << 20, 1 << 30, 1000), (1 << 21, 1 << 31, 7)) if table is None else table
     return call(lib, "adamw", steps._ADAMW_ARGS,
-                dict(count=len(t), tensors=t.ctypes.data, exp_avg=P, exp_avg_sq=P, step=P, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
-                     weight_decay=0.01, grad_scale=1.0, dtype=0, grad_dtype=0, bits=32), kw)
+                dict(count=t.shape[1], params=t[0].ctypes.data, grads=t[1].ctypes.data, elements=t[2].ctypes.data, exp_avg=P, exp_avg_sq=P,
+                     step=P, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=1.0, dtype=0, grad_dtype=0, bits=32),
+                kw)
 
 
 def test_argument_errors_come_before_any_device_work(lib):
@@ -111,7 +113,7 @@ def test_argument_errors_come_before_any_device_work(lib):
         (logprobs_backward, [dict(rows=-1), dict(vocab=0), dict(logits=0), dict(targets=0), dict(dlogprobs=0), dict(logprobs=0),
                              dict(z_max=0), dict(log_sum=0), dict(dlogits=0), dict(ld=49), dict(ldd=49), dict(dentropy=P),
                              dict(temperature=0.0), dict(dtype=7), dict(reserved=2)]),
-        (adamw, [dict(count=-1), dict(tensors=0), dict(exp_avg=0), dict(exp_avg_sq=0), dict(step=0), dict(beta1=1.0), dict(beta2=-0.1),
+        (adamw, [dict(count=-1), dict(params=0), dict(grads=0), dict(elements=0), dict(exp_avg=0), dict(exp_avg_sq=0), dict(step=0), dict(beta1=1.0), dict(beta2=-0.1),
                  dict(beta1=NAN), dict(eps=-1.0), dict(lr=INF), dict(lr=NAN), dict(weight_decay=NAN), dict(grad_scale=INF),
                  dict(dtype=3), dict(grad_dtype=1), dict(bits=16), dict(bits=8), dict(bits=8, exp_avg_scale=P),
                  dict(bits=8, exp_avg_scale=P, exp_avg_sq_scale=P, exp_avg=12), dict(dtype=2, grad_dtype=2, master=P), dict(reserved=1),
