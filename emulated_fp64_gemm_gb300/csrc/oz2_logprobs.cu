@@ -265,12 +265,24 @@ __device__ __forceinline__ Parts relative_to(float top, float from, Parts v, flo
 
 // ------------------------------------------------------------------ alternatives
 // The block's `top` largest place keys go into sh.list, in order (0: there are fewer).
-template <int THREADS>
-__device__ __forceinline__ void take(Shared<THREADS>& sh, float x, int column, uint32_t least) {
-  const uint32_t k = order_key(x);
-  if (k < least) return;
-  const uint32_t at = atomicAdd(&sh.count, 1u);  // the order is made up for by the sorting
-  if (at < Shared<THREADS>::kCandidates) sh.candidates[at] = place_key(k, column);
+// Those of N neighbouring elements whose key is at least `least`, into room that one atomic gives: the order is made up for
+// by the sorting.
+template <int THREADS, int N>
+__device__ __forceinline__ void take(Shared<THREADS>& sh, const float (&x)[N], int column, uint32_t least) {
+  uint32_t keys[N], hits = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    keys[e] = order_key(x[e]);
+    hits |= keys[e] >= least ? 1u << e : 0u;
+  }
+  if (!hits) return;
+  uint32_t at = atomicAdd(&sh.count, static_cast<uint32_t>(__popc(hits)));
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (hits >> e & 1) {
+      if (at < Shared<THREADS>::kCandidates) sh.candidates[at] = place_key(keys[e], column + e);
+      ++at;
+    }
 }
 
 // Of what the jobs name, the elements whose key is at least `least`; four lanes to a job.
@@ -288,8 +300,7 @@ __device__ __forceinline__ void collect_at_least(Shared<THREADS>& sh, const Slic
       if (order_key(top8(raw)) < least) continue;
       float x[8];
       raw.values(x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) take(sh, x[e], static_cast<int>(base + v * 8 + e), least);
+      take(sh, x, static_cast<int>(base + v * 8), least);
     }
   }
 }
@@ -358,42 +369,53 @@ __device__ __forceinline__ void collect_in_turn(Shared<THREADS>& sh, const Slice
   if (threadIdx.x == 0) sh.count = top;
 }
 
-// m: the thread's largest element.
+// The search begins beside the sums, whose barriers it shares: first every thread's largest element m goes into its
+// group's, ...
 template <typename T, int THREADS>
-__device__ __forceinline__ void find_alternatives(Shared<THREADS>& sh, const Slice<T, THREADS>& s, float m, int top) {
-  using S = Shared<THREADS>;
+__device__ __forceinline__ uint32_t note_groups(Shared<THREADS>& sh, const Slice<T, THREADS>& s, float m) {
+  constexpr int WIDTH = THREADS / Shared<THREADS>::kGroups;
   const int tid = threadIdx.x;
   const uint32_t mine = s.has(tid) ? order_key(m) : 0u;
   uint32_t k = mine;
 #pragma unroll
-  for (int i = 1; i < THREADS / S::kGroups; i <<= 1) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, i));
-  if (tid % (THREADS / S::kGroups) == 0) sh.group_top[tid / (THREADS / S::kGroups)] = k;
+  for (int i = 1; i < WIDTH; i <<= 1) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, i));
+  if (tid % WIDTH == 0) sh.group_top[tid / WIDTH] = k;
   if (tid < OZ2_TOP_MAX) sh.list[tid] = 0;
   if (tid == 0) sh.count = sh.job_count = 0;
-  __syncthreads();
-  if (tid < S::kGroups) {
-    k = sh.group_top[tid];
-    int above = 0;
-    const uint4* four = reinterpret_cast<const uint4*>(sh.group_top);
+  return mine;
+}
+// ... behind a barrier the `top`-th largest of these is found, ...
+template <int THREADS>
+__device__ __forceinline__ void find_threshold(Shared<THREADS>& sh, int top) {
+  const int tid = threadIdx.x;
+  if (tid >= Shared<THREADS>::kGroups) return;
+  const uint32_t k = sh.group_top[tid];
+  const uint4* four = reinterpret_cast<const uint4*>(sh.group_top);
+  int above = 0;
 #pragma unroll
-    for (int i = 0; i < S::kGroups / 4; ++i) {
-      const uint4 g = four[i];
-      above += (g.x > k || (g.x == k && 4 * i < tid)) + (g.y > k || (g.y == k && 4 * i + 1 < tid)) +
-               (g.z > k || (g.z == k && 4 * i + 2 < tid)) + (g.w > k || (g.w == k && 4 * i + 3 < tid));
-    }
-    if (above == top - 1) sh.threshold = k;
+  for (int i = 0; i < Shared<THREADS>::kGroups / 4; ++i) {
+    const uint4 g = four[i];
+    above += (g.x > k || (g.x == k && 4 * i < tid)) + (g.y > k || (g.y == k && 4 * i + 1 < tid)) +
+             (g.z > k || (g.z == k && 4 * i + 2 < tid)) + (g.w > k || (g.w == k && 4 * i + 3 < tid));
   }
-  __syncthreads();
+  if (above == top - 1) sh.threshold = k;
+}
+// ... and behind another the elements that reach it.  mine: the key of m, 0 for a thread without elements.
+template <typename T, int THREADS>
+__device__ __forceinline__ void find_alternatives(Shared<THREADS>& sh, const Slice<T, THREADS>& s, uint32_t mine, int top) {
+  using S = Shared<THREADS>;
+  const int tid = threadIdx.x;
   // the passes that hold elements at the threshold or above, and the thread's single element
   const uint32_t threshold = sh.threshold;
   const int column = s.single(tid), slots = s.v0 + tid < s.v1 ? (((s.v1 - s.v0 - tid - 1) / THREADS) >> s.shift) + 1 : 0;
   auto name_jobs = [&](uint32_t least) {
     if (mine < least || !mine) return;
-    for (int i = 0; i < slots; ++i)
-      if (order_key(sh.noted[i][tid]) >= least) {
-        const uint32_t at = atomicAdd(&sh.job_count, 1u);
-        if (at < S::kJobs) sh.jobs[at] = static_cast<uint16_t>(i * THREADS + tid);
-      }
+    uint32_t hits = 0;
+    for (int i = 0; i < slots; ++i) hits |= order_key(sh.noted[i][tid]) >= least ? 1u << i : 0u;
+    if (!hits) return;
+    uint32_t at = atomicAdd(&sh.job_count, static_cast<uint32_t>(__popc(hits)));
+    for (; hits; hits &= hits - 1, ++at)
+      if (at < S::kJobs) sh.jobs[at] = static_cast<uint16_t>((__ffs(hits) - 1) * THREADS + tid);
   };
   uint32_t least = max(threshold, 1u);
   name_jobs(least);
@@ -412,7 +434,10 @@ __device__ __forceinline__ void find_alternatives(Shared<THREADS>& sh, const Sli
   }
   if (!crowded && !(many && threshold == 0xFFFFFFFFu)) {
     collect_at_least(sh, s, least);
-    if (column >= 0) take(sh, Elem<T>::up(s.row[column]), column, least);
+    if (column >= 0) {
+      const float x[1] = {Elem<T>::up(s.row[column])};
+      take(sh, x, column, least);
+    }
   }
   __syncthreads();
   if (crowded || sh.count > S::kCandidates) {
@@ -480,12 +505,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel
   }
 
   // the block's maximum
+  const uint32_t mine_key = p.top ? note_groups(sh, s, a.m) : 0u;
   float top = warp_max_nan(a.m);
-  if (THREADS > 32) {
-    if (lane == 0) sh.warp_top[tid >> 5] = top;
-    __syncthreads();
-    top = warp_max_nan(sh.warp_top[lane % (THREADS / 32)]);
-  }
+  if (lane == 0) sh.warp_top[tid >> 5] = top;
+  __syncthreads();
+  if (THREADS > 32) top = warp_max_nan(sh.warp_top[lane % (THREADS / 32)]);
+  if (p.top) find_threshold(sh, p.top);
   Parts sum{0.0f, 0.0f, 0.0f};
   if (fabsf(top) < infinity()) {
     Parts mine{0.0f, 0.0f, 0.0f};
@@ -514,7 +539,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel
       sum = sum_parts(sh, mine);
     }
   }
-  if (p.top) find_alternatives(sh, s, a.m, p.top);
+  if (p.top) {
+    if (THREADS == 32 || !(fabsf(top) < infinity())) __syncthreads();  // else the sums' barrier is behind the threshold
+    find_alternatives(sh, s, mine_key, p.top);
+  }
 
   // the row's, by its first block
   if (ranks > 1) {
