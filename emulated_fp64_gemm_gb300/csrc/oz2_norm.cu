@@ -675,10 +675,11 @@ __global__ void __launch_bounds__(512) rms_norm_backward_kernel(const __grid_con
   write_partial<T, true, N>(p, at, acc);
 }
 
-// The same for rows off the boundaries of 16 bytes, by single elements.  Bound by latency: 8192 x 5001 takes 147 us (read a
-// second time after the sums instead of kept, with more warps, 221).
+// The same for rows off the boundaries of 16 bytes, by single elements.  Bound by latency: 8192 x 5001 takes 114 us with two
+// blocks of ten warps per SM, where dresidual is read after the sums (144 with one block, which has read it before; 221
+// with three, which read everything again).
 template <typename T, int N>
-__global__ void __launch_bounds__(512) rms_norm_ragged_backward_kernel(const __grid_constant__ NormBackwardParams p) {
+__global__ void __maxnreg__(N == 4 ? 128 : 96) rms_norm_ragged_backward_kernel(const __grid_constant__ NormBackwardParams p) {
   __shared__ float2 room[2][3][16];
   const Place<T, false, N> at(p.warps, p.cols);
   wait_for_predecessor();
@@ -696,16 +697,19 @@ __global__ void __launch_bounds__(512) rms_norm_ragged_backward_kernel(const __g
     const T* dy = static_cast<const T*>(p.dy) + row * p.lddy + at.c0;
     const T* x = static_cast<const T*>(p.x) + row * p.ldx + at.c0;
     const T* d = static_cast<const T*>(p.dresidual) + row * p.ldd + at.c0;
-    Part<T, false> dys[N], xs[N], ds[N];
+    Part<T, false> dys[N], xs[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       dys[j].read(dy, at.left, j);
       xs[j].read(x, at.left, j);
-      if (p.dresidual) ds[j].read(d, at.left, j);
     }
     norm_row_backward<T, false, N>(
         p, at, row, ws, acc, room[turn], [&](int j, Pairs& v) { dys[j].pairs(v); }, [&](int j, Pairs& v) { xs[j].pairs(v); },
-        [&](int j, Pairs& v) { ds[j].pairs(v); });
+        [&](int j, Pairs& v) {
+          Part<T, false> ds;
+          ds.read(d, at.left, j);
+          ds.pairs(v);
+        });
   }
   write_partial<T, false, N>(p, at, acc);
 }
@@ -831,7 +835,7 @@ constexpr int64_t kRingMost = 224 * 1024;  // shared memory of an SM's rows on t
 struct ResidentWarps {
   int one, two, four;
 };
-constexpr ResidentWarps kForward{32, 32, 16}, kBackward{24, 16, 16};
+constexpr ResidentWarps kForward{32, 32, 16}, kBackward{24, 16, 16}, kBackwardRagged{20, 20, 16};
 // How rows are shared out: warps and spans per warp of a row, teams per block, blocks, rows on their way.
 struct Shape {
   bool is_long;  // more than a block's registers, or than two of its rows in shared memory
@@ -886,7 +890,7 @@ bool backward_vec(const oz2_rms_norm_backward_args& a) {
 }
 Shape backward_shape(const oz2_rms_norm_backward_args& a, int num_sms) {
   // (as for three inputs, with or without dresidual: the weight's sums are then the same)
-  return row_shape(a.rows, a.cols, dtype_bytes(static_cast<oz2_dtype>(a.dtype)) * 3, backward_vec(a), 2, kBackward, num_sms);
+  return row_shape(a.rows, a.cols, dtype_bytes(static_cast<oz2_dtype>(a.dtype)) * 3, backward_vec(a), 2, backward_vec(a) ? kBackward : kBackwardRagged, num_sms);
 }
 int64_t partial_rows(const oz2_rms_norm_backward_args& a, int num_sms) {
   if (!a.dweight) return 0;
