@@ -31,7 +31,7 @@ namespace oz2 {
 namespace {
 
 constexpr int kVectors = 4;         // of eight elements, in flight per thread
-constexpr float kExtreme = 1e30f;   // |x| c from here on: c x may overflow, the row is summed as (x - max) c
+constexpr float kExtreme = 1048576.0f;  // |max| c from here on: fl(c max) is off by too much, the row is summed again as (x - max) c
 constexpr float kLeast = -150.0f;   // 2^d is zero below (and at) it, and its product with d stays zero for d = -inf
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -41,8 +41,8 @@ struct LogprobParams {
   const int64_t* targets;
   float *logprobs, *z_max, *log_sum, *entropy, *top_logprobs;
   int64_t* top_ids;
-  float inv_t, c, low;  // low = -kExtreme / c
-  uint32_t floor2;      // low as two bfloat16, towards zero: c times it is finite, and 2^ of that 0
+  float inv_t, c;
+  uint32_t floor2;  // -1e30 / c as two bfloat16, towards zero: c times it is finite, and 2^ of that 0
   int top, ranks;
 };
 
@@ -128,13 +128,12 @@ struct Running {
   float2 s = make_float2(0.0f, 0.0f), t = make_float2(0.0f, 0.0f);
   __device__ __forceinline__ void raise(float top, const LogprobParams& p) {
     if (top <= m || m != m) return;  // a NaN comes in, and stays
-    const float mc_new = top * p.c;
-    if (m < p.low) {  // nothing before counts (and its sums may be lost)
+    const float mc_new = top * p.c, by = mc - mc_new, f = m > -infinity() ? fast_exp2(by) : 0.0f;
+    if (f > 0.0f) {
+      if (ENTROPY) t = mul2(both(f), fma2(s, both(by), t));
+      s = mul2(s, both(f));
+    } else {  // nothing before counts; where it was of extreme size (a mask's 1e10) its sums may be infinite
       s = t = both(0.0f);
-    } else {
-      const float2 f = both(fast_exp2(mc - mc_new));
-      if (ENTROPY) t = mul2(f, fma2(s, both(fmaxf(mc - mc_new, kLeast)), t));
-      s = mul2(s, f);
     }
     m = top;
     mc = mc_new;
@@ -518,12 +517,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel
     const bool extreme = !(fabsf(mc) < kExtreme);
     if (extreme) {
       s.again(tid, 0, 1, [&](float x, int) { add_exactly(mine, x, top, p.c); });
-    } else if (a.m >= p.low) {
+    } else {
       // every sum is relative to fl(c m), which is off the maximum by `delta`
-      const float delta = fmaf(top, p.c, -mc), by = fmaxf(a.mc - mc, kLeast), f = fast_exp2(by) * fast_exp2(-delta), all = a.sum() * f;
-      mine.bent = fmaf(f, fmaf(a.sum(), by, a.bent()), -delta * all);
-      mine.equal = a.m == top ? 1.0f : 0.0f;
-      mine.rest = all - mine.equal;
+      const float delta = fmaf(top, p.c, -mc), by = a.mc - mc, f = a.m > -infinity() ? fast_exp2(by) * fast_exp2(-delta) : 0.0f;
+      if (f > 0.0f) {
+        const float all = a.sum() * f;
+        mine.bent = fmaf(f, fmaf(a.sum(), by, a.bent()), -delta * all);
+        mine.equal = a.m == top ? 1.0f : 0.0f;
+        mine.rest = all - mine.equal;
+      }
     }
     sum = sum_parts(sh, mine);
     if (sum.equal + sum.rest < 1.0625f && !extreme) {  // the same in all of the block's threads
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(kBackThreads) token_logprobs_backward_kernel(c
   r.z_max = z_max;
   r.log_sum2 = log_sum * kLog2e;
   r.shift = fmaf(z_max, kLog2e, r.log_sum2);
-  r.exact = sizeof(T) == 4 || !(fabsf(z_max) < 4096.0f);
+  r.exact = sizeof(T) == 4 || !(fabsf(z_max) < 256.0f);
   r.target = !ignored && inside ? static_cast<int>(target) : -1;
   if (z_max == -infinity()) {  // no distribution, no gradient
     r.a = r.b = r.shift = r.z_max = r.log_sum2 = 0.0f;
@@ -760,9 +762,9 @@ cudaError_t launch_token_logprobs(const oz2_token_logprobs_args& a, const Device
   p.top_ids = a.top_ids;
   p.inv_t = static_cast<float>(1.0 / a.temperature);
   p.c = static_cast<float>(kLog2eDouble / a.temperature);
-  p.low = -kExtreme / p.c;
+  const float floor = std::max(-1e30f / p.c, -3.3895314e38f);  // no less than bfloat16's lowest number
   uint32_t bits;
-  std::memcpy(&bits, &p.low, 4);
+  std::memcpy(&bits, &floor, 4);
   p.floor2 = (bits & 0xFFFF0000u) | bits >> 16;
   p.top = a.top;
   p.ranks = ranks_for(a.rows, a.vocab, res.num_sms);

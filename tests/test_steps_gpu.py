@@ -334,9 +334,9 @@ def mask_rows(logits, value):
 
 @pytest.mark.parametrize("vocab", [9, 100, 5000, 33333, 131072])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
-@pytest.mark.parametrize("lowest", [False, True])
+@pytest.mark.parametrize("lowest", [False, True, -30000.0, -1e10, -3e25])
 def test_logprobs_of_masked_rows(oz2, vocab, dtype, lowest):
-    value = torch.finfo(dtype).min if lowest else -INF
+    value = (torch.finfo(dtype).min if lowest is True or lowest < torch.finfo(dtype).min else lowest) if lowest else -INF
     logits, keep = mask_rows(normal(8, vocab, dtype=dtype, scale=3.0), value)
     targets = torch.arange(8, device="cuda") % vocab
     targets[1], targets[5] = vocab // 2, vocab - 1
@@ -438,10 +438,37 @@ def test_logprobs_of_special_rows(oz2, vocab, dtype):
     assert one.logprobs[1] == 0 and bool(one.logprobs[3].isnan())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shift", [300.0, -5e3, 6e4, 1e6, -3e7, 1e12])
+def test_logprobs_of_logits_far_from_zero(oz2, dtype, shift):
+    if abs(shift) > torch.finfo(dtype).max:
+        return
+    # (their differences are multiples of the type's steps there, some of them of an ordinary size)
+    step = abs(shift) * torch.finfo(dtype).eps
+    logits = (normal(6, 5000, scale=3.0) * max(1.0, step) + shift).to(dtype)
+    targets = logits.float().argmax(-1)
+    targets[3:] = 7
+    check_logprobs(oz2, logits, targets, top=5)
+    if shift < 0:  # beside ordinary ones nothing is left of them
+        logits[:, 4000:] = normal(6, 1000, dtype=dtype)
+        check_logprobs(oz2, logits, torch.full_like(targets, 4321), top=5)
+    check_logprobs_backward(oz2, logits, targets)
+
+
 def test_logprobs_temperatures(oz2):
     x = normal(5, 3000, scale=4.0)
     for temperature in (1e-3, 0.1, 30.0, 1e6):
         check_logprobs(oz2, x, some_targets(5, 3000), temperature, top=4)
+    # so high that masked logits alone leave the softmax, however low the others are; so low that one logit is left
+    for dtype in (F32, BF16, F16):
+        logits, _ = mask_rows(normal(8, 9000, dtype=dtype, scale=3.0), -INF)
+        targets = torch.tensor([0, 4500, 0, 3000, 0, 8999, 1, 0], device="cuda")
+        check_logprobs(oz2, logits, targets, 1e-20, top=3)
+        logits[0, ::3] = torch.finfo(dtype).min
+        logits[6] = torch.finfo(dtype).min
+        logits[6, 7] = -INF
+        for temperature in (1e9, 1e30):
+            check_logprobs(oz2, logits, targets, temperature, top=3)
     # z passes the 32-bit range: where it falls to -inf it is masked, a row of nothing else has no distribution
     low = torch.full((2, 100), -3e38, device="cuda")
     low[1, 5] = 1.0
@@ -506,9 +533,10 @@ def test_logprobs_backward_strides(oz2, dtype, pad, shift):
 
 @pytest.mark.parametrize("vocab", [9, 5000, 33333])
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("lowest", [False, True])
+@pytest.mark.parametrize("lowest", [False, True, -30000.0, -1e10, -3e25])
 def test_logprobs_backward_of_masked_rows(oz2, vocab, dtype, lowest):
-    logits, keep = mask_rows(normal(8, vocab, dtype=dtype, scale=3.0), torch.finfo(dtype).min if lowest else -INF)
+    value = (torch.finfo(dtype).min if lowest is True or lowest < torch.finfo(dtype).min else lowest) if lowest else -INF
+    logits, keep = mask_rows(normal(8, vocab, dtype=dtype, scale=3.0), value)
     targets = torch.arange(8, device="cuda") % vocab
     targets[1], targets[4] = vocab // 2, -100
     for entropy in (False, True):
