@@ -13,7 +13,7 @@
 //    largest logit.  Each thread has noted the maxima of its passes in shared memory, so
 //    that only passes (of 32 elements, mostly) that reach the bound can hold
 //    alternatives: a few dozen, which are read again (whole threads' elements, sixteen times
-//    as many, cost 4096 x 131072 with 20 alternatives 75 us instead of NEW);
+//    as many, made 20 alternatives of 4096 x 131072 cost 75 us, this 21);
 //  * where one token has almost all of the probability, its log p is -log1p of the others'
 //    sum, which 32 bits have lost beside it: the elements of the thread that holds the
 //    maximum are summed again without it.
@@ -199,7 +199,7 @@ struct Shared {
   uint64_t candidates[kCandidates];
   float noted[kSlots][THREADS];
   uint64_t list[OZ2_TOP_MAX];  // the block's alternatives, in order
-  uint64_t merged[8 * OZ2_TOP_MAX];
+  uint64_t merged[(THREADS == 256 ? 8 : 1) * OZ2_TOP_MAX];  // of the blocks of a row
   alignas(16) uint32_t group_top[kGroups];
   uint16_t jobs[kJobs];  // slot * THREADS + thread
   float warp_top[32];
@@ -620,17 +620,22 @@ int ranks_for(int64_t rows, int64_t vocab, int num_sms) {
   return ranks;
 }
 
-// Few threads for short rows, whose work behind the pass would else be most of it.
 template <typename T, int THREADS>
 cudaError_t forward(const LogprobParams& p, int64_t rows, cudaStream_t st) {
   const int64_t blocks = rows * p.ranks;
   return p.entropy ? launch_kernel(token_logprobs_kernel<T, true, THREADS>, blocks, THREADS, 0, p.ranks, st, p)
                    : launch_kernel(token_logprobs_kernel<T, false, THREADS>, blocks, THREADS, 0, p.ranks, st, p);
 }
+// Threads per row.  Where blocks of a warp or four give the SMs enough rows at a time, what is done behind the pass (and
+// waits on barriers for the slowest thread) is hidden by the other rows' passes: with at least eight rows per SM 8192 x 8000
+// bfloat16 logits and 5 alternatives take 45 us with a warp and 56 with four, 8192 x 10000 43 and 39; 8192 x 32000 86 with
+// four warps and 103 with eight, 4096 x 131072 158 and 164.  With fewer rows each row's own time counts: 517 x 50021 takes 19 us
+// with four warps and 16 with eight.  The blocks of a cluster have eight.
 template <typename T>
-cudaError_t forward(const LogprobParams& p, int64_t rows, cudaStream_t st) {
-  if (p.vocab <= 1024) return forward<T, 32>(p, rows, st);
-  if (p.vocab < 8192) return forward<T, 128>(p, rows, st);
+cudaError_t forward(const LogprobParams& p, int64_t rows, int num_sms, cudaStream_t st) {
+  const bool many = rows >= 8 * num_sms;
+  if (p.vocab <= (many ? 8191 : 1024)) return forward<T, 32>(p, rows, st);
+  if (p.ranks == 1 && (many || p.vocab < 8192)) return forward<T, 128>(p, rows, st);
   return forward<T, 256>(p, rows, st);
 }
 
@@ -769,9 +774,9 @@ cudaError_t launch_token_logprobs(const oz2_token_logprobs_args& a, const Device
   p.top = a.top;
   p.ranks = ranks_for(a.rows, a.vocab, res.num_sms);
   switch (a.dtype) {
-    case OZ2_BF16: return forward<__nv_bfloat16>(p, a.rows, st);
-    case OZ2_F16: return forward<__half>(p, a.rows, st);
-    default: return forward<float>(p, a.rows, st);
+    case OZ2_BF16: return forward<__nv_bfloat16>(p, a.rows, res.num_sms, st);
+    case OZ2_F16: return forward<__half>(p, a.rows, res.num_sms, st);
+    default: return forward<float>(p, a.rows, res.num_sms, st);
   }
 }
 

@@ -203,8 +203,9 @@ def token_logprobs(logits, targets, *, temperature=1.0, top=0, entropy=False, ig
     With z = logits / temperature: log p of each row's target, 0 where that is
     `ignore_index` and NaN where it is any other number outside the vocabulary;
     with `entropy` the entropy; with `top` (at most 32) the most likely tokens,
-    the lowest id first among equal ones.  -inf masks a logit; a row of -inf alone
-    has log p -inf and entropy 0, a row with NaN or +inf has NaN."""
+    the lowest id first among equal ones.  -inf masks a logit, and so does any z below
+    the 32-bit range; a row of those alone has log p -inf and entropy 0, a row with NaN
+    or +inf has NaN."""
     dtype, device = logits.dtype, logits.get_device()
     if dtype not in _FLOATS or logits.dim() != 2 or device < 0:
         _refuse("logits", logits, 2, _FLOATS)
@@ -340,34 +341,36 @@ def adamw_state(params, *, bits=32, master=False):
     return state._replace(master=copies)
 
 
+def _fits(t, dtype, device, shape):
+    return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
+
+
 def _check_state(state, blocks, dtype, device):
     """The states' bits."""
     step, m, v, scale_m, scale_v, master = state
     eight = m.dtype is torch.float8_e4m3fn
-    total, scales = (blocks * ADAMW_BLOCK,), (blocks,)
-    _check("state.step", step, torch.int64, device, (2,))
-    _check("state.exp_avg", m, torch.float8_e4m3fn if eight else torch.float32, device, total)
-    _check("state.exp_avg_sq", v, torch.uint8 if eight else torch.float32, device, total)
+    wanted = {"step": (step, torch.int64, (2,)), "exp_avg": (m, torch.float8_e4m3fn if eight else torch.float32, (blocks * ADAMW_BLOCK,)),
+              "exp_avg_sq": (v, torch.uint8 if eight else torch.float32, (blocks * ADAMW_BLOCK,))}
     if eight:
-        if scale_m is None or scale_v is None:
-            raise ValueError("8-bit states have scales")
-        _check("state.exp_avg_scale", scale_m, torch.float32, device, scales)
-        _check("state.exp_avg_sq_scale", scale_v, torch.float32, device, scales)
+        wanted["exp_avg_scale"], wanted["exp_avg_sq_scale"] = (scale_m, torch.float32, (blocks,)), (scale_v, torch.float32, (blocks,))
     elif scale_m is not None or scale_v is not None:
         raise ValueError("scales belong to 8-bit states")
     if master is not None:
-        _check("state.master", master, torch.float32, device, total)
         if dtype not in _HALVES:
             raise TypeError("master weights are for 16-bit parameters")
-    for t in state:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("states must be contiguous")
+        wanted["master"] = (master, torch.float32, (blocks * ADAMW_BLOCK,))
+    for name, (t, kind, shape) in wanted.items():
+        if t is None or not _fits(t, kind, device, shape):
+            if t is None:
+                raise ValueError(f"8-bit states need state.{name}")
+            _check("state." + name, t, kind, device, shape)
+            raise ValueError(f"state.{name} must be contiguous")
     return 8 if eight else 32
 
 
 def _number(name, v, device):
     """(address, value) of a number that may be in device memory."""
-    if not isinstance(v, torch.Tensor):
+    if type(v) is float or not isinstance(v, torch.Tensor):
         return 0, v
     _check(name, v, torch.float32, device, v.shape)
     if v.numel() != 1:

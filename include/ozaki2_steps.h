@@ -101,8 +101,8 @@ oz2_status ozaki2_rms_norm_backward(const oz2_rms_norm_backward_args* args, void
  * dtype: any, of the logits.  rows and vocab may be zero only together with
  * their outputs: vocab is 1 at least where there are rows.
  *
- * -inf is a logit that is masked: probability 0, nothing to the entropy.  A row
- * of -inf alone has z_max and every log p -inf, log_sum and entropy 0.  A row
+ * -inf is a logit that is masked, and so is one whose logit / temperature falls
+ * below the float range: probability 0, nothing to the entropy.  A row of these alone has z_max and every log p -inf, log_sum and entropy 0.  A row
  * with a NaN or +inf has NaN in all but its top_ids and an ignored target's
  * logprob; NaN comes first among the alternatives.  log p and the entropy stay
  * relatively exact where one token has almost all of the probability.

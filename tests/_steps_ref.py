@@ -28,7 +28,9 @@ def rms_norm_backward(dy, x, w, dres, eps):
 
 def token_logprobs(logits, targets, temperature, ignore):
     """z_max, log_sum, the targets' log p, entropy and all log p of rows that have a distribution, or -inf alone."""
+    # z below the 32-bit range is masked, like -inf: the lowest logits there are over a temperature below 1 (max / 0.7 > max)
     z = logits.double() / temperature
+    z = torch.where(z < -torch.finfo(torch.float32).max, -np.inf, z)
     z_max = z.amax(-1)
     some = z_max > -np.inf
     d = z - torch.where(some, z_max, 0.0)[:, None]

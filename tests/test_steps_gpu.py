@@ -258,13 +258,13 @@ def test_norm_empty(oz2):
 
 
 # ------------------------------------------------------------------ token_logprobs
-def check_logprobs(oz2, logits, targets, temperature=1.0, top=0, ignore=-100, kind=None):
-    """Against 64 bits.  A sum of V exponentials of 2^-21 each in 32 bits, about V / 512 in a chain, is off by
-    (V / 512 + 64) 2^-24 + 2^-21 relatively, and log p by the sizes of z - z_max and z_max times 2^-22 besides."""
+def check_logprobs(oz2, logits, targets, temperature=1.0, top=0, ignore=-100, chains=512):
+    """Against 64 bits.  A sum of V exponentials of 2^-21 each in 32 bits, about V / 512 in a chain (two per thread), is
+    off by (V / 512 + 64) 2^-24 + 2^-21 relatively, and log p by the sizes of z - z_max and z_max times 2^-22 besides."""
     v = logits.shape[1]
     got = oz2.token_logprobs(logits, targets, temperature=temperature, top=top, entropy=True, ignore_index=ignore)
     z_max, log_sum, logp, entropy, every = ref.token_logprobs(logits, targets, temperature, ignore)
-    rel = (v / 512 + 64) * 2.0**-24 + 2.0**-21
+    rel = (v / chains + 64) * 2.0**-24 + 2.0**-21
     off = rel * (1 + log_sum) + 2.0**-22 * z_max.nan_to_num(0, 0, 0).abs()
     far = 2.0**-22
     assert_within(got.z_max, z_max, 2.0**-23 * z_max.nan_to_num(0, 0, 0).abs(), "z_max")
@@ -366,6 +366,29 @@ def test_logprobs_ties(oz2, vocab):
     for dtype in (F32, BF16):
         for top in (1, 7, 32):
             check_logprobs(oz2, logits.to(dtype), torch.zeros(7, dtype=torch.int64, device="cuda"), top=top)
+
+
+@pytest.mark.parametrize("vocab", [1030, 5003, 8191, 8192, 20011, 70000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_logprobs_of_many_rows(oz2, vocab, dtype):
+    # a warp or four to a row: what the tests above have in few rows, among ordinary ones
+    rows = 8 * torch.cuda.get_device_properties(0).multi_processor_count + 3
+    logits, columns = normal(rows, vocab, dtype=dtype, scale=3.0), torch.arange(vocab, device="cuda")
+    for at, value in ((0, -INF), (8, torch.finfo(dtype).min), (16, -30000.0), (24, -1e10)):
+        logits[at:at + 8] = mask_rows(logits[at:at + 8].clone(), value)[0]
+    logits[32] = 0.0
+    logits[33] = (columns % 3).to(dtype)
+    logits[34, vocab // 2:] = 20.0
+    for row, width in ((35, 8), (36, 32), (37, 100), (38, 248)):
+        logits[row] = torch.where(columns % 1024 < width, 25 + torch.rand(vocab, generator=generator(row), device="cuda"), logits[row].float()).to(dtype)
+    logits[39] = columns.to(dtype)
+    logits[40] = (logits[40].float() * 100 + 1e6).to(dtype)
+    logits[41, vocab - 1] = 60.0
+    targets = some_targets(rows, vocab)
+    targets[41] = vocab - 1
+    for top in (0, 3, 32):
+        check_logprobs(oz2, logits, targets, top=top, chains=64 if vocab < 8192 else 256)
+    check_logprobs(oz2, strided(logits, 3, 1), targets, 0.7, top=9, chains=64 if vocab < 8192 else 256)
 
 
 @pytest.mark.parametrize("vocab", [40000, 262144])
