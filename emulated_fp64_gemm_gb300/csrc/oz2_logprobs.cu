@@ -630,11 +630,13 @@ cudaError_t forward(const LogprobParams& p, int64_t rows, cudaStream_t st) {
 // waits on barriers for the slowest thread) is hidden by the other rows' passes: with at least eight rows per SM 8192 x 8000
 // bfloat16 logits and 5 alternatives take 45 us with a warp and 56 with four, 8192 x 10000 43 and 39; 8192 x 32000 86 with
 // four warps and 103 with eight, 4096 x 131072 158 and 164.  With fewer rows each row's own time counts: 517 x 50021 takes 19 us
-// with four warps and 16 with eight.  The blocks of a cluster have eight.
+// with four warps and 16 with eight, 24 x 1000 with 20 alternatives 7.3 with one and 5.0 with four; at 512 and below more
+// threads than a warp would leave fewer groups with elements than there are alternatives (24 x 300: 15 us, a warp 6.8).  The
+// blocks of a cluster have eight.
 template <typename T>
 cudaError_t forward(const LogprobParams& p, int64_t rows, int num_sms, cudaStream_t st) {
   const bool many = rows >= 8 * num_sms;
-  if (p.vocab <= (many ? 8191 : 1024)) return forward<T, 32>(p, rows, st);
+  if (p.vocab <= (many ? 8191 : 512)) return forward<T, 32>(p, rows, st);
   if (p.ranks == 1 && (many || p.vocab < 8192)) return forward<T, 128>(p, rows, st);
   return forward<T, 256>(p, rows, st);
 }

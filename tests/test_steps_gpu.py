@@ -257,6 +257,30 @@ def test_norm_empty(oz2):
     assert oz2.rms_norm(none, w[:0], out_dtype=E4M3, block=128)[1].shape == (3, 0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols", [300_000, 1_000_003])
+def test_norm_of_the_longest_rows(oz2, dtype, cols):
+    """A chain is of cols / 1024 squares: the norm is off by half of (cols / 1024 + 32) 2^-24, sums for dweight by their few rows."""
+    rows, rel = 5, (cols / 1024 + 64) * 2.0**-24
+    x, r, dy, ds, w = (normal(rows, cols, dtype=dtype, seed=i) for i in range(5))
+    w = w[0]
+    y, s = oz2.rms_norm(x, w, residual=r)
+    want, ws = ref.rms_norm(x.double(), w.double(), r.double(), 1e-6)
+    u = UNIT[dtype]
+    assert_within(s, ws, (u + 2.0**-23) * ws.abs() + TINY[dtype])
+    assert_within(y, want, (rel + u * (1 + rel)) * want.abs() + TINY[dtype])
+    q, scale = oz2.rms_norm(x, w, residual=r, out_dtype=E4M3)[:2]
+    top = want.abs().amax(-1, keepdim=True)
+    assert_within(scale, top / 448, 2 * rel * top / 448)
+    assert_within(values(q) * scale.double(), want, (2.0**-4 + 4 * rel) * want.abs() + 2.0**-10 * scale.double() * (1 + rel))
+    dx, dw = oz2.rms_norm_backward(dy, x, w, dresidual=ds)
+    wdx, wdw, size, wsize = ref.rms_norm_backward(dy.double(), x.double(), w.double(), ds.double(), 1e-6)
+    # (the products' sum is not of one sign: off by that part of the sum of magnitudes, of which a row's x has its share)
+    spread = (dy.double() * w.double() * x.double()).abs().mean(-1, keepdim=True) * x.double().abs() / (x.double()**2).mean(-1, keepdim=True).sqrt()**3
+    assert_within(dx, wdx, 4 * rel * (size + spread) + u * (wdx.abs() + 4 * rel * (size + spread)) + TINY[dtype])
+    assert_within(dw, wdw, 2 * rel * wsize + u * (wdw.abs() + 2 * rel * wsize) + TINY[dtype])
+
+
 # ------------------------------------------------------------------ token_logprobs
 def check_logprobs(oz2, logits, targets, temperature=1.0, top=0, ignore=-100, chains=512):
     """Against 64 bits.  A sum of V exponentials of 2^-21 each in 32 bits, about V / 512 in a chain (two per thread), is
@@ -389,6 +413,25 @@ def test_logprobs_of_many_rows(oz2, vocab, dtype):
     for top in (0, 3, 32):
         check_logprobs(oz2, logits, targets, top=top, chains=64 if vocab < 8192 else 256)
     check_logprobs(oz2, strided(logits, 3, 1), targets, 0.7, top=9, chains=64 if vocab < 8192 else 256)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(2, 3_000_001, F32), (90, 1_000_003, BF16), (330, 300_001, BF16), (1300, 150_001, F16)])
+def test_logprobs_of_the_longest_rows(oz2, rows, vocab, dtype):
+    # more passes of a thread than it notes apart: a cluster of eight, of two, eight warps, four
+    logits = normal(rows, vocab, dtype=dtype, scale=3.0)
+    logits[1, ::2] = -INF
+    targets = some_targets(rows, vocab)
+    got = oz2.token_logprobs(logits, targets, top=32, entropy=True)
+    few = torch.tensor([0, 1, rows - 1], device="cuda")
+    some = check_logprobs(oz2, logits[few], targets[few], top=32)
+    assert torch.equal(got.top_ids[few], some.top_ids)
+    rel = (vocab / 256 + 64) * 2.0**-24 + 2.0**-21  # of either one
+    assert_within(got.logprobs[few], some.logprobs.double(), 2 * rel * (1 + some.log_sum.double()) + 2.0**-20 * some.logprobs.double().abs())
+    d = oz2.token_logprobs_backward(torch.ones(rows, device="cuda"), logits, targets, got)
+    p = torch.softmax(logits[few].double(), -1)
+    onehot = torch.zeros_like(p).scatter_(1, targets[few].clamp(min=0)[:, None], 1.0) * (targets[few] >= 0)[:, None]
+    want = torch.where((targets[few] >= 0)[:, None], onehot - p, 0.0)
+    assert_within(d[few], want, (UNIT[dtype] + 2 * rel + 2.0**-18) * want.abs() + TINY[dtype])
 
 
 @pytest.mark.parametrize("vocab", [40000, 262144])
@@ -757,6 +800,25 @@ def test_second_moment_follows_its_mean_in_8_bits(oz2):
     assert float((ratio - 1).abs().max()) <= 6 * 0.11
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype,master", [(F32, False), (BF16, True)])
+def test_adamw_states_within_a_storage(oz2, bits, dtype, master):
+    # parameters and states that begin anywhere
+    params, grads = tensors([1000, 77, 513], dtype, dtype, shift=3)
+    state = oz2.adamw_state(params, bits=bits, master=master)
+    by = [1, 3 if bits == 32 else 8, 5 if bits == 32 else 16, 1, 3, 7]
+    moved = [None if t is None else torch.zeros(t.numel() + n + 4, dtype=t.dtype, device="cuda")[n:n + t.numel()] for t, n in zip(state, by)]
+    if master:
+        moved[5].copy_(state.master)
+    state = oz2.AdamWState(*moved)
+    for _ in range(2):
+        check_step(oz2, params, grads, state, seed=4)
+    if bits == 8:
+        with pytest.raises(oz2.Ozaki2Error):
+            oz2.adamw(params, grads, state._replace(exp_avg=torch.zeros(state.exp_avg.numel() + 1, dtype=E4M3, device="cuda")[1:]), **OPTIONS)
+        assert state.step.tolist() == [2, 0]
+
+
 def test_adamw_refusals(oz2):
     params, grads = tensors([64, 32], BF16, BF16)
     state = oz2.adamw_state(params)
@@ -821,6 +883,66 @@ def test_streams_and_graphs(oz2):
     torch.cuda.synchronize()
     for a, b in zip([*got, *p, *state], [*want, *wanted]):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_calls_at_once(oz2):
+    """Two streams' calls, two graphs captured on them, and two host threads: each as if it were alone."""
+    import threading
+
+    rows, dim, vocab = 3000, 2048, 20001
+    sets = []
+    for seed in (0, 100):
+        x, dy, w = normal(rows, dim, dtype=BF16, seed=seed), normal(rows, dim, dtype=BF16, seed=seed + 1), normal(dim, dtype=BF16, seed=seed + 2)
+        sets.append((x, dy, w, normal(1200, vocab, dtype=BF16, seed=seed + 3), some_targets(1200, vocab, seed), normal(1200, seed=seed + 4),
+                     *tensors([500_000, 33, 70_001], BF16, BF16, seed=seed)))
+
+    def calls(data, stream=None):
+        x, dy, w, logits, targets, g, params, grads = data
+        p = [t.clone() for t in params]
+        state = oz2.adamw_state(p, bits=8)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        out = []
+        for _ in range(3):
+            out += oz2.rms_norm_backward(dy, x, w, stream=stream)
+            saved = oz2.token_logprobs(logits, targets, top=4, stream=stream)
+            out += [saved.logprobs, saved.top_ids, oz2.token_logprobs_backward(g, logits, targets, saved, stream=stream)]
+            oz2.adamw(p, grads, state, seed=2, stream=stream, **OPTIONS)
+        return [*out, *p, *(t for t in state if t is not None)]
+
+    def same(got):
+        torch.cuda.synchronize()
+        for a, b in zip(got, wanted):
+            for s, t in zip(a, b):
+                assert torch.equal(s.view(torch.uint8), t.view(torch.uint8))
+
+    wanted = [calls(data) for data in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    same([calls(data, stream) for data, stream in zip(sets, streams)])
+
+    got = [None, None]
+
+    def thread(i):
+        with torch.cuda.stream(streams[i]):
+            got[i] = calls(sets[i])
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    same(got)
+
+    graphs, got = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for graph, stream, data in zip(graphs, streams, sets):
+        with torch.cuda.graph(graph, stream=stream):
+            got.append(calls(data))
+    for _ in range(2):  # (a replay makes its own copies of the parameters and states)
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        same(got)
 
 
 def test_autograd_notices_the_step(oz2):
