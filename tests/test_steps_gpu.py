@@ -257,6 +257,52 @@ def test_norm_empty(oz2):
     assert oz2.rms_norm(none, w[:0], out_dtype=E4M3, block=128)[1].shape == (3, 0)
 
 
+@pytest.mark.parametrize("rows,cols,pad,shift", [(1, 9, 0, 1), (40, 5001, 0, 3), (700, 8, 1, 0), (650, 31, 0, 0), (1300, 777, 2, 5), (900, 2051, 0, 0),
+                                                 (2000, 2041, 4, 7), (640, 4095, 0, 2), (5000, 130, 3, 1), (611, 8193, 0, 0), (620, 9999, 6, 6)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_norm_of_rows_off_boundaries(oz2, dtype, rows, cols, pad, shift):
+    """All matrices' rows begin alike, within storages of NaN that no result may show and no call may change."""
+    def within(t):
+        store = torch.full((rows * (cols + pad) + shift + 16,), NAN, dtype=t.dtype, device="cuda")
+        view = store[shift:].as_strided((rows, cols), (cols + pad, 1))
+        view.copy_(t)
+        return store, view
+
+    def around(store, view):  # what is not the view's
+        left = store.clone()
+        left[shift:].as_strided((rows, cols), (cols + pad, 1)).fill_(0.0)
+        return int(left.isnan().sum()) == store.numel() - rows * cols
+
+    x, r, dy, d = (normal(rows, cols, dtype=dtype, seed=i) for i in range(4))
+    w = within(normal(1, cols, dtype=dtype, seed=5).expand(rows, cols))[1][0]
+    (_, xv), (_, rv), (_, dyv), (_, dv) = (within(t) for t in (x, r, dy, d))
+    y_store, y = within(torch.zeros_like(x))
+    s_store, s = within(torch.zeros_like(x))
+    check_norm(oz2, xv, w, rv, out=y, residual_out=s)
+    assert around(y_store, y) and around(s_store, s)
+    check_norm(oz2, xv, w)
+    check_norm(oz2, xv, w, rv, quantize=True)
+    check_norm(oz2, xv, w, rv, quantize=True, block=128)
+    q_store = torch.full((rows * (cols + pad) + shift + 16,), 0x7F, dtype=torch.uint8, device="cuda")
+    q = q_store.view(E4M3)[shift:].as_strided((rows, cols), (cols + pad, 1))
+    check_norm(oz2, xv, w, quantize=True, out=q)
+    q_store[shift:].as_strided((rows, cols), (cols + pad, 1)).zero_()
+    assert int((q_store == 0x7F).sum()) == q_store.numel() - rows * cols
+    o_store, o = within(torch.zeros_like(x))
+    got = check_norm_backward(oz2, dyv, xv, w, dv, out=o)
+    assert around(o_store, o)
+    plain = oz2.rms_norm_backward(dyv, xv, w, dresidual=dv)  # dx on boundaries, or as the inputs' rows are: one value
+    check_norm_backward(oz2, dyv, xv, w)
+    for into in range(3):
+        ts = [within(t) for t in (dy, x, d)]
+        over = oz2.rms_norm_backward(ts[0][1], ts[1][1], w, dresidual=ts[2][1], out=ts[into][1])
+        assert torch.equal(over[0], got[0]) and torch.equal(over[1], got[1]) and around(*ts[into])
+    assert_within(plain[0], got[0].double(), 2.0**-6 * got[0].double().abs() + 2.0**-7)
+    xs, rs = within(x), within(r)
+    z = oz2.rms_norm(xs[1], w, residual=rs[1], out=xs[1], residual_out=rs[1])
+    assert torch.equal(z[0], y) and torch.equal(z[1], s) and around(*xs) and around(*rs)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("cols", [300_000, 1_000_003])
 def test_norm_of_the_longest_rows(oz2, dtype, cols):
