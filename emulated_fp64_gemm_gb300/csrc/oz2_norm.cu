@@ -655,7 +655,7 @@ struct NormBackwardParams {
   int64_t ldd;
   void* dx;
   int64_t lddx;
-  float* partial;  // [teams][cols], sums for dweight; null: not formed
+  float* partial;  // [blocks or teams][cols], sums for dweight; null: not formed
   float4* stats;   // long rows: [rows] of (f, r, r^2 mean(g u))
   int cols, warps, depth;
   float eps, inv_cols;
@@ -762,6 +762,27 @@ __device__ __forceinline__ void write_partial(const NormBackwardParams& p, const
   }
 }
 
+// The parts of a block's teams of one warp, joined in their order in `sums` ([cols], shared memory): column_sums_kernel has few
+// blocks where rows are short, each part read costs it time (65536 x 512 47 -> 46 us, 16384 x 777 30.7 -> 29.8).
+template <typename T, int N>
+__device__ __forceinline__ void write_joined_partial(const NormBackwardParams& p, const Place<T, true, N>& at, const Pairs (&acc)[N], float* sums) {
+  if (!p.partial) return;
+  for (int team = 0; team < blockDim.x >> 5; ++team) {
+    __syncthreads();
+    if (threadIdx.x >> 5 != team) continue;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = j * 256 + distance<T, true>(e), c = at.c0 + d;
+        const float v = e & 1 ? acc[j][e >> 1].y : acc[j][e >> 1].x;
+        if (c >= 0 && d < at.left) sums[c] = team ? sums[c] + v : v;
+      }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.cols; c += blockDim.x) p.partial[static_cast<int64_t>(blockIdx.x) * p.cols + c] = sums[c];
+}
+
 // Rows of aligned pieces.  The weight's gradient is summed in registers, a part per team.
 // SHIFTED: the number of teams is a multiple of the rows' period.
 template <typename T, int N, bool SHIFTED>
@@ -819,13 +840,13 @@ __global__ void __launch_bounds__(512) rms_norm_backward_kernel(const __grid_con
     if (++slot == p.depth) slot = 0;
     turn ^= 1;
   }
-  write_partial<T, true, N, SHIFTED>(p, at, acc);
+  if (p.warps == 1) write_joined_partial(p, at, acc, reinterpret_cast<float*>(ring_memory));
+  else write_partial<T, true, N, SHIFTED>(p, at, acc);
 }
 
 // The same for rows off boundaries that do not all start alike, or are few, by single elements.  Bound by latency: 8192 x 5001
-// takes 114 us (68 by pieces) with two
-// blocks of ten warps per SM, where dresidual is read after the sums (144 with one block, which has read it before; 221
-// with three, which read everything again).
+// takes 114 us (68 by pieces) with two blocks of ten warps per SM, where dresidual is read after the sums (144 with one
+// block, which has read it before; 221 with three, which read everything again).
 template <typename T, int N>
 __global__ void __maxnreg__(N == 4 ? 128 : 96) rms_norm_ragged_backward_kernel(const __grid_constant__ NormBackwardParams p) {
   __shared__ float2 room[2][3][16];
@@ -1001,7 +1022,9 @@ Shape row_shape(int64_t rows, int64_t cols, int64_t element_bytes, bool vec, int
   if (s.is_long) return s;
   const bool many = rows >= 4 * num_sms;
   s.spans = spans <= 4 && !many ? 1 : spans <= 32 ? 2 : 4;
-  if (many && (spans <= 4 || wide == 4)) s.spans = spans == 1 ? 1 : spans == 2 ? 2 : 4;
+  if (many && wide == 4) s.spans = spans == 1 ? 1 : spans == 2 ? 2 : 4;
+  // (gradients: 4000 x 1024 in one, two and four spans per warp 11.0, 13.8 and 14.3 us, 8000 x 1024 17.8, 16.8 and 20.8)
+  if (many && wide == 2 && spans <= 4) s.spans = spans == 1 || (spans > 2 && rows < 32 * num_sms) ? 1 : 2;
   s.warps = static_cast<int>(ceil_div(spans, s.spans));
   // nine to twelve warps leave the registers of a fourth or more unused: half as many with twice the spans (gradient of
   // 8192 x 5120: 64 -> 57.5 us, 8192 x 4608: 63 -> 52)
@@ -1089,8 +1112,9 @@ Plan backward_plan(const oz2_rms_norm_backward_args& a, int num_sms) {
 }
 int64_t partial_rows(const oz2_rms_norm_backward_args& a, int num_sms) {
   if (!a.dweight) return 0;
-  const Shape s = backward_plan(a, num_sms).shape;
-  return s.is_long ? weight_slices(a, num_sms) : s.blocks * s.per_block;
+  const Plan plan = backward_plan(a, num_sms);
+  const Shape& s = plan.shape;
+  return s.is_long ? weight_slices(a, num_sms) : plan.access == kSingle ? s.blocks * s.per_block : s.blocks;
 }
 size_t stats_bytes(const oz2_rms_norm_backward_args& a, int num_sms) {
   return backward_plan(a, num_sms).shape.is_long ? static_cast<size_t>(a.rows) * sizeof(float4) : 0;
