@@ -581,15 +581,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel
     if (ranks > 1) cluster_arrive();
     for (int i = tid; i < n; i += THREADS) {
       const uint64_t key = sh.merged[i];
-      const int mine = i / p.top;
-      int above = i % p.top;  // the lists are in order: of each other one, how many are above
-      for (int r = 0; r < ranks; ++r) {
-        if (r == mine) continue;
-        int from = 0;
+      int above = i;
+      if (THREADS == 256 && ranks > 1) {  // the lists are in order: how many of each are above, all searches at once
+        int from[8] = {};
 #pragma unroll
         for (int step = OZ2_TOP_MAX; step; step >>= 1)
-          if (from + step <= p.top && sh.merged[r * p.top + from + step - 1] > key) from += step;
-        above += from;
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < ranks && from[r] + step <= p.top && sh.merged[r * p.top + from[r] + step - 1] > key) from[r] += step;
+        above = 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) above += from[r];
       }
       if (key && above < p.top) {
         const float x = key_value(static_cast<uint32_t>(key >> 32));
