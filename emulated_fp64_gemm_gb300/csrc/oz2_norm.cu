@@ -762,8 +762,8 @@ __device__ __forceinline__ void write_partial(const NormBackwardParams& p, const
   }
 }
 
-// The parts of a block's teams of one warp, joined in their order in `sums` ([cols], shared memory): column_sums_kernel has few
-// blocks where rows are short, each part read costs it time (65536 x 512 47 -> 46 us, 16384 x 777 30.7 -> 29.8).
+// The parts of a block's teams of one warp, joined in their order in `sums` ([cols], shared memory): fewer to add up
+// (65536 x 512 47 -> 46 us, 16384 x 777 30.7 -> 29.8).
 template <typename T, int N>
 __device__ __forceinline__ void write_joined_partial(const NormBackwardParams& p, const Place<T, true, N>& at, const Pairs (&acc)[N], float* sums) {
   if (!p.partial) return;
@@ -995,6 +995,33 @@ __global__ void __launch_bounds__(512) rms_norm_long_dx_kernel(const __grid_cons
     }
     write_span<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx + c0, left, 0, out);
   }
+}
+
+// The weight's gradient from its parts, `rows` of them, where columns are few: eight of them (a sector) per block and eight lanes
+// to a part, so that there are blocks for all SMs and a trip or two of loads per thread.  (column_sums_kernel takes 32 columns
+// per block.  The whole gradient with either, this one first: 16384 x 777 24.8 and 26.5 us, 2000 x 512 8.0 and 8.9, 1003 x 2048
+// 7.6 and 7.5, 300 x 8192 9.4 and 8.4.)
+template <typename T>
+__global__ void __launch_bounds__(512) weight_sums_kernel(const float* partial, int64_t rows, int64_t cols, T* out) {
+  __shared__ float sums[16][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (lane & 7);
+  wait_for_predecessor();
+  let_successor_come();
+  float s = 0.0f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int64_t r = warp * 4 + (lane >> 3); r < rows; r += 64) s += partial[r * cols + c];
+  }
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+  if (lane < 8) sums[warp][lane] = s;
+  __syncthreads();
+  if (threadIdx.x >= 8 || c >= cols) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += sums[w][lane];
+  out[c] = Elem<T>::down(s);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1263,7 +1290,14 @@ cudaError_t launch_rms_norm_backward(const oz2_rms_norm_backward_args& a, const 
     default: e = backward<float>(p, a, res, st); break;
   }
   if (e != cudaSuccess || !a.dweight) return e;
-  return launch_column_sums(ColumnSums{p.partial, partial_rows(a, res.num_sms), a.dweight}, ColumnSums{}, a.cols, t, st);
+  const float* parts = p.partial;
+  const int64_t rows = partial_rows(a, res.num_sms), blocks = ceil_div(a.cols, 8);
+  if (a.cols >= 2048) return launch_column_sums(ColumnSums{p.partial, rows, a.dweight}, ColumnSums{}, a.cols, t, st);
+  switch (t) {
+    case OZ2_BF16: return launch_kernel(weight_sums_kernel<__nv_bfloat16>, blocks, 512, 0, 1, st, parts, rows, a.cols, static_cast<__nv_bfloat16*>(a.dweight));
+    case OZ2_F16: return launch_kernel(weight_sums_kernel<__half>, blocks, 512, 0, 1, st, parts, rows, a.cols, static_cast<__half*>(a.dweight));
+    default: return launch_kernel(weight_sums_kernel<float>, blocks, 512, 0, 1, st, parts, rows, a.cols, static_cast<float*>(a.dweight));
+  }
 }
 
 }  // namespace oz2
