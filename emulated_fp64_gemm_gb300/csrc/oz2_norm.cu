@@ -1027,11 +1027,12 @@ __global__ void __launch_bounds__(512) weight_sums_kernel(const float* partial, 
 // ------------------------------------------------------------------ host side
 constexpr int64_t kLongSpans = 64;
 constexpr int64_t kRingMost = 224 * 1024;  // shared memory of an SM's rows on their way
-// Warps that an SM's registers hold, by the spans of each.
+// Warps that an SM's registers hold, by the spans of each.  (65536 x 512 by 24 and 32 warps: 16 bits 22.8 and 27 us, 32 bits 44.7
+// and 43.)
 struct ResidentWarps {
   int one, two, four;
 };
-constexpr ResidentWarps kForward{32, 32, 16}, kBackward{24, 16, 16}, kBackwardRagged{20, 20, 16};
+constexpr ResidentWarps kForward{32, 24, 16}, kForward32{32, 32, 16}, kBackward{24, 16, 16}, kBackwardRagged{20, 20, 16};
 // How rows are shared out: warps and spans per warp of a row, teams per block, blocks, rows on their way.
 struct Shape {
   bool is_long;  // more than a block's registers, or than two of its rows in shared memory
@@ -1161,13 +1162,20 @@ template <typename T>
 cudaError_t forward(NormParams& p, Access access, const DeviceResources& res, cudaStream_t st) {
   constexpr int64_t PER = 16 / sizeof(T);
   const int arrays = p.residual ? 2 : 1;
-  const Plan plan = plan_rows(p.rows, p.cols, sizeof(T) * arrays, access, PER, 4, kForward, kForward, res.num_sms);
+  const Plan plan = plan_rows(p.rows, p.cols, sizeof(T) * arrays, access, PER, 4, sizeof(T) == 2 ? kForward : kForward32, kForward, res.num_sms);
   const Shape& s = plan.shape;
   const bool shifted = plan.access == kShifted;
   p.warps = s.warps;
-  p.depth = std::min(s.depth, 2);
-  // four rows per team, 16 where the rows have one input (8192 x 4096: 22.7 us, in fours 24.6), but no fewer blocks than run at once
-  p.run = static_cast<int>(std::min<int64_t>(p.residual ? 4 : 16, ceil_div(p.rows, s.blocks * s.per_block)));
+  // a row on its way beside the one that is worked on; two where that is still little per SM (one input: 2730 x 12288 25.8 and
+  // 24.1 us, 4681 x 7168 24.2 and 22.6; with 64 KB 8192 x 4096 22.6 and 23.1; 32 bits, 82 KB, 4096 x 10240 53 and 59)
+  const bool two = !p.residual && 2 * ring_bytes<T>(s, arrays, 1) * ceil_div(s.blocks, res.num_sms) <= 60 * 1024;
+  p.depth = std::min(s.depth, two ? 3 : 2);
+  // Runs of four rows where there is a residual (8192 x 4096: 41.5 us, all of a team's rows in one run 45); all of them where
+  // rows have one input (8192 x 4096 24.6 and 22.7, 2730 x 12288 40 and 26) or one block of nine to twelve warps is all that an
+  // SM holds, so that nothing covers the gaps between blocks (3276 x 10240: 47 and 42).  Of a span per warp 16 at most
+  // (131072 x 128: 34 and 27.5).
+  const int64_t all = ceil_div(p.rows, s.blocks * s.per_block);
+  p.run = static_cast<int>(std::min<int64_t>(p.residual && (s.warps <= 8 || s.warps > 12) ? 4 : s.spans == 1 ? 16 : all, all));
   p.period = static_cast<int>(shifted ? row_period(p.ldx, PER) : 1);
   if (s.is_long) {
     return plan.access == kAligned ? launch_kernel(rms_norm_long_kernel<T, true>, p.rows, 512, 0, 1, st, p)
