@@ -11,10 +11,9 @@ Definitions that both sides share:
   q = e4m3(y / scale) with scale = max(1e-30, largest |y|) / 448 of each row or each 128 columns;
 * rms_norm_backward: with r = 1 / sqrt(mean(x^2) + eps) and g = dy w, dx = dresidual + r (g - x r^2 mean(g x)),
   dweight = the rows' sum of dy x r;
-* token_logprobs: z = logits / temperature, their largest, log_sum = log sum exp(z - largest), the target's
-  log p = z - largest - log_sum (0 where the target is -100), entropy -sum p log p, and the largest log p with
-  their places, the lowest place first among equals; in a row of -inf alone the largest z and every log p are
-  -inf, log_sum and entropy 0;
+* token_logprobs: z = logits / temperature, lse = log sum exp z, the target's z - lse (0 where the target is -100),
+  entropy -sum p log p, and the largest z - lse with their places, the lowest place first among equals;
+  a row without a finite logit has lse and log probabilities -inf and entropy 0;
 * token_logprobs_backward: dlogits = (g (onehot - p) - h p (log p + entropy)) / temperature;
 * adamw: m = b1 m + (1 - b1) g, v = b2 v + (1 - b2) g^2, p = p (1 - lr wd) - lr m' / (sqrt(v') + eps), m' and v'
   divided by 1 - b^t.  Each tensor's states start at a multiple of 256 elements in flat buffers.  In 8 bits every
@@ -141,8 +140,8 @@ def work(case):
     if case["op"] == "token_logprobs":
         n, rows = case["rows"] * case["vocab"], case["rows"]
         if case["backward"]:
-            return {"bytes": 2 * size * n + rows * (24 + 8 * case["entropy"]), "flops": (4.0 + 2 * case["entropy"]) * n}
-        return {"bytes": size * n + rows * (20 + 4 * case["entropy"] + 12 * case["top"]), "flops": (3.0 + 2 * case["entropy"]) * n}
+            return {"bytes": 2 * size * n + rows * (16 + 8 * (1 + case["entropy"])), "flops": (4.0 + 2 * case["entropy"]) * n}
+        return {"bytes": size * n + rows * (16 + 4 * case["entropy"] + 12 * case["top"]), "flops": (3.0 + 2 * case["entropy"]) * n}
     n, rows = case["rows"] * case["cols"], case["rows"]
     if case["op"] == "rms_norm_backward":
         return {"bytes": size * (n * (3 + case["dresidual"]) + 2 * case["cols"]), "flops": 12.0 * n}
@@ -252,16 +251,15 @@ def _norm_backward_plain(s):
 
 
 def _logprobs_plain(s):
-    z = s["logits"].float() * (1.0 / s["temperature"])
+    z = s["logits"].float() / s["temperature"]
     top = z.amax(-1, keepdim=True)
-    some = top > -math.inf
-    z = z - torch.where(some, top, 0.0)
+    z = z - torch.where(top > -math.inf, top, 0.0)
     e = torch.exp(z)
-    log_sum = torch.where(some, torch.log(e.sum(-1, keepdim=True)), 0.0)
-    logp = z - log_sum
+    log_sum = torch.log(e.sum(-1, keepdim=True))
+    logp = z - torch.where(log_sum > -math.inf, log_sum, 0.0)
     known = s["targets"] != IGNORED
     target = logp.gather(1, torch.where(known, s["targets"], 0)[:, None])[:, 0]
-    out = {"logprob": torch.where(known, target, 0.0), "z_max": top[:, 0], "log_sum": log_sum[:, 0]}
+    out = {"logprob": torch.where(known, target, 0.0), "lse": (top + log_sum)[:, 0]}
     if s["entropy"]:
         out["entropy_value"] = -torch.where(e > 0, torch.exp(logp) * logp, 0.0).sum(-1)
     if s["top"]:
@@ -271,8 +269,8 @@ def _logprobs_plain(s):
 
 
 def _logprobs_backward_plain(s):
-    some = s["z_max"] > -math.inf
-    logp = s["logits"].float() * (1.0 / s["temperature"]) - torch.where(some, s["z_max"], 0.0)[:, None] - s["log_sum"][:, None]
+    some = s["lse"] > -math.inf
+    logp = s["logits"].float() / s["temperature"] - torch.where(some, s["lse"], 0.0)[:, None]
     p = torch.exp(logp)
     known = s["targets"] != IGNORED
     g = torch.where(known & some, s["dlogprob"], 0.0)
@@ -281,7 +279,7 @@ def _logprobs_backward_plain(s):
     d.scatter_(1, at, torch.where(known[:, None], -g[:, None] * torch.expm1(s["logprob"][:, None]), d.gather(1, at)))
     if s["entropy"]:
         d = d - torch.where(p > 0, s["dentropy"][:, None] * p * (logp + s["entropy_value"][:, None]), 0.0)
-    return (d * (1.0 / s["temperature"])).to(s["logits"].dtype)
+    return (d / s["temperature"]).to(s["logits"].dtype)
 
 
 def _draws(elements, step, seed):
@@ -362,13 +360,12 @@ def _run_own(s):
         oz2.adamw(s["params"], s["grads"], state, lr=LR, betas=(B1, B2), eps=ADAM_EPS, weight_decay=DECAY, seed=s["seed"])
         return _adamw_outputs(s)
     if s["backward"]:
-        saved = oz2.TokenLogprobs(logprobs=s["logprob"], z_max=s["z_max"], log_sum=s["log_sum"], entropy=s.get("entropy_value"),
-                                  top_logprobs=None, top_ids=None)
+        saved = oz2.TokenLogprobs(logprobs=s["logprob"], lse=s["lse"], entropy=s.get("entropy_value"), top_logprobs=None, top_ids=None)
         return oz2.token_logprobs_backward(s["dlogprob"], s["logits"], s["targets"], saved, dentropy=s["dentropy"],
                                            temperature=s["temperature"], ignore_index=IGNORED)
     r = oz2.token_logprobs(s["logits"], s["targets"], temperature=s["temperature"], top=s["top"], entropy=s["entropy"],
                            ignore_index=IGNORED)
-    out = {"logprob": r.logprobs, "z_max": r.z_max, "log_sum": r.log_sum}
+    out = {"logprob": r.logprobs, "lse": r.lse}
     if s["entropy"]:
         out["entropy_value"] = r.entropy
     if s["top"]:
@@ -419,9 +416,8 @@ def _exact_logprobs(s):
     parts = []
     for rows in torch.arange(s["rows"], device="cuda").split(max(1, (1 << 27) // s["vocab"])):
         lse, logp = _exact_rows(s, rows)
-        target, z_max = s["targets"][rows], s["logits"][rows].amax(-1).double() / s["temperature"]
-        part = {"z_max": z_max, "log_sum": torch.where(torch.isinf(lse), 0.0, lse - z_max),
-                "logprob": torch.where(target == IGNORED, 0.0, logp.gather(1, target.clamp(min=0)[:, None])[:, 0])}
+        target = s["targets"][rows]
+        part = {"lse": lse, "logprob": torch.where(target == IGNORED, 0.0, logp.gather(1, target.clamp(min=0)[:, None])[:, 0])}
         if s["entropy"]:
             part["entropy_value"] = -torch.special.xlogy(logp.exp(), logp.exp()).sum(-1)
         if s["top"]:
