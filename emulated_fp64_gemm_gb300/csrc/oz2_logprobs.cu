@@ -39,7 +39,7 @@ struct LogprobParams {
   const void* logits;
   int64_t ld, vocab, ignore_index;
   const int64_t* targets;
-  float *logprobs, *z_max, *log_sum, *entropy, *top_logprobs;
+  float *logprobs, *z_max, *log_sum, *lse, *entropy, *top_logprobs;
   int64_t* top_ids;
   float inv_t, c;
   uint32_t floor2;  // -1e30 / c as two bfloat16, towards zero: c times it is finite, and 2^ of that 0
@@ -609,6 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel
     p.logprobs[row] = logprob;
     p.z_max[row] = bad ? nan : z_max;
     p.log_sum[row] = log_sum;
+    if (p.lse) p.lse[row] = bad ? nan : fmaf(top, p.inv_t, log_sum);
     if (ENTROPY) p.entropy[row] = bad ? nan : none ? 0.0f : log_sum - kLn2 * sum.bent / (1.0f + others);
   }
   __syncwarp();
@@ -650,7 +651,7 @@ struct LogprobBackwardParams {
   const void* logits;
   int64_t ld, vocab, ignore_index;
   const int64_t* targets;
-  const float *dlogprobs, *dentropy, *logprobs, *z_max, *log_sum, *entropy;
+  const float *dlogprobs, *dentropy, *logprobs, *z_max, *log_sum, *entropy;  // log_sum null: z_max has it in it
   void* dlogits;
   int64_t ldd;
   float inv_t, c;
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(kBackThreads) token_logprobs_backward_kernel(c
 
   RowGradient r;
   const int64_t target = p.targets[row];
-  const float z_max = p.z_max[row], log_sum = p.log_sum[row];
+  const float z_max = p.z_max[row], log_sum = p.log_sum ? p.log_sum[row] : 0.0f;
   const bool ignored = target == p.ignore_index, inside = target >= 0 && target < p.vocab;
   const float g = ignored ? 0.0f : p.dlogprobs[row];
   const float h = ENTROPY ? p.dentropy[row] : 0.0f, entropy = ENTROPY ? p.entropy[row] : 0.0f;
@@ -766,6 +767,7 @@ cudaError_t launch_token_logprobs(const oz2_token_logprobs_args& a, const Device
   p.logprobs = a.logprobs;
   p.z_max = a.z_max;
   p.log_sum = a.log_sum;
+  p.lse = a.lse;
   p.entropy = a.entropy;
   p.top_logprobs = a.top_logprobs;
   p.top_ids = a.top_ids;
@@ -794,8 +796,9 @@ cudaError_t launch_token_logprobs_backward(const oz2_token_logprobs_backward_arg
   p.dlogprobs = a.dlogprobs;
   p.dentropy = a.dentropy;
   p.logprobs = a.logprobs;
-  p.z_max = a.z_max;
-  p.log_sum = a.log_sum;
+  // lse in the place of both
+  p.z_max = a.z_max && a.log_sum ? a.z_max : a.lse;
+  p.log_sum = a.z_max ? a.log_sum : nullptr;
   p.entropy = a.entropy;
   p.dlogits = a.dlogits;
   p.ldd = a.ldd;

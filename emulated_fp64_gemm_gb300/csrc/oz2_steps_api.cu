@@ -105,7 +105,7 @@ bool token_logprobs_ok(const oz2_token_logprobs_args& a) {
 bool token_logprobs_backward_ok(const oz2_token_logprobs_backward_args& a) {
   return logits_ok(a.rows, a.vocab, a.dtype, a.temperature) && a.reserved == 0 && matrix_ok(a.logits, a.rows, a.vocab, a.ld) &&
          matrix_ok(a.dlogits, a.rows, a.vocab, a.ldd) &&
-         (a.rows == 0 || (a.targets && a.dlogprobs && a.logprobs && a.z_max && a.log_sum && (!a.dentropy || a.entropy)));
+         (a.rows == 0 || (a.targets && a.dlogprobs && a.logprobs && ((a.z_max && a.log_sum) || a.lse) && (!a.dentropy || a.entropy)));
 }
 
 bool finite(double v) { return std::isfinite(v) && std::fabs(v) <= 1e30; }

@@ -31,8 +31,8 @@ ADAMW_BLOCK = 256
 # the argument structures of include/ozaki2_steps.h, field by field
 _RMS_NORM_ARGS = struct.Struct("@qqPqPqPPqPqPqdii")
 _RMS_NORM_BACKWARD_ARGS = struct.Struct("@qqPqPqPPqPqPdii")
-_TOKEN_LOGPROBS_ARGS = struct.Struct("@qqPqPqPPPPPPdii")
-_TOKEN_LOGPROBS_BACKWARD_ARGS = struct.Struct("@qqPqPqPPPPPPPqdii")
+_TOKEN_LOGPROBS_ARGS = struct.Struct("@qqPqPqPPPPPPPdii")
+_TOKEN_LOGPROBS_BACKWARD_ARGS = struct.Struct("@qqPqPqPPPPPPPPqdii")
 _ADAMW_ARGS = struct.Struct("@qPPPPPPPPPPPddddddQiiii")
 
 _lib = None
@@ -175,14 +175,18 @@ def rms_norm_backward(dy, x, weight, *, dresidual=None, eps=1e-6, need_dweight=T
 
 # ------------------------------------------------------------------ token_logprobs
 class TokenLogprobs(NamedTuple):
-    """What `token_logprobs` returns; None for what was not asked for."""
+    """What `token_logprobs` returns; None for what was not asked for.
 
-    logprobs: torch.Tensor                 # (rows,) log p of each row's target
-    z_max: torch.Tensor                    # (rows,) the largest logit / temperature
-    log_sum: torch.Tensor                  # (rows,) log of the sum of exp(z - z_max)
-    entropy: Optional[torch.Tensor]        # (rows,) -sum p log p
-    top_logprobs: Optional[torch.Tensor]   # (rows, top) the largest log p, falling
-    top_ids: Optional[torch.Tensor]        # (rows, top) int64, their places
+    Log p is z - z_max - log_sum, or z - lse with a rounding of lse's size: a program that keeps a single number per row
+    may keep lse, and give its gradient TokenLogprobs(logprobs=..., lse=...)."""
+
+    logprobs: torch.Tensor                        # (rows,) log p of each row's target
+    z_max: Optional[torch.Tensor] = None          # (rows,) the largest logit / temperature
+    log_sum: Optional[torch.Tensor] = None        # (rows,) log of the sum of exp(z - z_max)
+    entropy: Optional[torch.Tensor] = None        # (rows,) -sum p log p
+    top_logprobs: Optional[torch.Tensor] = None   # (rows, top) the largest log p, falling
+    top_ids: Optional[torch.Tensor] = None        # (rows, top) int64, their places
+    lse: Optional[torch.Tensor] = None            # (rows,) z_max + log_sum
 
 
 def _check_targets(logits, targets, device):
@@ -223,7 +227,7 @@ def token_logprobs(logits, targets, *, temperature=1.0, top=0, entropy=False, ig
     targets = _vector(targets)
     # an allocation each, like the first: parts of one are slower to make, 7.8 instead of 4.3 us on the Grace host
     logprobs = torch.empty((rows,), dtype=torch.float32, device=where)
-    z_max, log_sum = torch.empty_like(logprobs), torch.empty_like(logprobs)
+    z_max, log_sum, lse = torch.empty_like(logprobs), torch.empty_like(logprobs), torch.empty_like(logprobs)
     h = top_logprobs = top_ids = None
     at_h = at_top = at_ids = 0
     if entropy:
@@ -235,10 +239,10 @@ def token_logprobs(logits, targets, *, temperature=1.0, top=0, entropy=False, ig
         at_top, at_ids = top_logprobs.data_ptr(), top_ids.data_ptr()
     code = _library().ozaki2_token_logprobs(
         _TOKEN_LOGPROBS_ARGS.pack(rows, vocab, logits.data_ptr(), ld, targets.data_ptr(), ignore_index, logprobs.data_ptr(), z_max.data_ptr(),
-                                  log_sum.data_ptr(), at_h, at_top, at_ids, temperature, top, _FLOATS[dtype]), _stream_of(device))
+                                  log_sum.data_ptr(), lse.data_ptr(), at_h, at_top, at_ids, temperature, top, _FLOATS[dtype]), _stream_of(device))
     if code:
         _fail(code, "ozaki2_token_logprobs")
-    return TokenLogprobs(logprobs, z_max, log_sum, h, top_logprobs, top_ids)
+    return TokenLogprobs(logprobs, z_max, log_sum, h, top_logprobs, top_ids, lse)
 
 
 def token_logprobs_backward(dlogprobs, logits, targets, saved, *, dentropy=None, temperature=1.0, ignore_index=-100, out=None,
@@ -246,7 +250,8 @@ def token_logprobs_backward(dlogprobs, logits, targets, saved, *, dentropy=None,
     """The gradient of `token_logprobs`' logits, in their type, from those of its logprobs and, if given, its entropy.
 
     `saved` is the forward call's TokenLogprobs (with its entropy where
-    `dentropy` is given); logits, targets, temperature and ignore_index are the
+    `dentropy` is given; of z_max, log_sum and lse the first two or the last one
+    may be None); logits, targets, temperature and ignore_index are the
     forward call's.  dlogprobs, dentropy (rows,) float32.  `out` may be the logits."""
     dtype, device = logits.dtype, logits.get_device()
     if dtype not in _FLOATS or logits.dim() != 2 or device < 0:
@@ -255,7 +260,10 @@ def token_logprobs_backward(dlogprobs, logits, targets, saved, *, dentropy=None,
     _check_targets(logits, targets, device)
     vector = (rows,)
     _check("dlogprobs", dlogprobs, torch.float32, device, vector)
-    for name in ("logprobs", "z_max", "log_sum"):
+    split = saved.z_max is not None and saved.log_sum is not None
+    if not split and saved.lse is None:
+        raise ValueError("saved needs z_max and log_sum, or lse")
+    for name in ("logprobs", "z_max", "log_sum") if split else ("logprobs", "lse"):
         _check("saved." + name, getattr(saved, name), torch.float32, device, vector)
     if dentropy is not None:
         _check("dentropy", dentropy, torch.float32, device, vector)
@@ -266,15 +274,21 @@ def token_logprobs_backward(dlogprobs, logits, targets, saved, *, dentropy=None,
     if out is not None:
         _check_out("out", out, dtype, device, shape)
     if stream is not None or device != _current_device():
-        tensors = (dlogprobs, logits, targets, saved.logprobs, saved.z_max, saved.log_sum, saved.entropy, dentropy, out)
+        tensors = (dlogprobs, logits, targets, saved.logprobs, saved.z_max, saved.log_sum, saved.lse, saved.entropy, dentropy, out)
         return _elsewhere(token_logprobs_backward, device, stream, tensors, dlogprobs, logits, targets, saved, dentropy=dentropy,
                           temperature=temperature, ignore_index=ignore_index, out=out)
 
     like = logits.is_contiguous()
     logits, ld = _rows(logits, vocab)
     targets, dlogprobs = _vector(targets), _vector(dlogprobs)
-    logprobs, z_max, log_sum = _vector(saved.logprobs), _vector(saved.z_max), _vector(saved.log_sum)
-    h = s = 0
+    logprobs = _vector(saved.logprobs)
+    at_max = at_sum = at_lse = h = s = 0
+    if split:
+        z_max, log_sum = _vector(saved.z_max), _vector(saved.log_sum)
+        at_max, at_sum = z_max.data_ptr(), log_sum.data_ptr()
+    else:
+        lse = _vector(saved.lse)
+        at_lse = lse.data_ptr()
     if dentropy is not None:
         dentropy, entropy = _vector(dentropy), _vector(saved.entropy)
         h, s = dentropy.data_ptr(), entropy.data_ptr()
@@ -284,7 +298,7 @@ def token_logprobs_backward(dlogprobs, logits, targets, saved, *, dentropy=None,
         d, ldd = torch.empty_like(logits) if like else torch.empty(shape, dtype=dtype, device=logits.device), vocab
     code = _library().ozaki2_token_logprobs_backward(
         _TOKEN_LOGPROBS_BACKWARD_ARGS.pack(rows, vocab, logits.data_ptr(), ld, targets.data_ptr(), ignore_index, dlogprobs.data_ptr(), h,
-                                           logprobs.data_ptr(), z_max.data_ptr(), log_sum.data_ptr(), s, d.data_ptr(), ldd, temperature,
+                                           logprobs.data_ptr(), at_max, at_sum, at_lse, s, d.data_ptr(), ldd, temperature,
                                            _FLOATS[dtype], 0), _stream_of(device))
     if code:
         _fail(code, "ozaki2_token_logprobs_backward")

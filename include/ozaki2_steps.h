@@ -92,17 +92,19 @@ oz2_status ozaki2_rms_norm_backward(const oz2_rms_norm_backward_args* args, void
  * For each row of logits [rows][vocab], with z = logits / temperature (times
  * 1 / temperature, rounded to 32 bits) and m their largest,
  *   z_max = m,  log_sum = log sum exp(z - m),  log p_i = z_i - m - log_sum,
+ *   lse = m + log_sum = log sum exp z,
  *   logprobs = log p of the row's target,  entropy = -sum p log p,
  *   top_logprobs, top_ids [rows][top] = the `top` largest log p and their places,
  *   in falling order, the lowest place first among equals.
  * targets [rows]; a target that is ignore_index has logprob 0, any other one
- * outside [0, vocab) NaN.  entropy may be NULL, and where top is 0 the last two.
+ * outside [0, vocab) NaN.  lse and entropy may be NULL, and where top is 0 the last two.
  * 0 <= top <= OZ2_TOP_MAX, top <= vocab; temperature finite, 1e-30 at least;
  * dtype: any, of the logits.  rows and vocab may be zero only together with
  * their outputs: vocab is 1 at least where there are rows.
  *
  * -inf is a logit that is masked, and so is one whose logit / temperature falls
- * below the float range: probability 0, nothing to the entropy.  A row of these alone has z_max and every log p -inf, log_sum and entropy 0.  A row
+ * below the float range: probability 0, nothing to the entropy.  A row of these
+ * alone has z_max, lse and every log p -inf, log_sum and entropy 0.  A row
  * with a NaN or +inf has NaN in all but its top_ids and an ignored target's
  * logprob; NaN comes first among the alternatives.  log p and the entropy stay
  * relatively exact where one token has almost all of the probability.
@@ -116,6 +118,7 @@ typedef struct {
   float* logprobs;
   float* z_max;
   float* log_sum;
+  float* lse;
   float* entropy;
   float* top_logprobs;
   int64_t* top_ids;
@@ -128,7 +131,10 @@ oz2_status ozaki2_token_logprobs(const oz2_token_logprobs_args* args, void* stre
  * The logits' gradient from g = dlogprobs [rows] and h = dentropy [rows] or NULL:
  *   dlogits_i = (g ((i == target) - p_i) - h p_i (log p_i + entropy)) / temperature,
  * with g taken as 0 where the target is ignore_index.  logprobs, z_max, log_sum
- * and entropy (used with dentropy) are ozaki2_token_logprobs'.  Masked logits
+ * and entropy (used with dentropy) are ozaki2_token_logprobs'.  z_max and log_sum
+ * may be NULL where its lse is given instead, which is not read beside them: log p
+ * then has a rounding of lse's size, which shows where one token has almost all of
+ * the probability.  Masked logits
  * and rows of -inf alone get 0; rows with NaN, +inf or a target outside
  * [0, vocab) get NaN.  dlogits [rows][vocab] of the logits' type may be the
  * logits themselves (same leading dimension).
@@ -144,6 +150,7 @@ typedef struct {
   const float* logprobs;
   const float* z_max;
   const float* log_sum;
+  const float* lse;
   const float* entropy;
   void* dlogits;
   int64_t ldd;

@@ -1,0 +1,82 @@
+"""The step operators where they leave the ordinary path: what may be kept between a pass and its gradient, codes at
+ties, rows that share blocks, confident rows, crowded alternatives and long steps."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+from tests import _steps_ref as ref  # noqa: E402
+from tests._layers_ref import TINY, UNIT, assert_within  # noqa: E402
+from tests.test_steps_gpu import check_norm, check_step, normal, some_targets, strided, tensors, values  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32, E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def oz2():
+    import __graft_entry__ as g
+
+    g.build()
+    import emulated_fp64_gemm_gb300 as m
+
+    assert torch.cuda.is_available()
+    yield m
+    assert m.last_error() == 0
+
+
+# ------------------------------------------------------------------ one number per row between the passes
+@pytest.mark.parametrize("rows,vocab", [(3, 9), (7, 1000), (4, 20001), (2, 131072), (1300, 700)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_gradient_from_lse_alone(oz2, rows, vocab, dtype):
+    """lse is off by a sum of vocab exponentials (see test_steps_gpu) and roundings of z_max's and its own size, 2^-22 of
+    them; log p = z - lse then by that and 2^-22 |z| once more (e), p by a factor 1 + e, p (log p + H) by p e (2 + |log p| + H)."""
+    for temperature, entropy in ((1.0, True), (0.7, False), (1.3, True)):
+        logits, targets = normal(rows, vocab, dtype=dtype, scale=3.0), some_targets(rows, vocab)
+        logits[0, ::2] = -INF
+        got = oz2.token_logprobs(logits, targets, temperature=temperature, entropy=entropy)
+        z_max, log_sum, _, ent, logp = ref.token_logprobs(logits, targets, temperature, -100)
+        lse = z_max + log_sum
+        rel = (vocab / 64 + 64) * 2.0**-24 + 2.0**-21
+        off = rel * (1 + log_sum) + 2.0**-22 * (z_max.abs() + lse.abs())
+        assert_within(got.lse, lse, off, "lse")
+        g, h = normal(rows, seed=5), normal(rows, seed=6) if entropy else None
+        saved = oz2.TokenLogprobs(logprobs=got.logprobs, lse=got.lse, entropy=got.entropy)
+        d = oz2.token_logprobs_backward(g, logits, targets, saved, dentropy=h, temperature=temperature)
+        p, known = torch.exp(logp), targets != -100
+        gd = torch.where(known, g.double(), 0.0)[:, None]
+        onehot = torch.zeros_like(p).scatter_(1, targets.clamp(min=0)[:, None], 1.0) * known[:, None]
+        near = logp.clamp(min=-200)
+        # (the target's own element comes from its log p, which keeps its precision)
+        at_target = -torch.expm1(torch.where(torch.isfinite(logp), logp, -1e300))
+        want = torch.where(onehot > 0, gd * at_target, -gd * p)
+        e = off[:, None] + 2.0**-22 * (near.abs() + lse.abs()[:, None]) + 2.0**-20
+        err = gd.abs() * torch.where(onehot > 0, at_target, p) * e
+        if entropy:
+            want = want - h.double()[:, None] * p * (near + ent[:, None])
+            err = err + h.double().abs()[:, None] * p * e * (2 + near.abs() + ent[:, None])
+        err = (2 * err + 2.0**-120) / temperature
+        assert_within(d, want / temperature, err + UNIT[dtype] * (want.abs() / temperature + err) + TINY[dtype], "dlogits")
+    # beside both numbers lse is not read
+    saved = got._replace(lse=torch.full_like(got.lse, NAN))
+    again = oz2.token_logprobs_backward(g, logits, targets, got, dentropy=h, temperature=temperature)
+    assert torch.equal(oz2.token_logprobs_backward(g, logits, targets, saved, dentropy=h, temperature=temperature), again)
+
+
+def test_lse_of_special_rows(oz2):
+    x = normal(5, 3000, dtype=F32)
+    x[0], x[1, 7], x[2, 8] = -INF, NAN, INF
+    x[3] = -3e38
+    targets = torch.zeros(5, dtype=torch.int64, device="cuda")
+    got = oz2.token_logprobs(x, targets, temperature=0.5)
+    assert got.lse[0] == got.lse[3] == -INF and bool(got.lse[1:3].isnan().all()) and bool(torch.isfinite(got.lse[4]))
+    saved = oz2.TokenLogprobs(logprobs=got.logprobs, lse=got.lse)
+    d = oz2.token_logprobs_backward(torch.ones(5, device="cuda"), x, targets, saved, temperature=0.5)
+    assert not d[[0, 3]].any() and bool(d[1:3].isnan().all()) and bool(torch.isfinite(d[4]).all())
+    for saved in (oz2.TokenLogprobs(got.logprobs), got._replace(z_max=None, lse=None), got._replace(log_sum=None, lse=None)):
+        with pytest.raises(ValueError, match="lse"):
+            oz2.token_logprobs_backward(torch.ones(5, device="cuda"), x, targets, saved)
+    with pytest.raises(ValueError):
+        oz2.token_logprobs_backward(torch.ones(5, device="cuda"), x, targets, oz2.TokenLogprobs(got.logprobs, lse=got.lse[:2]))
