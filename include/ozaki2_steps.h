@@ -35,8 +35,8 @@ extern "C" {
  * fraction; largest 448) and stands for y * scale, scale [rows][ceil(cols /
  * block)], one for every `block` columns: block is 128, or 0 for whole rows
  * (then one per row).
- * scale = max(1e-30, largest |y| of the block) / 448; y / scale is rounded once,
- * from 32 bits.  A NaN makes its block's scale and elements NaN.
+ * scale = max(1e-30, largest |y| of the block) / 448; each element is y / scale,
+ * held in 32 bits like y and scale, rounded to e4m3 once.  A NaN makes its block's scale and elements NaN.
  *
  * y may be x or residual itself (without quantize), residual_out may be x or
  * residual itself; otherwise outputs overlap nothing.

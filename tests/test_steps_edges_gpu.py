@@ -8,7 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 from tests import _steps_ref as ref  # noqa: E402
 from tests._layers_ref import TINY, UNIT, assert_within  # noqa: E402
-from tests.test_steps_gpu import check_norm, check_step, normal, some_targets, strided, tensors, values  # noqa: E402
+from tests.test_steps_gpu import check_norm, check_step, generator, normal, some_targets, strided, tensors, values  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32, E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
@@ -80,3 +80,53 @@ def test_lse_of_special_rows(oz2):
             oz2.token_logprobs_backward(torch.ones(5, device="cuda"), x, targets, saved)
     with pytest.raises(ValueError):
         oz2.token_logprobs_backward(torch.ones(5, device="cuda"), x, targets, oz2.TokenLogprobs(got.logprobs, lse=got.lse[:2]))
+
+
+# ------------------------------------------------------------------ 8-bit codes
+TIES = torch.tensor((ref.E4M3[:126] + ref.E4M3[1:127]) / 2, dtype=torch.float64)
+
+
+def weights_at_ties(cols, width, dtype):
+    """Weights of which each `width` have a largest one T and, for the others, products of T / 448 with the midpoints of
+    neighbouring codes, and what lies up to three 32-bit steps beside them (less, where the type has fewer bits)."""
+    rng = np.random.default_rng(cols)
+    w = np.zeros(cols, np.float32)
+    for at in range(0, cols, width):
+        n = min(width, cols - at)
+        # (a largest one of few bits in 16 bits: three quarters of its multiples are ties' products, to the bit)
+        top = np.float32(rng.uniform(1, 2)) if dtype is F32 else np.float32(rng.choice([1.3125, 1.5, 1.125, 1.6875]))
+        scale = top / np.float32(448)
+        near = (rng.choice(TIES.numpy(), n) * np.float64(scale)).astype(np.float32)
+        if dtype is F32:
+            near = (near.view(np.int32) + rng.integers(-3, 4, n).astype(np.int32)).view(np.float32)
+        w[at:at + n] = near
+        w[at + rng.integers(n)] = 0.0  # of both signs in the rows
+        w[at + rng.integers(n)] = top
+    return torch.from_numpy(w).cuda().to(dtype)
+
+
+def exactly_one(n):
+    return np.float32(n) * np.float32(1 / n) == 1
+
+
+@pytest.mark.parametrize("cols", [c for c in (128, 1024, 1003, 4096, 5001, 8200, 16384, 20000, 20002) if exactly_one(c)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("block", [None, 128])
+def test_codes_are_those_of_the_quotient(oz2, cols, dtype, block):
+    """Rows of 1 and -1 have the norm 1, so that y is the weight to the bit, scale its largest magnitude over 448 and each
+    code y / scale, both rounded to 32 bits, rounded once: a tie goes to the even code, its neighbours to theirs."""
+    w = weights_at_ties(cols, block or cols, dtype)
+    for rows in (3, 700):
+        x = torch.where(normal(rows, cols) < 0, -1.0, 1.0).to(dtype)
+        y = oz2.rms_norm(x, w, eps=0.0)
+        assert torch.equal(y, x * w)
+        for residual in (None, torch.zeros_like(x)):
+            q, scale = oz2.rms_norm(x, w, residual=residual, eps=0.0, out_dtype=E4M3, block=block)[:2]
+            exact = y.float().cpu().numpy()
+            width = block or cols
+            tops = np.stack([np.abs(exact[:, at:at + width]).max(1) for at in range(0, cols, width)], 1)
+            want = tops / np.float32(448)
+            assert np.array_equal(scale.cpu().numpy(), want)
+            codes = ref.to_e4m3((exact / want.repeat(width, 1)[:, :cols]).ravel()).reshape(rows, cols)
+            got = q.view(torch.uint8).cpu().numpy()
+            assert np.array_equal(got, codes), int((got != codes).sum())
