@@ -386,10 +386,25 @@ __device__ __forceinline__ float scale_of(float top) {
   return fmaf(y, kHi, y * kLo);
 }
 
-// The e4m3 of a span, and its scales where they are its own.  An element over the row's norm is y = t r, its code that of
-// y / scale.  (Not t times r / scale: that overflows where a row of small elements has a scale at its floor.)
+// How a whole row with one scale becomes codes.  Its elements v, over the norm and times the weight g, are y = v r g.  The
+// largest v g is known before r is, and (v g) / (the largest / 448) are the same codes, so that one exchange among the row's
+// warps serves both.  Where products v g leave the range, or the scale is at its floor, y itself is formed, its
+// largest sought in an exchange of its own, and divided.
+struct RowCodes {
+  Inverse inverse;
+  float r;  // of what it divides: y's r, as where scales are of 128 columns, or 1 (a branch instead costs 3 %)
+};
+// Whether the largest v g says that some have overflowed, or lost bits that a code shows (the least is 2^-19 of the largest), or
+// is NaN; or y is below the scale's floor.
+__device__ __forceinline__ bool products_out_of_range(float top, float r) { return !(top >= 1e-30f && top <= 1e38f && top * r >= 1e-30f); }
+__device__ __forceinline__ void normed_products(const Pairs& v, const Pairs& g, float r, Pairs& y) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(v[i], both(r)), g[i]);
+}
+
+// The e4m3 of a span's y, or of what stands for it in its row, and its scales where they are its own.
 template <typename T, bool VEC, bool SHIFTED>
-__device__ __forceinline__ void quantize_span(const NormParams& p, int64_t at_row, uint8_t* y, int head, int left, int first_span, int j, float r,
+__device__ __forceinline__ void quantize_span(const NormParams& p, int64_t at_row, uint8_t* y, int head, int left, int first_span, int j,
                                               const Inverse& row, Pairs& t) {
   constexpr bool HALF_WARPS = kHalfWarps<T, VEC>;
   constexpr int HALVES = HALF_WARPS ? 1 : 2;  // a lane's elements are of one block, or of two
@@ -402,26 +417,25 @@ __device__ __forceinline__ void quantize_span(const NormParams& p, int64_t at_ro
       float top = 0.0f;
 #pragma unroll
       for (int i = h * 2; i < (HALF_WARPS ? 4 : h * 2 + 2); ++i) top = max_abs_nan(top, t[i].x, t[i].y);
-      const float s = scale_of((HALF_WARPS ? half_warp_max_nan(top) : warp_max_nan(top)) * r);
+      const float s = scale_of(HALF_WARPS ? half_warp_max_nan(top) : warp_max_nan(top));
       const int g = (first_span + j) * 2 + (HALF_WARPS ? lane >> 4 : h);
       if ((HALF_WARPS ? lane & 15 : lane) == 0 && g < p.scales) p.scale[at_row * p.scales + g] = s;
       inv[h] = inverse_of(s);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t[i] = inv[HALF_WARPS ? 0 : i >> 1].times(mul2(t[i], both(r)));
+  for (int i = 0; i < 4; ++i) t[i] = inv[HALF_WARPS ? 0 : i >> 1].times(t[i]);
   write_e4m3<T, VEC, SHIFTED>(y, left, j, p.whole, t, head);
 }
 
 // What becomes of a span's elements v (scaled as r is): y = v g r.
 template <typename T, bool VEC, bool SHIFTED = false>
-__device__ __forceinline__ void finish_span(const NormParams& p, int64_t row, int c0, int left, int first_span, int j, float r, const Inverse& inverse,
+__device__ __forceinline__ void finish_span(const NormParams& p, int64_t row, int c0, int left, int first_span, int j, float r, const RowCodes& codes,
                                             const Pairs& g, const Pairs& v) {
   Pairs y;
   if (p.quantize) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = mul2(v[i], g[i]);
-    quantize_span<T, VEC, SHIFTED>(p, row, static_cast<uint8_t*>(p.y) + row * p.ldy + c0, -c0, left, first_span, j, r, inverse, y);
+    normed_products(v, g, codes.r, y);
+    quantize_span<T, VEC, SHIFTED>(p, row, static_cast<uint8_t*>(p.y) + row * p.ldy + c0, -c0, left, first_span, j, codes.inverse, y);
   } else {  // not first by g: the product of two small ones would lose bits that r brings back
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = mul2(v[i], mul2(g[i], both(r)));
@@ -481,17 +495,29 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const Place<T, VEC
     row_reduce<kMax>(sum, top, p.warps, room[2]);
   }
   const float r = inverse_norm(sum, p.inv_cols, p.eps, f);
-  Inverse inverse{};
+  RowCodes codes{Inverse{}, r};
   if (row_top) {
-    const float scale = scale_of(top * r);
-    inverse = inverse_of(scale);
-    if (at.w == 0 && at.lane == 0) p.scale[row] = scale;
+    const bool normed = products_out_of_range(top, r);  // the same in all of the row's threads
+    if (normed) {
+      top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        Pairs g, y;
+        ws[j].pairs(g);
+        normed_products(v[j], g, r, y);
+        top = max_magnitude(y, top);
+      }
+      row_reduce<kMax>(sum, top, p.warps, room[3]);
+    }
+    const float scale = scale_of(top);
+    codes = RowCodes{inverse_of(scale), normed ? r : 1.0f};
+    if (at.w == 0 && at.lane == 0) p.scale[row] = normed ? scale : scale * r;
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     Pairs g;
     ws[j].pairs(g);
-    finish_span<T, VEC, SHIFTED>(p, row, at.c0, at.left, at.w * N, j, r, inverse, g, v[j]);
+    finish_span<T, VEC, SHIFTED>(p, row, at.c0, at.left, at.w * N, j, r, codes, g, v[j]);
   }
 }
 
@@ -501,7 +527,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const Place<T, VEC
 template <typename T, int N, bool SHIFTED>
 __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ uint4 ring_memory[];
-  __shared__ float2 room[2][3][16];
+  __shared__ float2 room[2][4][16];
   Place<T, true, N> at(p.warps, p.cols);
   const int64_t step = SHIFTED ? p.period : 1;
   const int64_t first = SHIFTED ? at.team / step * step * p.run + at.team % step : at.team * p.run, end = min(first + p.run * step, p.rows);
@@ -557,7 +583,7 @@ __global__ void __launch_bounds__(512) rms_norm_kernel(const __grid_constant__ N
 // elements.
 template <typename T, int N>
 __global__ void __launch_bounds__(512) rms_norm_ragged_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float2 room[3][16];
+  __shared__ float2 room[4][16];
   const Place<T, false, N> at(p.warps, p.cols);
   const int64_t row = at.team;
   wait_for_predecessor();
@@ -604,7 +630,7 @@ __device__ __forceinline__ void read_sum(const NormParams& p, int64_t row, int c
 // (Three blocks per SM where the registers allow it: 1024 x 20000 bfloat16 with residual to 8 bits 35 us, with two 42.)
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512, VEC && sizeof(T) == 2 ? 3 : 2) rms_norm_long_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float2 room[3][16];
+  __shared__ float2 room[4][16];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, spans = (p.cols + 255) / 256;
   const int64_t row = blockIdx.x;
   wait_for_predecessor();
@@ -645,9 +671,30 @@ __global__ void __launch_bounds__(512, VEC && sizeof(T) == 2 ? 3 : 2) rms_norm_l
     row_reduce<kMax>(sum, top, p.warps, room[2]);
   }
   const float r = inverse_norm(sum, p.inv_cols, p.eps, f);
-  const float scale = scale_of(top * r);
-  const Inverse inverse = inverse_of(scale);
-  if (p.quantize && !p.block && threadIdx.x == 0) p.scale[row] = scale;
+  RowCodes codes{Inverse{}, r};
+  if (p.quantize && !p.block) {
+    const bool normed = products_out_of_range(top, r);
+    if (normed) {
+      top = 0.0f;
+#pragma unroll 1
+      for (int span = w; span < spans; span += p.warps) {
+        Pairs v, g;
+        Part<T, VEC> ws;
+        const int c0 = first_column<T, VEC>(span, lane);
+        ws.read(weight + c0, p.cols - c0, 0);
+        read_sum<T, VEC>(p, row, c0, v);
+        ws.pairs(g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(f));
+        normed_products(v, g, r, v);
+        top = max_magnitude(v, top);
+      }
+      row_reduce<kMax>(sum, top, p.warps, room[3]);
+    }
+    const float scale = scale_of(top);
+    codes = RowCodes{inverse_of(scale), normed ? r : 1.0f};
+    if (threadIdx.x == 0) p.scale[row] = normed ? scale : scale * r;
+  }
   // (all reads of the row for its statistics are behind the last barrier: outputs may be inputs)
 #pragma unroll 2
   for (int span = w; span < spans; span += p.warps) {
@@ -660,7 +707,7 @@ __global__ void __launch_bounds__(512, VEC && sizeof(T) == 2 ? 3 : 2) rms_norm_l
     ws.pairs(g);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(f));
-    finish_span<T, VEC>(p, row, c0, left, span, 0, r, inverse, g, v);
+    finish_span<T, VEC>(p, row, c0, left, span, 0, r, codes, g, v);
   }
 }
 

@@ -130,3 +130,16 @@ def test_codes_are_those_of_the_quotient(oz2, cols, dtype, block):
             codes = ref.to_e4m3((exact / want.repeat(width, 1)[:, :cols]).ravel()).reshape(rows, cols)
             got = q.view(torch.uint8).cpu().numpy()
             assert np.array_equal(got, codes), int((got != codes).sum())
+
+
+@pytest.mark.parametrize("cols", [200, 2048, 1003, 9000, 20000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size,weight", [(1e10, 1e30), (1e18, 1e21), (1e-14, 1e-29), (1e-9, 1e-34), (1e30, 1e-25), (1e-30, 1e25)])
+def test_codes_of_products_out_of_range(oz2, cols, dtype, size, weight):
+    # x times the weight leaves the 32-bit range, x over its norm times the weight does not
+    x, w = normal(7, cols, dtype=dtype, scale=size), normal(cols, dtype=dtype, scale=weight, seed=1)
+    x[2] = 0
+    for residual in (None, torch.zeros_like(x)):
+        for block in (None, 128):
+            x[2, 0] = 0
+            check_norm(oz2, x, w, residual, eps=1e-38, quantize=True, block=block)
