@@ -13,6 +13,7 @@
 
 #include "../../include/ozaki2_layers.h"
 #include "oz2_internal.cuh"
+#include "oz2_sizes.h"
 
 namespace oz2 {
 
@@ -64,7 +65,6 @@ inline FastDiv make_fast_div(uint32_t d) {
   return f;
 }
 
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t dtype_bytes(oz2_dtype t) { return t == OZ2_F32 ? 4 : 2; }
 // Whether groups of eight elements start on boundaries of their own size: 16 bytes, or 32 of 32-bit elements.
 inline bool groups_aligned(const void* p, int64_t ld, oz2_dtype t) {

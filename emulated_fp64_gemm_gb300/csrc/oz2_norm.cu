@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "oz2_norm_plan.h"
 #include "oz2_steps.cuh"
 
 namespace oz2 {
@@ -1093,94 +1094,11 @@ __global__ void __launch_bounds__(512) weight_sums_kernel(const float* partial, 
 }
 
 // ------------------------------------------------------------------ host side
-constexpr int64_t kLongSpans = 64;
-constexpr int64_t kRingMost = 224 * 1024;  // shared memory of an SM's rows on their way
-// Warps that an SM's registers hold, by the spans of each.  (65536 x 512 by 24 and 32 warps: 16 bits 22.8 and 27 us, 32 bits 44.7
-// and 43.)
-struct ResidentWarps {
-  int one, two, four;
-};
-constexpr ResidentWarps kForward{32, 24, 16}, kForward32{32, 32, 16}, kBackward{24, 16, 16}, kBackwardRagged{20, 20, 16};
-// How rows are shared out: warps and spans per warp of a row, teams per block, blocks, rows on their way.
-struct Shape {
-  bool is_long;  // more than a block's registers, or than two of its rows in shared memory
-  int warps, spans, per_block, depth;
-  int64_t blocks;
-  int threads() const { return 32 * warps * per_block; }
-};
-// `element_bytes`: of all of a row's inputs together; `wide`: the most spans per warp where there are rows enough to fill
-// the SMs.  Few rows are spread over more warps each.
-Shape row_shape(int64_t rows, int64_t cols, int64_t element_bytes, bool vec, int wide, const ResidentWarps& warps, int num_sms) {
-  const int64_t spans = ceil_div(cols, 256);
-  Shape s{};
-  s.warps = 16;
-  s.is_long = spans > kLongSpans;
-  if (s.is_long) return s;
-  const bool many = rows >= 4 * num_sms;
-  s.spans = spans <= 4 && !many ? 1 : spans <= 32 ? 2 : 4;
-  if (many && wide == 4) s.spans = spans == 1 ? 1 : spans == 2 ? 2 : 4;
-  // (gradients: 4000 x 1024 in one, two and four spans per warp 11.0, 13.8 and 14.3 us, 8000 x 1024 17.8, 16.8 and 20.8)
-  if (many && wide == 2 && spans <= 4) s.spans = spans == 1 || (spans > 2 && rows < 32 * num_sms) ? 1 : 2;
-  s.warps = static_cast<int>(ceil_div(spans, s.spans));
-  // nine to twelve warps leave the registers of a fourth or more unused: half as many with twice the spans (gradient of
-  // 8192 x 5120: 64 -> 57.5 us, 8192 x 4608: 63 -> 52)
-  if (many && vec && s.spans == 2 && 2 * s.warps > warps.two && 4 * s.warps <= 3 * warps.two) {
-    s.spans = 4;
-    s.warps = static_cast<int>(ceil_div(spans, s.spans));
-  }
-  s.per_block = s.warps == 1 ? 4 : 1;
-  const int64_t slot = element_bytes * 256 * s.per_block * s.warps * s.spans;
-  s.is_long = vec && 2 * slot > kRingMost;
-  if (s.is_long) {
-    s.warps = 16;
-    return s;
-  }
-  // as many blocks as the registers hold, with up to 50 KB per SM on their way, and 100 where rows are long (more is served
-  // worse: the gradient of 16384 x 4096 with 49, 98 and 147 KB 84.0, 82.9 and 88.8 us, of 65536 x 512 47, 50 and 53)
-  int64_t resident = std::max(1, (s.spans == 1 ? warps.one : s.spans == 2 ? warps.two : warps.four) / (s.warps * s.per_block));
-  if (vec) {
-    const int64_t most = s.per_block == 1 ? 100 * 1024 : 50 * 1024;
-    s.depth = 4;
-    while (s.depth > 2 && (resident * (s.depth * slot + 1024) > kRingMost || resident * (s.depth - 1) * slot > most)) --s.depth;
-    resident = std::max<int64_t>(1, std::min(resident, kRingMost / (s.depth * slot + 1024)));
-  }
-  s.blocks = std::min(ceil_div(rows, s.per_block), resident * num_sms);
-  return s;
-}
-template <typename T>
-size_t ring_bytes(const Shape& s, int arrays, int depth) { return static_cast<size_t>(s.threads()) * depth * arrays * s.spans * kPieces<T> * 16; }
-
 int64_t weight_slices(const oz2_rms_norm_backward_args& a, int num_sms) {
   return std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.rows, 32), 4 * num_sms / std::max<int64_t>(1, ceil_div(a.cols, 256))));
 }
 bool pieces_aligned(const void* p, int64_t ld, oz2_dtype t) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<int64_t>(dtype_bytes(t)) % 16 == 0;
-}
-// How rows are read: by aligned pieces, by pieces from the boundary before them on, or by single elements.
-enum Access { kAligned, kShifted, kSingle };
-// Whether rows of p start as far behind boundaries of 16 bytes' elements as those of q, in elements of their own types.
-bool start_alike(const void* p, int64_t ldp, int64_t size_p, const void* q, int64_t ldq, int64_t size_q, int64_t per) {
-  return reinterpret_cast<uintptr_t>(p) / size_p % per == reinterpret_cast<uintptr_t>(q) / size_q % per && ldp % per == ldq % per;
-}
-// How many rows there are from one to the next that starts as far from a boundary.
-int64_t row_period(int64_t ld, int64_t per) {
-  int64_t period = 1;
-  while (period * ld % per) period *= 2;
-  return period;
-}
-struct Plan {
-  Access access;
-  Shape shape;
-};
-// `element_bytes`, `wide`, `warps`: see row_shape.  Rows too long for shared memory, but not for registers, are read by
-// single elements.
-Plan plan_rows(int64_t rows, int64_t cols, int64_t element_bytes, Access access, int64_t per, int wide, const ResidentWarps& warps,
-               const ResidentWarps& warps_single, int num_sms) {
-  if (access != kSingle) {
-    const Shape s = row_shape(rows, access == kShifted ? cols + per - 1 : cols, element_bytes, true, wide, warps, num_sms);
-    if (access == kAligned || !s.is_long) return Plan{access, s};
-  }
-  return Plan{kSingle, row_shape(rows, cols, element_bytes, false, 2, warps_single, num_sms)};
 }
 // (A piece must not hold both ends of a row.)
 Access backward_access(const oz2_rms_norm_backward_args& a, int num_sms) {
@@ -1228,23 +1146,13 @@ cudaError_t with_spans(int spans, F&& f) {
 
 template <typename T>
 cudaError_t forward(NormParams& p, Access access, const DeviceResources& res, cudaStream_t st) {
-  constexpr int64_t PER = 16 / sizeof(T);
-  const int arrays = p.residual ? 2 : 1;
-  const Plan plan = plan_rows(p.rows, p.cols, sizeof(T) * arrays, access, PER, 4, sizeof(T) == 2 ? kForward : kForward32, kForward, res.num_sms);
+  const ForwardPlan rows = forward_plan(p.rows, p.cols, sizeof(T), p.residual != nullptr, access, p.ldx, res.num_sms);
+  const Plan& plan = rows.plan;
   const Shape& s = plan.shape;
-  const bool shifted = plan.access == kShifted;
   p.warps = s.warps;
-  // a row on its way beside the one that is worked on; two where that is still little per SM (one input: 2730 x 12288 25.8 and
-  // 24.1 us, 4681 x 7168 24.2 and 22.6; with 64 KB 8192 x 4096 22.6 and 23.1; 32 bits, 82 KB, 4096 x 10240 53 and 59)
-  const bool two = !p.residual && 2 * ring_bytes<T>(s, arrays, 1) * ceil_div(s.blocks, res.num_sms) <= 60 * 1024;
-  p.depth = std::min(s.depth, two ? 3 : 2);
-  // Runs of four rows where there is a residual (8192 x 4096: 41.5 us, all of a team's rows in one run 45); all of them where
-  // rows have one input (8192 x 4096 24.6 and 22.7, 2730 x 12288 40 and 26) or one block of nine to twelve warps is all that an
-  // SM holds, so that nothing covers the gaps between blocks (3276 x 10240: 47 and 42).  Of a span per warp 16 at most
-  // (131072 x 128: 34 and 27.5).
-  const int64_t all = ceil_div(p.rows, s.blocks * s.per_block);
-  p.run = static_cast<int>(std::min<int64_t>(p.residual && (s.warps <= 8 || s.warps > 12) ? 4 : s.spans == 1 ? 16 : all, all));
-  p.period = static_cast<int>(shifted ? row_period(p.ldx, PER) : 1);
+  p.depth = rows.depth;
+  p.run = rows.run;
+  p.period = rows.period;
   if (s.is_long) {
     return plan.access == kAligned ? launch_kernel(rms_norm_long_kernel<T, true>, p.rows, 512, 0, 1, st, p)
                                    : launch_kernel(rms_norm_long_kernel<T, false>, p.rows, 512, 0, 1, st, p);
@@ -1256,10 +1164,10 @@ cudaError_t forward(NormParams& p, Access access, const DeviceResources& res, cu
       constexpr auto kernel = rms_norm_kernel<T, N, decltype(is_shifted)::value>;
       const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
       const int64_t teams = ceil_div(p.rows, static_cast<int64_t>(p.run) * p.period) * p.period;
-      return e == cudaSuccess ? launch_kernel(kernel, ceil_div(teams, s.per_block), s.threads(), ring_bytes<T>(s, arrays, p.depth), 1, st, p) : e;
+      return e == cudaSuccess ? launch_kernel(kernel, ceil_div(teams, s.per_block), s.threads(), s.ring_bytes(p.residual ? 2 : 1, sizeof(T), p.depth), 1, st, p) : e;
     };
     if constexpr (sizeof(T) == 2) {
-      if (shifted) return launch(std::true_type());
+      if (plan.access == kShifted) return launch(std::true_type());
     }
     return launch(std::false_type());
   });
@@ -1290,7 +1198,7 @@ cudaError_t backward(NormBackwardParams& p, const oz2_rms_norm_backward_args& a,
     const auto launch = [&](auto shifted) {
       constexpr auto kernel = rms_norm_backward_kernel<T, N, decltype(shifted)::value>;
       const cudaError_t e = allow_smem<kernel>(kRingMost, res.device);
-      return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), ring_bytes<T>(s, a.dresidual ? 3 : 2, s.depth), 1, st, p) : e;
+      return e == cudaSuccess ? launch_kernel(kernel, s.blocks, s.threads(), s.ring_bytes(a.dresidual ? 3 : 2, sizeof(T), s.depth), 1, st, p) : e;
     };
     return access == kShifted ? launch(std::true_type()) : launch(std::false_type());
   });
