@@ -654,7 +654,8 @@ struct LogprobBackwardParams {
   const float *dlogprobs, *dentropy, *logprobs, *z_max, *log_sum, *entropy;  // log_sum null: z_max has it in it
   void* dlogits;
   int64_t ldd;
-  float inv_t, c;
+  float temperature, inv_t, c;
+  float minus_one;  // see sub_exact
   int segments;  // blocks per row
 };
 
@@ -662,19 +663,22 @@ constexpr int kBackThreads = 256, kBackVectors = 4;  // at most
 
 // What a row's elements share.
 struct RowGradient {
-  float a, b, shift, z_max, log_sum2, target_value;
+  float a, b, z_max, x_max, log_sum2, target_value;
   int target;  // -1: none
-  bool exact;
 };
 
+// Of two elements.  log2 p is (z - z_max) log2 e - log_sum2, where the difference has no rounding if it is small; of 16-bit
+// logits (x - x_max) c - log_sum2.  (x c - (z_max + log_sum) log2 e as one FFMA has a rounding of z_max's size, which
+// shows where z_max is large, and in the entropy's gradient everywhere: the element of a token with almost all of the
+// probability is p (log p + H), both of which are far below it.)
 template <typename T, bool ENTROPY>
-__device__ __forceinline__ float gradient_of(const RowGradient& r, const LogprobBackwardParams& p, float x) {
-  // z - z_max is exact where it is small; as one FFMA, log2 p has a rounding of z_max's size, which 16-bit gradients of
-  // logits of ordinary size do not see
-  float u = r.exact ? fmaf(__fmul_rn(x, p.inv_t) - r.z_max, kLog2e, -r.log_sum2) : fmaf(x, p.c, -r.shift);
-  if (ENTROPY) u = max_nan(u, kLeast);
-  const float e = fast_exp2(u);
-  return ENTROPY ? e * fmaf(r.b, u, r.a) : e * r.a;
+__device__ __forceinline__ float2 gradient_of(const RowGradient& r, const LogprobBackwardParams& p, float2 x) {
+  float2 u;
+  if (sizeof(T) == 4) u = fma2(sub_exact(mul2(x, both(p.inv_t)), both(r.z_max), p.minus_one), both(kLog2e), both(-r.log_sum2));
+  else u = fma2(add2(x, both(-r.x_max)), both(p.c), both(-r.log_sum2));
+  if (ENTROPY) u = make_float2(max_nan(u.x, kLeast), max_nan(u.y, kLeast));
+  const float2 e = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+  return mul2(e, ENTROPY ? fma2(both(r.b), u, both(r.a)) : both(r.a));
 }
 
 template <typename T, bool ENTROPY>
@@ -704,12 +708,12 @@ __global__ void __launch_bounds__(kBackThreads) token_logprobs_backward_kernel(c
   r.b = -h * kLn2 * p.inv_t;
   r.z_max = z_max;
   r.log_sum2 = log_sum * kLog2e;
-  r.shift = fmaf(z_max, kLog2e, r.log_sum2);
-  r.exact = sizeof(T) == 4 || !(fabsf(z_max) < 256.0f);
+  // the largest logit again, to the bit: z_max is off its quotient by three roundings of 32 bits at most, far less than half a
+  // step of 16 (lse in its place is not a logit's)
+  r.x_max = p.log_sum && sizeof(T) == 2 ? Elem<T>::up(Elem<T>::down(z_max * p.temperature)) : z_max * p.temperature;
   r.target = !ignored && inside ? static_cast<int>(target) : -1;
   if (z_max == -infinity()) {  // no distribution, no gradient
-    r.a = r.b = r.shift = r.z_max = r.log_sum2 = 0.0f;
-    r.exact = false;
+    r.a = r.b = r.z_max = r.x_max = r.log_sum2 = 0.0f;
     r.target = -1;
   }
   if (!ignored && !inside || z_max != z_max) r.a = __int_as_float(0x7FFFFFFF);
@@ -727,7 +731,11 @@ __global__ void __launch_bounds__(kBackThreads) token_logprobs_backward_kernel(c
     float y[8];
     raw[u].values(y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = gradient_of<T, ENTROPY>(r, p, y[e]);
+    for (int e = 0; e < 8; e += 2) {
+      const float2 d = gradient_of<T, ENTROPY>(r, p, make_float2(y[e], y[e + 1]));
+      y[e] = d.x;
+      y[e + 1] = d.y;
+    }
     if (r.target >= column && r.target < column + 8) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -739,7 +747,7 @@ __global__ void __launch_bounds__(kBackThreads) token_logprobs_backward_kernel(c
   if (segment == 0 && tid < 16) {
     const int at = tid < 8 ? tid : lead + vectors * 8 + tid - 8;
     if (tid < 8 ? tid < lead : at < vocab)
-      out[at] = Elem<T>::down(at == r.target ? r.target_value : gradient_of<T, ENTROPY>(r, p, Elem<T>::up(x[at])));
+      out[at] = Elem<T>::down(at == r.target ? r.target_value : gradient_of<T, ENTROPY>(r, p, both(Elem<T>::up(x[at]))).x);
   }
 }
 
@@ -804,6 +812,8 @@ cudaError_t launch_token_logprobs_backward(const oz2_token_logprobs_backward_arg
   p.ldd = a.ldd;
   p.inv_t = static_cast<float>(1.0 / a.temperature);
   p.c = static_cast<float>(kLog2eDouble / a.temperature);
+  p.temperature = static_cast<float>(a.temperature);
+  p.minus_one = -1.0f;
   switch (a.dtype) {
     case OZ2_BF16: return backward<__nv_bfloat16>(p, a.rows, st);
     case OZ2_F16: return backward<__half>(p, a.rows, st);

@@ -143,3 +143,29 @@ def test_codes_of_products_out_of_range(oz2, cols, dtype, size, weight):
         for block in (None, 128):
             x[2, 0] = 0
             check_norm(oz2, x, w, residual, eps=1e-38, quantize=True, block=block)
+
+
+# ------------------------------------------------------------------ token_logprobs
+@pytest.mark.parametrize("vocab", [10, 5003, 131072])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("temperature", [1.0, 0.7])
+def test_entropy_gradient_of_confident_rows(oz2, vocab, dtype, temperature):
+    """Where one token has almost all of the probability, its element is -h p (log p + H), which is far smaller than z_max:
+    log p and H are each off by a factor (see test_logprobs_of_confident_rows), H is more than eight times -log p, and the
+    others' p and log p by 2^-22 of z's size: 2^-13 of every element in all, beside the output's rounding."""
+    gaps = torch.tensor([10.0, 14.0, 20.0, 30.0, 40.0, 60.0], device="cuda") * temperature
+    at = torch.tensor([0, vocab // 2, vocab - 1, 3, 5, 1], device="cuda")
+    logits = (normal(6, vocab) * 0.5).to(dtype).float()
+    logits.scatter_(1, at[:, None], (gaps + math.log(vocab)).to(dtype).float()[:, None])
+    logits = logits.to(dtype)
+    h = normal(6, seed=3) + 300.0
+    for targets, g in ((torch.full_like(at, -100), normal(6, seed=4)), ((at + 1) % vocab, torch.zeros(6, device="cuda"))):
+        saved = oz2.token_logprobs(logits, targets, temperature=temperature, entropy=True)
+        got = oz2.token_logprobs_backward(g, logits, targets, saved, dentropy=h, temperature=temperature)
+        z = logits.double() / temperature
+        d = z - z.gather(1, at[:, None])
+        others = torch.exp(d).scatter(1, at[:, None], 0.0)
+        rho, bent = others.sum(1, keepdim=True), -(others * d).sum(1, keepdim=True)
+        # log p + H = d + bent / (1 + rho): nothing of it is a difference of larger numbers
+        want = -h.double()[:, None] * torch.exp(d) / (1 + rho) * (d + bent / (1 + rho)) / temperature
+        assert_within(got, want, 2.0**-13 * want.abs() + UNIT[dtype] * (1 + 2.0**-13) * want.abs() + TINY[dtype])
