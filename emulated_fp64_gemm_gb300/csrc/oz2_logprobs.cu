@@ -346,21 +346,22 @@ __device__ __forceinline__ void collect_equal(Shared<THREADS>& sh, const Slice<T
 // room for reach the threshold (many large logits in a few threads' elements).  Reads the slice `top` times.
 template <typename T, int THREADS>
 __device__ __forceinline__ void collect_in_turn(Shared<THREADS>& sh, const Slice<T, THREADS>& s, int top) {
-  uint64_t limit = ~uint64_t(0);
+  uint64_t most = ~uint64_t(0);  // the key of a NaN at the first place
   for (int i = 0; i < top; ++i) {
     uint64_t best = 0;
     s.again(threadIdx.x, 0, 1, [&](float x, int column) {
       const uint64_t k = place_key(order_key(x), column);
-      if (k < limit && k > best) best = k;
+      if (k <= most && k > best) best = k;
     });
     if (threadIdx.x == 0) sh.best = 0;
     __syncthreads();
     atomicMax(reinterpret_cast<unsigned long long*>(&sh.best), static_cast<unsigned long long>(best));
     __syncthreads();
-    limit = sh.best;
-    if (threadIdx.x == 0) sh.candidates[i] = limit;
+    const uint64_t found = sh.best;
+    if (threadIdx.x == 0) sh.candidates[i] = found;
     __syncthreads();
-    if (limit == 0) {  // the slice has no more
+    most = found - 1;
+    if (found == 0) {  // the slice has no more
       if (threadIdx.x == 0) sh.count = i;
       return;
     }

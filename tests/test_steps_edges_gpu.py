@@ -169,3 +169,18 @@ def test_entropy_gradient_of_confident_rows(oz2, vocab, dtype, temperature):
         # log p + H = d + bent / (1 + rho): nothing of it is a difference of larger numbers
         want = -h.double()[:, None] * torch.exp(d) / (1 + rho) * (d + bent / (1 + rho)) / temperature
         assert_within(got, want, 2.0**-13 * want.abs() + UNIT[dtype] * (1 + 2.0**-13) * want.abs() + TINY[dtype])
+
+
+def test_nan_at_the_first_place_of_crowded_rows(oz2):
+    # more large logits in the reach of 31 groups of threads than there is room for, and a NaN before them
+    vocab, rows = 262144, 400
+    columns = torch.arange(vocab, device="cuda")
+    logits = normal(rows, vocab, scale=0.1)
+    some = columns % 2048 < 992
+    logits[::40] = torch.where(some, 5 + torch.rand(vocab, generator=generator(1), device="cuda"), logits[::40])
+    logits[0, 0] = logits[40, 0] = logits[40, 77] = logits[80, 8] = NAN
+    order = torch.sort(logits[::40].nan_to_num(100.0), dim=-1, descending=True, stable=True).indices[:, :32]
+    got = oz2.token_logprobs(logits, torch.zeros(rows, dtype=torch.int64, device="cuda"), top=32)
+    assert torch.equal(got.top_ids[::40], order)
+    assert got.top_ids[0, 0] == 0 and got.top_ids[40, :2].tolist() == [0, 77] and got.top_ids[80, 0] == 8
+    assert bool(got.top_logprobs[[0, 40, 80]].isnan().all()) and bool(torch.isfinite(got.top_logprobs[120]).all())
