@@ -308,16 +308,29 @@ def token_logprobs_backward(dlogprobs, logits, targets, saved, *, dentropy=None,
 
 
 # ------------------------------------------------------------------ adamw
-class AdamWState(NamedTuple):
-    """The states of `adamw`, as flat tensors: tensor i of the call begins where those before it end, each rounded up to
-    256 elements.  They are plain tensors, to be saved and loaded like any other."""
-
+class _AdamWTensors(NamedTuple):
     step: torch.Tensor                                # int64 (2,): the steps taken, and 0
     exp_avg: torch.Tensor                             # float32, or float8_e4m3fn
     exp_avg_sq: torch.Tensor                          # float32, or uint8: fourth roots, 0 to 255
     exp_avg_scale: Optional[torch.Tensor] = None      # float32, for every 256 elements of 8-bit states
     exp_avg_sq_scale: Optional[torch.Tensor] = None
     master: Optional[torch.Tensor] = None             # float32: the parameters themselves, where theirs are 16-bit copies
+
+
+class AdamWState(_AdamWTensors):
+    """The states of `adamw`, as flat tensors: tensor i of the call begins where those before it end, each rounded up to
+    256 elements.  They are plain tensors, to be saved and loaded like any other.
+
+    One of `adamw_state` knows its parameters' sizes besides, copies and pickles of it too, and `adamw` refuses it for
+    other sizes or another order of them.  One that is put together from tensors has none (they may be set); there only
+    the length of all is checked.  Parameters of equal sizes are told apart by their order alone."""
+
+    sizes = None  # a list of the parameters' sizes, or None
+
+    def _replace(self, **changes):
+        new = super()._replace(**changes)
+        new.sizes = self.sizes
+        return new
 
 
 _dtype_of, _device_of = attrgetter("dtype"), torch.Tensor.get_device
@@ -344,6 +357,7 @@ def adamw_state(params, *, bits=32, master=False):
 
     state = AdamWState(zeros(2, torch.int64), zeros(total, torch.float32 if bits == 32 else torch.float8_e4m3fn),
                        zeros(total, torch.float32 if bits == 32 else torch.uint8), *(zeros(blocks) for _ in range(2 if bits == 8 else 0)))
+    state.sizes = sizes
     if not master:
         return state
     if any(t.dtype not in _HALVES for t in params):
@@ -359,9 +373,12 @@ def _fits(t, dtype, device, shape):
     return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
 
 
-def _check_state(state, blocks, dtype, device):
+def _check_state(state, sizes, dtype, device):
     """The states' bits."""
     step, m, v, scale_m, scale_v, master = state
+    if state.sizes is not None and state.sizes != sizes:
+        raise ValueError("the state is that of parameters of other sizes, or in another order")
+    blocks = _blocks(sizes)
     eight = m.dtype is torch.float8_e4m3fn
     wanted = {"step": (step, torch.int64, (2,)), "exp_avg": (m, torch.float8_e4m3fn if eight else torch.float32, (blocks * ADAMW_BLOCK,)),
               "exp_avg_sq": (v, torch.uint8 if eight else torch.float32, (blocks * ADAMW_BLOCK,))}
@@ -423,7 +440,7 @@ def adamw(params, grads, state, *, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
         raise ValueError("each gradient must have as many elements as its parameter")
     if not all(map(tensor.is_contiguous, params)):
         raise ValueError("params must be contiguous")
-    bits = _check_state(state, _blocks(sizes), dtype, device)
+    bits = _check_state(state, sizes, dtype, device)
     lr_at, lr_value = _number("lr", lr, device)
     scale_at, scale_value = _number("grad_scale", grad_scale, device)
     if stream is not None or device != _current_device():

@@ -1,4 +1,7 @@
 """Host-side checks of the step operators beside those of test_steps_cpu: what a call may leave out, and what it refuses."""
+import copy
+import io
+
 import pytest
 
 import emulated_fp64_gemm_gb300 as oz2  # noqa: F401
@@ -30,3 +33,27 @@ def test_names_of_what_log_probabilities_keep():
     assert oz2.TokenLogprobs._fields == ("logprobs", "z_max", "log_sum", "entropy", "top_logprobs", "top_ids", "lse")
     saved = oz2.TokenLogprobs(logprobs=one, lse=one, entropy=None, top_logprobs=None, top_ids=None)
     assert saved.lse is one and saved.z_max is None and saved.log_sum is None
+
+
+# ------------------------------------------------------------------ adamw
+def test_a_state_is_that_of_its_parameters():
+    sizes = [300, 10, 5]
+    for bits, master in ((32, False), (8, True)):
+        state = oz2.adamw_state([torch.ones(n, dtype=torch.bfloat16) for n in sizes], bits=bits, master=master)
+        copies = [state, state._replace(exp_avg=state.exp_avg.clone()), copy.copy(state), copy.deepcopy(state)]
+        file = io.BytesIO()
+        torch.save(state, file)
+        file.seek(0)
+        copies.append(torch.load(file, weights_only=False))
+        for s in copies:
+            assert type(s) is oz2.AdamWState and s.sizes == sizes
+            assert steps._check_state(s, sizes, torch.bfloat16, -1) == bits
+            # as many blocks of 256 each
+            for other in ([10, 300, 5], [300, 5, 10], [301, 10, 5], [300, 10, 5, 0], [1, 1, 1, 1]):
+                with pytest.raises(ValueError, match="another order"):
+                    steps._check_state(s, other, torch.bfloat16, -1)
+        # tensors alone: their length is known, and no more
+        loose = oz2.AdamWState(*state)
+        assert loose.sizes is None and steps._check_state(loose, [10, 300, 5], torch.bfloat16, -1) == bits
+        with pytest.raises(ValueError):
+            steps._check_state(loose, [300, 300, 5], torch.bfloat16, -1)

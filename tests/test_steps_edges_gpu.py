@@ -184,3 +184,14 @@ def test_nan_at_the_first_place_of_crowded_rows(oz2):
     assert torch.equal(got.top_ids[::40], order)
     assert got.top_ids[0, 0] == 0 and got.top_ids[40, :2].tolist() == [0, 77] and got.top_ids[80, 0] == 8
     assert bool(got.top_logprobs[[0, 40, 80]].isnan().all()) and bool(torch.isfinite(got.top_logprobs[120]).all())
+
+
+def test_adamw_refuses_the_state_of_other_parameters(oz2):
+    params, grads = tensors([300, 10], BF16, F32)
+    state = oz2.adamw_state(params, bits=8, master=True)
+    before = [t.clone() for t in (*params, *state)]
+    with pytest.raises(ValueError, match="another order"):
+        oz2.adamw(params[::-1], grads[::-1], state, lr=1e-3)
+    for a, b in zip((*params, *state), before):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    check_step(oz2, params, grads, state)
