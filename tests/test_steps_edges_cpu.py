@@ -57,3 +57,11 @@ def test_a_state_is_that_of_its_parameters():
         assert loose.sizes is None and steps._check_state(loose, [10, 300, 5], torch.bfloat16, -1) == bits
         with pytest.raises(ValueError):
             steps._check_state(loose, [300, 300, 5], torch.bfloat16, -1)
+
+
+def test_what_is_no_tensor_is_named():
+    params = [torch.ones(4), torch.ones(3)]
+    state = oz2.adamw_state(params)
+    for p, g, name in ((params, [torch.ones(4), None], r"grads\[1\]"), (params, [None, None], r"grads\[0\]"), ([None, params[1]], params, r"params\[0\]")):
+        with pytest.raises(TypeError, match=name + " must be a tensor, got NoneType"):
+            oz2.adamw(p, g, state, lr=1e-3)
