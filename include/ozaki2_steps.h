@@ -134,9 +134,9 @@ oz2_status ozaki2_token_logprobs(const oz2_token_logprobs_args* args, void* stre
  * and entropy (used with dentropy) are ozaki2_token_logprobs'.  z_max and log_sum
  * may be NULL where its lse is given instead, which is not read beside them: log p
  * then has a rounding of lse's size, which shows where one token has almost all of
- * the probability.  Masked logits
- * and rows of -inf alone get 0; rows with NaN, +inf or a target outside
- * [0, vocab) get NaN.  dlogits [rows][vocab] of the logits' type may be the
+ * the probability.  Masked logits get 0, but for a target among them, which gets
+ * g / temperature like one of probability 0; rows of -inf alone get 0; rows with
+ * NaN, +inf or a target outside [0, vocab) get NaN.  dlogits [rows][vocab] of the logits' type may be the
  * logits themselves (same leading dimension).
  */
 typedef struct {

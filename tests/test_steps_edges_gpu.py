@@ -195,3 +195,21 @@ def test_adamw_refuses_the_state_of_other_parameters(oz2):
     for a, b in zip((*params, *state), before):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     check_step(oz2, params, grads, state)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_gradient_of_masked_targets(oz2, dtype, entropy):
+    # a target that is masked has log p -inf, whose gradient is that of probability 0; no other masked logit has one
+    for vocab, temperature in ((9, 1.0), (3001, 0.5)):
+        logits = normal(4, vocab, dtype=dtype)
+        logits[:3, ::2] = -INF
+        logits[3] = -INF
+        targets = torch.tensor([2, 1, -100, 4], device="cuda")
+        saved = oz2.token_logprobs(logits, targets, temperature=temperature, entropy=entropy)
+        assert saved.logprobs[0] == saved.logprobs[3] == -INF
+        g = torch.full((4,), 3.0, device="cuda")
+        d = oz2.token_logprobs_backward(g, logits, targets, saved, dentropy=g if entropy else None, temperature=temperature)
+        assert d[0, 2] == 3.0 / temperature
+        d[0, 2] = 0
+        assert not d[:, ::2].any() and not d[3].any() and bool(d[:2, 1::2].all())
