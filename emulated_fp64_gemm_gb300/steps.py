@@ -207,7 +207,7 @@ def token_logprobs(logits, targets, *, temperature=1.0, top=0, entropy=False, ig
     With z = logits / temperature: log p of each row's target, 0 where that is
     `ignore_index` and NaN where it is any other number outside the vocabulary;
     with `entropy` the entropy; with `top` (at most 32) the most likely tokens,
-    the lowest id first among equal ones.  -inf masks a logit, and so does any z below
+    by their logits, the lowest id first among equal ones.  -inf masks a logit, and so does any z below
     the 32-bit range; a row of those alone has log p -inf and entropy 0, a row with NaN
     or +inf has NaN."""
     dtype, device = logits.dtype, logits.get_device()

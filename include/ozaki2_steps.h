@@ -95,7 +95,9 @@ oz2_status ozaki2_rms_norm_backward(const oz2_rms_norm_backward_args* args, void
  *   lse = m + log_sum = log sum exp z,
  *   logprobs = log p of the row's target,  entropy = -sum p log p,
  *   top_logprobs, top_ids [rows][top] = the `top` largest log p and their places,
- *   in falling order, the lowest place first among equals.
+ *   in falling order of their logits, the lowest place first among equal ones (so
+ *   that different logits whose log p are one number of 32 bits, or both -inf, are
+ *   in order too).
  * targets [rows]; a target that is ignore_index has logprob 0, any other one
  * outside [0, vocab) NaN.  lse and entropy may be NULL, and where top is 0 the last two.
  * 0 <= top <= OZ2_TOP_MAX, top <= vocab; temperature finite, 1e-30 at least;

@@ -213,3 +213,22 @@ def test_gradient_of_masked_targets(oz2, dtype, entropy):
         assert d[0, 2] == 3.0 / temperature
         d[0, 2] = 0
         assert not d[:, ::2].any() and not d[3].any() and bool(d[:2, 1::2].all())
+
+
+@pytest.mark.parametrize("vocab", [40, 5000, 70000])
+def test_alternatives_fall_by_their_logits(oz2, vocab):
+    """Also where the temperature, or the sum of a row, leaves nothing of the difference: -3e38 / 0.5 is masked like -inf,
+    and logits of 2^-24 and less beside 1 have one log p."""
+    logits = torch.full((3, vocab), -INF, device="cuda")
+    logits[0, 7::3] = -3e38
+    logits[0, 5] = 1.0
+    logits[1, 9::2] = -3.2e38
+    logits[1, 30] = -3.1e38
+    logits[2] = 1.0
+    logits[2, ::2] = torch.arange((vocab + 1) // 2, device="cuda") * 2.0**-149
+    targets = torch.zeros(3, dtype=torch.int64, device="cuda")
+    for top in (1, 9, 32):
+        got = oz2.token_logprobs(logits, targets, temperature=0.5, top=top)
+        want = torch.sort(logits, dim=-1, descending=True, stable=True).indices[:, :top]
+        assert torch.equal(got.top_ids, want)
+        assert got.top_logprobs[0, 0] == 0 and bool((got.top_logprobs[0, 1:] == -INF).all() & (got.top_logprobs[1] == -INF).all())
