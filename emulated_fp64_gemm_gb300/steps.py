@@ -197,7 +197,7 @@ def _check_targets(logits, targets, device):
 
 def _temperature(t) -> float:
     if not 1e-30 <= t <= 1e30:
-        raise ValueError(f"temperature must be positive and finite, got {t}")
+        raise ValueError(f"temperature must lie between 1e-30 and 1e30, got {t}")
     return t
 
 

@@ -100,7 +100,7 @@ oz2_status ozaki2_rms_norm_backward(const oz2_rms_norm_backward_args* args, void
  *   in order too).
  * targets [rows]; a target that is ignore_index has logprob 0, any other one
  * outside [0, vocab) NaN.  lse and entropy may be NULL, and where top is 0 the last two.
- * 0 <= top <= OZ2_TOP_MAX, top <= vocab; temperature finite, 1e-30 at least;
+ * 0 <= top <= OZ2_TOP_MAX, top <= vocab; 1e-30 <= temperature <= 1e30;
  * dtype: any, of the logits.  rows and vocab may be zero only together with
  * their outputs: vocab is 1 at least where there are rows.
  *

@@ -1,6 +1,7 @@
 """Host-side checks of the step operators beside those of test_steps_cpu: what a call may leave out, and what it refuses."""
 import copy
 import io
+import os
 
 import pytest
 
@@ -9,6 +10,7 @@ from emulated_fp64_gemm_gb300 import _build
 
 torch = pytest.importorskip("torch")
 from emulated_fp64_gemm_gb300 import steps  # noqa: E402
+from tests._util import ROOT  # noqa: E402
 from tests.test_steps_cpu import CUDA, INVALID, P, logprobs, logprobs_backward  # noqa: E402
 
 
@@ -65,3 +67,14 @@ def test_what_is_no_tensor_is_named():
     for p, g, name in ((params, [torch.ones(4), None], r"grads\[1\]"), (params, [None, None], r"grads\[0\]"), ([None, params[1]], params, r"params\[0\]")):
         with pytest.raises(TypeError, match=name + " must be a tensor, got NoneType"):
             oz2.adamw(p, g, state, lr=1e-3)
+
+
+# ------------------------------------------------------------------ temperatures
+def test_temperatures_are_refused_by_their_bounds(lib):
+    for t in (1e31, 9.9e-31, -1.0, float("inf"), float("nan")):
+        assert logprobs(lib, temperature=t) == logprobs_backward(lib, temperature=t) == INVALID
+        with pytest.raises(ValueError, match="between 1e-30 and 1e30"):
+            steps._temperature(t)
+    assert "1e-30 <= temperature <= 1e30" in open(os.path.join(ROOT, "include", "ozaki2_steps.h")).read()
+    for t in (1e-30, 1, 1e30):
+        assert steps._temperature(t) == t
