@@ -282,17 +282,12 @@ template <typename T>
 struct Raw8 {
   uint4 u;
   __device__ __forceinline__ void read(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void values(float (&v)[8]) const { values8<T>(&u, v); }
 };
 template <>
 struct Raw8<float> {
   float f[8];
   __device__ __forceinline__ void read(const float* p) { load8(p, true, 8, f); }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-  }
   __device__ __forceinline__ void values(float (&v)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = f[i];

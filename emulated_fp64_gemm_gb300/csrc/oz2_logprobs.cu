@@ -263,7 +263,6 @@ __device__ __forceinline__ Parts relative_to(float top, float from, Parts v, flo
 }
 
 // ------------------------------------------------------------------ alternatives
-// The block's `top` largest place keys go into sh.list, in order (0: there are fewer).
 // Those of N neighbouring elements whose key is at least `least`, into room that one atomic gives: the order is made up for
 // by the sorting.
 template <int THREADS, int N>
@@ -400,7 +399,8 @@ __device__ __forceinline__ void find_threshold(Shared<THREADS>& sh, int top) {
   }
   if (above == top - 1) sh.threshold = k;
 }
-// ... and behind another the elements that reach it.  mine: the key of m, 0 for a thread without elements.
+// ... and behind another the elements that reach it: the block's `top` largest place keys go into sh.list, in order (0: there
+// are fewer).  mine: the key of m, 0 for a thread without elements.
 template <typename T, int THREADS>
 __device__ __forceinline__ void find_alternatives(Shared<THREADS>& sh, const Slice<T, THREADS>& s, uint32_t mine, int top) {
   using S = Shared<THREADS>;
