@@ -232,3 +232,66 @@ def test_alternatives_fall_by_their_logits(oz2, vocab):
         want = torch.sort(logits, dim=-1, descending=True, stable=True).indices[:, :top]
         assert torch.equal(got.top_ids, want)
         assert got.top_logprobs[0, 0] == 0 and bool((got.top_logprobs[0, 1:] == -INF).all() & (got.top_logprobs[1] == -INF).all())
+
+
+# ------------------------------------------------------------------ rows that share blocks
+# rows enough for every choice of warps per row and rows per run, a number that no run divides
+MANY_ROWS = [(9001, 128), (5003, 1024), (5003, 2048), (2731, 4096), (1307, 8192), (1409, 8200), (1003, 10240), (701, 10240), (1103, 12288),
+             (709, 16384)]
+
+
+@pytest.mark.parametrize("rows,cols", MANY_ROWS)
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_norm_of_many_aligned_rows(oz2, rows, cols, dtype):
+    x, r, w = normal(rows, cols, dtype=dtype), normal(rows, cols, dtype=dtype, seed=1), normal(cols, dtype=dtype, seed=2)
+    # rows unlike each other, so that one in the place of another shows
+    x *= torch.logspace(-2, 2, rows, base=2, device="cuda")[:, None].to(dtype)
+    plain, = check_norm(oz2, x, w)
+    y, s = check_norm(oz2, x, w, r)
+    for block in (None, 128):
+        check_norm(oz2, x, w, quantize=True, block=block)
+        check_norm(oz2, x, w, r, quantize=True, block=block)
+    over, res = x.clone(), r.clone()
+    got = oz2.rms_norm(over, w, residual=res, out=over, residual_out=res)
+    assert got[0] is over and got[1] is res and torch.equal(over, y) and torch.equal(res, s)
+    over = x.clone()
+    assert torch.equal(oz2.rms_norm(over, w, out=over), plain)
+
+
+@pytest.mark.parametrize("rows,cols", [(1409, 8200), (1003, 10240), (701, 12288), (305, 16384), (4001, 1000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_gradient_of_many_aligned_rows(oz2, rows, cols, dtype):
+    """Sums of cols products are off by 2^-17 of their magnitudes (as in test_steps_gpu), those of `rows` parts by 2^-16."""
+    x, dy, ds, w = (normal(rows, cols, dtype=dtype, seed=i) for i in range(4))
+    w = w[0]
+    u, tiny = UNIT[dtype], TINY[dtype]
+    for d in (None, ds):
+        dx, dw = oz2.rms_norm_backward(dy, x, w, dresidual=d)
+        wdx, wdw, size, wsize = ref.rms_norm_backward(dy.double(), x.double(), w.double(), None if d is None else d.double(), 1e-6)
+        err = 2.0**-15 * size
+        assert_within(dx, wdx, err + u * (wdx.abs() + err) + tiny, "dx")
+        err = 2.0**-16 * wsize
+        assert_within(dw, wdw, err + u * (wdw.abs() + err) + tiny, "dw")
+        over = dy.clone()
+        assert torch.equal(oz2.rms_norm_backward(over, x, w, dresidual=d, out=over)[0], dx)
+
+
+# ------------------------------------------------------------------ adamw
+@pytest.mark.parametrize("dtype,grad_dtype,master", [(BF16, BF16, False), (F16, F32, True)])
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("sizes", [[1_500_000, 7, 900_001], [3_000_003, 12_345, 4_000_000]])
+def test_adamw_of_long_tensors(oz2, dtype, grad_dtype, master, bits, sizes):
+    # several blocks of 256 elements per warp: 8-bit states to the bit over steps
+    params, _ = tensors(sizes, dtype, grad_dtype)
+    state = oz2.adamw_state(params, bits=bits, master=master)
+    for step in range(2):
+        check_step(oz2, params, tensors(sizes, dtype, grad_dtype, seed=1000 * step)[1], state, seed=99)
+
+
+@pytest.mark.parametrize("count", [24, 25, 128, 160, 880, 881])
+def test_adamw_of_as_many_tensors_as_a_launch_takes(oz2, count):
+    sizes = [1 + (i * 37) % 600 for i in range(count)]
+    params, _ = tensors(sizes, BF16, BF16)
+    state = oz2.adamw_state(params, bits=8)
+    for step in range(2):
+        check_step(oz2, params, tensors(sizes, BF16, BF16, seed=1000 * step)[1], state, seed=5)
