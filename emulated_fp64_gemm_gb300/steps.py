@@ -174,19 +174,34 @@ def rms_norm_backward(dy, x, weight, *, dresidual=None, eps=1e-6, need_dweight=T
 
 
 # ------------------------------------------------------------------ token_logprobs
-class TokenLogprobs(NamedTuple):
-    """What `token_logprobs` returns; None for what was not asked for.
-
-    Log p is z - z_max - log_sum, or z - lse with a rounding of lse's size: a program that keeps a single number per row
-    may keep lse, and give its gradient TokenLogprobs(logprobs=..., lse=...)."""
-
+class _TokenLogprobs(NamedTuple):
     logprobs: torch.Tensor                        # (rows,) log p of each row's target
     z_max: Optional[torch.Tensor] = None          # (rows,) the largest logit / temperature
     log_sum: Optional[torch.Tensor] = None        # (rows,) log of the sum of exp(z - z_max)
     entropy: Optional[torch.Tensor] = None        # (rows,) -sum p log p
     top_logprobs: Optional[torch.Tensor] = None   # (rows, top) the largest log p, falling
     top_ids: Optional[torch.Tensor] = None        # (rows, top) int64, their places
-    lse: Optional[torch.Tensor] = None            # (rows,) z_max + log_sum
+
+
+class TokenLogprobs(_TokenLogprobs):
+    """What `token_logprobs` returns; None for what was not asked for.
+
+    Beside the tuple's six it has `lse` (rows,), z_max + log_sum.  Log p is z - z_max - log_sum, or z - lse with a
+    rounding of lse's size: a program that keeps a single number per row may keep lse, and give its gradient
+    TokenLogprobs(logprobs=..., lse=...)."""
+
+    lse = None
+
+    def __new__(cls, logprobs, z_max=None, log_sum=None, entropy=None, top_logprobs=None, top_ids=None, lse=None):
+        self = super().__new__(cls, logprobs, z_max, log_sum, entropy, top_logprobs, top_ids)
+        self.lse = lse
+        return self
+
+    def _replace(self, **changes):
+        lse = changes.pop("lse", self.lse)
+        new = super()._replace(**changes)
+        new.lse = lse
+        return new
 
 
 def _check_targets(logits, targets, device):

@@ -32,7 +32,12 @@ def test_lse_stands_for_both_numbers(lib):
 
 def test_names_of_what_log_probabilities_keep():
     one = torch.zeros(1)
-    assert oz2.TokenLogprobs._fields == ("logprobs", "z_max", "log_sum", "entropy", "top_logprobs", "top_ids", "lse")
+    assert oz2.TokenLogprobs._fields == ("logprobs", "z_max", "log_sum", "entropy", "top_logprobs", "top_ids")
+    logprobs, z_max, log_sum, entropy, top_logprobs, top_ids = oz2.TokenLogprobs(*range(6), lse=7)  # six, as ever
+    assert (logprobs, z_max, log_sum, entropy, top_logprobs, top_ids) == (0, 1, 2, 3, 4, 5)
+    for t in (oz2.TokenLogprobs(*range(6), lse=7), oz2.TokenLogprobs(*range(6), 7)):
+        assert t.lse == copy.copy(t).lse == t._replace(z_max=9).lse == 7 and t._replace(z_max=9).z_max == 9
+        assert t._replace(lse=8).lse == 8 and t._replace(lse=None).lse is None and t[:4] == (0, 1, 2, 3)
     saved = oz2.TokenLogprobs(logprobs=one, lse=one, entropy=None, top_logprobs=None, top_ids=None)
     assert saved.lse is one and saved.z_max is None and saved.log_sum is None
 
