@@ -371,7 +371,7 @@ __device__ __forceinline__ float infinity() { return __int_as_float(0x7F800000);
 // 1 / s as the sum of two numbers, hi below it and lo what is left but for 2^-40 of it.  y hi + y lo, the latter rounded and
 // the sum rounded once, is then y / s off by half an ulp and a little, and exact where y / s is a number of 32 bits, as
 // all those are that lie between two codes: with a single reciprocal a tie may go to the other side.  (8192 x 8192 with
-// residual, a scale per row 70.1 us and per 128 columns 73.6; with a single reciprocal 69.9 and 71.8.)
+// residual, a scale per row 70.4 us and per 128 columns 73.4; with a single reciprocal 69.9 and 71.8.)
 struct Inverse {
   float hi, lo;
   __device__ __forceinline__ float2 times(float2 y) const { return fma2(y, both(hi), mul2(y, both(lo))); }

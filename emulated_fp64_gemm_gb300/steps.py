@@ -442,7 +442,8 @@ def adamw(params, grads, state, *, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
     lr and grad_scale (what the gradients are multiplied with) are numbers, or
     float32 tensors of one element on the device, which a captured call reads anew
     at each replay.  8-bit states are rounded by draws that are a function of (element,
-    step, seed)."""
+    step, seed).  16-bit parameters without master copies are rounded to nearest at every
+    step: small rates want `master`."""
     params, grads = list(params), list(grads)
     n = len(params)
     if n == 0 or len(grads) != n:

@@ -109,7 +109,8 @@ oz2_status ozaki2_rms_norm_backward(const oz2_rms_norm_backward_args* args, void
  * alone has z_max, lse and every log p -inf, log_sum and entropy 0.  A row
  * with a NaN or +inf has NaN in all but its top_ids and an ignored target's
  * logprob; NaN comes first among the alternatives.  log p and the entropy stay
- * relatively exact where one token has almost all of the probability.
+ * relatively exact where one token has almost all of the probability; probabilities
+ * below 2^-126 count as 0.
  */
 typedef struct {
   int64_t rows, vocab;
@@ -181,7 +182,9 @@ oz2_status ozaki2_token_logprobs_backward(const oz2_token_logprobs_backward_args
  * bits exp_avg and exp_avg_sq start on 8-byte boundaries.
  * dtype (any) is that of every param, grad_dtype of every gradient: the same,
  * or OZ2_F32.  master: NULL, or the flat 32-bit copies of 16-bit params, which
- * the step then reads and writes; params are their rounding.
+ * the step then reads and writes; params are their rounding.  Without them 16-bit
+ * params are rounded to nearest at every step, and an update of less than half a
+ * step of theirs (2^-9 of a bfloat16 param's size) is lost.
  *
  * bits = 32: exp_avg and exp_avg_sq are floats.  bits = 8: OZ2_ADAMW_BLOCK
  * neighbouring elements share one scale of each (exp_avg_scale, exp_avg_sq_scale):
