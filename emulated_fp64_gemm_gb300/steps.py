@@ -193,7 +193,7 @@ class TokenLogprobs(_TokenLogprobs):
     lse = None
 
     def __new__(cls, logprobs, z_max=None, log_sum=None, entropy=None, top_logprobs=None, top_ids=None, lse=None):
-        self = super().__new__(cls, logprobs, z_max, log_sum, entropy, top_logprobs, top_ids)
+        self = tuple.__new__(cls, (logprobs, z_max, log_sum, entropy, top_logprobs, top_ids))
         self.lse = lse
         return self
 
