@@ -382,7 +382,7 @@ __device__ __forceinline__ Inverse inverse_of(float s) {
 }
 // top / 448, rounded once; infinity and NaN stay.
 __device__ __forceinline__ float scale_of(float top) {
-  constexpr float kHi = 1.0f / 448.0f, kLo = static_cast<float>(1.0 / 448.0 - kHi);
+  constexpr float kHi = 0x1.249248p-9f, kLo = static_cast<float>(1.0 / 448.0 - kHi);  // below 1 / 448, and what is left
   const float y = top < 1e-30f ? 1e-30f : top;
   return fmaf(y, kHi, y * kLo);
 }

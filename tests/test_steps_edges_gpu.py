@@ -295,3 +295,22 @@ def test_adamw_of_as_many_tensors_as_a_launch_takes(oz2, count):
     state = oz2.adamw_state(params, bits=8)
     for step in range(2):
         check_step(oz2, params, tensors(sizes, BF16, BF16, seed=1000 * step)[1], state, seed=5)
+
+
+@pytest.mark.parametrize("cols", [256, 1003, 2048, 20000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_codes_beside_an_infinite_one(oz2, cols, dtype):
+    # an element over the norm times its weight is past the 32-bit range: its block's scale is infinite and stands for
+    # 0 where y is finite (y / scale), itself for NaN
+    x, w = normal(5, cols, dtype=dtype), normal(cols, dtype=dtype, seed=1)
+    x[2, 100], w[100] = 50.0, 3e38
+    x[[0, 1, 3, 4], 100] = 0
+    for residual in (None, torch.zeros_like(x)):
+        for block in (None, 128):
+            q, scale = oz2.rms_norm(x, w, residual=residual, out_dtype=E4M3, block=block)[:2]
+            v, width = values(q), block or cols
+            assert scale[2, 0] == INF and bool(v[2, 100].isnan())
+            v[2, 100] = 0
+            assert not v[2, :width].any()
+            assert bool(torch.isfinite(scale[[0, 1, 3, 4]]).all()) and bool(torch.isfinite(scale[2, 1:]).all())
+            assert bool(torch.isfinite(v).all()) and (block is None or bool(v[2, 128:].abs().sum() > 0))
